@@ -1,0 +1,53 @@
+// Operand helpers shared by the attention kernels (internal header).
+#pragma once
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+namespace csa2 {
+
+// byte offset of 16-B chunk `ch` (0..7) in row r of a 128B-swizzled 1024-B atom
+__device__ __forceinline__ uint32_t sw128(uint32_t r, uint32_t ch) { return r * 128u + ((ch ^ (r & 7u)) << 4); }
+
+// kind::f16 instruction descriptor: bf16 x bf16 (or f16 x f16) -> f32, M=128,
+// N = n (a multiple of 16), A K- or MN-major.
+__host__ __device__ constexpr uint32_t idesc_m128(uint32_t a_mn_major, bool f16, uint32_t n) {
+  return (1u << 4)                     // D format f32
+         | ((f16 ? 0u : 1u) << 7)      // A: f16 0, bf16 1
+         | ((f16 ? 0u : 1u) << 10)     // B: f16 0, bf16 1
+         | (a_mn_major << 15)          // A major-ness
+         | ((n >> 3) << 17)            // N / 8
+         | ((128u >> 4) << 24);        // M / 16
+}
+
+// Eight E2M1 codes (channel i in nibble i of w) -> eight f16 values as four
+// f16x2 words, by the hardware converter (exact: E2M1 is a subset of f16).
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&out)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3])
+      : "r"(w));
+}
+
+// Two E4M3 codes (low byte first) -> f16x2 bits (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)two));
+  return h;
+}
+
+// cos and sin of theta = pos * inv_freq (inv_freq = rope_base^(-2i/64), computed
+// on the host in fp64): the product and its reduction modulo 2 pi are done in
+// fp64 (pos reaches 2^20, so theta reaches ~1e6 rad), the sine and cosine of the
+// reduced angle in fp32.
+__device__ __forceinline__ void rope_cs(double inv_freq, int pos, float &c, float &s) {
+  const double th = (double)pos * inv_freq;
+  const double k = rint(th * 0.15915494309189535);            // 1 / (2 pi)
+  const double r = fma(-k, 6.283185307179586, th);
+  sincosf((float)r, &s, &c);
+}
+
+}  // namespace csa2
