@@ -7,7 +7,8 @@ library is not built, importing the binding raises.
 """
 from ._lib import (  # noqa: F401
     CSA2_IDX_MXFP4, CSA2_KV_NVFP4, CSA2_OP_BUILD_CACHE, CSA2_OP_DECODE, CSA2_OP_DECODE_HOST, CSA2_OP_DECODE_MQ,
-    CSA2_OP_DECODE_REINDEX, CSA2_OP_SPARSE_ATTN, csa2_build_cache, csa2_decode_reindex, csa2_index_key_proj,
+    CSA2_OP_DECODE_REINDEX, CSA2_OP_PAGED_ATTN, CSA2_OP_SPARSE_ATTN, csa2_cache_read, csa2_page_plan,
+    csa2_paged_attn, csa2_qk_norm_rope, csa2_build_cache, csa2_decode_reindex, csa2_index_key_proj,
     csa2_profile_events,
     CSA2_OP_TOPK, CSA2_OUT_BF16, CSA2_OUT_F32, CSA2_SWA_MXFP8, CSA2Error, EXPORTS, LIB_PATH, csa2_check_bounded_wait,
     csa2_decode,

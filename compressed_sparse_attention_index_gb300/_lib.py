@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(HERE, "libcsa2.so")
 CSA2_KV_NVFP4, CSA2_IDX_MXFP4, CSA2_SWA_MXFP8 = 0, 1, 2
 CSA2_OUT_BF16, CSA2_OUT_F32 = 0, 1
 CSA2_OP_TOPK, CSA2_OP_SPARSE_ATTN, CSA2_OP_DECODE, CSA2_OP_DECODE_HOST, CSA2_OP_DECODE_MQ = 0, 1, 2, 3, 4
-CSA2_OP_BUILD_CACHE, CSA2_OP_DECODE_REINDEX = 5, 6
+CSA2_OP_BUILD_CACHE, CSA2_OP_DECODE_REINDEX, CSA2_OP_PAGED_ATTN = 5, 6, 7
 STATUS = {0: "CSA2_OK", 1: "CSA2_ERR_INVALID_ARG", 2: "CSA2_ERR_UNSUPPORTED", 3: "CSA2_ERR_CUDA",
           4: "CSA2_ERR_BOUNDS", 5: "CSA2_ERR_TIMEOUT", 6: "CSA2_ERR_WORKSPACE"}
 
@@ -25,7 +25,8 @@ EXPORTS = ["csa2_default_params", "csa2_entry_bytes", "csa2_status_string", "csa
            "csa2_index_score", "csa2_topk", "csa2_sparse_attn", "csa2_workspace_size",
            "csa2_get_device_status", "csa2_topk_noalloc", "csa2_decode", "csa2_decode_host",
            "csa2_index_score_mq", "csa2_decode_mq", "csa2_check_bounded_wait", "csa2_index_key_proj",
-           "csa2_build_cache", "csa2_decode_reindex", "csa2_profile_events"]
+           "csa2_build_cache", "csa2_decode_reindex", "csa2_profile_events", "csa2_page_plan", "csa2_qk_norm_rope",
+           "csa2_cache_read", "csa2_paged_attn"]
 
 
 class CSA2Error(RuntimeError):
@@ -76,6 +77,11 @@ def load(path: str = LIB_PATH):
         "csa2_check_bounded_wait": (i32, [ctypes.c_uint, P]),
         "csa2_index_key_proj": (i32, [P, i64, P, P, P]),
         "csa2_build_cache": (i32, [P, i64, i32, P, P, P, P, P, P, sz, P]),
+        "csa2_page_plan": (i32, [P, P, i32, i32, i32, P, i32, P, P, i64, i32, P, i32, P, P, P]),
+        "csa2_qk_norm_rope": (i32, [P, i64, P, P, P, i64, P, P, P, P, P, i32, ctypes.c_double, P, i64, P, i64, PP, P]),
+        "csa2_cache_read": (i32, [i32, P, i64, P, i64, P, i32, P]),
+        "csa2_paged_attn": (i32, [P, P, i32, i32, P, i64, i32, P, i32, P, i32, P, P, P, P, P, i32, P, i32, P, PP, P, sz,
+                                  P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -241,3 +247,36 @@ def csa2_build_cache(tokens, n_tokens, m, gate_logits, w_idx, kv, idx_nib, idx_s
     _check("csa2_build_cache", load().csa2_build_cache(_ptr(tokens), int(n_tokens), int(m), _ptr(gate_logits),
                                                          _ptr(w_idx), _ptr(kv), _ptr(idx_nib), _ptr(idx_scale),
                                                          _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def csa2_page_plan(seq_len, new_len, n_seq, page_size, n_pages, free_pages, n_free, free_head, block_table,
+                   table_stride, swa_cap, desc, max_tokens, first, totals, stream=None):
+    _check("csa2_page_plan", load().csa2_page_plan(
+        _ptr(seq_len), _ptr(new_len), int(n_seq), int(page_size), int(n_pages), _ptr(free_pages), int(n_free),
+        _ptr(free_head), _ptr(block_table), int(table_stride), int(swa_cap), _ptr(desc), int(max_tokens), _ptr(first),
+        _ptr(totals), _stream(stream)))
+
+
+def csa2_qk_norm_rope(q, q_stride, q_gain, q_out, latent, latent_stride, latent_gain, latent_out, pos, slot, swa_slot,
+                      n, eps, kv_cache, kv_slots, swa_cache, swa_slots, params=None, stream=None):
+    pp = ctypes.byref(params) if params is not None else None
+    _check("csa2_qk_norm_rope", load().csa2_qk_norm_rope(
+        _ptr(q), int(q_stride), _ptr(q_gain), _ptr(q_out), _ptr(latent), int(latent_stride), _ptr(latent_gain),
+        _ptr(latent_out), _ptr(pos), _ptr(slot), _ptr(swa_slot), int(n), float(eps), _ptr(kv_cache), int(kv_slots),
+        _ptr(swa_cache), int(swa_slots), pp, _stream(stream)))
+
+
+def csa2_cache_read(kind, cache, n_slots, slots, n, out, out_dtype, stream=None):
+    _check("csa2_cache_read", load().csa2_cache_read(int(kind), _ptr(cache), int(n_slots), _ptr(slots), int(n),
+                                                     _ptr(out), int(out_dtype), _stream(stream)))
+
+
+def csa2_paged_attn(q, pages, n_pages, page_size, block_table, table_stride, n_seq, sel, sel_stride, swa_cache,
+                    swa_cap, q_seq, n_vis, pos, swa_first, swa_cnt, n_q, out, out_dtype, lse=None, params=None,
+                    workspace=None, workspace_bytes=0, stream=None):
+    pp = ctypes.byref(params) if params is not None else None
+    _check("csa2_paged_attn", load().csa2_paged_attn(
+        _ptr(q), _ptr(pages), int(n_pages), int(page_size), _ptr(block_table), int(table_stride), int(n_seq),
+        _ptr(sel), int(sel_stride), _ptr(swa_cache), int(swa_cap), _ptr(q_seq), _ptr(n_vis), _ptr(pos),
+        _ptr(swa_first), _ptr(swa_cnt), int(n_q), _ptr(out), int(out_dtype), _ptr(lse), pp, _ptr(workspace),
+        int(workspace_bytes), _stream(stream)))

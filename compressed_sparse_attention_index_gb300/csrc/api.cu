@@ -32,7 +32,7 @@ int *status_word_ptr() { return status_ptr(); }
 
 static bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
-static bool params_ok(const csa2_params *p) {
+bool params_ok(const csa2_params *p) {
   if (p == nullptr) return true;   // null = the pages' constants
   return p->heads == kHeads && p->dim == kDim && p->rope_dim == kRopeDim && p->rope_off == kRopeOff &&
          p->idx_heads == kIdxHeads && p->idx_dim == kIdxDim && p->topk == kTopK && p->swa == kSwa &&
@@ -212,6 +212,10 @@ csa2_status csa2_workspace_size(int op, int n_q, int64_t n_items, int k, size_t 
   if (op == CSA2_OP_BUILD_CACHE) {
     if (n_items < 0 || (k != 1 && k != 2)) return CSA2_ERR_INVALID_ARG;
     *bytes = build_cache_workspace_bytes(n_items, k);
+    return CSA2_OK;
+  }
+  if (op == CSA2_OP_PAGED_ATTN) {
+    *bytes = paged_attn_workspace_bytes();
     return CSA2_OK;
   }
   if (op == CSA2_OP_DECODE_MQ) {

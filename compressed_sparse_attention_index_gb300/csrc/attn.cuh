@@ -1,7 +1,10 @@
 // Operand helpers shared by the attention kernels (internal header).
 #pragma once
 #include <cuda_fp16.h>
+#include <math.h>
 #include <stdint.h>
+
+#include "common.cuh"
 
 namespace csa2 {
 
@@ -48,6 +51,19 @@ __device__ __forceinline__ void rope_cs(double inv_freq, int pos, float &c, floa
   const double k = rint(th * 0.15915494309189535);            // 1 / (2 pi)
   const double r = fma(-k, 6.283185307179586, th);
   sincosf((float)r, &s, &c);
+}
+
+// The same angles in turns, as 64-bit fixed-point fractions: one position's
+// turns modulo one in 2^-64ths, so that pos * turn (wrapping) drops whole turns
+// exactly; the fraction (53 bits) goes to fp32 for the sine and cosine.
+inline void rope_turns(double rope_base, uint64_t (&turn)[kRopeDim / 2]) {
+  for (int i = 0; i < kRopeDim / 2; i++) {
+    const double t = pow(rope_base, -2.0 * i / (double)kRopeDim) / 6.283185307179586;
+    turn[i] = (uint64_t)ldexp(t - floor(t), 64);
+  }
+}
+__device__ __forceinline__ void turn_cs(uint64_t u, float &c, float &s) {
+  sincospif((float)(int64_t)u * 0x1p-63f, &s, &c);
 }
 
 }  // namespace csa2

@@ -7,6 +7,8 @@
 
 #include <atomic>
 
+#include "csa2.h"
+
 namespace csa2 {
 
 // Host-side caches, one entry per device ordinal below kMaxDevices.  Host
@@ -225,8 +227,81 @@ cudaError_t launch_attn_tc(const void *q, const void *kv, int64_t n_max, int n_s
 // selection: one chunk per CTA for n_q queries.
 bool attn_handoff_fits(int n_q);
 
+// csa2_qk_norm_rope (see csa2.h).  The launch fills the last block of fields.
+struct NormArgs {
+  const uint16_t *q;          // null: no queries
+  int64_t q_stride;
+  const float *q_gain;
+  uint16_t *q_out;
+  const uint16_t *lat;        // null: no latents
+  int64_t lat_stride;
+  const float *lat_gain;
+  uint16_t *lat_out;
+  const int32_t *pos, *slot, *swa_slot;
+  int n;
+  uint8_t *kv;
+  int64_t kv_slots;
+  uint8_t *swa;
+  int64_t swa_slots;
+  int *status;
+  double eps;
+  float eps_hi, eps_lo;
+  int lat_ctas;
+  uint64_t turn[32];
+};
+cudaError_t launch_qk_norm_rope(NormArgs A, double eps, double rope_base, cudaStream_t st);
+
+// csa2_page_plan (see csa2.h).  row_cap: entries a block table row can hold.
+constexpr int kPlanThreads = 1024, kPlanMaxSeq = 16384;
+struct PlanArgs {
+  const int32_t *seq_len, *new_len;
+  int n_seq, page, n_pages;
+  const int32_t *free_pages;
+  int n_free;
+  const int32_t *free_head;
+  int32_t *block_table;
+  int64_t table_stride, row_cap;
+  int swa_cap;
+  int32_t *desc;
+  int max_tokens;
+  int32_t *first, *totals;
+  int *status;
+};
+cudaError_t launch_page_plan(const PlanArgs &P, cudaStream_t st);
+
+cudaError_t launch_cache_read(int kind, const void *cache, int64_t n_slots, const int32_t *slots, int64_t n, void *out,
+                              int out_dtype, int *status, cudaStream_t st);
+
+// csa2_paged_attn (see csa2.h).  The launch fills the last block of fields.
+struct PagedArgs {
+  const uint16_t *q;
+  const uint8_t *pages;
+  int n_pages, page;
+  const int32_t *table;
+  int64_t table_stride;
+  int n_seq;
+  const int32_t *sel;         // null: every visible entry
+  int sel_stride;
+  const uint8_t *swa;
+  int swa_cap;
+  const int32_t *q_seq, *n_vis, *pos, *swa_first, *swa_cnt;
+  int n_q;
+  void *out;
+  int out_f32;
+  float *lse;                 // null: not wanted
+  int *status;
+  float scale;
+  uint64_t turn[32];
+  float *part, *part_ml;      // split partials and their (maximum, denominator)
+  int4 *joins;                // per CTA: the query whose partials are joined there
+};
+size_t paged_attn_workspace_bytes();
+cudaError_t launch_paged_attn(PagedArgs A, double rope_base, void *ws, cudaStream_t st);
+
 cudaError_t launch_bounded_wait_check(int *status, unsigned long long limit_ns, cudaStream_t st);
 
 int *status_word_ptr();
+// Null, or the pages' constants with a positive scale and RoPE base.
+bool params_ok(const csa2_params *p);
 
 }  // namespace csa2

@@ -9,6 +9,11 @@
  *   3. dequantisation of the selected FP4 latents + 64-head MQA
  *      attention over them and the 128-token FP8 window          csa2_sparse_attn
  *   0. cache write: FP4 / FP8 packing (m=1 or gated m=2)          csa2_fp4_pack
+ * and around it, for caches kept in pages: the plan of a step from the
+ * sequences' lengths (csa2_page_plan), the norm, rotation and cache write of its
+ * tokens (csa2_qk_norm_rope), reading records back (csa2_cache_read), and
+ * attention over paged latents, all visible ones or a selection
+ * (csa2_paged_attn).
  *
  * Conventions (every entry point):
  *   - Returns a csa2_status.  Nothing aborts, prints or allocates device memory.
@@ -81,7 +86,7 @@ enum { CSA2_KV_NVFP4 = 0, CSA2_IDX_MXFP4 = 1, CSA2_SWA_MXFP8 = 2 };
 enum { CSA2_OUT_BF16 = 0, CSA2_OUT_F32 = 1 };
 /* Operations for csa2_workspace_size. */
 enum { CSA2_OP_TOPK = 0, CSA2_OP_SPARSE_ATTN = 1, CSA2_OP_DECODE = 2, CSA2_OP_DECODE_HOST = 3, CSA2_OP_DECODE_MQ = 4,
-       CSA2_OP_BUILD_CACHE = 5, CSA2_OP_DECODE_REINDEX = 6 };
+       CSA2_OP_BUILD_CACHE = 5, CSA2_OP_DECODE_REINDEX = 6, CSA2_OP_PAGED_ATTN = 7 };
 
 /* Model constants.  The kernels are built for the pages' values only
  * (study, reading notes: 64 heads, 512-wide latent, RoPE on 64 of the 512
@@ -441,6 +446,145 @@ csa2_status csa2_build_cache(const void *tokens, int64_t n_tokens, int m, const 
 csa2_status csa2_profile_events(void *begin, void *end);
 
 /*
+ * Paged caches.  The main cache is n_pages pages of page_size KV records,
+ * [n_pages][page_size][288], 32-B aligned; page_size is any positive number.
+ * Row b of a block table (int32 [n_seq][table_stride]) names the pages of
+ * sequence b in order: its entry j is record j % page_size of page
+ * block_table[b][j / page_size], and the entry's slot is its place in the whole
+ * cache, page * page_size + j % page_size (csa2_sparse_attn and csa2_decode keep
+ * their contiguous caches).  The window stays a ring of swa_cap records per
+ * sequence, [n_seq][swa_cap][528], position p of sequence b in slot
+ * b * swa_cap + p % swa_cap.  All pointers belong to the current device.
+ *
+ * csa2_page_plan -- block tables, slots and descriptors of a step from the
+ * sequences' lengths.  Sequence b holds seq_len[b] entries and gets new_len[b]
+ * tokens, at positions seq_len[b], seq_len[b] + 1, ...  The step's tokens are
+ * numbered in sequence order, and so are the pages it needs: columns
+ * ceil(seq_len / page_size) .. ceil((seq_len + new_len) / page_size) - 1 of row b
+ * of the block table are written with the next pages of the free list; no other
+ * column is written.  One launch; the host reads nothing.
+ *
+ *   seq_len, new_len  (device) int32 [n_seq]; n_seq in 0 .. 16384.  A sequence
+ *                with a negative length, or with more entries than its row of
+ *                the block table can hold, records CSA2_ERR_BOUNDS and gets no
+ *                tokens.
+ *   free_pages   (device) int32 [n_free] page ids; free_head (device) int32 [1]
+ *                or NULL (0): the first one to take.  Where the list ends, or
+ *                names no page, CSA2_ERR_BOUNDS is recorded, the column gets -1
+ *                and the tokens on it get slot -1 (so do tokens on an earlier
+ *                column that names no page).
+ *   desc         (device) int32 [7][max_tokens], per token: its sequence
+ *                (q_seq); the entries it sees, itself included (n_vis = pos + 1);
+ *                pos; the window's first ring slot and length (swa_first,
+ *                swa_cnt = min(128, swa_cap, pos + 1)); its slot in the main
+ *                cache; its slot in the window cache, or -1 where a later token
+ *                of the same step takes the same ring slot.  Rows 0 .. 4 are
+ *                csa2_decode_host's h_desc rows.  Columns behind the last token
+ *                get 0, 0, 0, 0, 0, -1, -1: queries that attend to nothing and
+ *                write nothing.  Tokens from max_tokens on are dropped and record
+ *                CSA2_ERR_BOUNDS.  A token that sees later tokens' window records
+ *                in a ring too short for both (swa_cap < 127 + new_len) is the
+ *                caller's to avoid.
+ *   first        (device) int32 [n_seq + 1]: the first token of each sequence,
+ *                then the number of tokens (sums beyond 2^31 - 1 stay there).
+ *   totals       (device) int32 [2]: the tokens, and the pages the step needs
+ *                (advance free_head by as many).
+ *   Limits: n_pages * page_size and n_seq * swa_cap below 2^31.
+ */
+csa2_status csa2_page_plan(const int32_t *seq_len, const int32_t *new_len, int n_seq, int page_size, int n_pages,
+                           const int32_t *free_pages, int n_free, const int32_t *free_head, int32_t *block_table,
+                           int64_t table_stride, int swa_cap, int32_t *desc, int max_tokens, int32_t *first,
+                           int32_t *totals, csa2_stream_t stream);
+
+/*
+ * csa2_qk_norm_rope -- the norm of every query head and of the latent, the
+ * rotation of their last 64 dims, and the latent's cache write, in one pass:
+ * what csa2_sparse_attn and csa2_paged_attn expect "already rotated by
+ * upstream".  ("An infra-oriented diagram of the DeepSeek-V4.1-Flash
+ * architecture", reading notes: RoPE acts on 64 of the 512 dims, and the cache
+ * stays in one rotated form.)  Per 512-wide row x with gain g:
+ *     y_c = g_c x_c / sqrt(mean_c(x_c^2) + eps)
+ * then the pairs (rope_off + 2i, rope_off + 2i + 1), i < 32, are rotated by
+ * +pos:  (a, b) <- (a cos t - b sin t, a sin t + b cos t),
+ * t = pos * rope_base^(-2i/64).  Queries are computed in fp32 and rounded once;
+ * the latent is the exact value rounded once to bf16 (to 2^-32 of it), and its
+ * records are those csa2_fp4_pack makes of that bf16 row, byte for byte.
+ *
+ *   q            (device) bf16, token t's 64 heads at q + t * q_stride elements
+ *                ([64][512] each; q_stride >= 32768, a multiple of 8); NULL: no
+ *                queries.  q_out (device) bf16 [n][64][512]; it may be q itself
+ *                where q_stride is 32768, and must not overlap q otherwise.
+ *   latent       (device) bf16, row t at latent + t * latent_stride elements
+ *                (>= 512, a multiple of 8); NULL: none.  latent_out (device) bf16
+ *                [n][512] or NULL: the normed, rotated latents (the input of
+ *                csa2_index_key_proj); in place as q_out.
+ *   q_gain, latent_gain   (device) fp32 [512], 16-B aligned, or NULL: all ones.
+ *   pos          (device) int32 [n].
+ *   slot         (device) int32 [n]: the KV record of kv_cache (kv_slots records)
+ *                that row t is written to, -1: none; kv_cache NULL: no records.
+ *   swa_slot     the same for the window cache (swa_slots records of 528 B).
+ *                A slot at or above kv_slots / swa_slots is skipped and records
+ *                CSA2_ERR_BOUNDS.  Each slot may be named once per call (the
+ *                bytes of a record named twice are unspecified).
+ *   n            tokens; 0 launches nothing.  eps > 0.
+ */
+csa2_status csa2_qk_norm_rope(const void *q, int64_t q_stride, const float *q_gain, void *q_out, const void *latent,
+                              int64_t latent_stride, const float *latent_gain, void *latent_out, const int32_t *pos,
+                              const int32_t *slot, const int32_t *swa_slot, int n, double eps, void *kv_cache,
+                              int64_t kv_slots, void *swa_cache, int64_t swa_slots, const csa2_params *params,
+                              csa2_stream_t stream);
+
+/*
+ * csa2_cache_read -- records back to 512-wide latents: out[i] is the dequantised
+ * record slots[i], exact in fp32 and rounded once for bf16 (exact there too for
+ * KV records, and for window records down to bf16's smallest value).
+ *   kind      CSA2_KV_NVFP4 or CSA2_SWA_MXFP8 (indexer keys: unsupported).
+ *   cache     (device) n_slots records, 16-B aligned.
+ *   slots     (device) int32 [n]; a negative slot gives zeros, one at or above
+ *             n_slots zeros and CSA2_ERR_BOUNDS.
+ *   out       (device) [n][512], bf16 or fp32 per out_dtype, 16-B aligned.
+ */
+csa2_status csa2_cache_read(int kind, const void *cache, int64_t n_slots, const int32_t *slots, int64_t n, void *out,
+                            int out_dtype, csa2_stream_t stream);
+
+/*
+ * csa2_paged_attn -- csa2_sparse_attn's attention (64 heads, k = v, window, RoPE
+ * undone on the output) over a paged main cache, for every visible entry or for
+ * a selection, with the log-sum-exp of the logits.  A query q of sequence b
+ * attends to the entries [0, n_vis[q]) of b -- or, with sel, to the entries
+ * sel[q] -- and to its window; one new token or several of a sequence, each
+ * with its own n_vis.  A long row is split over the SMs and joined, whatever the
+ * rows' lengths; the same inputs give the same bits on every call.
+ * Arithmetic as csa2_sparse_attn on FP4 latents (f16 products of exact
+ * dequantised latents, fp32 sums, numerators rounded to 11 bits): row-normalised
+ * error against an fp64 evaluation about 2e-4 (under 2e-3), lse to about 1e-6.
+ *
+ *   q            (device) bf16 [n_q][64][512], rotated (csa2_qk_norm_rope).
+ *   pages .. n_seq   the paged cache and its block table (above).  A table entry
+ *                outside [0, n_pages) in a row's visible part: its entries are
+ *                skipped and CSA2_ERR_BOUNDS is recorded.
+ *   sel          NULL, or (device) int32 [n_q][sel_stride], sel_stride in 1 ..
+ *                512: entry indices below n_vis[q], or negative (none); an index at
+ *                or above n_vis[q] is skipped and records CSA2_ERR_BOUNDS.
+ *   swa_cache .. swa_cnt, pos, out, out_dtype, params   as csa2_sparse_attn.
+ *   n_vis        (device) int32 [n_q], at most table_stride * page_size; a query
+ *                with q_seq, n_vis or the window out of range records
+ *                CSA2_ERR_BOUNDS and gets zeros.  A query with no entry at all
+ *                gets zeros and an lse of -inf.
+ *   lse          NULL, or (device) fp32 [n_q][64]: log sum_i exp(l_i), which joins
+ *                outputs over disjoint sets of entries (the un-rotation is linear).
+ *   workspace    (device) >= csa2_workspace_size(CSA2_OP_PAGED_ATTN, 0, 0, 0)
+ *                bytes, 256-B aligned; no initialisation.  Calls that may run at
+ *                the same time need one each.
+ */
+csa2_status csa2_paged_attn(const void *q, const void *pages, int n_pages, int page_size, const int32_t *block_table,
+                            int64_t table_stride, int n_seq, const int32_t *sel, int sel_stride, const void *swa_cache,
+                            int swa_cap, const int32_t *q_seq, const int32_t *n_vis, const int32_t *pos,
+                            const int32_t *swa_first, const int32_t *swa_cnt, int n_q, void *out, int out_dtype,
+                            float *lse, const csa2_params *params, void *workspace, size_t workspace_bytes,
+                            csa2_stream_t stream);
+
+/*
  * csa2_workspace_size -- scratch bytes needed by an operation.
  *   op = CSA2_OP_TOPK:        n_q queries, n_items = items per row (entries,
  *                             blocks, or 16384 pool slots), k.
@@ -451,6 +595,8 @@ csa2_status csa2_profile_events(void *begin, void *end);
  *   op = CSA2_OP_DECODE_MQ:   n_q queries, n_items = n_max, k unused (512).
  *   op = CSA2_OP_BUILD_CACHE: n_q unused, n_items = tokens, k = m (1 or 2).
  *   op = CSA2_OP_DECODE_REINDEX: n_q queries, n_items = n_max, k unused (512).
+ *   op = CSA2_OP_PAGED_ATTN:  n_q, n_items and k unused: the same for every call
+ *                             (two partial outputs per SM, 40 MB).
  * Sizes are for the current device (the attention's split plan follows its
  * SM count).
  */
