@@ -44,31 +44,38 @@
 namespace csa2 {
 
 constexpr int kPgChunk = 128;
-constexpr int kPgSoftWarps = 8, kPgLoadWarps = 16;
-constexpr int kPgSoft = kPgSoftWarps * 32, kPgLoad = kPgLoadWarps * 32;
-constexpr int kPgThreads = kPgSoft + kPgLoad + 128;
-// Registers: 896 threads are launched with 72 each; the softmax groups take what
+constexpr int kPgSoft = 256, kPgLoad = 256;        // threads of the softmax group and of each loading group
+constexpr int kPgThreads = kPgSoft + 2 * kPgLoad + 128;
+// Registers: 896 threads are launched with 72 each; the softmax group takes what
 // the others give up.
-constexpr int kPgRegsSoft = 104, kPgRegsLoad = 64, kPgRegsIssue = 40;
-static_assert(kPgSoft * kPgRegsSoft + kPgLoad * kPgRegsLoad + 128 * kPgRegsIssue <= 72 * kPgThreads, "register split");
-constexpr int kPgSmK = 0;                          // 128 entries x 512 dims f16: [e/8][dim/64][e%8][128 B]
-constexpr int kPgSmQ = kPgSmK + 128 * 1024;        // 64 heads x 512 dims f16, the same order
+constexpr int kPgRegsSoft = 104, kPgRegsK = 64, kPgRegsV = 56, kPgRegsRest = 56;
+static_assert(kPgSoft * kPgRegsSoft + kPgLoad * (kPgRegsK + kPgRegsV) + 128 * kPgRegsRest <= 72 * kPgThreads, "register split");
+constexpr int kPgSlab = 128 * 128 * 2;             // one slab: 128 entries x 128 dims f16
+constexpr int kPgRaw = kPgChunk * kKvBytes;        // one chunk's records
+constexpr int kPgSmV = 0;                          // two slabs: [e/8][dim/64][e%8][128 B]
+constexpr int kPgSmQ = kPgSmV + 2 * kPgSlab;       // 64 heads x 512 dims f16: [h/8][dim/64][h%8][128 B]
 constexpr int kPgSmP = kPgSmQ + 64 * 1024;         // 128 entries x 64 heads f16: [e/8][e%8][128 B]
-constexpr int kPgSmEnd = kPgSmP + 16 * 1024;
+constexpr int kPgSmRaw = kPgSmP + 16 * 1024;       // two chunks of records
+constexpr int kPgSmEnd = kPgSmRaw + 2 * kPgRaw;
 constexpr int kPgSmAlloc = kPgSmEnd + 1024;
-constexpr uint32_t kPgColS = 0, kPgColO = 64, kPgTmemCols = 512;
-constexpr float kPgRaise = 8.f, kPgShift = 7.f;
+static_assert(kPgSmAlloc + 4608 <= 227 * 1024, "shared memory");
+// tensor memory: two S^T tiles, O^T, a ring of two 128-dim slabs of K
+constexpr uint32_t kPgColS = 0, kPgColO = 128, kPgColK = 384, kPgTmemCols = 512;
+constexpr float kPgRaise = 8.f, kPgShift = 7.f, kPgNoRef = 3e38f;   // (kPgNoRef: no entry met yet)
+constexpr int kPgInfo = 8;                         // chunks described in shared memory at a time
 
-// Barriers among the softmax warps (1) and among the loading warps (2); every
-// warp of a group reaches each of them, whatever its waits returned.
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kPgSoft) : "memory"); }
-__device__ __forceinline__ void load_sync() { asm volatile("bar.sync 2, %0;" ::"n"(kPgLoad) : "memory"); }
+// Barriers among the threads of a group; every one of its warps reaches each of
+// them, whatever its waits returned.
+template <int ID>
+__device__ __forceinline__ void group_sync() {
+  asm volatile("bar.sync %0, 256;" ::"n"(ID) : "memory");
+}
 __device__ __forceinline__ bool soft_any(bool p) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)p), "n"(kPgSoft)
+      : "r"((uint32_t)p)
       : "memory");
   return r != 0u;
 }
@@ -119,73 +126,665 @@ struct PagedCursor {
   __device__ __forceinline__ bool window() const { return Q.win > 0 && c == off; }
 };
 
-// The record of row e of an entry chunk, or null (none, or out of range: recorded).
-__device__ __forceinline__ const uint8_t *paged_record(const PagedArgs &A, const PagedCursor &C, int e, bool report) {
-  const int i = (C.local() - (C.Q.win > 0 ? 1 : 0)) * kPgChunk + e;
-  if (i >= C.Q.n) return nullptr;
-  int j = i;
-  if (A.sel != nullptr) {
-    j = __ldg(A.sel + (int64_t)C.qi * A.sel_stride + i);
-    if (j < 0) return nullptr;
-    if (j >= __ldg(A.n_vis + C.qi)) {
-      if (report) record_error(A.status, CSA2_ERR_BOUNDS);
-      return nullptr;
+// What the roles need to know of a chunk (kPgInfo of them, by chunk number).
+// j / page by a multiplication: exact for j below 2^31 (page_mul = ceil(2^(31 + s) /
+// page) with 2^s >= page is at most 2^32 and off by less than one in 2^s)
+__device__ __forceinline__ unsigned paged_col(unsigned j, const PagedArgs &A) {
+  return (unsigned)(((uint64_t)j * A.page_mul) >> A.page_shift);
+}
+
+struct PagedInfo {
+  int4 at;                      // query, place in it, its chunks, its first chunk
+  uint32_t valid[4];            // rows that hold an entry
+  int seq, win;                 // sequence; window entries, 0: entries of the cache
+  float f;                      // logits in log2 units per unit of S
+  int kx;                       // a window's scale (its tile holds 2^kx times its values)
+};
+
+struct PagedShared {
+  uint64_t raw_full[2], raw_free[2], k_full[2], k_free[2], s_full[2], s_free[2], v_full[2], v_free[2];
+  uint64_t p_full, o_done, drain;
+  PagedInfo info[kPgInfo];
+  __align__(16) float less[kHeads];    // minus a head's reference, which is kPgShift below a maximum
+  float alpha[kHeads];
+  float l[4][kHeads], red[4][kHeads];
+  uint32_t tmem, qmax[8];
+  int emin[2], emax[2];         // (per loading group)
+  int scan[kPgThreads / 32], start, off;
+  volatile int bad;
+};
+
+// A wait that runs out marks the CTA bad; from then on no role waits, so that all
+// of them run out of chunks (and meet their groups' barriers) in bounded time.
+__device__ __forceinline__ void paged_wait(const PagedArgs &A, PagedShared &S, uint64_t *bar, uint32_t parity) {
+  // (asleep in hardware until the phase ends; the timer is read only after many tries)
+  uint64_t t0 = 0;
+  for (int i = 0; !ptx::mbar_try_wait_sleep(bar, parity, 1000000u); i++) {
+    if (S.bad) return;
+    if (i < 64) {
+      t0 = ptx::globaltimer();
+    } else if (ptx::globaltimer() - t0 > 2000000000ull) {
+      record_error(A.status, CSA2_ERR_TIMEOUT);
+      S.bad = 1;
+      return;
     }
   }
-  const int col = (int)((unsigned)j / (unsigned)A.page);
-  const int id = __ldg(A.table + (int64_t)C.Q.seq * A.table_stride + col);
-  if (id < 0 || id >= A.n_pages) {
-    if (report) record_error(A.status, CSA2_ERR_BOUNDS);
-    return nullptr;
-  }
-  return A.pages + ((int64_t)id * A.page + (j - col * A.page)) * kKvBytes;
 }
 
-// 32 heads' dot products of this lane's entry.
-__device__ __forceinline__ void paged_scores(uint32_t ta, float (&r)[32]) {
-  uint32_t a[32];
-  ptx::tmem_ld_32x32b_x32(ta + kPgColS, a);
-  ptx::tmem_wait_ld();
+// ------------------------------------------------------------------ records
+// Two warps walk the chunks, one for each buffer: a lane finds the records of four
+// rows, and the first lane of every run of rows that are neighbours in the cache
+// copies the run into shared memory.  A warp's next chunk is looked up, and its
+// records asked into L2, before the wait for the buffer (one warp for both buffers
+// took longer over a chunk than the MMAs).  A window chunk is read by the loading groups
+// themselves (its records do not fit the buffer).
+__device__ __forceinline__ void paged_fetch(const PagedArgs &A, PagedShared &S, unsigned char *sm, int c_begin, int c_end, int first) {
+  const int lane = threadIdx.x & 31;
+  PagedCursor C;
+  C.c = c_begin + first;
+  C.end = c_end;
+  C.qi = S.start;
+  C.off = S.off;
+  if (c_begin < c_end) C.Q = paged_query(A, C.qi);
+  const uint8_t *rec[4];                             // rows 32 g + lane
+  uint32_t valid[4], lead[4];
+  int4 at;
+  int seq, win;
+  auto look_up = [&]() {
+    at = make_int4(C.qi, C.local(), C.Q.chunks, C.off);
+    seq = C.Q.seq;
+    win = C.window() ? C.Q.win : 0;
+    const int i0 = (C.local() - (C.Q.win > 0 ? 1 : 0)) * kPgChunk + lane;
+    int j[4];
 #pragma unroll
-  for (int i = 0; i < 32; i++) r[i] = __uint_as_float(a[i]);
+    for (int g = 0; g < 4; g++) {
+      const int i = i0 + 32 * g;
+      j[g] = win == 0 && i < C.Q.n ? i : -1;
+      if (j[g] >= 0 && A.sel != nullptr) j[g] = __ldg(A.sel + (int64_t)C.qi * A.sel_stride + i);
+    }
+    const int vis = A.sel != nullptr ? __ldg(A.n_vis + C.qi) : C.Q.n;
+    int id[4], off[4];
+    bool out = false;
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+      const int col = (int)paged_col((unsigned)j[g], A);
+      off[g] = j[g] - col * A.page;
+      id[g] = j[g] >= 0 && j[g] < vis ? __ldg(A.table + (int64_t)C.Q.seq * A.table_stride + col) : -1;
+    }
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+      const bool ok = id[g] >= 0 && id[g] < A.n_pages;
+      out |= j[g] >= 0 && !ok;
+      if (!ok) id[g] = -1;
+      rec[g] = A.pages + ((int64_t)id[g] * A.page + off[g]) * kKvBytes;
+      const int pid = __shfl_up_sync(0xFFFFFFFFu, id[g], 1), poff = __shfl_up_sync(0xFFFFFFFFu, off[g], 1);
+      valid[g] = __ballot_sync(0xFFFFFFFFu, ok);
+      lead[g] = __ballot_sync(0xFFFFFFFFu, ok && (lane == 0 || pid != id[g] || poff + 1 != off[g]));
+    }
+    if (out) record_error(A.status, CSA2_ERR_BOUNDS);
+  };
+  // rows of the run that this lane leads, in group g (0: none)
+  auto run_rows = [&](int g) -> int {
+    if (((lead[g] >> lane) & 1u) == 0u) return 0;
+    const uint32_t stop = (lead[g] | ~valid[g]) & ~((2u << lane) - 1u);    // (lane 31: 2 << 31 is 0)
+    return (stop != 0u ? __ffs(stop) - 1 : 32) - lane;
+  };
+  bool more = C.settle(A);
+  if (more) look_up();
+  int k = first;
+  for (; more; k += 2) {
+    if (k >= 2) paged_wait(A, S, &S.raw_free[k & 1], ((k >> 1) - 1) & 1);
+    if (__any_sync(0xFFFFFFFFu, S.bad)) break;       // no copy is started any more
+    PagedInfo &I = S.info[k & (kPgInfo - 1)];
+    uint64_t *full = &S.raw_full[k & 1];
+    if (lane == 0) {
+      I.at = at;
+      I.seq = seq;
+      I.win = win;
+      int rows = 0;
+#pragma unroll
+      for (int g = 0; g < 4; g++) {
+        I.valid[g] = win == 0 ? valid[g] : win > 32 * g ? (win >= 32 * g + 32 ? 0xFFFFFFFFu : (1u << (win - 32 * g)) - 1u) : 0u;
+        rows += __popc(valid[g]);
+      }
+      ptx::mbar_arrive_expect_tx(full, (uint32_t)(rows * kKvBytes));
+    }
+    __syncwarp();
+    unsigned char *raw = sm + kPgSmRaw + (k & 1) * kPgRaw;
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+      const int n = run_rows(g);
+      if (n > 0) ptx::bulk_load(raw + (32 * g + lane) * kKvBytes, rec[g], (uint32_t)(n * kKvBytes), full);
+    }
+    C.c += 2;
+    more = C.settle(A);
+    if (more) {
+      look_up();
+#pragma unroll
+      for (int g = 0; g < 4; g++) {
+        const int n = run_rows(g);
+        if (n > 0) ptx::bulk_prefetch_l2(rec[g], (uint32_t)(n * kKvBytes));
+      }
+    }
+  }
+  // its last copies have landed before the CTA may leave (bounded)
+  if (k >= 2) ptx::mbar_wait(&S.raw_full[first], ((k >> 1) - 1) & 1);
 }
 
-// Roles: warps 0-7 softmax, rescaling and read-out (warp w: TMEM lane quarter
-// w % 4, heads 32 (w / 4) ..); warps 8-23 load and dequantise (32 dims of each
-// slab of a row per thread) and stage Q; one lane of warp
-// 24 issues the MMAs.
-// A chunk's tile is four slabs of 128 dims, each with its own barriers: PV's
-// block b reads slab b only, so slab b of the next chunk is written, and its
-// part of the next QK runs, while the blocks behind b still run.  The records of
-// the next chunk are in registers by then.
+// Both loading groups walk the chunks in two halves of four warps, one for each
+// slot of its ring of slabs: half g has slabs g and g + 2 of every chunk, a row per
+// thread.  The K group puts slabs into tensor memory for QK and runs up to a chunk
+// ahead; the V group puts them into shared memory, MN-major operands of PV, as PV
+// frees them.  Reading K from shared memory too would cost QK 48 cycles an MMA
+// instead of 32 and tie its tile to PV's.
+template <bool V>
+__device__ __forceinline__ void paged_load(const PagedArgs &A, PagedShared &S, unsigned char *sm, int n_run, uint32_t tmem) {
+  constexpr int kBar = V ? 3 : 2;
+  const int lt = (int)threadIdx.x - (V ? kPgSoft + kPgLoad : kPgSoft), lane = lt & 31;
+  const int e = lt & 127, mine = lt >> 7;            // row; slot, and first of its two slabs
+  // the row's 128 B in the slab's first 64 dims, chunk c at `tile` ^ 16 c
+  unsigned char *tile = sm + kPgSmV + mine * kPgSlab + (e >> 3) * 2048 + (e & 7) * 128 + (e & 7) * 16;
+  const uint32_t kcol = tmem + ((uint32_t)(e & 96) << 16) + kPgColK + mine * 64;
+  float q_scale = 1.f;
+  for (int k = 0; k < n_run; k++) {
+    paged_wait(A, S, &S.raw_full[k & 1], (k >> 1) & 1);
+    PagedInfo &I = S.info[k & (kPgInfo - 1)];
+    const int win = I.win;
+    if (!V && (k == 0 || I.at.y == 0)) {
+      // ---------------------------------------------------- Q to f16, K-major, 128B swizzle
+      if (k > 0) paged_wait(A, S, &S.k_free[1], 1);  // (the chunk before is multiplied: its last slab, use 2 k - 1 of slot 1)
+      const uint4 *src = reinterpret_cast<const uint4 *>(A.q + (int64_t)I.at.x * kHeads * kDim) + lt;
+      uint32_t m = 0u;
+#pragma unroll 4
+      for (int i = 0; i < 16; i++) {
+        const uint4 x = __ldg(src + i * kPgLoad);
+        m = __vmaxu2(m, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+      }
+      m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
+      if (lane == 0) S.qmax[lt >> 5] = m;
+      group_sync<kBar>();
+#pragma unroll
+      for (int w = 0; w < 8; w++) m = max(m, S.qmax[w]);
+      const int qs = m == 0u ? 0 : max((int)(m >> 7) - 127 - 14, -100);
+      const float inv = ldexpf(1.f, -qs);
+      q_scale = A.scale * 1.4426950408889634f * ldexpf(1.f, qs);
+      unsigned char *dst = sm + kPgSmQ + ((lt & 63) >> 3) * 1024;
+#pragma unroll 4
+      for (int i = 0; i < 16; i++) {                 // 16-B chunk lt % 64 of head lt / 64 + 4 i
+        const uint4 x = __ldg(src + i * kPgLoad);
+        uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+          const __half2 h2 = __floats2half2_rn(bf16_lo(w[u]) * inv, bf16_hi(w[u]) * inv);
+          w[u] = *reinterpret_cast<const uint32_t *>(&h2);
+        }
+        const int h = (lt >> 6) + 4 * i;
+        *reinterpret_cast<uint4 *>(dst + (h >> 3) * 8192 + sw128(h & 7, lt & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      ptx::fence_proxy_async_smem();
+    }
+    int kx = 0;
+    uint4 ws = make_uint4(0u, 0u, 0u, 0u);           // a window record's 16 scales
+    const uint8_t *wrec = nullptr;
+    if (win > 0) {
+      // ---------------------------------------------------- a window's rows and scale
+      if (e < win) {
+        const int ring = (int)(((unsigned)__ldg(A.swa_first + I.at.x) + (unsigned)e) % (unsigned)A.swa_cap);
+        wrec = A.swa + ((int64_t)I.seq * A.swa_cap + ring) * kSwaBytes;
+        ws = __ldg(reinterpret_cast<const uint4 *>(wrec + 512));
+      }
+      // the range of the scales' exponents (0 marks a group of zeros)
+      const uint32_t w4[4] = {ws.x, ws.y, ws.z, ws.w};
+      int lo = 255, hi = 0;
+#pragma unroll
+      for (int i = 0; i < 16; i++) {
+        const int x = (int)((w4[i >> 2] >> (8 * (i & 3))) & 0xFFu);
+        if (x != 0) { lo = min(lo, x); hi = max(hi, x); }
+      }
+      lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+      hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+      if (lt == 0) { S.emin[V] = 255; S.emax[V] = 0; }
+      group_sync<kBar>();
+      if (lane == 0) { atomicMin(&S.emin[V], lo); atomicMax(&S.emax[V], hi); }
+      group_sync<kBar>();
+      const int emax = S.emax[V] - 127, emin = S.emin[V] - 127;
+      if (emax > -127 && (emax > 7 || emin < -15)) kx = 7 - emax;
+    }
+    if (!V && lt == 0) {
+      I.f = ldexpf(q_scale, -kx);
+      I.kx = kx;
+    }
+    // The row's two slabs, 32 dims (16 words of two f16) at a time; turn t is use
+    // 2 k + t of the slot.  (One slab's code, not the chunk's: six roles share the
+    // instruction caches, and with everything unrolled the warps waited for
+    // instructions four times as long as they issued them.)
+    auto begin = [&](int t) {
+      const int use = 2 * k + t;
+      if (use >= 1) paged_wait(A, S, V ? &S.v_free[mine] : &S.k_free[mine], (use - 1) & 1);
+      if (!V) ptx::tc_fence_after();
+    };
+    auto put = [&](int j, const uint32_t (&o)[16]) {
+      if (V) {
+#pragma unroll
+        for (int u = 0; u < 4; u++)
+          *reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(reinterpret_cast<uintptr_t>(tile) ^ (((j & 1) * 4 + u) << 4)) + (j >> 1) * 1024) =
+              make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+      } else {
+        ptx::tmem_st_32x32b_x16(kcol + j * 16, o);
+      }
+    };
+    auto end = [&]() {
+      if (V) {
+        ptx::fence_proxy_async_smem();
+      } else {
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(V ? &S.v_full[mine] : &S.k_full[mine]);
+    };
+    if (win > 0) {
+#pragma unroll 1
+      for (int i = 0; i < 8; i++) {
+        const int b = mine + 2 * (i >> 2), j = i & 3;
+        const uint32_t wb = b == 0 ? ws.x : b == 1 ? ws.y : b == 2 ? ws.z : ws.w;
+        const int eb = (int)((wb >> (8 * j)) & 0xFFu);
+        const __half2 fac = __float2half2_rn(eb == 0 ? 0.f : ldexpf(1.f, eb - 127 + kx));
+        uint32_t o[16];
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const uint4 x = wrec != nullptr ? __ldg(reinterpret_cast<const uint4 *>(wrec + b * 128 + j * 32 + h * 16)) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int q = 0; q < 8; q++) {
+            const uint32_t hv = e4m3x2_to_f16x2(w[q >> 1] >> (16 * (q & 1)));
+            const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&hv), fac);
+            o[8 * h + q] = *reinterpret_cast<const uint32_t *>(&y);
+          }
+        }
+        if (j == 0) begin(i >> 2);
+        // (j is a run-time number here)
+        if (V) {
+          unsigned char *row = reinterpret_cast<unsigned char *>(reinterpret_cast<uintptr_t>(tile) ^ (uintptr_t)((j & 1) << 6)) + (j >> 1) * 1024;
+#pragma unroll
+          for (int u = 0; u < 4; u++)
+            *reinterpret_cast<uint4 *>(reinterpret_cast<uintptr_t>(row) ^ (uintptr_t)(u << 4)) = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+        } else {
+          ptx::tmem_st_32x32b_x16(kcol + j * 16, o);
+        }
+        if (j == 3) end();
+      }
+    } else {
+      const bool ok = ((I.valid[e >> 5] >> lane) & 1u) != 0u;
+      const unsigned char *rec = sm + kPgSmRaw + (k & 1) * kPgRaw + e * kKvBytes + mine * 64;
+      const unsigned char *scales = rec + 256 - mine * 56;
+      uint4 code = make_uint4(0u, 0u, 0u, 0u);       // the 32 dims ahead
+      if (ok) code = *reinterpret_cast<const uint4 *>(rec);
+#pragma unroll 1
+      for (int t = 0; t < 2; t++) {
+        uint2 sc = make_uint2(0u, 0u);
+        if (ok) sc = *reinterpret_cast<const uint2 *>(scales);
+        scales += 16;
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          const uint32_t w[4] = {code.x, code.y, code.z, code.w};
+          const uint32_t two = e4m3x2_to_f16x2((j < 2 ? sc.x : sc.y) >> (16 * (j & 1)));
+          const uint32_t s2[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
+          if (ok) code = *reinterpret_cast<const uint4 *>(j < 3 ? rec + (j + 1) * 16 : rec + (t == 0 ? 128 : 0));
+          uint32_t o[16];
+#pragma unroll
+          for (int u = 0; u < 4; u++) {
+            uint32_t x[4];
+            e2m1x8_to_f16(w[u], x);
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+              const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x[q]), *reinterpret_cast<const __half2 *>(&s2[u >> 1]));
+              o[4 * u + q] = *reinterpret_cast<const uint32_t *>(&y);
+            }
+          }
+          if (j == 0) begin(t);
+          put(j, o);
+        }
+        rec += 128;
+        end();
+      }
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&S.raw_free[k & 1]);
+  }
+}
+
+// ------------------------------------------------------------------ softmax, read-out
+// Two fp32 at a time.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// This lane's entry: 32 heads' logits in log2 units (-inf for a row without an
+// entry: `none` = -inf, else 0), plus the heads' `less` where given.  (The product is
+// rounded before the sum, as the maximum's was: in one step, the difference of two
+// huge logits would be off by that rounding.)
+template <bool LESS>
+__device__ __forceinline__ void paged_logits(uint32_t ta, float f, float none, const float *less, uint64_t (&s)[16]) {
+  const uint64_t f2 = pair(f, f), n2 = pair(none, none);
+#pragma unroll
+  for (int h = 0; h < 32; h += 16) {
+    uint32_t a[16];
+    ptx::tmem_ld_32x32b_x16(ta + h, a);
+    ptx::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      uint64_t x = fma2(pair(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), f2, n2);
+      uint64_t y = fma2(pair(__uint_as_float(a[i + 2]), __uint_as_float(a[i + 3])), f2, n2);
+      if (LESS) {
+        const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(less + h + i);
+        x = add2(x, m.x);
+        y = add2(y, m.y);
+      }
+      s[(h + i) / 2] = x;
+      s[(h + i) / 2 + 1] = y;
+    }
+  }
+}
+// Their numerators 2^s, and rounded to f16; true where one is out of the range that
+// f16 should hold (or not a number).
+__device__ __forceinline__ bool paged_numerators(uint64_t (&s)[16], uint32_t (&o)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; i++) {
+    const float2 x = unpair(s[i]);
+    const float p0 = ex2(x.x), p1 = ex2(x.y);
+    s[i] = pair(p0, p1);
+    const __half2 h2 = __floats2half2_rn(p0, p1);
+    o[i] = *reinterpret_cast<const uint32_t *>(&h2);
+  }
+  // (positive f16 compare as integers; infinity and NaN are above all of them)
+  uint32_t top = o[0];
+#pragma unroll
+  for (int i = 1; i < 16; i++) top = __vmaxu2(top, o[i]);
+  return (top >> 16) > 0x7800u || (top & 0xFFFFu) > 0x7800u;           // 2^15
+}
+
+// Warp w has TMEM lane quarter w % 4 (S: entries, O: dims) and heads 32 (w / 4) ..
+__device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S, unsigned char *sm, int n_run, int T,
+                                              int G, uint32_t tmem) {
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int quarter = warp & 3, hb = (warp >> 2) * 32, e_row = quarter * 32 + lane;
+  const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16);
+  uint64_t l_acc[16];                                // 32 heads' denominators
+  float o_scale = 1.f;                               // what O still has to be multiplied by
+  bool acc = false;                                  // O holds something of this query
+  int lc0 = 0;
+  for (int k = 0; k < n_run; k++) {
+    paged_wait(A, S, &S.s_full[k & 1], (k >> 1) & 1);
+    ptx::tc_fence_after();
+    const PagedInfo &info = S.info[k & (kPgInfo - 1)];
+    const int4 I = info.at;
+    const int lc = I.y;
+    if (k == 0 || lc == 0) {                         // a query begins
+      lc0 = lc;
+      acc = false;
+      o_scale = 1.f;
+#pragma unroll
+      for (int i = 0; i < 16; i++) l_acc[i] = 0ull;
+      if (t < kHeads) S.less[t] = kPgNoRef;
+      group_sync<1>();
+    }
+    const float f = info.f;
+    const int kx = info.kx;
+    const float none = ((info.valid[quarter] >> lane) & 1u) != 0u ? 0.f : -INFINITY;
+    const uint32_t ta = tq + kPgColS + (k & 1) * kHeads + hb;
+    uint64_t s[16];
+    uint32_t o[16];
+    paged_logits<true>(ta, f, none, &S.less[hb], s);
+    const bool over = paged_numerators(s, o);
+    // (a window's 2^-kx is undone before the next chunk)
+    if (soft_any(over || (acc && o_scale != 1.f))) {
+      // the chunk's maximum of every head: lane L ends with head hb + L
+      float v[32];
+      paged_logits<false>(ta, f, none, nullptr, s);
+#pragma unroll
+      for (int i = 0; i < 16; i++) {
+        const float2 x = unpair(s[i]);
+        v[2 * i] = x.x;
+        v[2 * i + 1] = x.y;
+      }
+#pragma unroll
+      for (int w = 16; w >= 1; w >>= 1) {
+        const bool upper = (lane & w) != 0;
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+          if (i < w) {
+            const float keep = upper ? v[i + w] : v[i], send = upper ? v[i] : v[i + w];
+            v[i] = fmaxf(keep, __shfl_xor_sync(0xFFFFFFFFu, send, w));
+          }
+        }
+      }
+      S.red[quarter][hb + lane] = v[0];
+      group_sync<1>();
+      if (t < kHeads) {
+        const float cm = fmaxf(fmaxf(S.red[0][t], S.red[1][t]), fmaxf(S.red[2][t], S.red[3][t])) - kPgShift;
+        const float mo = -S.less[t];
+        float al = 1.f;
+        if (cm > mo + kPgRaise) {
+          al = mo == -kPgNoRef ? 0.f : exp2f(mo - cm);
+          S.less[t] = -cm;
+        }
+        S.alpha[t] = al;
+      }
+      group_sync<1>();
+      if (acc) {
+        // O *= alpha (and the window's factor), once PV of the chunk before is complete
+        paged_wait(A, S, &S.o_done, (k - 1) & 1);
+        ptx::tc_fence_after();
+        for (int blk = warp >> 2; blk < 4; blk += 2)
+#pragma unroll 1
+          for (int h = 0; h < kHeads; h += 16) {
+            uint32_t x[16];
+            const uint32_t to = tq + kPgColO + blk * kHeads + h;
+            ptx::tmem_ld_32x32b_x16(to, x);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; i++) x[i] = __float_as_uint(__uint_as_float(x[i]) * S.alpha[h + i] * o_scale);
+            ptx::tmem_st_32x32b_x16(to, x);
+          }
+        ptx::tmem_wait_st();
+        o_scale = 1.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; i++) {
+        const float2 l = unpair(l_acc[i]);
+        l_acc[i] = pair(l.x * S.alpha[hb + 2 * i], l.y * S.alpha[hb + 2 * i + 1]);
+      }
+      paged_logits<true>(ta, f, none, &S.less[hb], s);
+      paged_numerators(s, o);
+    }
+    ptx::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&S.s_free[k & 1]);
+#pragma unroll
+    for (int i = 0; i < 16; i++) l_acc[i] = add2(l_acc[i], s[i]);
+    // P is free once PV of the chunk before is complete
+    if (k > 0) paged_wait(A, S, &S.o_done, (k - 1) & 1);
+    unsigned char *row = sm + kPgSmP + (e_row >> 3) * 1024;
+#pragma unroll
+    for (int q = 0; q < 4; q++)
+      *reinterpret_cast<uint4 *>(row + sw128(e_row & 7, (hb >> 3) + q)) =
+          make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+    ptx::tc_fence_before();
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&S.p_full);
+    acc = true;
+    if (kx != 0) o_scale = ldexpf(1.f, -kx);
+    if (lc + 1 != I.z && k + 1 != n_run) continue;
+
+    // -------------------------------------------------------- the query's last chunk here: read-out
+    float l_sum[32];
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+      const float2 l = unpair(l_acc[i]);
+      l_sum[2 * i] = l.x;
+      l_sum[2 * i + 1] = l.y;
+    }
+#pragma unroll
+    for (int w = 16; w >= 1; w >>= 1) {
+      const bool upper = (lane & w) != 0;
+#pragma unroll
+      for (int i = 0; i < 16; i++) {
+        if (i < w) {
+          const float keep = upper ? l_sum[i + w] : l_sum[i], send = upper ? l_sum[i] : l_sum[i + w];
+          l_sum[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, w);
+        }
+      }
+    }
+    S.l[quarter][hb + lane] = l_sum[0];
+    group_sync<1>();
+    const bool whole = lc0 == 0 && lc + 1 == I.z;
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (lc0 > 0 ? 0 : 1);
+    if (t < kHeads) {
+      const float l = S.l[0][t] + S.l[1][t] + S.l[2][t] + S.l[3][t];
+      if (whole) {
+        if (A.lse != nullptr)
+          A.lse[(int64_t)I.x * kHeads + t] =
+              l > 0.f || l != l ? (log2f(l) - S.less[t]) * 0.6931471805599453f : -INFINITY;
+        S.alpha[t] = l != 0.f ? o_scale / l : 0.f;
+      } else {
+        A.part_ml[slot * 2 * kHeads + t] = -S.less[t];
+        A.part_ml[slot * 2 * kHeads + kHeads + t] = l;
+        S.alpha[t] = o_scale;
+      }
+    }
+    const int pos = __ldg(A.pos + I.x);
+    group_sync<1>();
+    paged_wait(A, S, &S.o_done, k & 1);              // PV is complete
+    ptx::tc_fence_after();
+    for (int blk = warp >> 2; blk < 4; blk += 2) {
+      const int d = blk * 128 + quarter * 32 + lane;
+      float cs = 1.f, sn = 0.f;
+      if (whole && d >= kRopeOff) turn_cs((uint64_t)(int64_t)pos * A.turn[(d - kRopeOff) >> 1], cs, sn);
+#pragma unroll 1
+      for (int hh = 0; hh < 2; hh++) {
+        uint32_t r[32];
+        ptx::tmem_ld_32x32b_x32(tq + kPgColO + blk * kHeads + hh * 32, r);
+        ptx::tmem_wait_ld();
+        if (!whole) {
+          float *P = A.part + (slot * kHeads + hh * 32) * kDim + d;
+#pragma unroll
+          for (int i = 0; i < 32; i++) P[i * kDim] = __uint_as_float(r[i]) * S.alpha[hh * 32 + i];
+          continue;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i++) {
+          float x = __uint_as_float(r[i]) * S.alpha[hh * 32 + i];
+          if (blk == 3 && quarter >= 2) {            // (a, b) by -pos; the partner is in the next lane
+            const float y = __shfl_xor_sync(0xFFFFFFFFu, x, 1);
+            x = (d & 1) ? x * cs - y * sn : x * cs + y * sn;
+          }
+          const int64_t at = ((int64_t)I.x * kHeads + hh * 32 + i) * kDim + d;
+          if (A.out_f32) static_cast<float *>(A.out)[at] = x;
+          else static_cast<__nv_bfloat16 *>(A.out)[at] = __float2bfloat16_rn(x);
+        }
+      }
+    }
+    ptx::tc_fence_before();                          // (before the next query's PV, behind p_full)
+    // the first CTA after the one that begins a cut query names it for the join
+    if (t == 0 && lc0 > 0 && I.w + lc0 == run_start(run_owner(I.w, T, G) + 1, T, G))
+      A.joins[blockIdx.x] = make_int4(I.x, I.z, I.w, T);
+  }
+}
+
+// ------------------------------------------------------------------ MMAs
+// One thread each for QK and PV, chosen by elect.sync, with operands addressed by
+// a base plus constants: it issues an MMA every 48 cycles, what N = 64 takes with
+// both operands in shared memory (6 KB).  With the descriptors built at each MMA
+// a thread issued one in 81 to 118 cycles.
+__device__ __forceinline__ void paged_issue_qk(const PagedArgs &A, PagedShared &S, unsigned char *sm, int n_run,
+                                               uint32_t tmem) {
+  constexpr uint32_t id = idesc_m128(0, true, kHeads);
+  const uint64_t d_q = ptx::smem_desc(ptx::smem_u32(sm + kPgSmQ), 16, 8192, 2);
+  for (int k = 0; k < n_run && !S.bad; k++) {
+    if (k >= 2) paged_wait(A, S, &S.s_free[k & 1], ((k >> 1) - 1) & 1);
+#pragma unroll 1
+    for (int b = 0; b < 4; b++) {                    // S^T += K Q^T over slab n = 4 k + b
+      paged_wait(A, S, &S.k_full[b & 1], ((4 * k + b) >> 1) & 1);
+      ptx::tc_fence_after();
+      const uint64_t qa = d_q + b * 128;
+      const uint32_t ka = tmem + kPgColK + (b & 1) * 64;
+#pragma unroll
+      for (int kk = 0; kk < 8; kk++)
+        ptx::tc_mma_f16_ts(tmem + kPgColS + (k & 1) * kHeads, ka + kk * 8, qa + (kk >> 2) * 64 + (kk & 3) * 2, id,
+                           kk > 0 ? 1u : (uint32_t)(b > 0));
+      ptx::tc_commit(&S.k_free[b & 1]);
+    }
+    ptx::tc_commit(&S.s_full[k & 1]);
+  }
+  ptx::tc_commit(&S.drain);
+}
+__device__ __forceinline__ void paged_issue_pv(const PagedArgs &A, PagedShared &S, unsigned char *sm, int n_run,
+                                               uint32_t tmem) {
+  constexpr uint32_t id = idesc_m128(1, true, kHeads) | (1u << 16);   // both operands MN-major
+  const uint64_t d_v = ptx::smem_desc(ptx::smem_u32(sm + kPgSmV), 1024, 2048, 2);
+  const uint64_t d_p = ptx::smem_desc(ptx::smem_u32(sm + kPgSmP), 1024, 1024, 2);
+  for (int k = 0; k < n_run && !S.bad; k++) {
+    paged_wait(A, S, &S.p_full, k & 1);
+    const uint32_t acc = k == 0 || S.info[k & (kPgInfo - 1)].at.y == 0 ? 0u : 1u;
+#pragma unroll 1
+    for (int b = 0; b < 4; b++) {                    // O^T block b += V^T P, slab n = 4 k + b
+      paged_wait(A, S, &S.v_full[b & 1], ((4 * k + b) >> 1) & 1);
+      ptx::tc_fence_after();
+      const uint64_t va = d_v + (b & 1) * (kPgSlab >> 4);
+#pragma unroll
+      for (int ks = 0; ks < kPgChunk / 16; ks++)
+        ptx::tc_mma_bf16(tmem + kPgColO + b * kHeads, va + ks * 256, d_p + ks * 128, id, ks > 0 ? 1u : acc);
+      ptx::tc_commit(&S.v_free[b & 1]);
+    }
+    ptx::tc_commit(&S.o_done);
+  }
+  ptx::tc_commit(&S.drain);
+}
+
 __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_constant__ PagedArgs A) {
   extern __shared__ __align__(1024) unsigned char pg_smem_raw[];
   unsigned char *sm = reinterpret_cast<unsigned char *>(
       (reinterpret_cast<uintptr_t>(pg_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  __shared__ __align__(8) uint64_t bar_full[4], bar_free[4], bar_s, bar_p, bar_drain;
-  __shared__ uint32_t tmem_sh, qmax_sh[kPgLoadWarps];
-  __shared__ __align__(16) float m_ref[kHeads], alpha_sh[kHeads];    // m_ref: the reference less kPgShift
-  __shared__ float l_sh[4][kHeads], red_sh[4][kHeads];
-  __shared__ uint8_t valid_sh[kPgChunk];
-  __shared__ int scan_sh[kPgThreads / 32], off_sh;
-  __shared__ int start_sh, emin_sh, emax_sh, kx_sh;
-  __shared__ float qscale_sh;
-  __shared__ int4 info_sh[2];                        // of chunk k: query, place in it, its chunks, its first chunk
-  __shared__ volatile int bad_sh;
+  __shared__ __align__(16) PagedShared S;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   if (t == 0) {
-    for (int b = 0; b < 4; b++) {
-      ptx::mbar_init(&bar_full[b], kPgLoadWarps);
-      ptx::mbar_init(&bar_free[b], 1);
+    for (int i = 0; i < 2; i++) {
+      ptx::mbar_init(&S.raw_full[i], 1);
+      ptx::mbar_init(&S.raw_free[i], 2 * kPgLoad / 32);
+      ptx::mbar_init(&S.k_full[i], kPgLoad / 64);
+      ptx::mbar_init(&S.k_free[i], 1);
+      ptx::mbar_init(&S.v_full[i], kPgLoad / 64);
+      ptx::mbar_init(&S.v_free[i], 1);
+      ptx::mbar_init(&S.s_full[i], 1);
+      ptx::mbar_init(&S.s_free[i], kPgSoft / 32);
     }
-    ptx::mbar_init(&bar_s, 1);
-    ptx::mbar_init(&bar_p, kPgSoftWarps);
-    ptx::mbar_init(&bar_drain, 1);
-    bad_sh = 0;
-    start_sh = 0;
+    ptx::mbar_init(&S.p_full, kPgSoft / 32);
+    ptx::mbar_init(&S.o_done, 1);
+    ptx::mbar_init(&S.drain, 2);
+    S.bad = 0;
+    S.start = S.off = 0;
     ptx::fence_mbar_init();
   }
-  if (warp == 0) ptx::tmem_alloc(&tmem_sh, kPgTmemCols);
+  if (warp == 0) ptx::tmem_alloc(&S.tmem, kPgTmemCols);
   griddep_wait();
   griddep_launch();
 
@@ -206,12 +805,12 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     const int x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
     if (lane >= o) inc += x;
   }
-  if (lane == 31) scan_sh[warp] = inc;
+  if (lane == 31) S.scan[warp] = inc;
   __syncthreads();
   int before = 0, total = 0;
   for (int w = 0; w < kPgThreads / 32; w++) {
-    if (w < warp) before += scan_sh[w];
-    total += scan_sh[w];
+    if (w < warp) before += S.scan[w];
+    total += S.scan[w];
   }
   before += inc - mine;
   const int G = gridDim.x, T = total;
@@ -223,8 +822,8 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
       if (c_begin < o + n) break;
       o += n;
     }
-    start_sh = q;
-    off_sh = o;
+    S.start = q;
+    S.off = o;
   }
   if (t == 0) A.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
   // queries with nothing to attend to: zeros
@@ -240,425 +839,34 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = tmem_sh;
-  // A wait that runs out marks the CTA bad; from then on no role waits, so that
-  // all of them run out of chunks (and meet their groups' barriers) in bounded time.
-  auto wait = [&](uint64_t *bar, uint32_t parity) {
-    if (bad_sh) return;
-    for (int i = 0; i < 64; i++)                     // (each try waits a while in hardware; no timer is read)
-      if (ptx::mbar_try_wait(bar, parity)) return;
-    if (ptx::mbar_wait(bar, parity)) return;
-    record_error(A.status, CSA2_ERR_TIMEOUT);
-    bad_sh = 1;
-  };
+  const uint32_t tmem = S.tmem;
   const int n_run = c_end - c_begin;
 
-  if (warp < kPgSoftWarps) {
+  if (warp < kPgSoft / 32) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPgRegsSoft));
-    // ======================================================== softmax, read-out
-    const int quarter = warp & 3, hb = (warp >> 2) * 32, e_row = quarter * 32 + lane;
-    const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16);
-    float l_acc[32];
-    float o_scale = 1.f;                             // what O still has to be multiplied by
-    bool acc = false;                                // O holds something of this query
-    int lc0 = 0;
-    for (int k = 0; k < n_run; k++) {
-      wait(&bar_s, k & 1);
-      ptx::tc_fence_after();
-      const int4 I = info_sh[k & 1];
-      const int lc = I.y;
-      if (k == 0 || lc == 0) {                       // a query begins
-        lc0 = lc;
-        acc = false;
-        o_scale = 1.f;
-#pragma unroll
-        for (int i = 0; i < 32; i++) l_acc[i] = 0.f;
-        if (t < kHeads) m_ref[t] = -INFINITY;
-        soft_sync();
-      }
-      const float f = A.scale * 1.4426950408889634f * ldexpf(qscale_sh, -kx_sh);
-      const int kx = kx_sh;
-      const bool ev = valid_sh[e_row] != 0;
-      float s[32];
-      {
-        float r[32];
-        paged_scores(tq + hb, r);
-        float top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const float4 m = *reinterpret_cast<const float4 *>(&m_ref[hb + i]);
-          // (the product rounded first, as the maximum's was: fused, the difference
-          // of two huge logits would be off by that rounding)
-          s[i] = __fmul_rn(r[i], f) - m.x;
-          s[i + 1] = __fmul_rn(r[i + 1], f) - m.y;
-          s[i + 2] = __fmul_rn(r[i + 2], f) - m.z;
-          s[i + 3] = __fmul_rn(r[i + 3], f) - m.w;
-          top = fmaxf(fmaxf(top, fmaxf(s[i], s[i + 1])), fmaxf(s[i + 2], s[i + 3]));
-        }
-        const bool rescale = acc && o_scale != 1.f;  // a window's 2^-kx, undone before the next chunk
-        if (soft_any((ev && top > kPgRaise + kPgShift) || rescale)) {
-          // the chunk's maximum of every head: lane L ends with head hb + L
-          // (S is read again rather than kept in registers)
-          float v[32];
-          paged_scores(tq + hb, r);
-#pragma unroll
-          for (int i = 0; i < 32; i++) v[i] = ev ? __fmul_rn(r[i], f) : -INFINITY;
-#pragma unroll
-          for (int w = 16; w >= 1; w >>= 1) {
-            const bool upper = (lane & w) != 0;
-#pragma unroll
-            for (int i = 0; i < 16; i++) {
-              if (i < w) {
-                const float keep = upper ? v[i + w] : v[i], send = upper ? v[i] : v[i + w];
-                v[i] = fmaxf(keep, __shfl_xor_sync(0xFFFFFFFFu, send, w));
-              }
-            }
-          }
-          red_sh[quarter][hb + lane] = v[0];
-          soft_sync();
-          if (t < kHeads) {
-            const float cm = fmaxf(fmaxf(red_sh[0][t], red_sh[1][t]), fmaxf(red_sh[2][t], red_sh[3][t])) - kPgShift;
-            const float mo = m_ref[t];
-            float al = 1.f;
-            if (cm > mo + kPgRaise) {
-              al = mo == -INFINITY ? 0.f : exp2f(mo - cm);
-              m_ref[t] = cm;
-            }
-            alpha_sh[t] = al;
-          }
-          soft_sync();
-          if (acc) {
-            // O *= alpha (and the window's factor); PV of the chunk before is complete (S is)
-            for (int blk = warp >> 2; blk < 4; blk += 2)
-#pragma unroll 1
-              for (int hh = 0; hh < 2; hh++) {
-                uint32_t o[32];
-                const uint32_t ta = tq + kPgColO + blk * kHeads + hh * 32;
-                ptx::tmem_ld_32x32b_x32(ta, o);
-                ptx::tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; i++)
-                  o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha_sh[hh * 32 + i] * o_scale);
-                ptx::tmem_st_32x32b_x32(ta, o);
-              }
-            ptx::tmem_wait_st();
-            o_scale = 1.f;
-          }
-          paged_scores(tq + hb, r);
-#pragma unroll
-          for (int i = 0; i < 32; i++) {
-            l_acc[i] *= alpha_sh[hb + i];
-            s[i] = __fmul_rn(r[i], f) - m_ref[hb + i];
-          }
-        }
-      }
-      unsigned char *row = sm + kPgSmP + (e_row >> 3) * 1024;
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        uint32_t o[4];
-#pragma unroll
-        for (int u = 0; u < 4; u++) {
-          const int i = 8 * j + 2 * u;
-          const float p0 = ev ? ex2(s[i]) : 0.f, p1 = ev ? ex2(s[i + 1]) : 0.f;
-          l_acc[i] += p0;
-          l_acc[i + 1] += p1;
-          const __half2 h2 = __floats2half2_rn(p0, p1);
-          o[u] = *reinterpret_cast<const uint32_t *>(&h2);
-        }
-        *reinterpret_cast<uint4 *>(row + sw128(e_row & 7, (hb >> 3) + j)) = make_uint4(o[0], o[1], o[2], o[3]);
-      }
-      ptx::tc_fence_before();
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&bar_p);
-      acc = true;
-      if (kx != 0) o_scale = ldexpf(1.f, -kx);
-      if (lc + 1 != I.z && k + 1 != n_run) continue;
-
-      // ------------------------------------------------------ the query's last chunk here: read-out
-#pragma unroll
-      for (int w = 16; w >= 1; w >>= 1) {
-        const bool upper = (lane & w) != 0;
-#pragma unroll
-        for (int i = 0; i < 16; i++) {
-          if (i < w) {
-            const float keep = upper ? l_acc[i + w] : l_acc[i], send = upper ? l_acc[i] : l_acc[i + w];
-            l_acc[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, w);
-          }
-        }
-      }
-      l_sh[quarter][hb + lane] = l_acc[0];
-      soft_sync();
-      const bool whole = lc0 == 0 && lc + 1 == I.z;
-      const int64_t slot = 2 * (int64_t)blockIdx.x + (lc0 > 0 ? 0 : 1);
-      if (t < kHeads) {
-        const float l = l_sh[0][t] + l_sh[1][t] + l_sh[2][t] + l_sh[3][t];
-        if (whole) {
-          if (A.lse != nullptr)
-            A.lse[(int64_t)I.x * kHeads + t] =
-                l > 0.f || l != l ? (m_ref[t] + log2f(l)) * 0.6931471805599453f : -INFINITY;
-          alpha_sh[t] = l != 0.f ? o_scale / l : 0.f;
-        } else {
-          A.part_ml[slot * 2 * kHeads + t] = m_ref[t];
-          A.part_ml[slot * 2 * kHeads + kHeads + t] = l;
-          alpha_sh[t] = o_scale;
-        }
-      }
-      const int pos = __ldg(A.pos + I.x);
-      soft_sync();
-      wait(&bar_free[3], k & 1);                     // PV is complete
-      ptx::tc_fence_after();
-      for (int blk = warp >> 2; blk < 4; blk += 2) {
-        const int d = blk * 128 + quarter * 32 + lane;
-        float cs = 1.f, sn = 0.f;
-        if (whole && d >= kRopeOff) turn_cs((uint64_t)(int64_t)pos * A.turn[(d - kRopeOff) >> 1], cs, sn);
-#pragma unroll 1
-        for (int hh = 0; hh < 2; hh++) {
-          uint32_t r[32];
-          ptx::tmem_ld_32x32b_x32(tq + kPgColO + blk * kHeads + hh * 32, r);
-          ptx::tmem_wait_ld();
-          if (!whole) {
-            float *P = A.part + (slot * kHeads + hh * 32) * kDim + d;
-#pragma unroll
-            for (int i = 0; i < 32; i++) P[i * kDim] = __uint_as_float(r[i]) * alpha_sh[hh * 32 + i];
-            continue;
-          }
-#pragma unroll
-          for (int i = 0; i < 32; i++) {
-            float x = __uint_as_float(r[i]) * alpha_sh[hh * 32 + i];
-            if (blk == 3 && quarter >= 2) {          // (a, b) by -pos; the partner is in the next lane
-              const float y = __shfl_xor_sync(0xFFFFFFFFu, x, 1);
-              x = (d & 1) ? x * cs - y * sn : x * cs + y * sn;
-            }
-            const int64_t o = ((int64_t)I.x * kHeads + hh * 32 + i) * kDim + d;
-            if (A.out_f32) static_cast<float *>(A.out)[o] = x;
-            else static_cast<__nv_bfloat16 *>(A.out)[o] = __float2bfloat16_rn(x);
-          }
-        }
-      }
-      ptx::tc_fence_before();                        // (before the next query's PV, behind bar_p)
-      // the first CTA after the one that begins a cut query names it for the join
-      if (t == 0 && lc0 > 0 && I.w + lc0 == run_start(run_owner(I.w, T, G) + 1, T, G))
-        A.joins[blockIdx.x] = make_int4(I.x, I.z, I.w, T);
-    }
-  } else if (warp < kPgSoftWarps + kPgLoadWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPgRegsLoad));
-    // ======================================================== records to f16, Q
-    const int lt = t - kPgSoft, lw = warp - kPgSoftWarps;
-    const int e = lt >> 2, part = lt & 3;            // row, 32-dim part of each slab
-    unsigned char *tile = sm + kPgSmK + (e >> 3) * 8192 + (part >> 1) * 1024;
-    const int ch0 = (part & 1) * 4;                  // the part's first 16-B chunk within its 128 B
-    // the chunk's records: this part's codes of each slab, and slab `part`'s
-    // eight scales (the row's four threads pass them around)
-    uint4 v[4];
-    uint2 sc = make_uint2(0u, 0u);
-    bool ok = false;
-    auto load = [&](const uint8_t *rec, int b) {
-      v[b] = rec != nullptr ? __ldg(reinterpret_cast<const uint4 *>(rec + b * 64 + part * 16)) : make_uint4(0u, 0u, 0u, 0u);
-    };
-    auto load_scales = [&](const uint8_t *rec) {
-      sc = rec != nullptr ? __ldg(reinterpret_cast<const uint2 *>(rec + 256 + part * 8)) : make_uint2(0u, 0u);
-    };
-    PagedCursor C;
-    C.c = c_begin;
-    C.end = c_end;
-    C.qi = start_sh;
-    C.off = n_run > 0 ? off_sh : 0;
-    if (n_run > 0) C.Q = paged_query(A, C.qi);
-    bool more = C.settle(A);
-    if (more && !C.window()) {
-      const uint8_t *rec = paged_record(A, C, e, part == 0);
-      ok = rec != nullptr;
-      load_scales(rec);
-#pragma unroll
-      for (int b = 0; b < 4; b++) load(rec, b);
-    }
-    uint32_t k = 0;
-    for (; more; k++) {
-      const int qi = C.qi;
-      const int4 info = make_int4(qi, C.local(), C.Q.chunks, C.off);
-      const bool win = C.window(), begins = k == 0 || C.local() == 0;
-      const uint8_t *wrec = nullptr;
-      if (win) {
-        ok = e < C.Q.win;
-        if (ok) {
-          const int ring = (int)(((unsigned)__ldg(A.swa_first + qi) + (unsigned)e) % (unsigned)A.swa_cap);
-          wrec = A.swa + ((int64_t)C.Q.seq * A.swa_cap + ring) * kSwaBytes;
-        }
-      }
-      // the next chunk's row
-      C.c++;
-      more = C.settle(A);
-      const uint8_t *next = more && !C.window() ? paged_record(A, C, e, part == 0) : nullptr;
-      // the chunk before is through with slab 0, the row marks, Q and the scales
-      if (k > 0) wait(&bar_free[0], (k - 1) & 1);
-      if (begins) {
-        // Q to f16, K-major, 128B swizzle
-        const uint4 *src = reinterpret_cast<const uint4 *>(A.q + (int64_t)qi * kHeads * kDim);
-        uint32_t m = 0u;
-#pragma unroll 2
-        for (int j = 0; j < 8; j++) {
-          const uint4 x = __ldg(src + lt + j * kPgLoad);
-          m = __vmaxu2(m, x.x & 0x7FFF7FFFu);
-          m = __vmaxu2(m, x.y & 0x7FFF7FFFu);
-          m = __vmaxu2(m, x.z & 0x7FFF7FFFu);
-          m = __vmaxu2(m, x.w & 0x7FFF7FFFu);
-        }
-        m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
-        if (lane == 0) qmax_sh[lw] = m;
-        load_sync();
-#pragma unroll
-        for (int w = 0; w < kPgLoadWarps; w++) m = max(m, qmax_sh[w]);
-        const int qs = m == 0u ? 0 : max((int)(m >> 7) - 127 - 14, -100);
-        const float inv = ldexpf(1.f, -qs);
-        if (lt == 0) qscale_sh = ldexpf(1.f, qs);
-#pragma unroll 2
-        for (int j = 0; j < 8; j++) {
-          const uint4 x = __ldg(src + lt + j * kPgLoad);
-          uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int u = 0; u < 4; u++) {
-            const __half2 h2 = __floats2half2_rn(bf16_lo(w[u]) * inv, bf16_hi(w[u]) * inv);
-            w[u] = *reinterpret_cast<const uint32_t *>(&h2);
-          }
-          const int i = lt + j * kPgLoad, h = i >> 6, ch = i & 63;
-          *reinterpret_cast<uint4 *>(sm + kPgSmQ + (h >> 3) * 8192 + (ch >> 3) * 1024 + sw128(h & 7, ch & 7)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-      if (part == 0) valid_sh[e] = ok ? 1 : 0;
-      int kx = 0;
-      uint32_t ws[4] = {0u, 0u, 0u, 0u};             // a window record's 16 scales
-      if (win) {
-        if (ok) {
-          const uint4 s4 = __ldg(reinterpret_cast<const uint4 *>(wrec + 512));
-          ws[0] = s4.x; ws[1] = s4.y; ws[2] = s4.z; ws[3] = s4.w;
-        }
-        // the range of the scales' exponents (0 marks a group of zeros)
-        int lo = 255, hi = 0;
-#pragma unroll
-        for (int i = 0; i < 16; i++) {
-          const int x = (int)((ws[i >> 2] >> (8 * (i & 3))) & 0xFFu);
-          if (x != 0) { lo = min(lo, x); hi = max(hi, x); }
-        }
-        lo = __reduce_min_sync(0xFFFFFFFFu, lo);
-        hi = __reduce_max_sync(0xFFFFFFFFu, hi);
-        if (lt == 0) { emin_sh = 255; emax_sh = 0; }
-        load_sync();
-        if (lane == 0) { atomicMin(&emin_sh, lo); atomicMax(&emax_sh, hi); }
-        load_sync();
-        if (emax_sh > 0 && (emax_sh - 127 > 7 || emin_sh - 127 < -15)) kx = 7 - (emax_sh - 127);
-      }
-      if (lt == 0) {
-        kx_sh = kx;
-        info_sh[k & 1] = info;
-      }
-      if (win) {
-#pragma unroll 1
-        for (int b = 0; b < 4; b++) {
-          if (b > 0 && k > 0) wait(&bar_free[b], (k - 1) & 1);
-          unsigned char *row = tile + 2 * b * 1024;
-          // 32 dims, one scale group
-          const uint32_t wsb = b == 0 ? ws[0] : b == 1 ? ws[1] : b == 2 ? ws[2] : ws[3];
-          const int eb = (int)((wsb >> (8 * part)) & 0xFFu);
-          const __half2 fac = __float2half2_rn(eb == 0 ? 0.f : ldexpf(1.f, eb - 127 + kx));
-#pragma unroll
-          for (int q = 0; q < 2; q++) {
-            const uint4 x = ok ? __ldg(reinterpret_cast<const uint4 *>(wrec + b * 128 + part * 32 + q * 16))
-                               : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-            uint32_t o[8];
-#pragma unroll
-            for (int u = 0; u < 8; u++) {
-              const uint32_t hv = e4m3x2_to_f16x2(w[u >> 1] >> (16 * (u & 1)));
-              const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&hv), fac);
-              o[u] = *reinterpret_cast<const uint32_t *>(&y);
-            }
-            *reinterpret_cast<uint4 *>(row + sw128(e & 7, ch0 + 2 * q)) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4 *>(row + sw128(e & 7, ch0 + 2 * q + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
-          }
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&bar_full[b]);
-        }
-#pragma unroll
-        for (int b = 0; b < 4; b++) load(next, b);
-      } else {
-#pragma unroll
-        for (int b = 0; b < 4; b++) {
-          if (b > 0 && k > 0) wait(&bar_free[b], (k - 1) & 1);
-          unsigned char *row = tile + 2 * b * 1024;
-          // 32 dims, two scale groups
-          const uint32_t sx = __shfl_sync(0xFFFFFFFFu, sc.x, b, 4), sy = __shfl_sync(0xFFFFFFFFu, sc.y, b, 4);
-          const uint32_t two = e4m3x2_to_f16x2(((part & 2) ? sy : sx) >> (16 * (part & 1)));
-          const uint32_t sg[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
-          const uint32_t w[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
-#pragma unroll
-          for (int u = 0; u < 4; u++) {              // 8 dims, half a scale group
-            uint32_t o[4];
-            e2m1x8_to_f16(w[u], o);
-#pragma unroll
-            for (int q = 0; q < 4; q++) {
-              const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&o[q]),
-                                        *reinterpret_cast<const __half2 *>(&sg[u >> 1]));
-              o[q] = *reinterpret_cast<const uint32_t *>(&y);
-            }
-            *reinterpret_cast<uint4 *>(row + sw128(e & 7, ch0 + u)) = make_uint4(o[0], o[1], o[2], o[3]);
-          }
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&bar_full[b]);
-          load(next, b);
-        }
-      }
-      load_scales(next);
-      ok = next != nullptr;
-    }
+    paged_softmax(A, S, sm, n_run, T, G, tmem);
+  } else if (warp < (kPgSoft + kPgLoad) / 32) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPgRegsK));
+    paged_load<false>(A, S, sm, n_run, tmem);
+  } else if (warp < (kPgSoft + 2 * kPgLoad) / 32) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPgRegsV));
+    paged_load<true>(A, S, sm, n_run, tmem);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPgRegsIssue));
-    // ======================================================== MMAs
-    // One thread, chosen by elect.sync, and descriptors that are a base plus a
-    // constant: 48 cycles an MMA, what N = 64 takes (6 KB of operands).  With the
-    // descriptors built at each MMA a thread issued one in 81 to 118 cycles.
-    if (warp == kPgSoftWarps + kPgLoadWarps && ptx::elect_one()) {
-      constexpr uint32_t id_qk = idesc_m128(0, true, kHeads);
-      constexpr uint32_t id_pv = idesc_m128(1, true, kHeads) | (1u << 16);   // both operands MN-major
-      const uint32_t base = ptx::smem_u32(sm);
-      const uint64_t d_k = ptx::smem_desc(base + kPgSmK, 16, 8192, 2), d_q = ptx::smem_desc(base + kPgSmQ, 16, 8192, 2);
-      const uint64_t d_v = ptx::smem_desc(base + kPgSmK, 1024, 8192, 2), d_p = ptx::smem_desc(base + kPgSmP, 1024, 1024, 2);
-      for (int k = 0; k < n_run && !bad_sh; k++) {
-#pragma unroll 1
-        for (int b = 0; b < 4; b++) {                // S^T += K Q^T over slab b
-          wait(&bar_full[b], k & 1);
-          ptx::tc_fence_after();
-          const uint64_t ka = d_k + b * 128, qa = d_q + b * 128;
-#pragma unroll
-          for (int kk = 0; kk < 8; kk++)
-            ptx::tc_mma_bf16(tmem + kPgColS, ka + (kk >> 2) * 64 + (kk & 3) * 2, qa + (kk >> 2) * 64 + (kk & 3) * 2,
-                             id_qk, kk > 0 ? 1u : (uint32_t)(b > 0));
-        }
-        ptx::tc_commit(&bar_s);
-        const uint32_t acc = k == 0 || info_sh[k & 1].y == 0 ? 0u : 1u;
-        wait(&bar_p, k & 1);
-        ptx::tc_fence_after();
-#pragma unroll 1
-        for (int b = 0; b < 4; b++) {                // O^T block b += K^T P
-          const uint64_t va = d_v + b * 128;
-#pragma unroll
-          for (int ks = 0; ks < kPgChunk / 16; ks++)
-            ptx::tc_mma_bf16(tmem + kPgColO + b * kHeads, va + ks * 1024, d_p + ks * 128, id_pv, ks > 0 ? 1u : acc);
-          ptx::tc_commit(&bar_free[b]);
-        }
-      }
-      ptx::tc_commit(&bar_drain);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPgRegsRest));
+    if (warp == (kPgSoft + 2 * kPgLoad) / 32) {
+      if (ptx::elect_one()) paged_issue_qk(A, S, sm, n_run, tmem);
+    } else if (warp == (kPgSoft + 2 * kPgLoad) / 32 + 1) {
+      if (ptx::elect_one()) paged_issue_pv(A, S, sm, n_run, tmem);
+    } else {
+      paged_fetch(A, S, sm, c_begin, c_end, warp - (kPgSoft + 2 * kPgLoad) / 32 - 2);
     }
     __syncwarp();
   }
   __syncthreads();
-  if (bad_sh) {
-    // a wait ran out: every MMA issued here finishes before the tensor memory goes back (bounded;
-    // the issuer commits to the drain barrier when it leaves)
-    ptx::mbar_wait(&bar_drain, 0);
+  if (S.bad) {
+    // a wait ran out: every MMA issued here finishes before the tensor memory goes
+    // back (bounded; each issuer commits to the drain barrier when it leaves)
+    ptx::mbar_wait(&S.drain, 0);
     ptx::tc_fence_after();
   }
   ptx::tc_fence_before();
@@ -693,7 +901,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
     const float m = __ldcg(A.part_ml + s * 2 * kHeads + h), l = __ldcg(A.part_ml + s * 2 * kHeads + kHeads + h);
     const float4 *src = reinterpret_cast<const float4 *>(A.part + (s * kHeads + h) * kDim + d);
     const float4 a = __ldcg(src), b = __ldcg(src + 1);
-    if (m == -INFINITY) continue;                    // nothing there to attend to
+    if (m == -kPgNoRef) continue;                    // nothing there to attend to
     const float w = exp2f(m - M);
     L += w * l;
     const float e[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -747,6 +955,10 @@ cudaError_t launch_paged_attn(PagedArgs A, double rope_base, void *ws, cudaStrea
   if (e != cudaSuccess) return e;
   const int64_t sms = device_sm_count(dev);
   rope_turns(rope_base, A.turn);
+  int shift = 0;
+  while (((int64_t)1 << shift) < A.page) shift++;
+  A.page_shift = 31 + shift;
+  A.page_mul = (uint64_t)((((unsigned __int128)1 << A.page_shift) + (unsigned)A.page - 1) / (unsigned)A.page);
   A.part = static_cast<float *>(ws);
   A.part_ml = A.part + 2 * (size_t)sms * kHeads * kDim;
   A.joins = reinterpret_cast<int4 *>(A.part_ml + 2 * (size_t)sms * 2 * kHeads);
