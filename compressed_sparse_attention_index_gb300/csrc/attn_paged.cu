@@ -48,7 +48,7 @@ constexpr int kPgSoft = 256, kPgLoad = 256;        // threads of the softmax gro
 constexpr int kPgThreads = kPgSoft + 2 * kPgLoad + 128;
 // Registers: 896 threads are launched with 72 each; the softmax group takes what
 // the others give up.
-constexpr int kPgRegsSoft = 104, kPgRegsK = 64, kPgRegsV = 56, kPgRegsRest = 56;
+constexpr int kPgRegsSoft = 104, kPgRegsK = 56, kPgRegsV = 72, kPgRegsRest = 40;
 static_assert(kPgSoft * kPgRegsSoft + kPgLoad * (kPgRegsK + kPgRegsV) + 128 * kPgRegsRest <= 72 * kPgThreads, "register split");
 constexpr int kPgSlab = 128 * 128 * 2;             // one slab: 128 entries x 128 dims f16
 constexpr int kPgRaw = kPgChunk * kKvBytes;        // one chunk's records
@@ -383,7 +383,12 @@ __device__ __forceinline__ void paged_load(const PagedArgs &A, PagedShared &S, u
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(V ? &S.v_full[mine] : &S.k_full[mine]);
     };
+    auto release = [&]() {                           // the buffer is read
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&S.raw_free[k & 1]);
+    };
     if (win > 0) {
+      release();
 #pragma unroll 1
       for (int i = 0; i < 8; i++) {
         const int b = mine + 2 * (i >> 2), j = i & 3;
@@ -418,39 +423,71 @@ __device__ __forceinline__ void paged_load(const PagedArgs &A, PagedShared &S, u
       const bool ok = ((I.valid[e >> 5] >> lane) & 1u) != 0u;
       const unsigned char *rec = sm + kPgSmRaw + (k & 1) * kPgRaw + e * kKvBytes + mine * 64;
       const unsigned char *scales = rec + 256 - mine * 56;
-      uint4 code = make_uint4(0u, 0u, 0u, 0u);       // the 32 dims ahead
-      if (ok) code = *reinterpret_cast<const uint4 *>(rec);
-#pragma unroll 1
-      for (int t = 0; t < 2; t++) {
-        uint2 sc = make_uint2(0u, 0u);
-        if (ok) sc = *reinterpret_cast<const uint2 *>(scales);
-        scales += 16;
+      auto convert = [&](int j, const uint4 &c, const uint2 &sc, uint32_t (&o)[16]) {
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+        const uint32_t two = e4m3x2_to_f16x2((j < 2 ? sc.x : sc.y) >> (16 * (j & 1)));
+        const uint32_t s2[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+          uint32_t x[4];
+          e2m1x8_to_f16(w[u], x);
+#pragma unroll
+          for (int q = 0; q < 4; q++) {
+            const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x[q]), *reinterpret_cast<const __half2 *>(&s2[u >> 1]));
+            o[4 * u + q] = *reinterpret_cast<const uint32_t *>(&y);
+          }
+        }
+      };
+      if (V) {
+        // both slabs are read at once, so that the buffer does not wait for PV
+        uint4 code[4], ahead[4];
+        uint2 sc = make_uint2(0u, 0u), sc_ahead = sc;
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-          const uint32_t w[4] = {code.x, code.y, code.z, code.w};
-          const uint32_t two = e4m3x2_to_f16x2((j < 2 ? sc.x : sc.y) >> (16 * (j & 1)));
-          const uint32_t s2[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
-          if (ok) code = *reinterpret_cast<const uint4 *>(j < 3 ? rec + (j + 1) * 16 : rec + (t == 0 ? 128 : 0));
-          uint32_t o[16];
-#pragma unroll
-          for (int u = 0; u < 4; u++) {
-            uint32_t x[4];
-            e2m1x8_to_f16(w[u], x);
-#pragma unroll
-            for (int q = 0; q < 4; q++) {
-              const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x[q]), *reinterpret_cast<const __half2 *>(&s2[u >> 1]));
-              o[4 * u + q] = *reinterpret_cast<const uint32_t *>(&y);
-            }
-          }
-          if (j == 0) begin(t);
-          put(j, o);
+          code[j] = ok ? *reinterpret_cast<const uint4 *>(rec + j * 16) : make_uint4(0u, 0u, 0u, 0u);
+          ahead[j] = ok ? *reinterpret_cast<const uint4 *>(rec + 128 + j * 16) : make_uint4(0u, 0u, 0u, 0u);
         }
-        rec += 128;
-        end();
+        if (ok) {
+          sc = *reinterpret_cast<const uint2 *>(scales);
+          sc_ahead = *reinterpret_cast<const uint2 *>(scales + 16);
+        }
+        release();
+#pragma unroll 1
+        for (int t = 0; t < 2; t++) {
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            uint32_t o[16];
+            convert(j, code[j], sc, o);
+            if (j == 0) begin(t);
+            put(j, o);
+            code[j] = ahead[j];
+          }
+          sc = sc_ahead;
+          end();
+        }
+      } else {
+        uint4 code = make_uint4(0u, 0u, 0u, 0u);     // the 32 dims ahead
+        if (ok) code = *reinterpret_cast<const uint4 *>(rec);
+#pragma unroll 1
+        for (int t = 0; t < 2; t++) {
+          uint2 sc = make_uint2(0u, 0u);
+          if (ok) sc = *reinterpret_cast<const uint2 *>(scales);
+          scales += 16;
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            const uint4 c = code;
+            if (ok) code = *reinterpret_cast<const uint4 *>(j < 3 ? rec + (j + 1) * 16 : rec + (t == 0 ? 128 : 0));
+            uint32_t o[16];
+            convert(j, c, sc, o);
+            if (j == 0) begin(t);
+            put(j, o);
+          }
+          rec += 128;
+          end();
+        }
+        release();
       }
     }
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(&S.raw_free[k & 1]);
   }
 }
 
@@ -849,7 +886,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPgRegsK));
     paged_load<false>(A, S, sm, n_run, tmem);
   } else if (warp < (kPgSoft + 2 * kPgLoad) / 32) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPgRegsV));
+    static_assert(kPgRegsV == 72, "the V group keeps what it was launched with");
     paged_load<true>(A, S, sm, n_run, tmem);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPgRegsRest));
