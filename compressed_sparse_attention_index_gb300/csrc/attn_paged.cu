@@ -48,19 +48,20 @@ constexpr int kPgSoft = 256, kPgLoad = 256;        // threads of the softmax gro
 constexpr int kPgThreads = kPgSoft + 2 * kPgLoad + 128;
 // Registers: 896 threads are launched with 72 each; the softmax group takes what
 // the others give up.
-constexpr int kPgRegsSoft = 104, kPgRegsK = 56, kPgRegsV = 72, kPgRegsRest = 40;
+constexpr int kPgRegsSoft = 96, kPgRegsK = 56, kPgRegsV = 80, kPgRegsRest = 40;
 static_assert(kPgSoft * kPgRegsSoft + kPgLoad * (kPgRegsK + kPgRegsV) + 128 * kPgRegsRest <= 72 * kPgThreads, "register split");
 constexpr int kPgSlab = 128 * 128 * 2;             // one slab: 128 entries x 128 dims f16
 constexpr int kPgRaw = kPgChunk * kKvBytes;        // one chunk's records
-constexpr int kPgSmV = 0;                          // two slabs: [e/8][dim/64][e%8][128 B]
-constexpr int kPgSmQ = kPgSmV + 2 * kPgSlab;       // 64 heads x 512 dims f16: [h/8][dim/64][h%8][128 B]
+constexpr unsigned kPgKRing = 3, kPgVRing = 3;     // slabs of K in tensor memory, of V in shared memory
+constexpr int kPgSmV = 0;                          // slabs: [e/8][dim/64][e%8][128 B]
+constexpr int kPgSmQ = kPgSmV + (int)kPgVRing * kPgSlab;       // 64 heads x 512 dims f16: [h/8][dim/64][h%8][128 B]
 constexpr int kPgSmP = kPgSmQ + 64 * 1024;         // 128 entries x 64 heads f16: [e/8][e%8][128 B]
-constexpr int kPgSmRaw = kPgSmP + 16 * 1024;       // two chunks of records
-constexpr int kPgSmEnd = kPgSmRaw + 2 * kPgRaw;
+constexpr int kPgSmRaw = kPgSmP + 16 * 1024;       // a chunk's records
+constexpr int kPgSmEnd = kPgSmRaw + kPgRaw;
 constexpr int kPgSmAlloc = kPgSmEnd + 1024;
 static_assert(kPgSmAlloc + 4608 <= 227 * 1024, "shared memory");
-// tensor memory: two S^T tiles, O^T, a ring of two 128-dim slabs of K
-constexpr uint32_t kPgColS = 0, kPgColO = 128, kPgColK = 384, kPgTmemCols = 512;
+// tensor memory: S^T, O^T, the ring of K
+constexpr uint32_t kPgColS = 0, kPgColO = 64, kPgColK = 320, kPgTmemCols = 512;
 constexpr float kPgRaise = 8.f, kPgShift = 7.f, kPgNoRef = 3e38f;   // (kPgNoRef: no entry met yet)
 constexpr int kPgInfo = 8;                         // chunks described in shared memory at a time
 
@@ -142,14 +143,17 @@ struct PagedInfo {
 };
 
 struct PagedShared {
-  uint64_t raw_full[2], raw_free[2], k_full[2], k_free[2], s_full[2], s_free[2], v_full[2], v_free[2];
-  uint64_t p_full, o_done, drain;
+  // of slab n: number n % 6 (each team passes every phase of what it waits on)
+  uint64_t k_full[6], k_free[6], v_full[6], v_free[6];
+  uint64_t raw_full[2], raw_free[2];   // one buffer; by the parity of the chunk, so that each fetching warp
+                                       // passes every phase of what it waits on
+  uint64_t q_done, s_full, s_free, p_full, o_done, drain;
   PagedInfo info[kPgInfo];
   __align__(16) float less[kHeads];    // minus a head's reference, which is kPgShift below a maximum
   float alpha[kHeads];
   float l[4][kHeads], red[4][kHeads];
   uint32_t tmem, qmax[8];
-  int emin[2], emax[2];         // (per loading group)
+  int emin, emax;
   int scan[kPgThreads / 32], start, off;
   volatile int bad;
 };
@@ -171,9 +175,32 @@ __device__ __forceinline__ void paged_wait(const PagedArgs &A, PagedShared &S, u
   }
 }
 
+// Where slab n of the run stands, for a role that takes slabs n, n + STEP, ..: its
+// slot in a ring of three and its barriers' number and phase.  Two teams take turns
+// at the slabs, so a slot passes from one to the other; the six barriers do not, and
+// a wait for the slab three before (the slot's last) is on a barrier of the other
+// parity, every phase of which that team waits for in turn.
+template <unsigned STEP>
+struct PagedSlab {
+  unsigned bar, phase, slot;
+  bool reuse;                   // the slot was used before (by slab n - 3)
+  __device__ __forceinline__ explicit PagedSlab(unsigned n) : bar(n), phase(0), slot(n), reuse(false) {}
+  __device__ __forceinline__ unsigned last_bar() const { return bar >= 3 ? bar - 3 : bar + 3; }
+  __device__ __forceinline__ unsigned last_phase() const { return bar >= 3 ? phase : phase ^ 1; }
+  __device__ __forceinline__ void next() {
+    bar += STEP;
+    if (bar >= 6) {
+      bar -= 6;
+      phase ^= 1;
+      reuse = true;
+    }
+    slot = bar >= 3 ? bar - 3 : bar;
+  }
+  __device__ __forceinline__ bool used() const { return reuse || bar >= 3; }
+};
+
 // ------------------------------------------------------------------ records
-// Two warps walk the chunks, one for each buffer: a lane finds the records of four
-// rows, and the first lane of every run of rows that are neighbours in the cache
+// Two warps take turns at the chunks: a lane finds the records of four rows, and the first lane of every run of rows that are neighbours in the cache
 // copies the run into shared memory.  A warp's next chunk is looked up, and its
 // records asked into L2, before the wait for the buffer (one warp for both buffers
 // took longer over a chunk than the MMAs).  A window chunk is read by the loading groups
@@ -233,10 +260,10 @@ __device__ __forceinline__ void paged_fetch(const PagedArgs &A, PagedShared &S, 
   if (more) look_up();
   int k = first;
   for (; more; k += 2) {
-    if (k >= 2) paged_wait(A, S, &S.raw_free[k & 1], ((k >> 1) - 1) & 1);
+    if (k >= 1) paged_wait(A, S, &S.raw_free[first ^ 1], ((k - 1) >> 1) & 1);
     if (__any_sync(0xFFFFFFFFu, S.bad)) break;       // no copy is started any more
     PagedInfo &I = S.info[k & (kPgInfo - 1)];
-    uint64_t *full = &S.raw_full[k & 1];
+    uint64_t *full = &S.raw_full[first];
     if (lane == 0) {
       I.at = at;
       I.seq = seq;
@@ -250,7 +277,7 @@ __device__ __forceinline__ void paged_fetch(const PagedArgs &A, PagedShared &S, 
       ptx::mbar_arrive_expect_tx(full, (uint32_t)(rows * kKvBytes));
     }
     __syncwarp();
-    unsigned char *raw = sm + kPgSmRaw + (k & 1) * kPgRaw;
+    unsigned char *raw = sm + kPgSmRaw;
 #pragma unroll
     for (int g = 0; g < 4; g++) {
       const int n = run_rows(g);
@@ -271,28 +298,28 @@ __device__ __forceinline__ void paged_fetch(const PagedArgs &A, PagedShared &S, 
   if (k >= 2) ptx::mbar_wait(&S.raw_full[first], ((k >> 1) - 1) & 1);
 }
 
-// Both loading groups walk the chunks in two halves of four warps, one for each
-// slot of its ring of slabs: half g has slabs g and g + 2 of every chunk, a row per
-// thread.  The K group puts slabs into tensor memory for QK and runs up to a chunk
-// ahead; the V group puts them into shared memory, MN-major operands of PV, as PV
-// frees them.  Reading K from shared memory too would cost QK 48 cycles an MMA
-// instead of 32 and tie its tile to PV's.
-template <bool V>
+// The K group dequantises the chunks into a ring of slabs in tensor memory, in two
+// teams of four warps, a row per thread: team g has slabs g and g + 2 of every chunk.
+// QK reads them there, 32 cycles an MMA (48 from shared memory, whose bandwidth PV
+// needs), and the V group copies them from there.
 __device__ __forceinline__ void paged_load(const PagedArgs &A, PagedShared &S, unsigned char *sm, int n_run, uint32_t tmem) {
-  constexpr int kBar = V ? 3 : 2;
-  const int lt = (int)threadIdx.x - (V ? kPgSoft + kPgLoad : kPgSoft), lane = lt & 31;
-  const int e = lt & 127, mine = lt >> 7;            // row; slot, and first of its two slabs
-  // the row's 128 B in the slab's first 64 dims, chunk c at `tile` ^ 16 c
-  unsigned char *tile = sm + kPgSmV + mine * kPgSlab + (e >> 3) * 2048 + (e & 7) * 128 + (e & 7) * 16;
-  const uint32_t kcol = tmem + ((uint32_t)(e & 96) << 16) + kPgColK + mine * 64;
+  constexpr int kBar = 2;
+  const int lt = (int)threadIdx.x - kPgSoft, lane = lt & 31;
+  const int e = lt & 127, team = lt >> 7;            // row
+  const uint32_t kcol0 = tmem + ((uint32_t)(e & 96) << 16) + kPgColK;
   float q_scale = 1.f;
+  PagedSlab<2> n((unsigned)team);                    // the next slab
+  unsigned q_parity = 0;                             // of the last query
   for (int k = 0; k < n_run; k++) {
     paged_wait(A, S, &S.raw_full[k & 1], (k >> 1) & 1);
     PagedInfo &I = S.info[k & (kPgInfo - 1)];
     const int win = I.win;
-    if (!V && (k == 0 || I.at.y == 0)) {
+    if (k == 0 || I.at.y == 0) {
       // ---------------------------------------------------- Q to f16, K-major, 128B swizzle
-      if (k > 0) paged_wait(A, S, &S.k_free[1], 1);  // (the chunk before is multiplied: its last slab, use 2 k - 1 of slot 1)
+      if (k > 0) {                                   // (the query before is multiplied)
+        paged_wait(A, S, &S.q_done, q_parity);
+        q_parity ^= 1;
+      }
       const uint4 *src = reinterpret_cast<const uint4 *>(A.q + (int64_t)I.at.x * kHeads * kDim) + lt;
       uint32_t m = 0u;
 #pragma unroll 4
@@ -343,45 +370,32 @@ __device__ __forceinline__ void paged_load(const PagedArgs &A, PagedShared &S, u
       }
       lo = __reduce_min_sync(0xFFFFFFFFu, lo);
       hi = __reduce_max_sync(0xFFFFFFFFu, hi);
-      if (lt == 0) { S.emin[V] = 255; S.emax[V] = 0; }
+      if (lt == 0) { S.emin = 255; S.emax = 0; }
       group_sync<kBar>();
-      if (lane == 0) { atomicMin(&S.emin[V], lo); atomicMax(&S.emax[V], hi); }
+      if (lane == 0) { atomicMin(&S.emin, lo); atomicMax(&S.emax, hi); }
       group_sync<kBar>();
-      const int emax = S.emax[V] - 127, emin = S.emin[V] - 127;
+      const int emax = S.emax - 127, emin = S.emin - 127;
       if (emax > -127 && (emax > 7 || emin < -15)) kx = 7 - emax;
     }
-    if (!V && lt == 0) {
+    if (lt == 0) {
       I.f = ldexpf(q_scale, -kx);
       I.kx = kx;
     }
-    // The row's two slabs, 32 dims (16 words of two f16) at a time; turn t is use
-    // 2 k + t of the slot.  (One slab's code, not the chunk's: six roles share the
-    // instruction caches, and with everything unrolled the warps waited for
-    // instructions four times as long as they issued them.)
-    auto begin = [&](int t) {
-      const int use = 2 * k + t;
-      if (use >= 1) paged_wait(A, S, V ? &S.v_free[mine] : &S.k_free[mine], (use - 1) & 1);
-      if (!V) ptx::tc_fence_after();
-    };
-    auto put = [&](int j, const uint32_t (&o)[16]) {
-      if (V) {
-#pragma unroll
-        for (int u = 0; u < 4; u++)
-          *reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(reinterpret_cast<uintptr_t>(tile) ^ (((j & 1) * 4 + u) << 4)) + (j >> 1) * 1024) =
-              make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-      } else {
-        ptx::tmem_st_32x32b_x16(kcol + j * 16, o);
-      }
+    // 32 dims (16 words of two f16) at a time.  (One slab's code, not the chunk's: six
+    // roles share the instruction caches, and with everything unrolled the warps waited
+    // for instructions four times as long as they issued them.)
+    uint32_t kcol = kcol0;
+    auto begin = [&]() {
+      kcol = kcol0 + n.slot * 64;
+      if (n.used()) paged_wait(A, S, &S.k_free[n.last_bar()], n.last_phase());
+      ptx::tc_fence_after();
     };
     auto end = [&]() {
-      if (V) {
-        ptx::fence_proxy_async_smem();
-      } else {
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
-      }
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(V ? &S.v_full[mine] : &S.k_full[mine]);
+      if (lane == 0) ptx::mbar_arrive(&S.k_full[n.bar]);
+      n.next();
     };
     auto release = [&]() {                           // the buffer is read
       __syncwarp();
@@ -391,7 +405,7 @@ __device__ __forceinline__ void paged_load(const PagedArgs &A, PagedShared &S, u
       release();
 #pragma unroll 1
       for (int i = 0; i < 8; i++) {
-        const int b = mine + 2 * (i >> 2), j = i & 3;
+        const int b = team + 2 * (i >> 2), j = i & 3;
         const uint32_t wb = b == 0 ? ws.x : b == 1 ? ws.y : b == 2 ? ws.z : ws.w;
         const int eb = (int)((wb >> (8 * j)) & 0xFFu);
         const __half2 fac = __float2half2_rn(eb == 0 ? 0.f : ldexpf(1.f, eb - 127 + kx));
@@ -407,87 +421,101 @@ __device__ __forceinline__ void paged_load(const PagedArgs &A, PagedShared &S, u
             o[8 * h + q] = *reinterpret_cast<const uint32_t *>(&y);
           }
         }
-        if (j == 0) begin(i >> 2);
-        // (j is a run-time number here)
-        if (V) {
-          unsigned char *row = reinterpret_cast<unsigned char *>(reinterpret_cast<uintptr_t>(tile) ^ (uintptr_t)((j & 1) << 6)) + (j >> 1) * 1024;
-#pragma unroll
-          for (int u = 0; u < 4; u++)
-            *reinterpret_cast<uint4 *>(reinterpret_cast<uintptr_t>(row) ^ (uintptr_t)(u << 4)) = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-        } else {
-          ptx::tmem_st_32x32b_x16(kcol + j * 16, o);
-        }
+        if (j == 0) begin();
+        ptx::tmem_st_32x32b_x16(kcol + j * 16, o);
         if (j == 3) end();
       }
     } else {
       const bool ok = ((I.valid[e >> 5] >> lane) & 1u) != 0u;
-      const unsigned char *rec = sm + kPgSmRaw + (k & 1) * kPgRaw + e * kKvBytes + mine * 64;
-      const unsigned char *scales = rec + 256 - mine * 56;
-      auto convert = [&](int j, const uint4 &c, const uint2 &sc, uint32_t (&o)[16]) {
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-        const uint32_t two = e4m3x2_to_f16x2((j < 2 ? sc.x : sc.y) >> (16 * (j & 1)));
-        const uint32_t s2[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
+      // Records are 18 16-B units apart, so rows r and r + 4 of a unit share their banks:
+      // every other four rows read the units of a pair the other way round (shared memory
+      // is what bounds the kernel; the selects are cheap).  Rows without an entry read
+      // what is there: any code is finite, and their scales are zeroed.
+      const bool flip = (e & 4) != 0;
+      const unsigned char *raw = sm + kPgSmRaw + e * kKvBytes + (flip ? 16 : 0);
+      const int other = flip ? -16 : 16;
+      uint32_t sc[4];                                // two slabs' eight scales
+      {
+        const uint4 x = *reinterpret_cast<const uint4 *>(raw + 256), y = *reinterpret_cast<const uint4 *>(raw + 256 + other);
+        const uint32_t x0 = team ? x.z : x.x, x1 = team ? x.w : x.y, y0 = team ? y.z : y.x, y1 = team ? y.w : y.y;
+        sc[0] = ok ? (flip ? y0 : x0) : 0u;
+        sc[1] = ok ? (flip ? y1 : x1) : 0u;
+        sc[2] = ok ? (flip ? x0 : y0) : 0u;
+        sc[3] = ok ? (flip ? x1 : y1) : 0u;
+      }
+      raw += team * 64;
+#pragma unroll 1
+      for (int t = 0; t < 2; t++) {
+        uint4 code[4];
 #pragma unroll
-        for (int u = 0; u < 4; u++) {
-          uint32_t x[4];
-          e2m1x8_to_f16(w[u], x);
-#pragma unroll
-          for (int q = 0; q < 4; q++) {
-            const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x[q]), *reinterpret_cast<const __half2 *>(&s2[u >> 1]));
-            o[4 * u + q] = *reinterpret_cast<const uint32_t *>(&y);
-          }
+        for (int j = 0; j < 4; j += 2) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(raw + j * 16), y = *reinterpret_cast<const uint4 *>(raw + j * 16 + other);
+          code[j] = flip ? y : x;
+          code[j + 1] = flip ? x : y;
         }
-      };
-      if (V) {
-        // both slabs are read at once, so that the buffer does not wait for PV
-        uint4 code[4], ahead[4];
-        uint2 sc = make_uint2(0u, 0u), sc_ahead = sc;
+        raw += 128;
+        if (t == 1) release();
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-          code[j] = ok ? *reinterpret_cast<const uint4 *>(rec + j * 16) : make_uint4(0u, 0u, 0u, 0u);
-          ahead[j] = ok ? *reinterpret_cast<const uint4 *>(rec + 128 + j * 16) : make_uint4(0u, 0u, 0u, 0u);
-        }
-        if (ok) {
-          sc = *reinterpret_cast<const uint2 *>(scales);
-          sc_ahead = *reinterpret_cast<const uint2 *>(scales + 16);
-        }
-        release();
-#pragma unroll 1
-        for (int t = 0; t < 2; t++) {
+          const uint32_t w[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
+          const uint32_t two = e4m3x2_to_f16x2(sc[j >> 1] >> (16 * (j & 1)));
+          const uint32_t s2[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
+          uint32_t o[16];
 #pragma unroll
-          for (int j = 0; j < 4; j++) {
-            uint32_t o[16];
-            convert(j, code[j], sc, o);
-            if (j == 0) begin(t);
-            put(j, o);
-            code[j] = ahead[j];
-          }
-          sc = sc_ahead;
-          end();
-        }
-      } else {
-        uint4 code = make_uint4(0u, 0u, 0u, 0u);     // the 32 dims ahead
-        if (ok) code = *reinterpret_cast<const uint4 *>(rec);
-#pragma unroll 1
-        for (int t = 0; t < 2; t++) {
-          uint2 sc = make_uint2(0u, 0u);
-          if (ok) sc = *reinterpret_cast<const uint2 *>(scales);
-          scales += 16;
+          for (int u = 0; u < 4; u++) {
+            uint32_t x[4];
+            e2m1x8_to_f16(w[u], x);
 #pragma unroll
-          for (int j = 0; j < 4; j++) {
-            const uint4 c = code;
-            if (ok) code = *reinterpret_cast<const uint4 *>(j < 3 ? rec + (j + 1) * 16 : rec + (t == 0 ? 128 : 0));
-            uint32_t o[16];
-            convert(j, c, sc, o);
-            if (j == 0) begin(t);
-            put(j, o);
+            for (int q = 0; q < 4; q++) {
+              const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x[q]), *reinterpret_cast<const __half2 *>(&s2[u >> 1]));
+              o[4 * u + q] = *reinterpret_cast<const uint32_t *>(&y);
+            }
           }
-          rec += 128;
-          end();
+          if (j == 0) begin();
+          ptx::tmem_st_32x32b_x16(kcol + j * 16, o);
         }
-        release();
+        sc[0] = sc[2];
+        sc[1] = sc[3];
+        end();
       }
     }
+  }
+}
+
+// The V group copies the slabs from tensor memory into a ring in shared memory, where
+// PV reads them MN-major, in two teams as the K group: a thread per row, holding a slab
+// in registers until PV has freed its slot.  (Dequantising them a second time cost more
+// arithmetic than everything else together.)
+__device__ __forceinline__ void paged_copy(const PagedArgs &A, PagedShared &S, unsigned char *sm, int n_run, uint32_t tmem) {
+  const int lt = (int)threadIdx.x - kPgSoft - kPgLoad, lane = lt & 31;
+  const int e = lt & 127, team = lt >> 7;
+  const uint32_t kcol = tmem + ((uint32_t)(e & 96) << 16) + kPgColK;
+  // the row's 128 B of the first 64 dims in slot 0, chunk c at `tile` ^ 16 c
+  const uintptr_t tile = reinterpret_cast<uintptr_t>(sm + kPgSmV + (e >> 3) * 2048 + (e & 7) * 128 + (e & 7) * 16);
+  static_assert(kPgVRing == kPgKRing, "one slot number for both rings");
+  PagedSlab<2> n((unsigned)team);
+#pragma unroll 1
+  for (int i = 0; i < 2 * n_run; i++, n.next()) {
+    uint32_t r[2][32];
+    paged_wait(A, S, &S.k_full[n.bar], n.phase);
+    ptx::tc_fence_after();
+    ptx::tmem_ld_32x32b_x32(kcol + n.slot * 64, r[0]);
+    ptx::tmem_ld_32x32b_x32(kcol + n.slot * 64 + 32, r[1]);
+    ptx::tmem_wait_ld();
+    ptx::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&S.k_free[n.bar]);
+    if (n.used()) paged_wait(A, S, &S.v_free[n.last_bar()], n.last_phase());
+    const uintptr_t at = tile + n.slot * kPgSlab;
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+#pragma unroll
+      for (int c = 0; c < 8; c++)
+        *reinterpret_cast<uint4 *>((at ^ (uintptr_t)(c << 4)) + h * 1024) =
+            make_uint4(r[h][4 * c], r[h][4 * c + 1], r[h][4 * c + 2], r[h][4 * c + 3]);
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&S.v_full[n.bar]);
   }
 }
 
@@ -540,22 +568,17 @@ __device__ __forceinline__ void paged_logits(uint32_t ta, float f, float none, c
     }
   }
 }
-// Their numerators 2^s, and rounded to f16; true where one is out of the range that
-// f16 should hold (or not a number).
-__device__ __forceinline__ bool paged_numerators(uint64_t (&s)[16], uint32_t (&o)[16]) {
+// Their numerators 2^s; true where one is out of the range that f16 should hold.
+__device__ __forceinline__ bool paged_numerators(uint64_t (&s)[16]) {
+  float top = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; i++) {
     const float2 x = unpair(s[i]);
     const float p0 = ex2(x.x), p1 = ex2(x.y);
     s[i] = pair(p0, p1);
-    const __half2 h2 = __floats2half2_rn(p0, p1);
-    o[i] = *reinterpret_cast<const uint32_t *>(&h2);
+    top = fmaxf(top, fmaxf(p0, p1));
   }
-  // (positive f16 compare as integers; infinity and NaN are above all of them)
-  uint32_t top = o[0];
-#pragma unroll
-  for (int i = 1; i < 16; i++) top = __vmaxu2(top, o[i]);
-  return (top >> 16) > 0x7800u || (top & 0xFFFFu) > 0x7800u;           // 2^15
+  return top > 32768.f;
 }
 
 // Warp w has TMEM lane quarter w % 4 (S: entries, O: dims) and heads 32 (w / 4) ..
@@ -569,7 +592,7 @@ __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S
   bool acc = false;                                  // O holds something of this query
   int lc0 = 0;
   for (int k = 0; k < n_run; k++) {
-    paged_wait(A, S, &S.s_full[k & 1], (k >> 1) & 1);
+    paged_wait(A, S, &S.s_full, k & 1);
     ptx::tc_fence_after();
     const PagedInfo &info = S.info[k & (kPgInfo - 1)];
     const int4 I = info.at;
@@ -586,11 +609,10 @@ __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S
     const float f = info.f;
     const int kx = info.kx;
     const float none = ((info.valid[quarter] >> lane) & 1u) != 0u ? 0.f : -INFINITY;
-    const uint32_t ta = tq + kPgColS + (k & 1) * kHeads + hb;
+    const uint32_t ta = tq + kPgColS + hb;
     uint64_t s[16];
-    uint32_t o[16];
     paged_logits<true>(ta, f, none, &S.less[hb], s);
-    const bool over = paged_numerators(s, o);
+    const bool over = paged_numerators(s);
     // (a window's 2^-kx is undone before the next chunk)
     if (soft_any(over || (acc && o_scale != 1.f))) {
       // the chunk's maximum of every head: lane L ends with head hb + L
@@ -650,20 +672,27 @@ __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S
         l_acc[i] = pair(l.x * S.alpha[hb + 2 * i], l.y * S.alpha[hb + 2 * i + 1]);
       }
       paged_logits<true>(ta, f, none, &S.less[hb], s);
-      paged_numerators(s, o);
+      paged_numerators(s);
     }
     ptx::tc_fence_before();
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(&S.s_free[k & 1]);
+    if (lane == 0) ptx::mbar_arrive(&S.s_free);
 #pragma unroll
     for (int i = 0; i < 16; i++) l_acc[i] = add2(l_acc[i], s[i]);
     // P is free once PV of the chunk before is complete
     if (k > 0) paged_wait(A, S, &S.o_done, (k - 1) & 1);
     unsigned char *row = sm + kPgSmP + (e_row >> 3) * 1024;
 #pragma unroll
-    for (int q = 0; q < 4; q++)
-      *reinterpret_cast<uint4 *>(row + sw128(e_row & 7, (hb >> 3) + q)) =
-          make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+    for (int q = 0; q < 4; q++) {
+      uint32_t o[4];
+#pragma unroll
+      for (int u = 0; u < 4; u++) {
+        const float2 x = unpair(s[4 * q + u]);
+        const __half2 h2 = __floats2half2_rn(x.x, x.y);
+        o[u] = *reinterpret_cast<const uint32_t *>(&h2);
+      }
+      *reinterpret_cast<uint4 *>(row + sw128(e_row & 7, (hb >> 3) + q)) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
     ptx::tc_fence_before();
     ptx::fence_proxy_async_smem();
     __syncwarp();
@@ -715,28 +744,43 @@ __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S
     for (int blk = warp >> 2; blk < 4; blk += 2) {
       const int d = blk * 128 + quarter * 32 + lane;
       float cs = 1.f, sn = 0.f;
-      if (whole && d >= kRopeOff) turn_cs((uint64_t)(int64_t)pos * A.turn[(d - kRopeOff) >> 1], cs, sn);
+      if (whole && d >= kRopeOff) {
+        turn_cs((uint64_t)(int64_t)pos * A.turn[(d - kRopeOff) >> 1], cs, sn);
+        if (d & 1) sn = -sn;                         // (a, b) -> (a c + b s, b c - a s)
+      }
 #pragma unroll 1
-      for (int hh = 0; hh < 2; hh++) {
-        uint32_t r[32];
-        ptx::tmem_ld_32x32b_x32(tq + kPgColO + blk * kHeads + hh * 32, r);
+      for (int h = 0; h < kHeads; h += 16) {
+        uint32_t r[16];
+        ptx::tmem_ld_32x32b_x16(tq + kPgColO + blk * kHeads + h, r);
         ptx::tmem_wait_ld();
         if (!whole) {
-          float *P = A.part + (slot * kHeads + hh * 32) * kDim + d;
+          float *P = A.part + (slot * kHeads + h) * kDim + d;
 #pragma unroll
-          for (int i = 0; i < 32; i++) P[i * kDim] = __uint_as_float(r[i]) * S.alpha[hh * 32 + i];
+          for (int i = 0; i < 16; i++) P[i * kDim] = __uint_as_float(r[i]) * S.alpha[h + i];
           continue;
         }
+        const int64_t at = ((int64_t)I.x * kHeads + h) * kDim + d;
 #pragma unroll
-        for (int i = 0; i < 32; i++) {
-          float x = __uint_as_float(r[i]) * S.alpha[hh * 32 + i];
-          if (blk == 3 && quarter >= 2) {            // (a, b) by -pos; the partner is in the next lane
-            const float y = __shfl_xor_sync(0xFFFFFFFFu, x, 1);
-            x = (d & 1) ? x * cs - y * sn : x * cs + y * sn;
+        for (int i = 0; i < 16; i += 2) {
+          // the lane's dim and its neighbour's, of two heads: the rotation by -pos needs
+          // both, and an even lane then stores the pair of one head, an odd lane of the other
+          float x0 = __uint_as_float(r[i]) * S.alpha[h + i], x1 = __uint_as_float(r[i + 1]) * S.alpha[h + i + 1];
+          float y0 = __shfl_xor_sync(0xFFFFFFFFu, x0, 1), y1 = __shfl_xor_sync(0xFFFFFFFFu, x1, 1);
+          if (blk == 3 && quarter >= 2) {
+            const float w0 = x0 * cs + y0 * sn, w1 = x1 * cs + y1 * sn;
+            y0 = y0 * cs - x0 * sn;
+            y1 = y1 * cs - x1 * sn;
+            x0 = w0;
+            x1 = w1;
           }
-          const int64_t at = ((int64_t)I.x * kHeads + hh * 32 + i) * kDim + d;
-          if (A.out_f32) static_cast<float *>(A.out)[at] = x;
-          else static_cast<__nv_bfloat16 *>(A.out)[at] = __float2bfloat16_rn(x);
+          if (A.out_f32) {
+            static_cast<float *>(A.out)[at + (int64_t)i * kDim] = x0;
+            static_cast<float *>(A.out)[at + (int64_t)(i + 1) * kDim] = x1;
+          } else {
+            const bool odd = (lane & 1) != 0;
+            const __nv_bfloat162 v = odd ? __floats2bfloat162_rn(y1, x1) : __floats2bfloat162_rn(x0, y0);
+            *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(A.out) + at + (int64_t)(i + (odd ? 1 : 0)) * kDim - (odd ? 1 : 0)) = v;
+          }
         }
       }
     }
@@ -756,21 +800,25 @@ __device__ __forceinline__ void paged_issue_qk(const PagedArgs &A, PagedShared &
                                                uint32_t tmem) {
   constexpr uint32_t id = idesc_m128(0, true, kHeads);
   const uint64_t d_q = ptx::smem_desc(ptx::smem_u32(sm + kPgSmQ), 16, 8192, 2);
+  PagedSlab<1> n(0u);
   for (int k = 0; k < n_run && !S.bad; k++) {
-    if (k >= 2) paged_wait(A, S, &S.s_free[k & 1], ((k >> 1) - 1) & 1);
+    if (k >= 1) paged_wait(A, S, &S.s_free, (k - 1) & 1);
 #pragma unroll 1
-    for (int b = 0; b < 4; b++) {                    // S^T += K Q^T over slab n = 4 k + b
-      paged_wait(A, S, &S.k_full[b & 1], ((4 * k + b) >> 1) & 1);
+    for (int b = 0; b < 4; b++) {                    // S^T += K Q^T over slab 4 k + b
+      paged_wait(A, S, &S.k_full[n.bar], n.phase);
       ptx::tc_fence_after();
       const uint64_t qa = d_q + b * 128;
-      const uint32_t ka = tmem + kPgColK + (b & 1) * 64;
+      const uint32_t ka = tmem + kPgColK + n.slot * 64;
 #pragma unroll
       for (int kk = 0; kk < 8; kk++)
-        ptx::tc_mma_f16_ts(tmem + kPgColS + (k & 1) * kHeads, ka + kk * 8, qa + (kk >> 2) * 64 + (kk & 3) * 2, id,
+        ptx::tc_mma_f16_ts(tmem + kPgColS, ka + kk * 8, qa + (kk >> 2) * 64 + (kk & 3) * 2, id,
                            kk > 0 ? 1u : (uint32_t)(b > 0));
-      ptx::tc_commit(&S.k_free[b & 1]);
+      ptx::tc_commit(&S.k_free[n.bar]);
+      n.next();
     }
-    ptx::tc_commit(&S.s_full[k & 1]);
+    ptx::tc_commit(&S.s_full);
+    const int4 at = S.info[k & (kPgInfo - 1)].at;
+    if (at.y + 1 == at.z) ptx::tc_commit(&S.q_done);
   }
   ptx::tc_commit(&S.drain);
 }
@@ -779,18 +827,20 @@ __device__ __forceinline__ void paged_issue_pv(const PagedArgs &A, PagedShared &
   constexpr uint32_t id = idesc_m128(1, true, kHeads) | (1u << 16);   // both operands MN-major
   const uint64_t d_v = ptx::smem_desc(ptx::smem_u32(sm + kPgSmV), 1024, 2048, 2);
   const uint64_t d_p = ptx::smem_desc(ptx::smem_u32(sm + kPgSmP), 1024, 1024, 2);
+  PagedSlab<1> n(0u);
   for (int k = 0; k < n_run && !S.bad; k++) {
     paged_wait(A, S, &S.p_full, k & 1);
     const uint32_t acc = k == 0 || S.info[k & (kPgInfo - 1)].at.y == 0 ? 0u : 1u;
 #pragma unroll 1
-    for (int b = 0; b < 4; b++) {                    // O^T block b += V^T P, slab n = 4 k + b
-      paged_wait(A, S, &S.v_full[b & 1], ((4 * k + b) >> 1) & 1);
+    for (int b = 0; b < 4; b++) {                    // O^T block b += V^T P over slab 4 k + b
+      paged_wait(A, S, &S.v_full[n.bar], n.phase);
       ptx::tc_fence_after();
-      const uint64_t va = d_v + (b & 1) * (kPgSlab >> 4);
+      const uint64_t va = d_v + n.slot * (kPgSlab >> 4);
 #pragma unroll
       for (int ks = 0; ks < kPgChunk / 16; ks++)
         ptx::tc_mma_bf16(tmem + kPgColO + b * kHeads, va + ks * 256, d_p + ks * 128, id, ks > 0 ? 1u : acc);
-      ptx::tc_commit(&S.v_free[b & 1]);
+      ptx::tc_commit(&S.v_free[n.bar]);
+      n.next();
     }
     ptx::tc_commit(&S.o_done);
   }
@@ -804,16 +854,19 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
   __shared__ __align__(16) PagedShared S;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   if (t == 0) {
-    for (int i = 0; i < 2; i++) {
-      ptx::mbar_init(&S.raw_full[i], 1);
-      ptx::mbar_init(&S.raw_free[i], 2 * kPgLoad / 32);
+    for (int i = 0; i < 6; i++) {
       ptx::mbar_init(&S.k_full[i], kPgLoad / 64);
-      ptx::mbar_init(&S.k_free[i], 1);
+      ptx::mbar_init(&S.k_free[i], 1 + kPgLoad / 64);
       ptx::mbar_init(&S.v_full[i], kPgLoad / 64);
       ptx::mbar_init(&S.v_free[i], 1);
-      ptx::mbar_init(&S.s_full[i], 1);
-      ptx::mbar_init(&S.s_free[i], kPgSoft / 32);
     }
+    for (int i = 0; i < 2; i++) {
+      ptx::mbar_init(&S.raw_full[i], 1);
+      ptx::mbar_init(&S.raw_free[i], kPgLoad / 32);
+    }
+    ptx::mbar_init(&S.q_done, 1);
+    ptx::mbar_init(&S.s_full, 1);
+    ptx::mbar_init(&S.s_free, kPgSoft / 32);
     ptx::mbar_init(&S.p_full, kPgSoft / 32);
     ptx::mbar_init(&S.o_done, 1);
     ptx::mbar_init(&S.drain, 2);
@@ -884,10 +937,10 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     paged_softmax(A, S, sm, n_run, T, G, tmem);
   } else if (warp < (kPgSoft + kPgLoad) / 32) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPgRegsK));
-    paged_load<false>(A, S, sm, n_run, tmem);
+    paged_load(A, S, sm, n_run, tmem);
   } else if (warp < (kPgSoft + 2 * kPgLoad) / 32) {
-    static_assert(kPgRegsV == 72, "the V group keeps what it was launched with");
-    paged_load<true>(A, S, sm, n_run, tmem);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPgRegsV));
+    paged_copy(A, S, sm, n_run, tmem);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPgRegsRest));
     if (warp == (kPgSoft + 2 * kPgLoad) / 32) {
