@@ -214,7 +214,8 @@ __device__ __forceinline__ void paged_fetch(const PagedArgs &A, PagedShared &S, 
   C.off = S.off;
   if (c_begin < c_end) C.Q = paged_query(A, C.qi);
   const uint8_t *rec[4];                             // rows 32 g + lane
-  uint32_t valid[4], lead[4];
+  uint32_t valid[4];
+  int rows[4], all_rows = 0;                         // of the run this lane leads, 0: none; of the chunk
   int4 at;
   int seq, win;
   auto look_up = [&]() {
@@ -245,53 +246,44 @@ __device__ __forceinline__ void paged_fetch(const PagedArgs &A, PagedShared &S, 
       if (!ok) id[g] = -1;
       rec[g] = A.pages + ((int64_t)id[g] * A.page + off[g]) * kKvBytes;
       const int pid = __shfl_up_sync(0xFFFFFFFFu, id[g], 1), poff = __shfl_up_sync(0xFFFFFFFFu, off[g], 1);
+      const bool leads = ok && (lane == 0 || pid != id[g] || poff + 1 != off[g]);
       valid[g] = __ballot_sync(0xFFFFFFFFu, ok);
-      lead[g] = __ballot_sync(0xFFFFFFFFu, ok && (lane == 0 || pid != id[g] || poff + 1 != off[g]));
+      // its run ends before the next leader or the next row without an entry
+      const uint32_t lead = __ballot_sync(0xFFFFFFFFu, leads);
+      const uint32_t stop = (lead | ~valid[g]) & ~((2u << lane) - 1u);     // (lane 31: 2 << 31 is 0)
+      rows[g] = leads ? (stop != 0u ? __ffs(stop) - 1 : 32) - lane : 0;
     }
+    all_rows = __popc(valid[0]) + __popc(valid[1]) + __popc(valid[2]) + __popc(valid[3]);
     if (out) record_error(A.status, CSA2_ERR_BOUNDS);
-  };
-  // rows of the run that this lane leads, in group g (0: none)
-  auto run_rows = [&](int g) -> int {
-    if (((lead[g] >> lane) & 1u) == 0u) return 0;
-    const uint32_t stop = (lead[g] | ~valid[g]) & ~((2u << lane) - 1u);    // (lane 31: 2 << 31 is 0)
-    return (stop != 0u ? __ffs(stop) - 1 : 32) - lane;
   };
   bool more = C.settle(A);
   if (more) look_up();
   int k = first;
   for (; more; k += 2) {
-    if (k >= 1) paged_wait(A, S, &S.raw_free[first ^ 1], ((k - 1) >> 1) & 1);
-    if (__any_sync(0xFFFFFFFFu, S.bad)) break;       // no copy is started any more
     PagedInfo &I = S.info[k & (kPgInfo - 1)];
-    uint64_t *full = &S.raw_full[first];
     if (lane == 0) {
       I.at = at;
       I.seq = seq;
       I.win = win;
-      int rows = 0;
 #pragma unroll
-      for (int g = 0; g < 4; g++) {
+      for (int g = 0; g < 4; g++)
         I.valid[g] = win == 0 ? valid[g] : win > 32 * g ? (win >= 32 * g + 32 ? 0xFFFFFFFFu : (1u << (win - 32 * g)) - 1u) : 0u;
-        rows += __popc(valid[g]);
-      }
-      ptx::mbar_arrive_expect_tx(full, (uint32_t)(rows * kKvBytes));
     }
+    if (k >= 1) paged_wait(A, S, &S.raw_free[first ^ 1], ((k - 1) >> 1) & 1);
+    if (__any_sync(0xFFFFFFFFu, S.bad)) break;       // no copy is started any more
+    uint64_t *full = &S.raw_full[first];
+    if (lane == 0) ptx::mbar_arrive_expect_tx(full, (uint32_t)(all_rows * kKvBytes));
     __syncwarp();
-    unsigned char *raw = sm + kPgSmRaw;
 #pragma unroll
-    for (int g = 0; g < 4; g++) {
-      const int n = run_rows(g);
-      if (n > 0) ptx::bulk_load(raw + (32 * g + lane) * kKvBytes, rec[g], (uint32_t)(n * kKvBytes), full);
-    }
+    for (int g = 0; g < 4; g++)
+      if (rows[g] > 0) ptx::bulk_load(sm + kPgSmRaw + (32 * g + lane) * kKvBytes, rec[g], (uint32_t)(rows[g] * kKvBytes), full);
     C.c += 2;
     more = C.settle(A);
     if (more) {
       look_up();
 #pragma unroll
-      for (int g = 0; g < 4; g++) {
-        const int n = run_rows(g);
-        if (n > 0) ptx::bulk_prefetch_l2(rec[g], (uint32_t)(n * kKvBytes));
-      }
+      for (int g = 0; g < 4; g++)
+        if (rows[g] > 0) ptx::bulk_prefetch_l2(rec[g], (uint32_t)(rows[g] * kKvBytes));
     }
   }
   // its last copies have landed before the CTA may leave (bounded)
