@@ -56,11 +56,18 @@ __device__ __forceinline__ void rope_cs(double inv_freq, int pos, float &c, floa
 // The same angles in turns, as 64-bit fixed-point fractions: one position's
 // turns modulo one in 2^-64ths, so that pos * turn (wrapping) drops whole turns
 // exactly; the fraction (53 bits) goes to fp32 for the sine and cosine.
+// (A host thread's last base is kept: 32 powers are a microsecond or two.)
 inline void rope_turns(double rope_base, uint64_t (&turn)[kRopeDim / 2]) {
-  for (int i = 0; i < kRopeDim / 2; i++) {
-    const double t = pow(rope_base, -2.0 * i / (double)kRopeDim) / 6.283185307179586;
-    turn[i] = (uint64_t)ldexp(t - floor(t), 64);
+  static thread_local double base = 0.0;           // (not a base)
+  static thread_local uint64_t last[kRopeDim / 2];
+  if (base != rope_base) {
+    for (int i = 0; i < kRopeDim / 2; i++) {
+      const double t = pow(rope_base, -2.0 * i / (double)kRopeDim) / 6.283185307179586;
+      last[i] = (uint64_t)ldexp(t - floor(t), 64);
+    }
+    base = rope_base;
   }
+  for (int i = 0; i < kRopeDim / 2; i++) turn[i] = last[i];
 }
 __device__ __forceinline__ void turn_cs(uint64_t u, float &c, float &s) {
   sincospif((float)(int64_t)u * 0x1p-63f, &s, &c);

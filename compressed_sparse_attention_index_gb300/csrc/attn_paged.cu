@@ -30,8 +30,8 @@
 // Window records (E4M3 x 2^e) are exact in f16 where -15 <= e <= 7; otherwise
 // the window is scaled by 2^kx, kx = 7 - (the largest e): exact but for values
 // below 2^-31 of the window's largest, and undone on its logits and, being the
-// first chunk, on O before the next one.  Q goes to f16 under the power of two
-// that brings max |q| into [2^14, 2^15), undone on the logits.
+// first chunk, on O before the next one.  Q out of f16's range goes to f16 under a
+// power of two, undone on the logits.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -312,34 +312,44 @@ __device__ __forceinline__ void paged_load(const PagedArgs &A, PagedShared &S, u
         paged_wait(A, S, &S.q_done, q_parity);
         q_parity ^= 1;
       }
+      // One pass as they are where max |q| lies in [2^-4, 2^15): f16 holds a bf16 value
+      // exactly down to 2^-17 and to 2^-25 below; else a second one under the power of two
+      // that brings it into [2^14, 2^15)
       const uint4 *src = reinterpret_cast<const uint4 *>(A.q + (int64_t)I.at.x * kHeads * kDim) + lt;
-      uint32_t m = 0u;
-#pragma unroll 4
-      for (int i = 0; i < 16; i++) {
-        const uint4 x = __ldg(src + i * kPgLoad);
-        m = __vmaxu2(m, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
-      }
-      m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
-      if (lane == 0) S.qmax[lt >> 5] = m;
-      group_sync<kBar>();
-#pragma unroll
-      for (int w = 0; w < 8; w++) m = max(m, S.qmax[w]);
-      const int qs = m == 0u ? 0 : max((int)(m >> 7) - 127 - 14, -100);
-      const float inv = ldexpf(1.f, -qs);
-      q_scale = A.scale * 1.4426950408889634f * ldexpf(1.f, qs);
       unsigned char *dst = sm + kPgSmQ + ((lt & 63) >> 3) * 1024;
-#pragma unroll 4
-      for (int i = 0; i < 16; i++) {                 // 16-B chunk lt % 64 of head lt / 64 + 4 i
-        const uint4 x = __ldg(src + i * kPgLoad);
-        uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      int qs = 0;
+      for (int pass = 0;; pass++) {
+        const float inv = ldexpf(1.f, -qs);
+        uint32_t m = 0u;
+#pragma unroll 1
+        for (int i0 = 0; i0 < 16; i0 += 8) {
+          uint4 x[8];
 #pragma unroll
-        for (int u = 0; u < 4; u++) {
-          const __half2 h2 = __floats2half2_rn(bf16_lo(w[u]) * inv, bf16_hi(w[u]) * inv);
-          w[u] = *reinterpret_cast<const uint32_t *>(&h2);
+          for (int i = 0; i < 8; i++) x[i] = __ldg(src + (i0 + i) * kPgLoad);
+#pragma unroll
+          for (int i = 0; i < 8; i++) {              // 16-B chunk lt % 64 of head lt / 64 + 4 (i0 + i)
+            uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+              m = __vmaxu2(m, w[u] & 0x7FFF7FFFu);
+              const __half2 h2 = __floats2half2_rn(bf16_lo(w[u]) * inv, bf16_hi(w[u]) * inv);
+              w[u] = *reinterpret_cast<const uint32_t *>(&h2);
+            }
+            const int h = (lt >> 6) + 4 * (i0 + i);
+            *reinterpret_cast<uint4 *>(dst + (h >> 3) * 8192 + sw128(h & 7, lt & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
-        const int h = (lt >> 6) + 4 * i;
-        *reinterpret_cast<uint4 *>(dst + (h >> 3) * 8192 + sw128(h & 7, lt & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (pass == 1) break;
+        m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
+        if (lane == 0) S.qmax[lt >> 5] = m;
+        group_sync<kBar>();
+#pragma unroll
+        for (int w = 0; w < 8; w++) m = max(m, S.qmax[w]);
+        const int ex = (int)(m >> 7) - 127;          // max |q| in [2^ex, 2^(ex + 1)) if normal
+        if (m == 0u || (ex >= -4 && ex < 15)) break;
+        qs = max(ex - 14, -100);
       }
+      q_scale = A.scale * 1.4426950408889634f * ldexpf(1.f, qs);
       ptx::fence_proxy_async_smem();
     }
     int kx = 0;
@@ -959,66 +969,120 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
   }
 }
 
-// Joins a cut query's partials over 32 output dims: grid (kDim / 32, CTAs of the
-// attention), thread = (head, 8 dims).  Weights 2^(m_s - max m) per head; the
-// sums run over the partials in CTA order, so the same inputs give the same bits.
-__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedArgs A) {
-  const int t = threadIdx.x, h = t >> 2, d = blockIdx.x * 32 + (t & 3) * 8;
+// Joins a cut query's partials: grid (kHeads / HEADS, as many as queries can be cut),
+// 512 threads.  A thread has four of its head's 512 dims, so a partial's row is read as
+// 2 KB in one piece; 4 / HEADS groups of 128 threads share a head, each taking every
+// (4 / HEADS)-th partial with four loads in flight, and meet in shared memory.  Each
+// warp finds its head's weights 2^(m_s - max m) by itself, a lane to a partial.  All
+// sums have a fixed order, so the same inputs give the same bits.
+template <int HEADS>
+__global__ void __launch_bounds__(512) paged_join_kernel(const __grid_constant__ PagedArgs A, int n_ctas) {
+  constexpr int NG = 4 / HEADS;
+  __shared__ float4 sum_sh[NG > 1 ? NG : 1][128];
+  const int t = threadIdx.x, lane = t & 31, grp = NG > 1 ? t >> 7 : 0;
+  const int h = blockIdx.x * HEADS + (NG > 1 ? 0 : t >> 7), d = (t & 127) * 4;
   griddep_wait();
   griddep_launch();
-  const int4 J = __ldcg(A.joins + blockIdx.y);
-  if (J.x < 0) return;
-  const int qi = J.x;
-  const int off = J.z, T = J.w, G = gridDim.y;
+  // the blockIdx.y-th CTA that names a cut query
+  int at = -1, left = (int)blockIdx.y;
+  for (int c0 = 0; c0 < n_ctas && at < 0; c0 += 256) {
+    int x[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) x[i] = c0 + i * 32 + lane < n_ctas ? __ldcg(&A.joins[c0 + i * 32 + lane].x) : -1;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const uint32_t named = __ballot_sync(0xFFFFFFFFu, x[i] >= 0);
+      const uint32_t hit = __ballot_sync(0xFFFFFFFFu, x[i] >= 0 && __popc(named & ((1u << lane) - 1u)) == left);
+      if (at < 0 && hit != 0u) at = c0 + i * 32 + __ffs((int)hit) - 1;
+      left -= __popc(named);
+    }
+  }
+  if (at < 0) return;
+  const int4 J = __ldcg(A.joins + at);               // query, its chunks, its first chunk, all chunks
+  const int qi = J.x, off = J.z, T = J.w, G = n_ctas;
   const int g0 = run_owner(off, T, G), g1 = run_owner(off + J.y - 1, T, G);
   auto slot_of = [&](int g) { return 2 * (int64_t)g + (g == g0 ? 1 : 0); };
+  // a CTA without chunks (more CTAs than chunks) has no partial
   auto empty = [&](int g) { return run_start(g, T, G) == run_start(g + 1, T, G); };
-  float M = -INFINITY;
-  for (int g = g0; g <= g1; g++)
-    if (!empty(g)) M = fmaxf(M, __ldcg(A.part_ml + slot_of(g) * 2 * kHeads + h));
-  float L = 0.f, y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int g = g0; g <= g1; g++) {
-    if (empty(g)) continue;
-    const int64_t s = slot_of(g);
-    const float m = __ldcg(A.part_ml + s * 2 * kHeads + h), l = __ldcg(A.part_ml + s * 2 * kHeads + kHeads + h);
-    const float4 *src = reinterpret_cast<const float4 *>(A.part + (s * kHeads + h) * kDim + d);
-    const float4 a = __ldcg(src), b = __ldcg(src + 1);
-    if (m == -kPgNoRef) continue;                    // nothing there to attend to
-    const float w = exp2f(m - M);
-    L += w * l;
-    const float e[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  float M = -kPgNoRef, m = -kPgNoRef;
+  int b0 = g0;
+  for (int b = g0; b <= g1; b += 32) {
+    m = b + lane <= g1 && !empty(b + lane) ? __ldcg(A.part_ml + slot_of(b + lane) * 2 * kHeads + h) : -kPgNoRef;
+    M = fmaxf(M, m);
+  }
 #pragma unroll
-    for (int j = 0; j < 8; j++) y[j] += w * e[j];
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  float L = 0.f;
+  for (; b0 <= g1; b0 += 32) {
+    float w = 0.f;                                   // of partial b0 + lane
+    if (b0 + lane <= g1 && !empty(b0 + lane)) {
+      const float *ml = A.part_ml + slot_of(b0 + lane) * 2 * kHeads + h;
+      if (g1 - g0 >= 32) m = __ldcg(ml);
+      w = exp2f(m - M);
+      L += w * __ldcg(ml + kHeads);
+    }
+    for (int i0 = grp; i0 < 32 && b0 + i0 <= g1; i0 += 4 * NG) {
+      float4 v[4];
+      float u[4];
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const int i = i0 + j * NG;
+        u[j] = __shfl_sync(0xFFFFFFFFu, w, i & 31);
+        if (i >= 32) u[j] = 0.f;
+        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (u[j] != 0.f)                             // (a partial that met no entry weighs nothing)
+          v[j] = __ldcg(reinterpret_cast<const float4 *>(A.part + (slot_of(b0 + i) * kHeads + h) * kDim + d));
+      }
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        y.x = fmaf(u[j], v[j].x, y.x);
+        y.y = fmaf(u[j], v[j].y, y.y);
+        y.z = fmaf(u[j], v[j].z, y.z);
+        y.w = fmaf(u[j], v[j].w, y.w);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
+  if (NG > 1) {
+    sum_sh[grp][t & 127] = y;
+    __syncthreads();
+    if (grp > 0) return;
+#pragma unroll
+    for (int g = 1; g < NG; g++) {
+      const float4 z = sum_sh[g][t];
+      y.x += z.x;
+      y.y += z.y;
+      y.z += z.z;
+      y.w += z.w;
+    }
   }
   const float inv = L != 0.f ? 1.f / L : 0.f;
-#pragma unroll
-  for (int j = 0; j < 8; j++) y[j] *= inv;
+  y.x *= inv;
+  y.y *= inv;
+  y.z *= inv;
+  y.w *= inv;
   if (d >= kRopeOff) {
     const uint64_t pos = (uint64_t)(int64_t)__ldg(A.pos + qi);
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      float c, s;
-      turn_cs(pos * A.turn[(d + j - kRopeOff) >> 1], c, s);
-      const float a = y[j], b = y[j + 1];
-      y[j] = a * c + b * s;
-      y[j + 1] = b * c - a * s;
-    }
+    float c, s;
+    turn_cs(pos * A.turn[(d - kRopeOff) >> 1], c, s);
+    const float a = y.x, b = y.z;
+    y.x = a * c + y.y * s;
+    y.y = y.y * c - a * s;
+    turn_cs(pos * A.turn[(d + 2 - kRopeOff) >> 1], c, s);
+    y.z = b * c + y.w * s;
+    y.w = y.w * c - b * s;
   }
   const int64_t o = ((int64_t)qi * kHeads + h) * kDim + d;
   if (A.out_f32) {
-    float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(A.out) + o);
-    p[0] = make_float4(y[0], y[1], y[2], y[3]);
-    p[1] = make_float4(y[4], y[5], y[6], y[7]);
+    *reinterpret_cast<float4 *>(static_cast<float *>(A.out) + o) = y;
   } else {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const __nv_bfloat162 b2 = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
-      w[j] = *reinterpret_cast<const uint32_t *>(&b2);
-    }
-    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(A.out) + o) = make_uint4(w[0], w[1], w[2], w[3]);
+    const __nv_bfloat162 a = __floats2bfloat162_rn(y.x, y.y), b = __floats2bfloat162_rn(y.z, y.w);
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(A.out) + o) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
   }
-  if (A.lse != nullptr && blockIdx.x == 0 && (t & 3) == 0)
+  if (A.lse != nullptr && d == 0)
     A.lse[(int64_t)qi * kHeads + h] = L > 0.f || L != L ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
 
@@ -1050,7 +1114,10 @@ cudaError_t launch_paged_attn(PagedArgs A, double rope_base, void *ws, cudaStrea
   const unsigned grid = (unsigned)(chunks < sms ? (chunks < 1 ? 1 : chunks) : sms);
   e = launch_pdl(paged_attn_kernel, dim3(grid), dim3(kPgThreads), (size_t)kPgSmAlloc, st, 1u, A);
   if (e != cudaSuccess || grid == 1) return e;
-  return launch_pdl(paged_join_kernel, dim3(kDim / 32, grid), dim3(256), 0, st, 1u, A);
+  // a query is cut at a border between two CTAs' runs
+  const unsigned cut = (unsigned)A.n_q < grid ? (unsigned)A.n_q : grid;
+  if (cut * kHeads <= 4 * sms) return launch_pdl(paged_join_kernel<1>, dim3(kHeads, cut), dim3(512), 0, st, 1u, A, (int)grid);
+  return launch_pdl(paged_join_kernel<4>, dim3(kHeads / 4, cut), dim3(512), 0, st, 1u, A, (int)grid);
 }
 
 }  // namespace csa2
