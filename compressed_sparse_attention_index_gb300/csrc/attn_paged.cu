@@ -48,7 +48,7 @@ constexpr int kPgSoft = 256, kPgLoad = 256;        // threads of the softmax gro
 constexpr int kPgThreads = kPgSoft + 2 * kPgLoad + 128;
 // Registers: 896 threads are launched with 72 each; the softmax group takes what
 // the others give up.
-constexpr int kPgRegsSoft = 96, kPgRegsK = 56, kPgRegsV = 80, kPgRegsRest = 40;
+constexpr int kPgRegsSoft = 88, kPgRegsK = 56, kPgRegsV = 80, kPgRegsRest = 56;
 static_assert(kPgSoft * kPgRegsSoft + kPgLoad * (kPgRegsK + kPgRegsV) + 128 * kPgRegsRest <= 72 * kPgThreads, "register split");
 constexpr int kPgSlab = 128 * 128 * 2;             // one slab: 128 entries x 128 dims f16
 constexpr int kPgRaw = kPgChunk * kKvBytes;        // one chunk's records
@@ -63,14 +63,12 @@ static_assert(kPgSmAlloc + 4608 <= 227 * 1024, "shared memory");
 // tensor memory: S^T, O^T, the ring of K
 constexpr uint32_t kPgColS = 0, kPgColO = 64, kPgColK = 320, kPgTmemCols = 512;
 constexpr float kPgRaise = 8.f, kPgShift = 7.f, kPgNoRef = 3e38f;   // (kPgNoRef: no entry met yet)
+constexpr int kPgScatter = 8;                      // pages of fewer entries are fetched as scattered records
+constexpr int kPgSnap = 2, kPgSnapRun = 2;
 constexpr int kPgInfo = 8;                         // chunks described in shared memory at a time
 
-// Barriers among the threads of a group; every one of its warps reaches each of
-// them, whatever its waits returned.
-template <int ID>
-__device__ __forceinline__ void group_sync() {
-  asm volatile("bar.sync %0, 256;" ::"n"(ID) : "memory");
-}
+// Votes of the softmax group, at places that each of its warps reaches once a chunk.
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool soft_any(bool p) {
   uint32_t r;
   asm volatile(
@@ -87,7 +85,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 struct PagedQuery {
-  int seq, n, chunks, win;      // entries (or selection slots), chunks in all, window entries
+  int seq, n, chunks, win, first;      // entries (or selection slots), chunks in all, the window's
   bool bad;
 };
 
@@ -96,18 +94,30 @@ __device__ __forceinline__ PagedQuery paged_query(const PagedArgs &A, int q) {
   r.seq = __ldg(A.q_seq + q);
   const int vis = __ldg(A.n_vis + q);
   r.win = __ldg(A.swa_cnt + q);
-  const int first = __ldg(A.swa_first + q);
+  r.first = __ldg(A.swa_first + q);
   r.bad = r.seq < 0 || r.seq >= A.n_seq || vis < 0 || (int64_t)vis > A.table_stride * A.page || r.win < 0 ||
-          r.win > kSwa || r.win > A.swa_cap || (r.win > 0 && (first < 0 || first >= A.swa_cap));
+          r.win > kSwa || r.win > A.swa_cap || (r.win > 0 && (r.first < 0 || r.first >= A.swa_cap));
   r.n = r.bad ? 0 : A.sel != nullptr ? (vis > 0 ? A.sel_stride : 0) : vis;
   if (r.bad) r.win = 0;
   r.chunks = (int)(((unsigned)r.n + kPgChunk - 1) / kPgChunk) + (r.win > 0 ? 1 : 0);
   return r;
 }
 
-// CTA g of G has chunks [g T / G, (g + 1) T / G) of T (T below 2^31)
-__device__ __forceinline__ int run_start(int g, int T, int G) { return (int)((int64_t)g * T / G); }
-__device__ __forceinline__ int run_owner(int c, int T, int G) { return (int)((((int64_t)c + 1) * G - 1) / T); }
+// The CTAs that share T chunks (a launch may have more)
+__device__ __forceinline__ int run_ctas(int T, int grid) { return min(grid, max(1, T)); }
+// Chunks are dealt to G CTAs in runs of T / G (T below 2^31), but a border that falls
+// within `snap` chunks of an end of a query is moved there: a piece of a query costs a
+// CTA its Q, a window or a read-out and a partial of 128 KB for the join, about as much
+// as three chunks.  Longer runs move their borders further.
+__device__ __forceinline__ int run_snap(int T, int G) { return min(kPgSnap, T / (kPgSnapRun * G)); }
+__device__ __forceinline__ int run_border(int g, int T, int G) { return (int)((int64_t)g * T / G); }
+// The first border that stays inside a query of n chunks from off, and the last one.
+__device__ __forceinline__ int run_first_cut(int off, int T, int G) {
+  return (int)((((int64_t)off + run_snap(T, G) + 1) * G + T - 1) / T);
+}
+__device__ __forceinline__ int run_last_cut(int off, int n, int T, int G) {
+  return (int)((((int64_t)off + n - run_snap(T, G)) * G + T - 1) / T) - 1;
+}
 
 // A position in a CTA's run of chunks.
 struct PagedCursor {
@@ -137,8 +147,8 @@ __device__ __forceinline__ unsigned paged_col(unsigned j, const PagedArgs &A) {
 struct PagedInfo {
   int4 at;                      // query, place in it, its chunks, its first chunk
   uint32_t valid[4];            // rows that hold an entry
-  int seq, win;                 // sequence; window entries, 0: entries of the cache
-  float f;                      // logits in log2 units per unit of S
+  int seq, win, first;          // sequence; window entries (0: entries of the cache), the oldest one's place
+  float f;                      // of a query's first chunk here: logits in log2 units per unit of Q K^T
   int kx;                       // a window's scale (its tile holds 2^kx times its values)
 };
 
@@ -147,14 +157,16 @@ struct PagedShared {
   uint64_t k_full[6], k_free[6], v_full[6], v_free[6];
   uint64_t raw_full[2], raw_free[2];   // one buffer; by the parity of the chunk, so that each fetching warp
                                        // passes every phase of what it waits on
-  uint64_t q_done, s_full, s_free, p_full, o_done, drain;
+  uint64_t q_full, q_done, s_full, s_free, p_full, o_done, drain;
+  uint64_t meet[3];             // of the softmax, K and V groups' warps
   PagedInfo info[kPgInfo];
   __align__(16) float less[kHeads];    // minus a head's reference, which is kPgShift below a maximum
   float alpha[kHeads];
   float l[4][kHeads], red[4][kHeads];
   uint32_t tmem, qmax[8];
   int emin, emax;
-  int scan[kPgThreads / 32], start, off;
+  int scan[kPgThreads / 32], end[2], start, off;       // the run's ends; its first query and that one's first chunk
+  PagedQuery Q;
   volatile int bad;
 };
 
@@ -174,6 +186,16 @@ __device__ __forceinline__ void paged_wait(const PagedArgs &A, PagedShared &S, u
     }
   }
 }
+
+// The warps of a group meet, where a chunk's description says so.  (Not a barrier of the
+// hardware's: once a wait has run out the warps may read different descriptions.)
+__device__ __forceinline__ void paged_meet(const PagedArgs &A, PagedShared &S, int group, uint32_t &parity) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&S.meet[group]);
+  paged_wait(A, S, &S.meet[group], parity);
+  parity ^= 1;
+}
+__device__ __forceinline__ bool paged_bad(const PagedShared &S) { return __any_sync(0xFFFFFFFFu, S.bad); }
 
 // Where slab n of the run stands, for a role that takes slabs n, n + STEP, ..: its
 // slot in a ring of three and its barriers' number and phase.  Two teams take turns
@@ -200,22 +222,26 @@ struct PagedSlab {
 };
 
 // ------------------------------------------------------------------ records
-// Two warps take turns at the chunks: a lane finds the records of four rows, and the first lane of every run of rows that are neighbours in the cache
-// copies the run into shared memory.  A warp's next chunk is looked up, and its
-// records asked into L2, before the wait for the buffer (one warp for both buffers
-// took longer over a chunk than the MMAs).  A window chunk is read by the loading groups
-// themselves (its records do not fit the buffer).
+// Two warps take turns at the chunks: a lane finds the records of four rows.  The first
+// lane of every run of rows that are neighbours in the cache copies the run into shared
+// memory by one bulk copy, and a warp's next chunk is looked up, and asked into L2, before
+// the wait for the buffer (one warp for both took longer over a chunk than the MMAs).
+// Bulk copies of single records take 65 cycles each, 8,300 a chunk: a selection, and
+// pages of a few entries, go by 16-B copies, two lanes to a record, in 1,700 (40 queries x
+// 512 selected: 45 -> 41 us).  A window chunk is read by the K group itself (its records
+// do not fit the buffer).
 __device__ __forceinline__ void paged_fetch(const PagedArgs &A, PagedShared &S, unsigned char *sm, int c_begin, int c_end, int first) {
   const int lane = threadIdx.x & 31;
+  const bool scattered = A.sel != nullptr || A.page < kPgScatter;
   PagedCursor C;
   C.c = c_begin + first;
   C.end = c_end;
   C.qi = S.start;
   C.off = S.off;
-  if (c_begin < c_end) C.Q = paged_query(A, C.qi);
-  const uint8_t *rec[4];                             // rows 32 g + lane
+  C.Q = S.Q;
+  unsigned rec[4];                                   // rows 32 g + lane: the record
   uint32_t valid[4];
-  int rows[4], all_rows = 0;                         // of the run this lane leads, 0: none; of the chunk
+  int rows[4], all_rows = 0;               // of the run this lane leads, 0: none; of the chunk
   int4 at;
   int seq, win;
   auto look_up = [&]() {
@@ -244,7 +270,7 @@ __device__ __forceinline__ void paged_fetch(const PagedArgs &A, PagedShared &S, 
       const bool ok = id[g] >= 0 && id[g] < A.n_pages;
       out |= j[g] >= 0 && !ok;
       if (!ok) id[g] = -1;
-      rec[g] = A.pages + ((int64_t)id[g] * A.page + off[g]) * kKvBytes;
+      rec[g] = (unsigned)id[g] * (unsigned)A.page + (unsigned)off[g];
       const int pid = __shfl_up_sync(0xFFFFFFFFu, id[g], 1), poff = __shfl_up_sync(0xFFFFFFFFu, off[g], 1);
       const bool leads = ok && (lane == 0 || pid != id[g] || poff + 1 != off[g]);
       valid[g] = __ballot_sync(0xFFFFFFFFu, ok);
@@ -265,25 +291,39 @@ __device__ __forceinline__ void paged_fetch(const PagedArgs &A, PagedShared &S, 
       I.at = at;
       I.seq = seq;
       I.win = win;
+      I.first = C.Q.first;
 #pragma unroll
       for (int g = 0; g < 4; g++)
         I.valid[g] = win == 0 ? valid[g] : win > 32 * g ? (win >= 32 * g + 32 ? 0xFFFFFFFFu : (1u << (win - 32 * g)) - 1u) : 0u;
     }
     if (k >= 1) paged_wait(A, S, &S.raw_free[first ^ 1], ((k - 1) >> 1) & 1);
-    if (__any_sync(0xFFFFFFFFu, S.bad)) break;       // no copy is started any more
+    if (paged_bad(S)) break;                         // no copy is started any more
     uint64_t *full = &S.raw_full[first];
-    if (lane == 0) ptx::mbar_arrive_expect_tx(full, (uint32_t)(all_rows * kKvBytes));
+    if (scattered) {
+#pragma unroll
+      for (int g = 0; g < 8; g++) {                  // two lanes to a row of 16
+        const int from = (g & 1) * 16 + (lane >> 1);
+        const uint8_t *src = A.pages + (int64_t)__shfl_sync(0xFFFFFFFFu, rec[g >> 1], from) * kKvBytes + (lane & 1) * 16;
+        unsigned char *dst = sm + kPgSmRaw + ((g >> 1) * 32 + from) * kKvBytes + (lane & 1) * 16;
+        if ((valid[g >> 1] >> from) & 1u)
+#pragma unroll
+          for (int i = 0; i < kKvBytes; i += 32) ptx::cp_async16(dst + i, src + i);
+      }
+      ptx::cp_async_arrive(full);                    // (each lane's copies, pending from here on)
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive_expect_tx(full, scattered ? 0u : (uint32_t)(all_rows * kKvBytes));
     __syncwarp();
 #pragma unroll
     for (int g = 0; g < 4; g++)
-      if (rows[g] > 0) ptx::bulk_load(sm + kPgSmRaw + (32 * g + lane) * kKvBytes, rec[g], (uint32_t)(rows[g] * kKvBytes), full);
+      if (!scattered && rows[g] > 0) ptx::bulk_load(sm + kPgSmRaw + (32 * g + lane) * kKvBytes, A.pages + (int64_t)rec[g] * kKvBytes, (uint32_t)(rows[g] * kKvBytes), full);
     C.c += 2;
     more = C.settle(A);
     if (more) {
       look_up();
 #pragma unroll
       for (int g = 0; g < 4; g++)
-        if (rows[g] > 0) ptx::bulk_prefetch_l2(rec[g], (uint32_t)(rows[g] * kKvBytes));
+        if (!scattered && rows[g] > 0) ptx::bulk_prefetch_l2(A.pages + (int64_t)rec[g] * kKvBytes, (uint32_t)(rows[g] * kKvBytes));
     }
   }
   // its last copies have landed before the CTA may leave (bounded)
@@ -295,73 +335,34 @@ __device__ __forceinline__ void paged_fetch(const PagedArgs &A, PagedShared &S, 
 // QK reads them there, 32 cycles an MMA (48 from shared memory, whose bandwidth PV
 // needs), and the V group copies them from there.
 __device__ __forceinline__ void paged_load(const PagedArgs &A, PagedShared &S, unsigned char *sm, int n_run, uint32_t tmem) {
-  constexpr int kBar = 2;
   const int lt = (int)threadIdx.x - kPgSoft, lane = lt & 31;
   const int e = lt & 127, team = lt >> 7;            // row
   const uint32_t kcol0 = tmem + ((uint32_t)(e & 96) << 16) + kPgColK;
-  float q_scale = 1.f;
   PagedSlab<2> n((unsigned)team);                    // the next slab
-  unsigned q_parity = 0;                             // of the last query
+  uint32_t met = 0;
   for (int k = 0; k < n_run; k++) {
     paged_wait(A, S, &S.raw_full[k & 1], (k >> 1) & 1);
     PagedInfo &I = S.info[k & (kPgInfo - 1)];
-    const int win = I.win;
-    if (k == 0 || I.at.y == 0) {
-      // ---------------------------------------------------- Q to f16, K-major, 128B swizzle
-      if (k > 0) {                                   // (the query before is multiplied)
-        paged_wait(A, S, &S.q_done, q_parity);
-        q_parity ^= 1;
-      }
-      // One pass as they are where max |q| lies in [2^-4, 2^15): f16 holds a bf16 value
-      // exactly down to 2^-17 and to 2^-25 below; else a second one under the power of two
-      // that brings it into [2^14, 2^15)
-      const uint4 *src = reinterpret_cast<const uint4 *>(A.q + (int64_t)I.at.x * kHeads * kDim) + lt;
-      unsigned char *dst = sm + kPgSmQ + ((lt & 63) >> 3) * 1024;
-      int qs = 0;
-      for (int pass = 0;; pass++) {
-        const float inv = ldexpf(1.f, -qs);
-        uint32_t m = 0u;
-#pragma unroll 1
-        for (int i0 = 0; i0 < 16; i0 += 8) {
-          uint4 x[8];
-#pragma unroll
-          for (int i = 0; i < 8; i++) x[i] = __ldg(src + (i0 + i) * kPgLoad);
-#pragma unroll
-          for (int i = 0; i < 8; i++) {              // 16-B chunk lt % 64 of head lt / 64 + 4 (i0 + i)
-            uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-            for (int u = 0; u < 4; u++) {
-              m = __vmaxu2(m, w[u] & 0x7FFF7FFFu);
-              const __half2 h2 = __floats2half2_rn(bf16_lo(w[u]) * inv, bf16_hi(w[u]) * inv);
-              w[u] = *reinterpret_cast<const uint32_t *>(&h2);
-            }
-            const int h = (lt >> 6) + 4 * (i0 + i);
-            *reinterpret_cast<uint4 *>(dst + (h >> 3) * 8192 + sw128(h & 7, lt & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-        if (pass == 1) break;
-        m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
-        if (lane == 0) S.qmax[lt >> 5] = m;
-        group_sync<kBar>();
-#pragma unroll
-        for (int w = 0; w < 8; w++) m = max(m, S.qmax[w]);
-        const int ex = (int)(m >> 7) - 127;          // max |q| in [2^ex, 2^(ex + 1)) if normal
-        if (m == 0u || (ex >= -4 && ex < 15)) break;
-        qs = max(ex - 14, -100);
-      }
-      q_scale = A.scale * 1.4426950408889634f * ldexpf(1.f, qs);
-      ptx::fence_proxy_async_smem();
-    }
+    const int win = __shfl_sync(0xFFFFFFFFu, I.win, 0);
+    if (win > 0 && paged_bad(S)) break;
     int kx = 0;
     uint4 ws = make_uint4(0u, 0u, 0u, 0u);           // a window record's 16 scales
     const uint8_t *wrec = nullptr;
+    uint4 x[2];                                      // 32 of its dims
+    auto window_dims = [&](int i) {
+#pragma unroll
+      for (int u = 0; u < 2; u++)
+        x[u] = wrec != nullptr ? __ldg(reinterpret_cast<const uint4 *>(wrec + (team + 2 * (i >> 2)) * 128 + (i & 3) * 32 + u * 16))
+                               : make_uint4(0u, 0u, 0u, 0u);
+    };
     if (win > 0) {
       // ---------------------------------------------------- a window's rows and scale
       if (e < win) {
-        const int ring = (int)(((unsigned)__ldg(A.swa_first + I.at.x) + (unsigned)e) % (unsigned)A.swa_cap);
+        const int ring = (int)(((unsigned)I.first + (unsigned)e) % (unsigned)A.swa_cap);
         wrec = A.swa + ((int64_t)I.seq * A.swa_cap + ring) * kSwaBytes;
         ws = __ldg(reinterpret_cast<const uint4 *>(wrec + 512));
       }
+      window_dims(0);
       // the range of the scales' exponents (0 marks a group of zeros)
       const uint32_t w4[4] = {ws.x, ws.y, ws.z, ws.w};
       int lo = 255, hi = 0;
@@ -373,16 +374,13 @@ __device__ __forceinline__ void paged_load(const PagedArgs &A, PagedShared &S, u
       lo = __reduce_min_sync(0xFFFFFFFFu, lo);
       hi = __reduce_max_sync(0xFFFFFFFFu, hi);
       if (lt == 0) { S.emin = 255; S.emax = 0; }
-      group_sync<kBar>();
+      paged_meet(A, S, 1, met);
       if (lane == 0) { atomicMin(&S.emin, lo); atomicMax(&S.emax, hi); }
-      group_sync<kBar>();
+      paged_meet(A, S, 1, met);
       const int emax = S.emax - 127, emin = S.emin - 127;
       if (emax > -127 && (emax > 7 || emin < -15)) kx = 7 - emax;
     }
-    if (lt == 0) {
-      I.f = ldexpf(q_scale, -kx);
-      I.kx = kx;
-    }
+    if (lt == 0) I.kx = kx;
     // 32 dims (16 words of two f16) at a time.  (One slab's code, not the chunk's: six
     // roles share the instruction caches, and with everything unrolled the warps waited
     // for instructions four times as long as they issued them.)
@@ -407,15 +405,15 @@ __device__ __forceinline__ void paged_load(const PagedArgs &A, PagedShared &S, u
       release();
 #pragma unroll 1
       for (int i = 0; i < 8; i++) {
-        const int b = team + 2 * (i >> 2), j = i & 3;
+        const int b = team + 2 * (i >> 2);
         const uint32_t wb = b == 0 ? ws.x : b == 1 ? ws.y : b == 2 ? ws.z : ws.w;
-        const int eb = (int)((wb >> (8 * j)) & 0xFFu);
+        if ((i & 3) == 0) begin();
+        const int eb = (int)((wb >> (8 * (i & 3))) & 0xFFu);
         const __half2 fac = __float2half2_rn(eb == 0 ? 0.f : ldexpf(1.f, eb - 127 + kx));
         uint32_t o[16];
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-          const uint4 x = wrec != nullptr ? __ldg(reinterpret_cast<const uint4 *>(wrec + b * 128 + j * 32 + h * 16)) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          const uint32_t w[4] = {x[h].x, x[h].y, x[h].z, x[h].w};
 #pragma unroll
           for (int q = 0; q < 8; q++) {
             const uint32_t hv = e4m3x2_to_f16x2(w[q >> 1] >> (16 * (q & 1)));
@@ -423,9 +421,9 @@ __device__ __forceinline__ void paged_load(const PagedArgs &A, PagedShared &S, u
             o[8 * h + q] = *reinterpret_cast<const uint32_t *>(&y);
           }
         }
-        if (j == 0) begin();
-        ptx::tmem_st_32x32b_x16(kcol + j * 16, o);
-        if (j == 3) end();
+        ptx::tmem_st_32x32b_x16(kcol + (i & 3) * 16, o);
+        if (i < 7) window_dims(i + 1);
+        if ((i & 3) == 3) end();
       }
     } else {
       const bool ok = ((I.valid[e >> 5] >> lane) & 1u) != 0u;
@@ -496,8 +494,65 @@ __device__ __forceinline__ void paged_copy(const PagedArgs &A, PagedShared &S, u
   const uintptr_t tile = reinterpret_cast<uintptr_t>(sm + kPgSmV + (e >> 3) * 2048 + (e & 7) * 128 + (e & 7) * 16);
   static_assert(kPgVRing == kPgKRing, "one slot number for both rings");
   PagedSlab<2> n((unsigned)team);
+  // Q of a query to f16, K-major, 128B swizzle.  One pass as they are where max |q| lies
+  // in [2^-4, 2^15): f16 holds a bf16 value exactly down to 2^-17 and to 2^-25 below; else
+  // a second one under the power of two that brings it into [2^14, 2^15)
+  uint32_t met = 0, q_parity = 0;
+  auto stage_q = [&](int qi, int k) {
+    const uint4 *src = reinterpret_cast<const uint4 *>(A.q + (int64_t)qi * kHeads * kDim) + lt;
+    unsigned char *dst = sm + kPgSmQ + ((lt & 63) >> 3) * 1024;
+    int qs = 0;
+    for (int pass = 0;; pass++) {
+      const float inv = ldexpf(1.f, -qs);
+      uint32_t m = 0u;
+#pragma unroll 1
+      for (int i0 = 0; i0 < 16; i0 += 8) {
+        uint4 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) x[i] = __ldg(src + (i0 + i) * kPgLoad);
+        if (pass == 0 && i0 == 0 && k > 0) {         // (the query before is multiplied)
+          paged_wait(A, S, &S.q_done, q_parity);
+          q_parity ^= 1;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i++) {                // 16-B chunk lt % 64 of head lt / 64 + 4 (i0 + i)
+          uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+          for (int u = 0; u < 4; u++) {
+            m = __vmaxu2(m, w[u] & 0x7FFF7FFFu);
+            const __half2 h2 = __floats2half2_rn(bf16_lo(w[u]) * inv, bf16_hi(w[u]) * inv);
+            w[u] = *reinterpret_cast<const uint32_t *>(&h2);
+          }
+          const int h = (lt >> 6) + 4 * (i0 + i);
+          *reinterpret_cast<uint4 *>(dst + (h >> 3) * 8192 + sw128(h & 7, lt & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      if (pass == 1) break;
+      m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
+      if (lane == 0) S.qmax[lt >> 5] = m;
+      paged_meet(A, S, 2, met);
+#pragma unroll
+      for (int w = 0; w < 8; w++) m = max(m, S.qmax[w]);
+      paged_meet(A, S, 2, met);                      // (before the next query's)
+      const int ex = (int)(m >> 7) - 127;            // max |q| in [2^ex, 2^(ex + 1)) if normal
+      if (m == 0u || (ex >= -4 && ex < 15)) break;
+      qs = max(ex - 14, -100);
+    }
+    if (lt == 0) S.info[k & (kPgInfo - 1)].f = A.scale * 1.4426950408889634f * ldexpf(1.f, qs);
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&S.q_full);
+  };
+  // (the first query's while its records are looked up)
+  if (n_run > 0) stage_q(S.start, 0);
+  bool last = false;                                 // the chunk is its query's last
 #pragma unroll 1
   for (int i = 0; i < 2 * n_run; i++, n.next()) {
+    if (last && (i & 1) == 0) {                      // the next query's, before its first slab
+      paged_wait(A, S, &S.raw_full[(i >> 1) & 1], (i >> 2) & 1);
+      if (paged_bad(S)) break;
+      stage_q(S.info[(i >> 1) & (kPgInfo - 1)].at.x, i >> 1);
+    }
     uint32_t r[2][32];
     paged_wait(A, S, &S.k_full[n.bar], n.phase);
     ptx::tc_fence_after();
@@ -518,6 +573,10 @@ __device__ __forceinline__ void paged_copy(const PagedArgs &A, PagedShared &S, u
     ptx::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&S.v_full[n.bar]);
+    if ((i & 1) == 0) {
+      const PagedInfo &I = S.info[(i >> 1) & (kPgInfo - 1)];
+      last = __shfl_sync(0xFFFFFFFFu, I.at.y + 1 == I.at.z, 0);
+    }
   }
 }
 
@@ -590,6 +649,8 @@ __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S
   const int quarter = warp & 3, hb = (warp >> 2) * 32, e_row = quarter * 32 + lane;
   const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16);
   uint64_t l_acc[16];                                // 32 heads' denominators
+  float q_f = 0.f;                                   // logits in log2 units per unit of S
+  uint32_t met = 0;
   float o_scale = 1.f;                               // what O still has to be multiplied by
   bool acc = false;                                  // O holds something of this query
   int lc0 = 0;
@@ -606,10 +667,11 @@ __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S
 #pragma unroll
       for (int i = 0; i < 16; i++) l_acc[i] = 0ull;
       if (t < kHeads) S.less[t] = kPgNoRef;
-      group_sync<1>();
+      q_f = info.f;
+      paged_meet(A, S, 0, met);
     }
-    const float f = info.f;
     const int kx = info.kx;
+    const float f = kx == 0 ? q_f : ldexpf(q_f, -kx);
     const float none = ((info.valid[quarter] >> lane) & 1u) != 0u ? 0.f : -INFINITY;
     const uint32_t ta = tq + kPgColS + hb;
     uint64_t s[16];
@@ -638,7 +700,7 @@ __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S
         }
       }
       S.red[quarter][hb + lane] = v[0];
-      group_sync<1>();
+      soft_sync();
       if (t < kHeads) {
         const float cm = fmaxf(fmaxf(S.red[0][t], S.red[1][t]), fmaxf(S.red[2][t], S.red[3][t])) - kPgShift;
         const float mo = -S.less[t];
@@ -649,7 +711,7 @@ __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S
         }
         S.alpha[t] = al;
       }
-      group_sync<1>();
+      soft_sync();
       if (acc) {
         // O *= alpha (and the window's factor), once PV of the chunk before is complete
         paged_wait(A, S, &S.o_done, (k - 1) & 1);
@@ -702,6 +764,7 @@ __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S
     acc = true;
     if (kx != 0) o_scale = ldexpf(1.f, -kx);
     if (lc + 1 != I.z && k + 1 != n_run) continue;
+    if ((unsigned)I.x >= (unsigned)A.n_q) continue;  // (a description left from before, once a wait has run out)
 
     // -------------------------------------------------------- the query's last chunk here: read-out
     float l_sum[32];
@@ -723,7 +786,7 @@ __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S
       }
     }
     S.l[quarter][hb + lane] = l_sum[0];
-    group_sync<1>();
+    paged_meet(A, S, 0, met);
     const bool whole = lc0 == 0 && lc + 1 == I.z;
     const int64_t slot = 2 * (int64_t)blockIdx.x + (lc0 > 0 ? 0 : 1);
     if (t < kHeads) {
@@ -740,7 +803,7 @@ __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S
       }
     }
     const int pos = __ldg(A.pos + I.x);
-    group_sync<1>();
+    paged_meet(A, S, 0, met);
     paged_wait(A, S, &S.o_done, k & 1);              // PV is complete
     ptx::tc_fence_after();
     for (int blk = warp >> 2; blk < 4; blk += 2) {
@@ -788,7 +851,7 @@ __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S
     }
     ptx::tc_fence_before();                          // (before the next query's PV, behind p_full)
     // the first CTA after the one that begins a cut query names it for the join
-    if (t == 0 && lc0 > 0 && I.w + lc0 == run_start(run_owner(I.w, T, G) + 1, T, G))
+    if (t == 0 && lc0 > 0 && (int)blockIdx.x == run_first_cut(I.w, T, G))
       A.joins[blockIdx.x] = make_int4(I.x, I.z, I.w, T);
   }
 }
@@ -802,12 +865,18 @@ __device__ __forceinline__ void paged_issue_qk(const PagedArgs &A, PagedShared &
                                                uint32_t tmem) {
   constexpr uint32_t id = idesc_m128(0, true, kHeads);
   const uint64_t d_q = ptx::smem_desc(ptx::smem_u32(sm + kPgSmQ), 16, 8192, 2);
+  uint32_t q_parity = 0;
+  bool fresh = true;                                 // the next chunk is a query's first here
   PagedSlab<1> n(0u);
   for (int k = 0; k < n_run && !S.bad; k++) {
     if (k >= 1) paged_wait(A, S, &S.s_free, (k - 1) & 1);
 #pragma unroll 1
     for (int b = 0; b < 4; b++) {                    // S^T += K Q^T over slab 4 k + b
       paged_wait(A, S, &S.k_full[n.bar], n.phase);
+      if (b == 0 && fresh) {
+        paged_wait(A, S, &S.q_full, q_parity);
+        q_parity ^= 1;
+      }
       ptx::tc_fence_after();
       const uint64_t qa = d_q + b * 128;
       const uint32_t ka = tmem + kPgColK + n.slot * 64;
@@ -820,7 +889,8 @@ __device__ __forceinline__ void paged_issue_qk(const PagedArgs &A, PagedShared &
     }
     ptx::tc_commit(&S.s_full);
     const int4 at = S.info[k & (kPgInfo - 1)].at;
-    if (at.y + 1 == at.z) ptx::tc_commit(&S.q_done);
+    fresh = at.y + 1 == at.z;
+    if (fresh) ptx::tc_commit(&S.q_done);
   }
   ptx::tc_commit(&S.drain);
 }
@@ -866,7 +936,9 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
       ptx::mbar_init(&S.raw_full[i], 1);
       ptx::mbar_init(&S.raw_free[i], kPgLoad / 32);
     }
+    ptx::mbar_init(&S.q_full, kPgLoad / 32);
     ptx::mbar_init(&S.q_done, 1);
+    for (int i = 0; i < 3; i++) ptx::mbar_init(&S.meet[i], 8);
     ptx::mbar_init(&S.s_full, 1);
     ptx::mbar_init(&S.s_free, kPgSoft / 32);
     ptx::mbar_init(&S.p_full, kPgSoft / 32);
@@ -884,11 +956,13 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
   // prefix sums of the queries' chunks: thread t has queries [u0, u1)
   const int per = (A.n_q + kPgThreads - 1) / kPgThreads, u0 = min(t * per, A.n_q), u1 = min(u0 + per, A.n_q);
   int mine = 0;
-  bool any_bad = false;
+  bool any_bad = false, none = false;
+  PagedQuery own = {};                               // the last of them
   for (int q = u0; q < u1; q++) {
-    const PagedQuery r = paged_query(A, q);
-    mine += r.chunks;
-    any_bad |= r.bad;
+    own = paged_query(A, q);
+    mine += own.chunks;
+    any_bad |= own.bad;
+    none |= own.chunks == 0;
   }
   if (any_bad && blockIdx.x == 0) record_error(A.status, CSA2_ERR_BOUNDS);
   int inc = mine;
@@ -898,28 +972,47 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     if (lane >= o) inc += x;
   }
   if (lane == 31) S.scan[warp] = inc;
-  __syncthreads();
+  none = __syncthreads_or(none) != 0;
   int before = 0, total = 0;
   for (int w = 0; w < kPgThreads / 32; w++) {
     if (w < warp) before += S.scan[w];
     total += S.scan[w];
   }
   before += inc - mine;
-  const int G = gridDim.x, T = total;
-  const int c_begin = run_start(blockIdx.x, T, G), c_end = run_start(blockIdx.x + 1, T, G);
-  if (c_begin < c_end && before <= c_begin && c_begin < before + mine) {
-    int o = before, q = u0;
-    for (; q < u1; q++) {
-      const int n = paged_query(A, q).chunks;
-      if (c_begin < o + n) break;
-      o += n;
+  const int T = total, G = run_ctas(T, gridDim.x);
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    // the run's two ends
+    const int g = min((int)blockIdx.x + i, G), raw = T > 0 ? run_border(g, T, G) : 0;
+    if (raw < T && before <= raw && raw < before + mine) {
+      int o = before, q = u0;
+      PagedQuery R = per == 1 ? own : paged_query(A, q);
+      while (raw >= o + R.chunks) {
+        o += R.chunks;
+        R = paged_query(A, ++q);
+      }
+      const int head = raw - o, tail = o + R.chunks - raw, snap = run_snap(T, G);
+      int c = raw;
+      if (head <= snap && head <= tail) {
+        c = o;
+      } else if (tail <= snap) {                     // the next query that has any
+        o += R.chunks;
+        c = o;
+        for (R.chunks = 0; R.chunks == 0 && ++q < A.n_q;) R = paged_query(A, q);
+      }
+      S.end[i] = c;
+      if (i == 0) {
+        S.start = q;
+        S.off = o;
+        S.Q = R;
+      }
+    } else if (raw >= T && t == 0) {
+      S.end[i] = T;
     }
-    S.start = q;
-    S.off = o;
   }
   if (t == 0) A.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
   // queries with nothing to attend to: zeros
-  for (int q = blockIdx.x; q < A.n_q; q += gridDim.x) {
+  for (int q = none ? blockIdx.x : A.n_q; q < A.n_q; q += gridDim.x) {
     if (paged_query(A, q).chunks > 0) continue;
     for (int i = t * 4; i < kHeads * kDim; i += kPgThreads * 4) {
       const int64_t o = (int64_t)q * kHeads * kDim + i;
@@ -932,7 +1025,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = S.tmem;
-  const int n_run = c_end - c_begin;
+  const int c_begin = S.end[0], c_end = S.end[1], n_run = c_end - c_begin;
 
   if (warp < kPgSoft / 32) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPgRegsSoft));
@@ -999,15 +1092,13 @@ __global__ void __launch_bounds__(512) paged_join_kernel(const __grid_constant__
   }
   if (at < 0) return;
   const int4 J = __ldcg(A.joins + at);               // query, its chunks, its first chunk, all chunks
-  const int qi = J.x, off = J.z, T = J.w, G = n_ctas;
-  const int g0 = run_owner(off, T, G), g1 = run_owner(off + J.y - 1, T, G);
+  const int qi = J.x, off = J.z, T = J.w, G = run_ctas(T, n_ctas);
+  const int g0 = run_first_cut(off, T, G) - 1, g1 = run_last_cut(off, J.y, T, G);
   auto slot_of = [&](int g) { return 2 * (int64_t)g + (g == g0 ? 1 : 0); };
-  // a CTA without chunks (more CTAs than chunks) has no partial
-  auto empty = [&](int g) { return run_start(g, T, G) == run_start(g + 1, T, G); };
   float M = -kPgNoRef, m = -kPgNoRef;
   int b0 = g0;
   for (int b = g0; b <= g1; b += 32) {
-    m = b + lane <= g1 && !empty(b + lane) ? __ldcg(A.part_ml + slot_of(b + lane) * 2 * kHeads + h) : -kPgNoRef;
+    m = b + lane <= g1 ? __ldcg(A.part_ml + slot_of(b + lane) * 2 * kHeads + h) : -kPgNoRef;
     M = fmaxf(M, m);
   }
 #pragma unroll
@@ -1016,7 +1107,7 @@ __global__ void __launch_bounds__(512) paged_join_kernel(const __grid_constant__
   float L = 0.f;
   for (; b0 <= g1; b0 += 32) {
     float w = 0.f;                                   // of partial b0 + lane
-    if (b0 + lane <= g1 && !empty(b0 + lane)) {
+    if (b0 + lane <= g1) {
       const float *ml = A.part_ml + slot_of(b0 + lane) * 2 * kHeads + h;
       if (g1 - g0 >= 32) m = __ldcg(ml);
       w = exp2f(m - M);
