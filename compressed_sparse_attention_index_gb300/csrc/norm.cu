@@ -67,7 +67,7 @@ __device__ __forceinline__ void load_gain(const float *gain, int lane, float *g)
 // ------------------------------------------------------------------ queries
 template <int HPW>
 __device__ __forceinline__ void query_rows(const NormArgs &A, int idx, float2 *cs_sh) {
-  constexpr int B = HPW < 4 ? HPW : 4;              // rows of a warp in flight
+  constexpr int B = HPW < 2 ? HPW : 2;              // rows of a warp in flight
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int parts = 8 / HPW;                        // CTAs per token
   const int64_t tok = idx / parts;
@@ -324,9 +324,12 @@ __device__ __forceinline__ void latent_row(const NormArgs &A, int tok, int lane)
 }
 
 // Grid: lat_ctas CTAs of eight latent rows (first: their rare fp64 rows take
-// longest), then 8 / HPW CTAs per token of 8 HPW query heads each.
+// longest), then 8 / HPW CTAs per token of 8 HPW query heads each.  Two rows of a warp
+// in flight and four CTAs an SM: of 8,192 tokens the queries take 162 us, as a copy of
+// their bytes does (163), the latents alone 38 (their arithmetic), both together 178; four
+// rows in flight, or what registers the compiler likes, made it 192 and 182.
 template <int HPW>
-__global__ void __launch_bounds__(kNormThreads) qk_norm_rope_kernel(const __grid_constant__ NormArgs A) {
+__global__ void __launch_bounds__(kNormThreads, 4) qk_norm_rope_kernel(const __grid_constant__ NormArgs A) {
   __shared__ float2 cs_sh[kRopeDim / 2];
   griddep_wait();
   griddep_launch();
