@@ -136,7 +136,10 @@ csa2_status csa2_paged_attn(const void *q, const void *pages, int n_pages, int p
     return CSA2_ERR_INVALID_ARG;
   if (out_dtype != CSA2_OUT_BF16 && out_dtype != CSA2_OUT_F32) return CSA2_ERR_INVALID_ARG;
   if (sel != nullptr && (sel_stride < 1 || sel_stride > kTopK)) return CSA2_ERR_INVALID_ARG;
-  if (n_q > 65535 || table_stride > INT_MAX) return CSA2_ERR_UNSUPPORTED;
+  if (n_q > 65535 || table_stride > INT_MAX || (int64_t)n_pages * page_size > INT_MAX) return CSA2_ERR_UNSUPPORTED;
+  // chunks of 128 entries are counted in 32 bits (a row of n_vis entries never has more)
+  const int64_t row = sel != nullptr ? sel_stride : table_stride * page_size < INT_MAX ? table_stride * page_size : INT_MAX;
+  if (n_q * ((row + 127) / 128 + 1) > (1 << 30)) return CSA2_ERR_UNSUPPORTED;
   if (n_q == 0) return CSA2_OK;
   if (!on(q, 16) || !on(pages, 32) || !on(block_table, 4) || !off_or_on(sel, 4) || !on(q_seq, 4) || !on(n_vis, 4) ||
       !on(pos, 4) || !on(swa_first, 4) || !on(swa_cnt, 4) || !on(out, 16) || !off_or_on(lse, 4))

@@ -498,6 +498,15 @@ __device__ __forceinline__ void paged_copy(const PagedArgs &A, PagedShared &S, u
   // in [2^-4, 2^15): f16 holds a bf16 value exactly down to 2^-17 and to 2^-25 below; else
   // a second one under the power of two that brings it into [2^14, 2^15)
   uint32_t met = 0, q_parity = 0;
+  auto q_max = [&](uint32_t m) {                     // of the group, from two halves each
+    m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
+    if (lane == 0) S.qmax[lt >> 5] = m;
+    paged_meet(A, S, 2, met);
+#pragma unroll
+    for (int w = 0; w < 8; w++) m = max(m, S.qmax[w]);
+    paged_meet(A, S, 2, met);                        // (before the next one)
+    return m;
+  };
   auto stage_q = [&](int qi, int k) {
     const uint4 *src = reinterpret_cast<const uint4 *>(A.q + (int64_t)qi * kHeads * kDim) + lt;
     unsigned char *dst = sm + kPgSmQ + ((lt & 63) >> 3) * 1024;
@@ -528,12 +537,21 @@ __device__ __forceinline__ void paged_copy(const PagedArgs &A, PagedShared &S, u
         }
       }
       if (pass == 1) break;
-      m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
-      if (lane == 0) S.qmax[lt >> 5] = m;
-      paged_meet(A, S, 2, met);
+      m = q_max(m);
+      if (m >= 0x7F80u) {                            // a head that is not finite spoils its own output alone
+        m = 0u;
+#pragma unroll 1
+        for (int i = 0; i < 16; i++) {
+          const uint4 x = __ldg(src + i * kPgLoad);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int w = 0; w < 8; w++) m = max(m, S.qmax[w]);
-      paged_meet(A, S, 2, met);                      // (before the next query's)
+          for (int u = 0; u < 8; u++) {
+            const uint32_t v = (w[u >> 1] >> (16 * (u & 1))) & 0x7FFFu;
+            if (v < 0x7F80u) m = max(m, v);
+          }
+        }
+        m = q_max(m);
+      }
       const int ex = (int)(m >> 7) - 127;            // max |q| in [2^ex, 2^(ex + 1)) if normal
       if (m == 0u || (ex >= -4 && ex < 15)) break;
       qs = max(ex - 14, -100);

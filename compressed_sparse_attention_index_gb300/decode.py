@@ -9,6 +9,8 @@
   lightning-indexer note: decoder Reindex layers score only a 16,384-position
   pool picked earlier as blocks of 8; perchy.ai/models/deepseek, card "Full.
   Reindex. Reuse.": the pool feeds the top-512 that attention reads.)
+* Paged cache (PagedCache): csa2_page_plan -> csa2_qk_norm_rope, which writes the
+  new latents -> csa2_paged_attn, over every visible entry or a selection.
 """
 from __future__ import annotations
 
@@ -149,3 +151,81 @@ class DecoderStep:
                                dl.swa.shape[2], dw.q_seq, dw.pos, dw.swa_first, dw.swa_cnt, n_q, self.outs[l],
                                self.out_dtype, params, b.ws, b.ws_attn_bytes, stream)
         return self.outs
+
+
+class PagedCache:
+    """A main cache in pages and a window ring for n_seq sequences, with the
+    buffers of a step of up to max_tokens new tokens.  A step is plan, write,
+    attend and advance, or step, which is all four.  Everything stays on the
+    device and on one stream (the current one, or `stream`, a torch.cuda.Stream),
+    so a step can be captured into a CUDA graph and replayed: new_len and the
+    inputs are read where they lie.
+
+    Tokens are numbered in sequence order.  Pages that run out, sequences beyond
+    max_len and tokens beyond max_tokens are reported by csa2_get_device_status.
+    A token's window holds the last min(128, swa_cap) positions; a ring of
+    127 + the longest new_len records keeps the windows of all new tokens."""
+
+    def __init__(self, n_seq: int, n_pages: int, page_size: int, max_len: int, max_tokens: int, swa_cap: int = SWA,
+                 out_dtype=L.CSA2_OUT_BF16, device="cuda"):
+        self.n_seq, self.n_pages, self.page_size, self.max_tokens = n_seq, n_pages, page_size, max_tokens
+        self.swa_cap, self.out_dtype = swa_cap, out_dtype
+        i32 = dict(dtype=torch.int32, device=device)
+        self.pages = torch.zeros((n_pages, page_size, 288), dtype=torch.uint8, device=device)
+        self.swa = torch.zeros((n_seq, swa_cap, 528), dtype=torch.uint8, device=device)
+        self.table = torch.full((n_seq, -(-max_len // page_size)), -1, **i32)
+        self.seq_len = torch.zeros(n_seq, **i32)
+        self.free = torch.arange(n_pages, **i32)
+        self.free_head = torch.zeros(1, **i32)
+        self.desc = torch.empty((7, max_tokens), **i32)
+        self.first = torch.empty(n_seq + 1, **i32)
+        self.totals = torch.empty(2, **i32)
+        self.q = torch.empty((max_tokens, 64, 512), dtype=torch.bfloat16, device=device)
+        self.latent = torch.empty((max_tokens, 512), dtype=torch.bfloat16, device=device)
+        odt = torch.bfloat16 if out_dtype == L.CSA2_OUT_BF16 else torch.float32
+        self.out = torch.empty((max_tokens, 64, 512), dtype=odt, device=device)
+        self.lse = torch.empty((max_tokens, 64), dtype=torch.float32, device=device)
+        self.ws = torch.empty(L.csa2_workspace_size(L.CSA2_OP_PAGED_ATTN, max_tokens, 0), dtype=torch.uint8,
+                              device=device)
+
+    def plan(self, new_len, stream=None):
+        """Pages, slots and descriptors for new_len (device int32 [n_seq]) new tokens per sequence."""
+        L.csa2_page_plan(self.seq_len, new_len, self.n_seq, self.page_size, self.n_pages, self.free, self.n_pages,
+                         self.free_head, self.table, self.table.shape[1], self.swa_cap, self.desc, self.max_tokens,
+                         self.first, self.totals, stream)
+
+    def write(self, q, latent, q_gain=None, latent_gain=None, eps=1e-6, params=None, stream=None):
+        """Norm and rotation of the planned tokens' queries (bf16 [max_tokens][64][512]) and latents
+        ([max_tokens][512]), into self.q and self.latent, and the latents' records into the caches."""
+        L.csa2_qk_norm_rope(q, q.stride(0), q_gain, self.q, latent, latent.stride(0), latent_gain, self.latent,
+                            self.desc[2], self.desc[5], self.desc[6], self.max_tokens, eps, self.pages,
+                            self.n_pages * self.page_size, self.swa, self.n_seq * self.swa_cap, params, stream)
+
+    def attend(self, sel=None, params=None, stream=None):
+        """(output [max_tokens][64][512], lse [max_tokens][64]) of the planned tokens, over all that they see
+        or over sel (device int32 [max_tokens][k]); places without a token get zeros and -inf."""
+        d = self.desc
+        L.csa2_paged_attn(self.q, self.pages, self.n_pages, self.page_size, self.table, self.table.shape[1],
+                          self.n_seq, sel, 0 if sel is None else sel.shape[1], self.swa, self.swa_cap, d[0], d[1],
+                          d[2], d[3], d[4], self.max_tokens, self.out, self.out_dtype, self.lse, params, self.ws,
+                          self.ws.numel(), stream)
+        return self.out, self.lse
+
+    def advance(self, stream=None):
+        """The planned tokens become part of the sequences, their pages are taken."""
+        with torch.cuda.stream(stream):
+            self.seq_len += self.first[1:] - self.first[:-1]
+            self.free_head += self.totals[1:]
+
+    def step(self, new_len, q, latent, q_gain=None, latent_gain=None, eps=1e-6, sel=None, params=None, stream=None):
+        self.plan(new_len, stream)
+        self.write(q, latent, q_gain, latent_gain, eps, params, stream)
+        out = self.attend(sel, params, stream)
+        self.advance(stream)
+        return out
+
+    def read(self, slots, out, stream=None):
+        """Latents of the main cache's records `slots` (device int32, as in desc[5]) into out, bf16 or fp32 [n][512]."""
+        L.csa2_cache_read(L.CSA2_KV_NVFP4, self.pages, self.n_pages * self.page_size, slots, slots.numel(), out,
+                          L.CSA2_OUT_F32 if out.dtype == torch.float32 else L.CSA2_OUT_BF16, stream)
+        return out

@@ -91,6 +91,14 @@ def test_attn_refusals(lib, kw, code):
     assert _attn(lib.load(), **kw) == code
 
 
+@pytest.mark.parametrize("kw,code", [
+    (dict(n_pages=1 << 16, page=1 << 15), UNSUP),                               # slots of 32 bits
+    (dict(n_q=65535, n_pages=10, page=64, stride=1 << 15), UNSUP),              # 65,535 rows of 2^21 entries: chunks of 32 bits
+    (dict(n_q=200, page=1 << 20, stride=1 << 30), UNSUP)])                      # (the product of both behind 64 bits' half)
+def test_attn_limits(lib, kw, code):
+    assert _attn(lib.load(), **kw) == code
+
+
 def test_params_other_than_the_constants(lib):
     p = lib.default_params()
     p.heads = 32
