@@ -15,23 +15,39 @@
 // and denominator, which paged_join_kernel combines.  A CTA has at most two cut
 // queries, so the partials take a fixed workspace.
 //
-// Per chunk: the 128 records are dequantised to f16 in shared memory (an
-// E2M1 x E4M3 product has <= 6 significant bits in [2^-10, 2688]: exact), then
+// Per chunk: the 128 records are dequantised to f16 (an E2M1 x E4M3 product has <= 6
+// significant bits in [2^-10, 2688]: exact), then
 //   S^T[entry][head] = K . Q^T        tcgen05 kind::f16, M = 128, N = 64, K = 512
 //   P[entry][head] = 2^(S - m + 7)    rounded to f16 (11 bits)
 //   O^T[dim][head] += K^T . P         M = 128 dims (4 blocks), N = 64, K = 128
-// with K^T read from the same tile MN-major.  m is a head's reference in log2
-// units: the maximum of the first chunk, raised only when a later logit exceeds
-// it by more than 8, so numerators stay within 2^15 and most chunks need no
-// maximum, no exchange between warps and no rescaling of O.  The factor 2^7
-// keeps the tail of a long row (2^-21 of the largest weight) in f16's normal
-// range.  The denominator sums the unrounded fp32 numerators.
+// m is a head's reference in log2 units: the maximum of the first chunk, raised only
+// when a later logit exceeds it by more than 8, so numerators stay within 2^15 and most
+// chunks need no maximum, no exchange between warps and no rescaling of O.  The factor
+// 2^7 keeps the tail of a long row (2^-21 of the largest weight) in f16's normal range.
+// The denominator sums the unrounded fp32 numerators.
 //
 // Window records (E4M3 x 2^e) are exact in f16 where -15 <= e <= 7; otherwise
 // the window is scaled by 2^kx, kx = 7 - (the largest e): exact but for values
 // below 2^-31 of the window's largest, and undone on its logits and, being the
 // first chunk, on O before the next one.  Q out of f16's range goes to f16 under a
 // power of two, undone on the logits.
+//
+// Warps, with their own barriers between them: two fetch records into shared memory;
+// eight (K) dequantise them, a row per thread, into slabs of 128 dims in tensor memory,
+// where QK reads them as its A operand; eight (V) copy the slabs from there into shared
+// memory, where PV reads them MN-major; eight (softmax) turn S into P and read O out; one
+// thread each issues QK and PV.
+//
+// What bounds it: the heads fill half of an MMA's width, so the tensor cores' 2,600
+// cycles a chunk are far from the peak rate by themselves, and shared memory moves more:
+// V's slabs 1,024 cycles to write and as much for PV to read, Q 512, P 128 to write and
+// 512 to read, the records 288 in and 320 out, and some 800 of waits, descriptions and
+// conflicts: 4,700 of the 5,000 to 5,300 cycles that a chunk takes.  That is why K goes
+// through tensor memory (both operands in shared memory took 512 cycles more), and why
+// its rows are dequantised once (a second time for V cost more arithmetic than
+// everything else together).  8 x 1,048,576 entries: 1,197 us, 0.92 PFLOP/s; 32 x 65,536:
+// 332 us; 33 sequences of up to 40,001: 147 us; 40 queries x 512 selected: 41 us.
+// A few short rows are a chain of latencies: 20 us for one chunk, the join included.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -46,8 +62,8 @@ namespace csa2 {
 constexpr int kPgChunk = 128;
 constexpr int kPgSoft = 256, kPgLoad = 256;        // threads of the softmax group and of each loading group
 constexpr int kPgThreads = kPgSoft + 2 * kPgLoad + 128;
-// Registers: 896 threads are launched with 72 each; the softmax group takes what
-// the others give up.
+// Registers: 896 threads are launched with 72 each; the softmax and V groups take what
+// the K group and the other warps give up.
 constexpr int kPgRegsSoft = 88, kPgRegsK = 56, kPgRegsV = 80, kPgRegsRest = 56;
 static_assert(kPgSoft * kPgRegsSoft + kPgLoad * (kPgRegsK + kPgRegsV) + 128 * kPgRegsRest <= 72 * kPgThreads, "register split");
 constexpr int kPgSlab = 128 * 128 * 2;             // one slab: 128 entries x 128 dims f16
@@ -165,7 +181,7 @@ struct PagedShared {
   float l[4][kHeads], red[4][kHeads];
   uint32_t tmem, qmax[8];
   int emin, emax;
-  int scan[kPgThreads / 32], end[2], start, off;       // the run's ends; its first query and that one's first chunk
+  int scan[kPgThreads / 32], end[2], start, off, T, G;      // the run's ends; its first query, that one's first chunk; all chunks, their CTAs
   PagedQuery Q;
   volatile int bad;
 };
@@ -189,11 +205,11 @@ __device__ __forceinline__ void paged_wait(const PagedArgs &A, PagedShared &S, u
 
 // The warps of a group meet, where a chunk's description says so.  (Not a barrier of the
 // hardware's: once a wait has run out the warps may read different descriptions.)
-__device__ __forceinline__ void paged_meet(const PagedArgs &A, PagedShared &S, int group, uint32_t &parity) {
+__device__ __forceinline__ void paged_meet(const PagedArgs &A, PagedShared &S, int group, uint32_t &met) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&S.meet[group]);
-  paged_wait(A, S, &S.meet[group], parity);
-  parity ^= 1;
+  paged_wait(A, S, &S.meet[group], met & 1);
+  met ^= 1;
 }
 __device__ __forceinline__ bool paged_bad(const PagedShared &S) { return __any_sync(0xFFFFFFFFu, S.bad); }
 
@@ -497,7 +513,7 @@ __device__ __forceinline__ void paged_copy(const PagedArgs &A, PagedShared &S, u
   // Q of a query to f16, K-major, 128B swizzle.  One pass as they are where max |q| lies
   // in [2^-4, 2^15): f16 holds a bf16 value exactly down to 2^-17 and to 2^-25 below; else
   // a second one under the power of two that brings it into [2^14, 2^15)
-  uint32_t met = 0, q_parity = 0;
+  uint32_t met = 0;                                  // parities: 1 of the group's meetings, 2 of q_done
   auto q_max = [&](uint32_t m) {                     // of the group, from two halves each
     m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
     if (lane == 0) S.qmax[lt >> 5] = m;
@@ -520,8 +536,8 @@ __device__ __forceinline__ void paged_copy(const PagedArgs &A, PagedShared &S, u
 #pragma unroll
         for (int i = 0; i < 8; i++) x[i] = __ldg(src + (i0 + i) * kPgLoad);
         if (pass == 0 && i0 == 0 && k > 0) {         // (the query before is multiplied)
-          paged_wait(A, S, &S.q_done, q_parity);
-          q_parity ^= 1;
+          paged_wait(A, S, &S.q_done, met >> 1);
+          met ^= 2;
         }
 #pragma unroll
         for (int i = 0; i < 8; i++) {                // 16-B chunk lt % 64 of head lt / 64 + 4 (i0 + i)
@@ -622,10 +638,9 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 }
 
 // This lane's entry: 32 heads' logits in log2 units (-inf for a row without an
-// entry: `none` = -inf, else 0), plus the heads' `less` where given.  (The product is
-// rounded before the sum, as the maximum's was: in one step, the difference of two
-// huge logits would be off by that rounding.)
-template <bool LESS>
+// entry: `none` = -inf, else 0), plus the heads' `less`.  (The product is rounded before
+// the sum, as the maximum's was: in one step, the difference of two huge logits would be
+// off by that rounding.)
 __device__ __forceinline__ void paged_logits(uint32_t ta, float f, float none, const float *less, uint64_t (&s)[16]) {
   const uint64_t f2 = pair(f, f), n2 = pair(none, none);
 #pragma unroll
@@ -635,15 +650,9 @@ __device__ __forceinline__ void paged_logits(uint32_t ta, float f, float none, c
     ptx::tmem_wait_ld();
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
-      uint64_t x = fma2(pair(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), f2, n2);
-      uint64_t y = fma2(pair(__uint_as_float(a[i + 2]), __uint_as_float(a[i + 3])), f2, n2);
-      if (LESS) {
-        const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(less + h + i);
-        x = add2(x, m.x);
-        y = add2(y, m.y);
-      }
-      s[(h + i) / 2] = x;
-      s[(h + i) / 2 + 1] = y;
+      const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(less + h + i);
+      s[(h + i) / 2] = add2(fma2(pair(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), f2, n2), m.x);
+      s[(h + i) / 2 + 1] = add2(fma2(pair(__uint_as_float(a[i + 2]), __uint_as_float(a[i + 3])), f2, n2), m.y);
     }
   }
 }
@@ -661,8 +670,8 @@ __device__ __forceinline__ bool paged_numerators(uint64_t (&s)[16]) {
 }
 
 // Warp w has TMEM lane quarter w % 4 (S: entries, O: dims) and heads 32 (w / 4) ..
-__device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S, unsigned char *sm, int n_run, int T,
-                                              int G, uint32_t tmem) {
+__device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S, unsigned char *sm, int n_run,
+                                              uint32_t tmem) {
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int quarter = warp & 3, hb = (warp >> 2) * 32, e_row = quarter * 32 + lane;
   const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -676,10 +685,8 @@ __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S
     paged_wait(A, S, &S.s_full, k & 1);
     ptx::tc_fence_after();
     const PagedInfo &info = S.info[k & (kPgInfo - 1)];
-    const int4 I = info.at;
-    const int lc = I.y;
-    if (k == 0 || lc == 0) {                         // a query begins
-      lc0 = lc;
+    if (k == 0 || info.at.y == 0) {                  // a query begins
+      lc0 = info.at.y;
       acc = false;
       o_scale = 1.f;
 #pragma unroll
@@ -693,31 +700,33 @@ __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S
     const float none = ((info.valid[quarter] >> lane) & 1u) != 0u ? 0.f : -INFINITY;
     const uint32_t ta = tq + kPgColS + hb;
     uint64_t s[16];
-    paged_logits<true>(ta, f, none, &S.less[hb], s);
+    paged_logits(ta, f, none, &S.less[hb], s);
     const bool over = paged_numerators(s);
     // (a window's 2^-kx is undone before the next chunk)
     if (soft_any(over || (acc && o_scale != 1.f))) {
-      // the chunk's maximum of every head: lane L ends with head hb + L
-      float v[32];
-      paged_logits<false>(ta, f, none, nullptr, s);
+      // the chunk's maximum of every head, 16 at a time: lanes L and L + 16 end with head L
+#pragma unroll 1
+      for (int h = 0; h < 32; h += 16) {
+        uint32_t a[16];
+        float v[16];
+        ptx::tmem_ld_32x32b_x16(ta + h, a);
+        ptx::tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 16; i++) {
-        const float2 x = unpair(s[i]);
-        v[2 * i] = x.x;
-        v[2 * i + 1] = x.y;
-      }
+        for (int i = 0; i < 16; i++) v[i] = __fmul_rn(__uint_as_float(a[i]), f) + none;
 #pragma unroll
-      for (int w = 16; w >= 1; w >>= 1) {
-        const bool upper = (lane & w) != 0;
+        for (int w = 8; w >= 1; w >>= 1) {
+          const bool upper = (lane & w) != 0;
 #pragma unroll
-        for (int i = 0; i < 16; i++) {
-          if (i < w) {
-            const float keep = upper ? v[i + w] : v[i], send = upper ? v[i] : v[i + w];
-            v[i] = fmaxf(keep, __shfl_xor_sync(0xFFFFFFFFu, send, w));
+          for (int i = 0; i < 8; i++) {
+            if (i < w) {
+              const float keep = upper ? v[i + w] : v[i], send = upper ? v[i] : v[i + w];
+              v[i] = fmaxf(keep, __shfl_xor_sync(0xFFFFFFFFu, send, w));
+            }
           }
         }
+        v[0] = fmaxf(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 16));
+        if (lane < 16) S.red[quarter][hb + h + lane] = v[0];
       }
-      S.red[quarter][hb + lane] = v[0];
       soft_sync();
       if (t < kHeads) {
         const float cm = fmaxf(fmaxf(S.red[0][t], S.red[1][t]), fmaxf(S.red[2][t], S.red[3][t])) - kPgShift;
@@ -753,7 +762,7 @@ __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S
         const float2 l = unpair(l_acc[i]);
         l_acc[i] = pair(l.x * S.alpha[hb + 2 * i], l.y * S.alpha[hb + 2 * i + 1]);
       }
-      paged_logits<true>(ta, f, none, &S.less[hb], s);
+      paged_logits(ta, f, none, &S.less[hb], s);
       paged_numerators(s);
     }
     ptx::tc_fence_before();
@@ -781,29 +790,35 @@ __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S
     if (lane == 0) ptx::mbar_arrive(&S.p_full);
     acc = true;
     if (kx != 0) o_scale = ldexpf(1.f, -kx);
+    const int4 I = info.at;
+    const int lc = I.y;
     if (lc + 1 != I.z && k + 1 != n_run) continue;
     if ((unsigned)I.x >= (unsigned)A.n_q) continue;  // (a description left from before, once a wait has run out)
 
     // -------------------------------------------------------- the query's last chunk here: read-out
-    float l_sum[32];
 #pragma unroll
-    for (int i = 0; i < 16; i++) {
-      const float2 l = unpair(l_acc[i]);
-      l_sum[2 * i] = l.x;
-      l_sum[2 * i + 1] = l.y;
-    }
+    for (int h = 0; h < 32; h += 16) {               // (as the maxima)
+      float v[16];
 #pragma unroll
-    for (int w = 16; w >= 1; w >>= 1) {
-      const bool upper = (lane & w) != 0;
+      for (int i = 0; i < 8; i++) {
+        const float2 l = unpair(l_acc[h / 2 + i]);
+        v[2 * i] = l.x;
+        v[2 * i + 1] = l.y;
+      }
 #pragma unroll
-      for (int i = 0; i < 16; i++) {
-        if (i < w) {
-          const float keep = upper ? l_sum[i + w] : l_sum[i], send = upper ? l_sum[i] : l_sum[i + w];
-          l_sum[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, w);
+      for (int w = 8; w >= 1; w >>= 1) {
+        const bool upper = (lane & w) != 0;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          if (i < w) {
+            const float keep = upper ? v[i + w] : v[i], send = upper ? v[i] : v[i + w];
+            v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, w);
+          }
         }
       }
+      v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], 16);
+      if (lane < 16) S.l[quarter][hb + h + lane] = v[0];
     }
-    S.l[quarter][hb + lane] = l_sum[0];
     paged_meet(A, S, 0, met);
     const bool whole = lc0 == 0 && lc + 1 == I.z;
     const int64_t slot = 2 * (int64_t)blockIdx.x + (lc0 > 0 ? 0 : 1);
@@ -869,8 +884,8 @@ __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S
     }
     ptx::tc_fence_before();                          // (before the next query's PV, behind p_full)
     // the first CTA after the one that begins a cut query names it for the join
-    if (t == 0 && lc0 > 0 && (int)blockIdx.x == run_first_cut(I.w, T, G))
-      A.joins[blockIdx.x] = make_int4(I.x, I.z, I.w, T);
+    if (t == 0 && lc0 > 0 && (int)blockIdx.x == run_first_cut(I.w, S.T, S.G))
+      A.joins[blockIdx.x] = make_int4(I.x, I.z, I.w, S.T);
   }
 }
 
@@ -1028,7 +1043,11 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
       S.end[i] = T;
     }
   }
-  if (t == 0) A.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (t == 0) {
+    S.T = T;
+    S.G = G;
+    A.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  }
   // queries with nothing to attend to: zeros
   for (int q = none ? blockIdx.x : A.n_q; q < A.n_q; q += gridDim.x) {
     if (paged_query(A, q).chunks > 0) continue;
@@ -1047,7 +1066,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
 
   if (warp < kPgSoft / 32) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPgRegsSoft));
-    paged_softmax(A, S, sm, n_run, T, G, tmem);
+    paged_softmax(A, S, sm, n_run, tmem);
   } else if (warp < (kPgSoft + kPgLoad) / 32) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPgRegsK));
     paged_load(A, S, sm, n_run, tmem);
