@@ -883,8 +883,9 @@ __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S
       }
     }
     ptx::tc_fence_before();                          // (before the next query's PV, behind p_full)
-    // the first CTA after the one that begins a cut query names it for the join
-    if (t == 0 && lc0 > 0 && (int)blockIdx.x == run_first_cut(I.w, S.T, S.G))
+    // the first CTA after the one that begins a cut query names it for the join (not by a
+    // description that may be none)
+    if (t == 0 && !S.bad && lc0 > 0 && (int)blockIdx.x == run_first_cut(I.w, S.T, S.G))
       A.joins[blockIdx.x] = make_int4(I.x, I.z, I.w, S.T);
   }
 }

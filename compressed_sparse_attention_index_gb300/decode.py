@@ -164,7 +164,8 @@ class PagedCache:
     Tokens are numbered in sequence order.  Pages that run out, sequences beyond
     max_len and tokens beyond max_tokens are reported by csa2_get_device_status.
     A token's window holds the last min(128, swa_cap) positions; a ring of
-    127 + the longest new_len records keeps the windows of all new tokens."""
+    127 + the longest new_len records keeps the windows of all new tokens.
+    max_tokens is at most 65,535."""
 
     def __init__(self, n_seq: int, n_pages: int, page_size: int, max_len: int, max_tokens: int, swa_cap: int = SWA,
                  out_dtype=L.CSA2_OUT_BF16, device="cuda"):
@@ -188,8 +189,18 @@ class PagedCache:
         self.ws = torch.empty(L.csa2_workspace_size(L.CSA2_OP_PAGED_ATTN, max_tokens, 0), dtype=torch.uint8,
                               device=device)
 
+    def _want(self, name, x, rows, cols, dtype):
+        """x: rows of `cols` elements (any stride between rows), on the cache's device."""
+        if x.dtype != dtype or x.device != self.seq_len.device or x.shape[0] != rows or x.numel() != rows * cols or \
+                (rows > 0 and not x[0].is_contiguous()):
+            raise ValueError(f"{name}: {rows} rows of {cols} contiguous {dtype} on {self.seq_len.device} expected, "
+                             f"not {tuple(x.shape)} {x.dtype} on {x.device}")
+
     def plan(self, new_len, stream=None):
         """Pages, slots and descriptors for new_len (device int32 [n_seq]) new tokens per sequence."""
+        if not new_len.is_contiguous():
+            raise ValueError("new_len: contiguous int32 expected")
+        self._want("new_len", new_len, self.n_seq, 1, torch.int32)
         L.csa2_page_plan(self.seq_len, new_len, self.n_seq, self.page_size, self.n_pages, self.free, self.n_pages,
                          self.free_head, self.table, self.table.shape[1], self.swa_cap, self.desc, self.max_tokens,
                          self.first, self.totals, stream)
@@ -197,6 +208,13 @@ class PagedCache:
     def write(self, q, latent, q_gain=None, latent_gain=None, eps=1e-6, params=None, stream=None):
         """Norm and rotation of the planned tokens' queries (bf16 [max_tokens][64][512]) and latents
         ([max_tokens][512]), into self.q and self.latent, and the latents' records into the caches."""
+        self._want("q", q, self.max_tokens, 64 * 512, torch.bfloat16)
+        self._want("latent", latent, self.max_tokens, 512, torch.bfloat16)
+        for gain in (q_gain, latent_gain):
+            if gain is not None:
+                self._want("gain", gain.reshape(-1, 1), 512, 1, torch.float32)
+                if not gain.is_contiguous():
+                    raise ValueError("gain: contiguous fp32 expected")
         L.csa2_qk_norm_rope(q, q.stride(0), q_gain, self.q, latent, latent.stride(0), latent_gain, self.latent,
                             self.desc[2], self.desc[5], self.desc[6], self.max_tokens, eps, self.pages,
                             self.n_pages * self.page_size, self.swa, self.n_seq * self.swa_cap, params, stream)
@@ -204,6 +222,10 @@ class PagedCache:
     def attend(self, sel=None, params=None, stream=None):
         """(output [max_tokens][64][512], lse [max_tokens][64]) of the planned tokens, over all that they see
         or over sel (device int32 [max_tokens][k]); places without a token get zeros and -inf."""
+        if sel is not None:
+            if not sel.is_contiguous():
+                raise ValueError("sel: contiguous int32 expected")
+            self._want("sel", sel, self.max_tokens, sel.shape[1], torch.int32)
         d = self.desc
         L.csa2_paged_attn(self.q, self.pages, self.n_pages, self.page_size, self.table, self.table.shape[1],
                           self.n_seq, sel, 0 if sel is None else sel.shape[1], self.swa, self.swa_cap, d[0], d[1],
@@ -226,6 +248,10 @@ class PagedCache:
 
     def read(self, slots, out, stream=None):
         """Latents of the main cache's records `slots` (device int32, as in desc[5]) into out, bf16 or fp32 [n][512]."""
+        if not slots.is_contiguous() or slots.dtype != torch.int32 or not out.is_contiguous() or \
+                out.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("read: contiguous int32 slots and contiguous bf16 or fp32 out expected")
+        self._want("out", out, slots.numel(), 512, out.dtype)
         L.csa2_cache_read(L.CSA2_KV_NVFP4, self.pages, self.n_pages * self.page_size, slots, slots.numel(), out,
                           L.CSA2_OUT_F32 if out.dtype == torch.float32 else L.CSA2_OUT_BF16, stream)
         return out

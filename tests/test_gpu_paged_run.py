@@ -249,3 +249,52 @@ def test_rows_of_the_same_sequence_and_entry(lib, oracle_lib):
                             R.swa_values(c.swa[0][(72 + np.arange(128)) % 128])])
         o, _ = R.attention(R.bf16_values(x[i]), k, 199)
         assert row_norm_err(out[i], o) <= ATTN_TOL_F32
+
+
+def test_offsets_beyond_32_bits(lib, oracle_lib):
+    """Records, rows and outputs behind the first 4 GiB of their tensors are those of a small call."""
+    page, n_pages = 64, 265_000                            # 16.96 M records, 4.9 GB
+    c = Case(oracle_lib, [1000, 70], page, seed=93)
+    far = n_pages - c.n_pages
+    pages = torch.zeros((n_pages, page, 288), dtype=torch.uint8, device="cuda")
+    pages[far:] = torch.from_numpy(c.pages).cuda()
+    q = _decode_queries([1000, 70])
+    want, want_l = c.run(lib, q)
+    table = np.where(c.table >= 0, c.table + far, -1)
+    a = np.array(q)
+    wsb = lib.csa2_workspace_size(lib.CSA2_OP_PAGED_ATTN, 2, 0)
+    ws, swa = torch.empty(wsb, dtype=torch.uint8, device="cuda"), torch.from_numpy(c.swa).cuda()
+    sel = np.tile(np.arange(0, 70), (2, 1))
+    near_sel, _ = _attend_rows(lib, c, c.q, q, sel=sel)
+    for s, w in ((None, want), (sel, near_sel)):
+        out, lse = torch.empty((2, 64, 512), device="cuda"), torch.empty((2, 64), device="cuda")
+        lib.csa2_paged_attn(_bf16(c.q), pages, n_pages, page, _i32(table), table.shape[1], 2, None if s is None else _i32(s),
+                            0 if s is None else s.shape[1], swa, 128, _i32(a[:, 0]), _i32(a[:, 1]), _i32(a[:, 2]), _i32(a[:, 3]),
+                            _i32(a[:, 4]), 2, out, lib.CSA2_OUT_F32, lse, None, ws, wsb)
+        assert np.array_equal(out.cpu().numpy(), w)
+    # a cache write there, and records read back into rows behind 4 GiB
+    m, slots = 66_000, n_pages * page
+    x = torch.randn((64, 64, 512), generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    lat = torch.randn((64, 512), generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+    big = torch.empty((m, 64, 512), dtype=torch.bfloat16, device="cuda")                 # 4.3 GB
+    big[-64:] = x
+    lats = torch.zeros((m, 512), dtype=torch.bfloat16, device="cuda")
+    lats[-64:] = lat
+    pos = torch.arange(m, dtype=torch.int32, device="cuda")
+    slot = torch.full((m,), -1, dtype=torch.int32, device="cuda")
+    slot[-64:] = torch.arange(slots - 64, slots, dtype=torch.int32, device="cuda")
+    lib.csa2_qk_norm_rope(big, 32768, None, big, lats, 512, None, lats, pos, slot, None, m, 1e-6, pages, slots, None, 0)
+    small_q, small_l = torch.empty_like(x), torch.empty_like(lat)
+    small = torch.zeros((64, 288), dtype=torch.uint8, device="cuda")
+    lib.csa2_qk_norm_rope(x, 32768, None, small_q, lat, 512, None, small_l, pos[-64:].clone(), _i32(range(64)), None, 64, 1e-6,
+                          small, 64, None, 0)
+    assert torch.equal(big[-64:], small_q) and torch.equal(lats[-64:], small_l)
+    assert torch.equal(pages.view(-1, 288)[-64:], small)
+    del big
+    n = 2_200_000
+    back = torch.empty((n, 512), dtype=torch.float32, device="cuda")                     # 4.5 GB
+    where = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    where[-64:] = slot[-64:]
+    lib.csa2_cache_read(lib.CSA2_KV_NVFP4, pages, slots, where, n, back, lib.CSA2_OUT_F32)
+    assert np.array_equal(back[-64:].cpu().numpy(), R.kv_values(small.cpu().numpy())) and not bool(back[:-64].any())
+    assert lib.csa2_get_device_status() == 0

@@ -111,6 +111,32 @@ def test_workspace_is_the_same_for_every_call(lib):
     assert a == lib.csa2_workspace_size(lib.CSA2_OP_PAGED_ATTN, 65535, 1 << 20, 7) and a > 0
 
 
+def test_paged_cache_refuses_what_does_not_fit():
+    import torch
+    from compressed_sparse_attention_index_gb300.decode import PagedCache
+    c = PagedCache(3, 8, 16, 64, 5, device="cpu")
+    q, lat = torch.zeros((5, 64, 512), dtype=torch.bfloat16), torch.zeros((5, 512), dtype=torch.bfloat16)
+    for new in (torch.zeros(2, dtype=torch.int32), torch.zeros(3, dtype=torch.int64), torch.zeros((3, 2), dtype=torch.int32)[:, 0]):
+        with pytest.raises(ValueError):
+            c.plan(new)
+    for a, b in ((q[:4], lat), (q, lat[:4]), (q.float(), lat), (q, lat.float()), (q.transpose(1, 2), lat), (q, lat[:, ::2]),
+                 (q.transpose(0, 1), lat), (q[:, :32], lat)):
+        with pytest.raises(ValueError):
+            c.write(a, b)
+    for gain in (torch.ones(256), torch.ones(512, dtype=torch.float64), torch.ones(1024)[::2]):
+        with pytest.raises(ValueError):
+            c.write(q, lat, gain)
+    for sel in (torch.zeros((4, 8), dtype=torch.int32), torch.zeros((5, 8)), torch.zeros((5, 16), dtype=torch.int32)[:, ::2]):
+        with pytest.raises(ValueError):
+            c.attend(sel)
+    slots = torch.zeros(6, dtype=torch.int32)
+    for out in (torch.zeros((5, 512)), torch.zeros((6, 512), dtype=torch.float16), torch.zeros((6, 1024))[:, ::2]):
+        with pytest.raises(ValueError):
+            c.read(slots, out)
+    with pytest.raises(ValueError):
+        c.read(slots.long(), torch.zeros((6, 512)))
+
+
 # ------------------------------------------------------------------ the restatements themselves
 def test_rounding_matches_the_library_conversion():
     import torch
