@@ -23,9 +23,10 @@
 // depend on the order of fp32 sums, the latent is the exact value rounded once
 // to bf16: the sum of squares (each square exact in fp32) and the normalised
 // values are carried as unevaluated sums of two fp32 (about 2^-44 relative),
-// the rotated channels in fp32 with an error bound; a row with a channel whose
-// bound straddles a bf16 border (about one row in forty), or whose range leaves
-// fp32, is recomputed in fp64.
+// the rotated channels in fp32 with an error bound; a pair whose bound straddles a
+// bf16 border (about one row in forty has one) is rotated again in fp64, and a row
+// whose range leaves fp32 is recomputed in fp64 (fp64 is slow here: with the
+// whole row recomputed for such a pair, 8,192 latents took 38 us instead of 23).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -186,6 +187,13 @@ __device__ __noinline__ void latent_row_f64(const float *x, const float *g, doub
   }
 }
 
+// A rotated pair in fp64: its bf16 bits, the first channel's in the lower half.
+__device__ __noinline__ uint32_t rotated_pair_f64(double a, double b, uint64_t turn) {
+  double c, s;
+  sincospi((double)(int64_t)turn * 0x1p-63, &s, &c);
+  return bf16_of_f64(a * c - b * s) | bf16_of_f64(a * s + b * c) << 16;
+}
+
 __device__ __forceinline__ void latent_row(const NormArgs &A, int tok, int lane) {
   const uint4 *p = reinterpret_cast<const uint4 *>(A.lat + (int64_t)tok * A.lat_stride + lane * 8);
   const uint4 v0 = __ldcs(p), v1 = __ldcs(p + 32);
@@ -244,6 +252,7 @@ __device__ __forceinline__ void latent_row(const NormArgs &A, int tok, int lane)
                         fabsf(h[i]) < 0x1p100f);
     y[i] = bf16_of_pair(h[i], l[i]);
   }
+  uint32_t close = 0u;                                               // pairs whose bound straddles a border
   if (lane >= (kRopeOff - 256) / 8) {
 #pragma unroll
     for (int k = 0; k < 4; k++) {
@@ -256,12 +265,25 @@ __device__ __forceinline__ void latent_row(const NormArgs &A, int tok, int lane)
       const uint32_t ah = __bfloat16_as_ushort(__float2bfloat16_rn(ra + d));
       const uint32_t bl = __bfloat16_as_ushort(__float2bfloat16_rn(rb - d));
       const uint32_t bh = __bfloat16_as_ushort(__float2bfloat16_rn(rb + d));
-      again |= al != ah || bl != bh;
+      close |= (uint32_t)(al != ah || bl != bh) << k;
       y[8 + 2 * k] = al;
       y[9 + 2 * k] = bl;
     }
   }
-  if (__any_sync(0xFFFFFFFFu, again)) latent_row_f64(x, g, A.eps, turn, lane, y);
+  if (__any_sync(0xFFFFFFFFu, again)) {
+    latent_row_f64(x, g, A.eps, turn, lane, y);
+  } else if (__any_sync(0xFFFFFFFFu, close != 0u)) {
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      if (!__any_sync(0xFFFFFFFFu, (close >> k) & 1u)) continue;
+      const uint64_t t = __shfl_sync(0xFFFFFFFFu, turn, (lane & 7) * 4 + k);
+      if ((close >> k) & 1u) {
+        const uint32_t two = rotated_pair_f64((double)h[8 + 2 * k] + l[8 + 2 * k], (double)h[9 + 2 * k] + l[9 + 2 * k], t);
+        y[8 + 2 * k] = two & 0xFFFFu;
+        y[9 + 2 * k] = two >> 16;
+      }
+    }
+  }
   if (A.lat_out != nullptr) {
     uint4 *o = reinterpret_cast<uint4 *>(A.lat_out + (int64_t)tok * kDim + lane * 8);
     o[0] = make_uint4(y[0] | y[1] << 16, y[2] | y[3] << 16, y[4] | y[5] << 16, y[6] | y[7] << 16);
@@ -326,8 +348,8 @@ __device__ __forceinline__ void latent_row(const NormArgs &A, int tok, int lane)
 // Grid: lat_ctas CTAs of eight latent rows (first: their rare fp64 rows take
 // longest), then 8 / HPW CTAs per token of 8 HPW query heads each.  Two rows of a warp
 // in flight and four CTAs an SM: of 8,192 tokens the queries take 162 us, as a copy of
-// their bytes does (163), the latents alone 38 (their arithmetic), both together 178; four
-// rows in flight, or what registers the compiler likes, made it 192 and 182.
+// their bytes does (163), the latents alone 23 (their arithmetic), both together 176; four
+// rows in flight, or what registers the compiler likes, took 14 and 4 us more.
 template <int HPW>
 __global__ void __launch_bounds__(kNormThreads, 4) qk_norm_rope_kernel(const __grid_constant__ NormArgs A) {
   __shared__ float2 cs_sh[kRopeDim / 2];
