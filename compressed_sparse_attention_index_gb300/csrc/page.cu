@@ -111,16 +111,16 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
   for (int64_t i = me; i < P.max_tokens; i += all) {
     int v[7] = {0, 0, 0, 0, 0, -1, -1};                        // a row without a token
     if (i < n_tok) {
-      const int b = seq_of(tok, P.n_seq, (int)i);
-      bool bad;
-      const PlanSeq s = plan_seq(P, b, bad);
-      const int pos = s.len + ((int)i - tok[b]), col = (int)((unsigned)pos / (unsigned)P.page);
+      const int b = seq_of(tok, P.n_seq, (int)i);              // (has tokens, so its lengths are sound)
+      const int len = __ldg(P.seq_len + b), add = __ldg(P.new_len + b);
+      const int have = (int)(((unsigned)len + (unsigned)P.page - 1u) / (unsigned)P.page);
+      const int pos = len + ((int)i - tok[b]), col = (int)((unsigned)pos / (unsigned)P.page);
       int id;
-      if (col < s.have) {                                      // (columns that this step does not write)
+      if (col < have) {                                      // (columns that this step does not write)
         id = P.block_table[(int64_t)b * P.table_stride + col];
         if (id >= P.n_pages) id = -1;
       } else {
-        id = free_page(pg[b] + (col - s.have));
+        id = free_page(pg[b] + (col - have));
       }
       err |= id < 0;
       const int cnt = min(min(kSwa, P.swa_cap), pos + 1);
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
       v[4] = cnt;
       v[5] = id < 0 ? -1 : id * P.page + (pos - col * P.page);
       // a ring slot that a later token of this step takes again is not written
-      v[6] = P.swa_cap > 0 && (int64_t)pos + P.swa_cap >= (int64_t)s.len + s.add
+      v[6] = P.swa_cap > 0 && (int64_t)pos + P.swa_cap >= (int64_t)len + add
                  ? b * P.swa_cap + (int)((unsigned)pos % (unsigned)P.swa_cap)
                  : -1;
     }
@@ -158,10 +158,11 @@ cudaError_t launch_page_plan(const PlanArgs &P, cudaStream_t st) {
   });
   if (e != cudaSuccess) return e;
   const size_t smem = 2 * (size_t)(P.n_seq + 1) * sizeof(int);
-  // a warp's worth of sequences or tokens needs no 1,024 threads; four tokens a thread before another CTA
+  // a warp's worth of sequences or tokens needs no 1,024 threads; a token a thread up to a CTA per SM (its
+  // search and loads are a chain: 1,000 sequences and 131,072 tokens take 5.7 us, 9.8 with four a thread)
   const int most = P.n_seq > P.max_tokens ? P.n_seq : P.max_tokens;
   const int threads = most <= 128 ? 128 : most <= 512 ? 512 : kPlanThreads;
-  const int64_t ctas = ((int64_t)P.max_tokens + 4 * threads - 1) / (4 * threads);
+  const int64_t ctas = ((int64_t)P.max_tokens + threads - 1) / threads;
   const int64_t cap = device_sm_count(dev);
   return launch_pdl(page_plan_kernel, dim3((unsigned)(ctas < 1 ? 1 : ctas < cap ? ctas : cap)), dim3(threads), smem, st,
                     1u, P);
