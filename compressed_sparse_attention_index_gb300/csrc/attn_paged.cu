@@ -45,9 +45,9 @@
 // conflicts: 4,700 of the 5,000 to 5,300 cycles that a chunk takes.  That is why K goes
 // through tensor memory (both operands in shared memory took 512 cycles more), and why
 // its rows are dequantised once (a second time for V cost more arithmetic than
-// everything else together).  8 x 1,048,576 entries: 1,197 us, 0.92 PFLOP/s; 32 x 65,536:
-// 332 us; 33 sequences of up to 40,001: 147 us; 40 queries x 512 selected: 41 us.
-// A few short rows are a chain of latencies: 20 us for one chunk, the join included.
+// everything else together).  8 x 1,048,576 entries: 1,200 us, 0.92 PFLOP/s; 32 x 65,536:
+// 333 us; 33 sequences of up to 40,001: 149 us; 40 queries x 512 selected: 41 us.
+// A few short rows are a chain of latencies: 18 us for one chunk each, the join included.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -100,6 +100,16 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// j / n by a multiplication: exact for j below 2^31 (mul = ceil(2^(31 + s) / n) with
+// 2^s >= n is at most 2^32 and off by less than one in 2^s)
+__device__ __forceinline__ unsigned magic_div(unsigned j, uint64_t mul, int shift) { return (unsigned)(((uint64_t)j * mul) >> shift); }
+static void magic_of(unsigned n, uint64_t &mul, int &shift) {
+  int s = 0;
+  while (((int64_t)1 << s) < (int64_t)n) s++;
+  shift = 31 + s;
+  mul = (uint64_t)((((unsigned __int128)1 << shift) + n - 1) / n);
+}
+
 struct PagedQuery {
   int seq, n, chunks, win, first;      // entries (or selection slots), chunks in all, the window's
   bool bad;
@@ -126,7 +136,6 @@ __device__ __forceinline__ int run_ctas(int T, int grid) { return min(grid, max(
 // CTA its Q, a window or a read-out and a partial of 128 KB for the join, about as much
 // as three chunks.  Longer runs move their borders further.
 __device__ __forceinline__ int run_snap(int T, int G) { return min(kPgSnap, T / (kPgSnapRun * G)); }
-__device__ __forceinline__ int run_border(int g, int T, int G) { return (int)((int64_t)g * T / G); }
 // The first border that stays inside a query of n chunks from off, and the last one.
 __device__ __forceinline__ int run_first_cut(int off, int T, int G) {
   return (int)((((int64_t)off + run_snap(T, G) + 1) * G + T - 1) / T);
@@ -154,11 +163,8 @@ struct PagedCursor {
 };
 
 // What the roles need to know of a chunk (kPgInfo of them, by chunk number).
-// j / page by a multiplication: exact for j below 2^31 (page_mul = ceil(2^(31 + s) /
-// page) with 2^s >= page is at most 2^32 and off by less than one in 2^s)
-__device__ __forceinline__ unsigned paged_col(unsigned j, const PagedArgs &A) {
-  return (unsigned)(((uint64_t)j * A.page_mul) >> A.page_shift);
-}
+// j / page
+__device__ __forceinline__ unsigned paged_col(unsigned j, const PagedArgs &A) { return magic_div(j, A.page_mul, A.page_shift); }
 
 struct PagedInfo {
   int4 at;                      // query, place in it, its chunks, its first chunk
@@ -357,9 +363,11 @@ __device__ __forceinline__ void paged_load(const PagedArgs &A, PagedShared &S, u
   PagedSlab<2> n((unsigned)team);                    // the next slab
   uint32_t met = 0;
   for (int k = 0; k < n_run; k++) {
-    paged_wait(A, S, &S.raw_full[k & 1], (k >> 1) & 1);
+    // (a run's first chunk, if a window, needs no records: its own description will do)
+    const bool ahead = k == 0 && S.Q.win > 0 && S.off == S.end[0];
+    if (!ahead) paged_wait(A, S, &S.raw_full[k & 1], (k >> 1) & 1);
     PagedInfo &I = S.info[k & (kPgInfo - 1)];
-    const int win = __shfl_sync(0xFFFFFFFFu, I.win, 0);
+    const int win = __shfl_sync(0xFFFFFFFFu, ahead ? S.Q.win : I.win, 0);
     if (win > 0 && paged_bad(S)) break;
     int kx = 0;
     uint4 ws = make_uint4(0u, 0u, 0u, 0u);           // a window record's 16 scales
@@ -374,8 +382,8 @@ __device__ __forceinline__ void paged_load(const PagedArgs &A, PagedShared &S, u
     if (win > 0) {
       // ---------------------------------------------------- a window's rows and scale
       if (e < win) {
-        const int ring = (int)(((unsigned)I.first + (unsigned)e) % (unsigned)A.swa_cap);
-        wrec = A.swa + ((int64_t)I.seq * A.swa_cap + ring) * kSwaBytes;
+        const int ring = (int)(((unsigned)(ahead ? S.Q.first : I.first) + (unsigned)e) % (unsigned)A.swa_cap);
+        wrec = A.swa + ((int64_t)(ahead ? S.Q.seq : I.seq) * A.swa_cap + ring) * kSwaBytes;
         ws = __ldg(reinterpret_cast<const uint4 *>(wrec + 512));
       }
       window_dims(0);
@@ -418,6 +426,7 @@ __device__ __forceinline__ void paged_load(const PagedArgs &A, PagedShared &S, u
       if (lane == 0) ptx::mbar_arrive(&S.raw_free[k & 1]);
     };
     if (win > 0) {
+      if (ahead) paged_wait(A, S, &S.raw_full[0], 0);
       release();
 #pragma unroll 1
       for (int i = 0; i < 8; i++) {
@@ -1014,10 +1023,14 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
   }
   before += inc - mine;
   const int T = total, G = run_ctas(T, gridDim.x);
+  // g T / G, by the launch's reciprocal of its grid (T <= grid: G = T)
+  const int each = T > (int)gridDim.x ? (int)magic_div((unsigned)T, A.grid_mul, A.grid_shift) : min(T, 1);
+  const int over = T - each * G, snap = min(kPgSnap, each / kPgSnapRun);
+  auto border = [&](int g) { return g * each + (over > 0 ? (int)magic_div((unsigned)(g * over), A.grid_mul, A.grid_shift) : 0); };
 #pragma unroll
   for (int i = 0; i < 2; i++) {
     // the run's two ends
-    const int g = min((int)blockIdx.x + i, G), raw = T > 0 ? run_border(g, T, G) : 0;
+    const int g = min((int)blockIdx.x + i, G), raw = border(g);
     if (raw < T && before <= raw && raw < before + mine) {
       int o = before, q = u0;
       PagedQuery R = per == 1 ? own : paged_query(A, q);
@@ -1025,7 +1038,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
         o += R.chunks;
         R = paged_query(A, ++q);
       }
-      const int head = raw - o, tail = o + R.chunks - raw, snap = run_snap(T, G);
+      const int head = raw - o, tail = o + R.chunks - raw;
       int c = raw;
       if (head <= snap && head <= tail) {
         c = o;
@@ -1230,10 +1243,7 @@ cudaError_t launch_paged_attn(PagedArgs A, double rope_base, void *ws, cudaStrea
   if (e != cudaSuccess) return e;
   const int64_t sms = device_sm_count(dev);
   rope_turns(rope_base, A.turn);
-  int shift = 0;
-  while (((int64_t)1 << shift) < A.page) shift++;
-  A.page_shift = 31 + shift;
-  A.page_mul = (uint64_t)((((unsigned __int128)1 << A.page_shift) + (unsigned)A.page - 1) / (unsigned)A.page);
+  magic_of((unsigned)A.page, A.page_mul, A.page_shift);
   A.part = static_cast<float *>(ws);
   A.part_ml = A.part + 2 * (size_t)sms * kHeads * kDim;
   A.joins = reinterpret_cast<int4 *>(A.part_ml + 2 * (size_t)sms * 2 * kHeads);
@@ -1241,6 +1251,7 @@ cudaError_t launch_paged_attn(PagedArgs A, double rope_base, void *ws, cudaStrea
   const int64_t longest = A.sel != nullptr ? A.sel_stride : A.table_stride * A.page;
   const int64_t chunks = (int64_t)A.n_q * ((longest + kPgChunk - 1) / kPgChunk + (A.swa_cap > 0 ? 1 : 0));
   const unsigned grid = (unsigned)(chunks < sms ? (chunks < 1 ? 1 : chunks) : sms);
+  magic_of(grid, A.grid_mul, A.grid_shift);
   e = launch_pdl(paged_attn_kernel, dim3(grid), dim3(kPgThreads), (size_t)kPgSmAlloc, st, 1u, A);
   if (e != cudaSuccess || grid == 1) return e;
   // a query is cut at a border between two CTAs' runs

@@ -294,6 +294,8 @@ struct PagedArgs {
   uint64_t turn[32];
   uint64_t page_mul;          // j / page as (j * page_mul) >> page_shift
   int page_shift;
+  uint64_t grid_mul;          // the same for the number of CTAs
+  int grid_shift;
   float *part, *part_ml;      // split partials and their (maximum, denominator)
   int4 *joins;                // per CTA: the query whose partials are joined there
 };
