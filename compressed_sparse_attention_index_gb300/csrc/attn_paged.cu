@@ -46,7 +46,7 @@
 // through tensor memory (both operands in shared memory took 512 cycles more), and why
 // its rows are dequantised once (a second time for V cost more arithmetic than
 // everything else together).  8 x 1,048,576 entries: 1,200 us, 0.92 PFLOP/s; 32 x 65,536:
-// 333 us; 33 sequences of up to 40,001: 149 us; 40 queries x 512 selected: 41 us.
+// 331 us; 33 sequences of up to 40,001: 147 us; 40 queries x 512 selected: 38 us.
 // A few short rows are a chain of latencies: 18 us for one chunk each, the join included.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -1113,39 +1113,61 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
   }
 }
 
-// Joins a cut query's partials: grid (kHeads / HEADS, as many as queries can be cut),
-// 512 threads.  A thread has four of its head's 512 dims, so a partial's row is read as
-// 2 KB in one piece; 4 / HEADS groups of 128 threads share a head, each taking every
-// (4 / HEADS)-th partial with four loads in flight, and meet in shared memory.  Each
-// warp finds its head's weights 2^(m_s - max m) by itself, a lane to a partial.  All
-// sums have a fixed order, so the same inputs give the same bits.
-template <int HEADS>
-__global__ void __launch_bounds__(512) paged_join_kernel(const __grid_constant__ PagedArgs A, int n_ctas) {
-  constexpr int NG = 4 / HEADS;
+// Joins a cut query's partials: grid (kHeads, as many as queries can be cut), 128 NG
+// threads.  A thread has four of its head's 512 dims, so a partial's row is read as 2 KB
+// in one piece; NG groups of 128 threads each take every NG-th partial, with four loads in
+// flight, the first of them beside the weights', and meet in shared memory.  Each warp
+// finds its head's weights 2^(m_s - max m) by itself, a lane to a partial.  All sums have a
+// fixed order, so the same inputs give the same bits.  A chain of L2 trips and a matter of
+// waves: 40 registers hold 12 groups on an SM (at 50, 128 x 1,000 entries took 81 us
+// instead of 75).  NG = 1 ends its waves evenly (32 x 4,096: 50 us; NG = 2: 57, NG = 4: 76;
+// 8 x 4,096: 28, NG = 4: 31); a query or two, which do not fill the SMs, take NG = 4
+// (1 x 4,096, 33 partials: 20.3 us, NG = 1: 21.0).
+template <int NG>
+__global__ void __launch_bounds__(128 * NG, 12 / NG) paged_join_kernel(const __grid_constant__ PagedArgs A, int n_ctas) {
   __shared__ float4 sum_sh[NG > 1 ? NG : 1][128];
-  const int t = threadIdx.x, lane = t & 31, grp = NG > 1 ? t >> 7 : 0;
-  const int h = blockIdx.x * HEADS + (NG > 1 ? 0 : t >> 7), d = (t & 127) * 4;
+  const int t = threadIdx.x, lane = t & 31, grp = t >> 7;
+  const int h = blockIdx.x, d = (t & 127) * 4;
   griddep_wait();
   griddep_launch();
-  // the blockIdx.y-th CTA that names a cut query
-  int at = -1, left = (int)blockIdx.y;
-  for (int c0 = 0; c0 < n_ctas && at < 0; c0 += 256) {
-    int x[8];
+  // what the blockIdx.y-th CTA that names a cut query says: query, its chunks, its first chunk, all chunks
+  int4 J = make_int4(-1, 0, 0, 0);
+  int left = (int)blockIdx.y;
+  for (int c0 = 0; c0 < n_ctas && J.x < 0; c0 += 160) {
+    int4 x[5];
 #pragma unroll
-    for (int i = 0; i < 8; i++) x[i] = c0 + i * 32 + lane < n_ctas ? __ldcg(&A.joins[c0 + i * 32 + lane].x) : -1;
+    for (int i = 0; i < 5; i++) x[i] = c0 + i * 32 + lane < n_ctas ? __ldcg(A.joins + c0 + i * 32 + lane) : make_int4(-1, 0, 0, 0);
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      const uint32_t named = __ballot_sync(0xFFFFFFFFu, x[i] >= 0);
-      const uint32_t hit = __ballot_sync(0xFFFFFFFFu, x[i] >= 0 && __popc(named & ((1u << lane) - 1u)) == left);
-      if (at < 0 && hit != 0u) at = c0 + i * 32 + __ffs((int)hit) - 1;
+    for (int i = 0; i < 5; i++) {
+      const uint32_t named = __ballot_sync(0xFFFFFFFFu, x[i].x >= 0);
+      const uint32_t hit = __ballot_sync(0xFFFFFFFFu, x[i].x >= 0 && __popc(named & ((1u << lane) - 1u)) == left);
+      if (J.x < 0 && hit != 0u) {
+        const int from = __ffs((int)hit) - 1;
+        J.x = __shfl_sync(0xFFFFFFFFu, x[i].x, from);
+        J.y = __shfl_sync(0xFFFFFFFFu, x[i].y, from);
+        J.z = __shfl_sync(0xFFFFFFFFu, x[i].z, from);
+        J.w = __shfl_sync(0xFFFFFFFFu, x[i].w, from);
+      }
       left -= __popc(named);
     }
   }
-  if (at < 0) return;
-  const int4 J = __ldcg(A.joins + at);               // query, its chunks, its first chunk, all chunks
+  if (J.x < 0) return;
   const int qi = J.x, off = J.z, T = J.w, G = run_ctas(T, n_ctas);
   const int g0 = run_first_cut(off, T, G) - 1, g1 = run_last_cut(off, J.y, T, G);
   auto slot_of = [&](int g) { return 2 * (int64_t)g + (g == g0 ? 1 : 0); };
+  // four of the group's partials, from the i0-th of a batch on
+  auto rows = [&](int b0, int i0, float4 (&v)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const int i = i0 + j * NG;
+      v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < 32 && b0 + i <= g1)
+        v[j] = __ldcg(reinterpret_cast<const float4 *>(A.part + (slot_of(b0 + i) * kHeads + h) * kDim + d));
+    }
+  };
+  float4 v[4];
+  rows(g0, grp, v);                                  // (the first ones beside the weights)
+  bool ahead = true;
   float M = -kPgNoRef, m = -kPgNoRef;
   int b0 = g0;
   for (int b = g0; b <= g1; b += 32) {
@@ -1165,23 +1187,18 @@ __global__ void __launch_bounds__(512) paged_join_kernel(const __grid_constant__
       L += w * __ldcg(ml + kHeads);
     }
     for (int i0 = grp; i0 < 32 && b0 + i0 <= g1; i0 += 4 * NG) {
-      float4 v[4];
-      float u[4];
+      if (!ahead) rows(b0, i0, v);
+      ahead = false;
 #pragma unroll
       for (int j = 0; j < 4; j++) {
         const int i = i0 + j * NG;
-        u[j] = __shfl_sync(0xFFFFFFFFu, w, i & 31);
-        if (i >= 32) u[j] = 0.f;
-        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (u[j] != 0.f)                             // (a partial that met no entry weighs nothing)
-          v[j] = __ldcg(reinterpret_cast<const float4 *>(A.part + (slot_of(b0 + i) * kHeads + h) * kDim + d));
-      }
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        y.x = fmaf(u[j], v[j].x, y.x);
-        y.y = fmaf(u[j], v[j].y, y.y);
-        y.z = fmaf(u[j], v[j].z, y.z);
-        y.w = fmaf(u[j], v[j].w, y.w);
+        const float u = __shfl_sync(0xFFFFFFFFu, w, i & 31);
+        if (i < 32 && u != 0.f) {                    // (a partial that met no entry weighs nothing)
+          y.x = fmaf(u, v[j].x, y.x);
+          y.y = fmaf(u, v[j].y, y.y);
+          y.z = fmaf(u, v[j].z, y.z);
+          y.w = fmaf(u, v[j].w, y.w);
+        }
       }
     }
   }
@@ -1256,8 +1273,8 @@ cudaError_t launch_paged_attn(PagedArgs A, double rope_base, void *ws, cudaStrea
   if (e != cudaSuccess || grid == 1) return e;
   // a query is cut at a border between two CTAs' runs
   const unsigned cut = (unsigned)A.n_q < grid ? (unsigned)A.n_q : grid;
-  if (cut * kHeads <= 4 * sms) return launch_pdl(paged_join_kernel<1>, dim3(kHeads, cut), dim3(512), 0, st, 1u, A, (int)grid);
-  return launch_pdl(paged_join_kernel<4>, dim3(kHeads / 4, cut), dim3(512), 0, st, 1u, A, (int)grid);
+  if (cut * kHeads <= sms) return launch_pdl(paged_join_kernel<4>, dim3(kHeads, cut), dim3(512), 0, st, 1u, A, (int)grid);
+  return launch_pdl(paged_join_kernel<1>, dim3(kHeads, cut), dim3(128), 0, st, 1u, A, (int)grid);
 }
 
 }  // namespace csa2
