@@ -46,7 +46,7 @@
 // through tensor memory (both operands in shared memory took 512 cycles more), and why
 // its rows are dequantised once (a second time for V cost more arithmetic than
 // everything else together).  8 x 1,048,576 entries: 1,200 us, 0.92 PFLOP/s; 32 x 65,536:
-// 331 us; 33 sequences of up to 40,001: 147 us; 40 queries x 512 selected: 38 us.
+// 331 us; 33 sequences of up to 40,001: 147 us; 40 queries x 512 selected: 35 us.
 // A few short rows are a chain of latencies: 18 us for one chunk each, the join included.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -80,7 +80,7 @@ static_assert(kPgSmAlloc + 4608 <= 227 * 1024, "shared memory");
 constexpr uint32_t kPgColS = 0, kPgColO = 64, kPgColK = 320, kPgTmemCols = 512;
 constexpr float kPgRaise = 8.f, kPgShift = 7.f, kPgNoRef = 3e38f;   // (kPgNoRef: no entry met yet)
 constexpr int kPgScatter = 8;                      // pages of fewer entries are fetched as scattered records
-constexpr int kPgSnap = 2, kPgSnapRun = 2;
+constexpr int kPgSnap = 2, kPgSnapRun = 2, kPgSnapFew = 5;
 constexpr int kPgInfo = 8;                         // chunks described in shared memory at a time
 
 // Votes of the softmax group, at places that each of its warps reaches once a chunk.
@@ -134,14 +134,19 @@ __device__ __forceinline__ int run_ctas(int T, int grid) { return min(grid, max(
 // Chunks are dealt to G CTAs in runs of T / G (T below 2^31), but a border that falls
 // within `snap` chunks of an end of a query is moved there: a piece of a query costs a
 // CTA its Q, a window or a read-out and a partial of 128 KB for the join, about as much
-// as three chunks.  Longer runs move their borders further.
-__device__ __forceinline__ int run_snap(int T, int G) { return min(kPgSnap, T / (kPgSnapRun * G)); }
-// The first border that stays inside a query of n chunks from off, and the last one.
-__device__ __forceinline__ int run_first_cut(int off, int T, int G) {
-  return (int)((((int64_t)off + run_snap(T, G) + 1) * G + T - 1) / T);
+// as two chunks.  Up to half a run, and no more than two chunks (256 x 512 entries: 79 us,
+// 98 with none; 100 x 2,000: 83, three 89); one at least where a query's chunks are a
+// few runs only (40 x 512 selected, four runs a query: 33 us, none 36; but 24 x 1,000, six runs
+// a query: 31 instead of 28, and 8 x 4,096: 32 instead of 28).
+__device__ __forceinline__ int run_snap(int T, int G, int n_q) {
+  return T <= G ? 0 : min(kPgSnap, max(T / (kPgSnapRun * G), kPgSnapFew * n_q > G ? 1 : 0));
 }
-__device__ __forceinline__ int run_last_cut(int off, int n, int T, int G) {
-  return (int)((((int64_t)off + n - run_snap(T, G)) * G + T - 1) / T) - 1;
+// The first border that stays inside a query of n chunks from off, and the last one.
+__device__ __forceinline__ int run_first_cut(int off, int T, int G, int n_q) {
+  return (int)((((int64_t)off + run_snap(T, G, n_q) + 1) * G + T - 1) / T);
+}
+__device__ __forceinline__ int run_last_cut(int off, int n, int T, int G, int n_q) {
+  return (int)((((int64_t)off + n - run_snap(T, G, n_q)) * G + T - 1) / T) - 1;
 }
 
 // A position in a CTA's run of chunks.
@@ -894,7 +899,7 @@ __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S
     ptx::tc_fence_before();                          // (before the next query's PV, behind p_full)
     // the first CTA after the one that begins a cut query names it for the join (not by a
     // description that may be none)
-    if (t == 0 && !S.bad && lc0 > 0 && (int)blockIdx.x == run_first_cut(I.w, S.T, S.G))
+    if (t == 0 && !S.bad && lc0 > 0 && (int)blockIdx.x == run_first_cut(I.w, S.T, S.G, A.n_q))
       A.joins[blockIdx.x] = make_int4(I.x, I.z, I.w, S.T);
   }
 }
@@ -1025,7 +1030,8 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
   const int T = total, G = run_ctas(T, gridDim.x);
   // g T / G, by the launch's reciprocal of its grid (T <= grid: G = T)
   const int each = T > (int)gridDim.x ? (int)magic_div((unsigned)T, A.grid_mul, A.grid_shift) : min(T, 1);
-  const int over = T - each * G, snap = min(kPgSnap, each / kPgSnapRun);
+  const int over = T - each * G;
+  const int snap = T <= G ? 0 : min(kPgSnap, max(each / kPgSnapRun, kPgSnapFew * A.n_q > G ? 1 : 0));      // (run_snap)
   auto border = [&](int g) { return g * each + (over > 0 ? (int)magic_div((unsigned)(g * over), A.grid_mul, A.grid_shift) : 0); };
 #pragma unroll
   for (int i = 0; i < 2; i++) {
@@ -1153,7 +1159,7 @@ __global__ void __launch_bounds__(128 * NG, 12 / NG) paged_join_kernel(const __g
   }
   if (J.x < 0) return;
   const int qi = J.x, off = J.z, T = J.w, G = run_ctas(T, n_ctas);
-  const int g0 = run_first_cut(off, T, G) - 1, g1 = run_last_cut(off, J.y, T, G);
+  const int g0 = run_first_cut(off, T, G, A.n_q) - 1, g1 = run_last_cut(off, J.y, T, G, A.n_q);
   auto slot_of = [&](int g) { return 2 * (int64_t)g + (g == g0 ? 1 : 0); };
   // four of the group's partials, from the i0-th of a batch on
   auto rows = [&](int b0, int i0, float4 (&v)[4]) {
