@@ -163,13 +163,18 @@ class PagedCache:
 
     Tokens are numbered in sequence order.  Pages that run out, sequences beyond
     max_len and tokens beyond max_tokens are reported by csa2_get_device_status.
-    A token's window holds the last min(128, swa_cap) positions; a ring of
-    127 + the longest new_len records keeps the windows of all new tokens.
+    A token's window holds the last min(128, swa_cap) positions, and a step writes
+    the window records of all its tokens before it attends: the ring has to hold the
+    windows of all of them, 127 + the longest new_len records.  The default,
+    127 + max_tokens, holds those of any step; of a shorter ring (128 for single
+    tokens) a sequence whose new tokens would overwrite their own windows gets none,
+    which is reported as CSA2_ERR_BOUNDS (four small launches more in each plan).
     max_tokens is at most 65,535."""
 
-    def __init__(self, n_seq: int, n_pages: int, page_size: int, max_len: int, max_tokens: int, swa_cap: int = SWA,
+    def __init__(self, n_seq: int, n_pages: int, page_size: int, max_len: int, max_tokens: int, swa_cap: int = None,
                  out_dtype=L.CSA2_OUT_BF16, device="cuda"):
         self.n_seq, self.n_pages, self.page_size, self.max_tokens = n_seq, n_pages, page_size, max_tokens
+        swa_cap = SWA - 1 + max_tokens if swa_cap is None else swa_cap
         self.swa_cap, self.out_dtype = swa_cap, out_dtype
         i32 = dict(dtype=torch.int32, device=device)
         self.pages = torch.zeros((n_pages, page_size, 288), dtype=torch.uint8, device=device)
@@ -201,6 +206,13 @@ class PagedCache:
         if not new_len.is_contiguous():
             raise ValueError("new_len: contiguous int32 expected")
         self._want("new_len", new_len, self.n_seq, 1, torch.int32)
+        win = min(SWA, self.swa_cap)
+        if 0 < self.swa_cap < win - 1 + self.max_tokens:
+            # the first new token's window reaches back to min(win - 1, seq_len) positions before it, and its records
+            # are there when it is read where the ring has room for them and for all new tokens; a length that
+            # cannot be makes the plan report the sequence and give it no tokens
+            with torch.cuda.stream(stream):
+                new_len = new_len.masked_fill(new_len > self.swa_cap - self.seq_len.clamp(0, win - 1), -1)
         L.csa2_page_plan(self.seq_len, new_len, self.n_seq, self.page_size, self.n_pages, self.free, self.n_pages,
                          self.free_head, self.table, self.table.shape[1], self.swa_cap, self.desc, self.max_tokens,
                          self.first, self.totals, stream)

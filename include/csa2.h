@@ -482,9 +482,13 @@ csa2_status csa2_profile_events(void *begin, void *end);
  *                csa2_decode_host's h_desc rows.  Columns behind the last token
  *                get 0, 0, 0, 0, 0, -1, -1: queries that attend to nothing and
  *                write nothing.  Tokens from max_tokens on are dropped and record
- *                CSA2_ERR_BOUNDS.  A token that sees later tokens' window records
- *                in a ring too short for both (swa_cap < 127 + new_len) is the
- *                caller's to avoid.
+ *                CSA2_ERR_BOUNDS.  The windows are those of tokens whose window
+ *                records are written one after another; a caller that writes all of
+ *                a step's records before it attends needs a ring that holds them
+ *                beside the first token's window, new_len + min(seq_len, w - 1) <=
+ *                swa_cap for w = min(128, swa_cap), or the first tokens see later
+ *                ones.  The plan does not know the order and reports nothing;
+ *                decode.PagedCache gives such a sequence no tokens.
  *   first        (device) int32 [n_seq + 1]: the first token of each sequence,
  *                then the number of tokens (sums beyond 2^31 - 1 stay there).
  *   totals       (device) int32 [2]: the tokens, and the pages the step needs

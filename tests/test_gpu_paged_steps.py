@@ -1,0 +1,108 @@
+"""PagedCache over several steps against a plain restatement that keeps every
+sequence's records: steps that fit, and steps of which a part does not."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import paged_reference as R  # noqa: E402
+from parity import ATTN_TOL_F32, row_norm_err  # noqa: E402
+from test_gpu_paged import BOUNDS, _bits, _i32  # noqa: E402
+from test_gpu_paged_run import _inputs  # noqa: E402
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import compressed_sparse_attention_index_gb300 as c
+    return c
+
+
+class Sequences:
+    """A PagedCache (fp32 outputs) and what its sequences hold, record by record."""
+
+    def __init__(self, oracle_lib, n_seq, n_pages, page, max_len, max_tokens, cap=None):
+        import compressed_sparse_attention_index_gb300 as lib
+        from compressed_sparse_attention_index_gb300.decode import PagedCache
+        kw = {} if cap is None else {"swa_cap": cap}
+        self.c = PagedCache(n_seq, n_pages, page, max_len, max_tokens, out_dtype=lib.CSA2_OUT_F32, **kw)
+        self.lib, self.oracle, self.n_seq, self.page = lib, oracle_lib, n_seq, page
+        self.kv = [np.zeros((0, 288), np.uint8)] * n_seq
+        self.swa = [np.zeros((0, 528), np.uint8)] * n_seq
+        self.seed = 0
+
+    def step(self, new, kept=None, first=None, status=0, rows=None, every=1):
+        """A step of `new` tokens a sequence, of which kept[b] are written (the others in
+        status); first[b]: where sequence b's tokens begin in the step."""
+        kept = new if kept is None else kept
+        first = np.cumsum([0] + list(new))[:-1] if first is None else first
+        c, cap = self.c, self.c.swa_cap
+        self.seed += 1
+        q, lat = _inputs(c.max_tokens if rows is None else rows, self.seed)
+        out, lse = (x.cpu().numpy() for x in c.step(_i32(new), q, lat))
+        assert self.lib.csa2_get_device_status() == status
+        got_q, w = R.bf16_values(_bits(c.q)), min(128, cap)
+        dead = np.ones(len(out), bool)
+        for b, n in enumerate(kept):
+            held, t = len(self.kv[b]), first[b]
+            dead[t:t + new[b]] = False
+            if n == 0:
+                continue
+            bits = R.round_bf16_bits(R.norm_rope(lat[t:t + n].float().cpu().numpy(), None, held + np.arange(n), 1e-6))
+            self.kv[b] = np.concatenate([self.kv[b], self.oracle.pack_kv(bits)])
+            self.swa[b] = np.concatenate([self.swa[b], self.oracle.pack_swa(bits)])
+            for i in sorted({0, 1, n - 1, *range(0, n, every)}):
+                if i >= n:
+                    continue
+                vis = held + i + 1
+                k = np.concatenate([R.kv_values(self.kv[b][:vis]), R.swa_values(self.swa[b][max(0, vis - w):vis])])
+                o, le = R.attention(got_q[t + i], k, vis - 1)
+                assert row_norm_err(out[t + i], o) <= ATTN_TOL_F32, (b, i)
+                # fp32 sums of 512 products: 512 half steps of the sum of their magnitudes
+                room = 2.0**-15 * 512**-0.5 * (np.abs(got_q[t + i].astype(np.float64)) @ np.abs(k).T).max()
+                assert np.abs(lse[t + i] - le).max() <= room + 1e-6 + 2.0**-23 * np.abs(le).max()
+        assert np.all(out[dead] == 0) and np.all(np.isneginf(lse[dead]))
+        self.check_state()
+
+    def check_state(self):
+        """The lengths, the pages and the records of the main cache are the model's."""
+        n = [len(x) for x in self.kv]
+        cols = [-(-x // self.page) for x in n]
+        assert self.c.seq_len.tolist() == n and self.c.free_head.tolist() == [sum(cols)]
+        table = self.c.table.cpu().numpy()
+        ids = [int(i) for b in range(self.n_seq) for i in table[b, :cols[b]]]
+        assert len(set(ids)) == len(ids) and all(0 <= i < self.c.n_pages for i in ids)
+        pages = self.c.pages.cpu().numpy()
+        for b in range(self.n_seq):
+            j = np.arange(n[b])
+            assert np.array_equal(pages[table[b, j // self.page], j % self.page], self.kv[b])
+
+
+# ------------------------------------------------------------------ the window's ring
+def test_prompts_and_drafts_through_the_default_ring(lib, oracle_lib):
+    """Every token of a step sees its own window: prompts longer than a window, drafts behind a full one."""
+    s = Sequences(oracle_lib, 3, 60, 16, 500, 210)
+    for new in ([200, 1, 0], [2, 5, 3], [1, 1, 1], [64, 0, 140], [2, 2, 2]):
+        s.step(new)
+
+
+@pytest.mark.parametrize("cap", [128, 150, 64, 1])
+def test_a_ring_too_short_for_a_sequences_tokens(lib, oracle_lib, cap):
+    """A sequence whose step would overwrite its own windows gets no tokens and is reported; the others go on."""
+    w, s = min(128, cap), Sequences(oracle_lib, 3, 60, 16, 500, 3 * cap + 5, cap)
+    s.step([cap + 1, cap, 1], [0, cap, 1], [0, 0, cap], BOUNDS)      # (from nothing, a ring of tokens is well)
+    s.step([1, 1, 1])
+    many = cap + 1 - w                                                # what a full window leaves room for
+    s.step([many, many, many])
+    if cap > 1:
+        s.step([0, many + 1, 1], [0, 0, 1], [0, 0, 0], BOUNDS)
+        s.step([2**31 - 1, 0, 0], [0, 0, 0], [0, 0, 0], BOUNDS)
+    s.step([1, 1, 1])
+
+
+def test_a_cache_without_a_window(lib, oracle_lib):
+    s = Sequences(oracle_lib, 2, 60, 16, 500, 210, 0)
+    s.step([200, 3])
+    s.step([1, 40])
+
+
