@@ -130,8 +130,10 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
       v[3] = P.swa_cap > 0 ? (int)((unsigned)(pos + 1 - cnt) % (unsigned)P.swa_cap) : 0;
       v[4] = cnt;
       v[5] = id < 0 ? -1 : id * P.page + (pos - col * P.page);
-      // a ring slot that a later token of this step takes again is not written
-      v[6] = P.swa_cap > 0 && (int64_t)pos + P.swa_cap >= (int64_t)len + add
+      // a ring slot that a later token of this step takes again is not written (a token
+      // without a descriptor takes none)
+      const int kept = min(add, P.max_tokens - tok[b]);
+      v[6] = P.swa_cap > 0 && (int64_t)pos + P.swa_cap >= (int64_t)len + kept
                  ? b * P.swa_cap + (int)((unsigned)pos % (unsigned)P.swa_cap)
                  : -1;
     }

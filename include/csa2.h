@@ -478,7 +478,7 @@ csa2_status csa2_profile_events(void *begin, void *end);
  *                pos; the window's first ring slot and length (swa_first,
  *                swa_cnt = min(128, swa_cap, pos + 1)); its slot in the main
  *                cache; its slot in the window cache, or -1 where a later token
- *                of the same step takes the same ring slot.  Rows 0 .. 4 are
+ *                of the same step (one below max_tokens) takes the same ring slot.  Rows 0 .. 4 are
  *                csa2_decode_host's h_desc rows.  Columns behind the last token
  *                get 0, 0, 0, 0, 0, -1, -1: queries that attend to nothing and
  *                write nothing.  Tokens from max_tokens on are dropped and record

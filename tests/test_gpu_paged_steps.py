@@ -106,3 +106,21 @@ def test_a_cache_without_a_window(lib, oracle_lib):
     s.step([1, 40])
 
 
+def test_tokens_without_a_descriptor_take_no_ring_slot(lib):
+    """A token keeps its window record where only dropped tokens would have taken its slot."""
+    cap, rows = 32, 20
+    desc = torch.full((7, rows), -77, dtype=torch.int32, device="cuda")
+    first, totals = torch.empty(3, dtype=torch.int32, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda")
+    table = _i32(np.arange(60).reshape(2, 30))
+    lib.csa2_page_plan(_i32([10, 300]), _i32([5, 60]), 2, 16, 64, _i32(range(60, 64)), 4, None, table, 30, cap, desc, rows, first, totals)
+    assert lib.csa2_get_device_status() == BOUNDS
+    pos = np.concatenate([np.arange(10, 15), np.arange(300, 315)])
+    assert desc[2].tolist() == pos.tolist() and first.tolist() == [0, 5, 65]
+    assert desc[6].tolist() == [(0 if i < 5 else cap) + p % cap for i, p in enumerate(pos)]
+    # 40 rows: tokens 300 .. 334, of which 300 .. 302 give way to 332 .. 334
+    desc = torch.full((7, 40), -77, dtype=torch.int32, device="cuda")
+    lib.csa2_page_plan(_i32([10, 300]), _i32([5, 60]), 2, 16, 64, _i32(range(60, 64)), 4, None, table, 30, cap, desc, 40, first, totals)
+    assert lib.csa2_get_device_status() == BOUNDS
+    assert desc[6][5:].tolist() == [-1] * 3 + [cap + p % cap for p in range(303, 335)]
+
+
