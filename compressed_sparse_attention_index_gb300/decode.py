@@ -162,7 +162,9 @@ class PagedCache:
     inputs are read where they lie.
 
     Tokens are numbered in sequence order.  Pages that run out, sequences beyond
-    max_len and tokens beyond max_tokens are reported by csa2_get_device_status.
+    max_len and tokens beyond max_tokens are reported by csa2_get_device_status; a
+    token that got no page or no row writes nothing and is not part of its sequence
+    afterwards, nor is a page taken that no token was written to.
     A token's window holds the last min(128, swa_cap) positions, and a step writes
     the window records of all its tokens before it attends: the ring has to hold the
     windows of all of them, 127 + the longest new_len records.  The default,
@@ -180,12 +182,20 @@ class PagedCache:
         self.pages = torch.zeros((n_pages, page_size, 288), dtype=torch.uint8, device=device)
         self.swa = torch.zeros((n_seq, swa_cap, 528), dtype=torch.uint8, device=device)
         self.table = torch.full((n_seq, -(-max_len // page_size)), -1, **i32)
-        self.seq_len = torch.zeros(n_seq, **i32)
+        # the sequences' lengths and, behind them, the pages taken: what a step adds to
+        self._state = torch.zeros(n_seq + 1, **i32)
+        self.seq_len, self.free_head = self._state[:n_seq], self._state[n_seq:]
         self.free = torch.arange(n_pages, **i32)
-        self.free_head = torch.zeros(1, **i32)
-        self.desc = torch.empty((7, max_tokens), **i32)
-        self.first = torch.empty(n_seq + 1, **i32)
-        self.totals = torch.empty(2, **i32)
+        # the descriptors' rows (no token anywhere before the first plan), and a row ahead of them that names free_head's
+        # place in the state as q_seq names seq_len's
+        self._desc = torch.zeros((8, max_tokens), **i32)
+        self._desc[0] = n_seq
+        self._desc[6:] = -1
+        self.desc = self._desc[1:]
+        added = torch.empty((2, max_tokens), **i32)
+        self._count = self._desc[:2].view(-1), added.view(-1), added[0], added[1], self.desc[5]
+        self.first = torch.zeros(n_seq + 1, **i32)
+        self.totals = torch.zeros(2, **i32)
         self.q = torch.empty((max_tokens, 64, 512), dtype=torch.bfloat16, device=device)
         self.latent = torch.empty((max_tokens, 512), dtype=torch.bfloat16, device=device)
         odt = torch.bfloat16 if out_dtype == L.CSA2_OUT_BF16 else torch.float32
@@ -246,10 +256,20 @@ class PagedCache:
         return self.out, self.lse
 
     def advance(self, stream=None):
-        """The planned tokens become part of the sequences, their pages are taken."""
-        with torch.cuda.stream(stream):
-            self.seq_len += self.first[1:] - self.first[:-1]
-            self.free_head += self.totals[1:]
+        """The tokens that were written become part of the sequences, the pages that they are on are taken."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.advance()
+        # a token with a slot counts as one of its sequence; where the slot is a page's first, as a page.  (Slots end
+        # within a sequence, pages of the free list within a step, so what is counted comes first in both.)
+        place, add, pages, tokens, slot = self._count
+        torch.ge(slot, 0, out=tokens)
+        if self.page_size > 1:
+            torch.remainder(slot, self.page_size, out=pages)           # (-1: a page's last place)
+            torch.eq(pages, 0, out=pages)
+        else:
+            pages.copy_(tokens)
+        self._state.index_add_(0, place, add)
 
     def step(self, new_len, q, latent, q_gain=None, latent_gain=None, eps=1e-6, sel=None, params=None, stream=None):
         self.plan(new_len, stream)

@@ -124,3 +124,33 @@ def test_tokens_without_a_descriptor_take_no_ring_slot(lib):
     assert desc[6][5:].tolist() == [-1] * 3 + [cap + p % cap for p in range(303, 335)]
 
 
+# ------------------------------------------------------------------ what a step commits
+@pytest.mark.parametrize("page", [16, 1, 7])
+def test_steps_beyond_the_last_page(lib, oracle_lib, page):
+    """Tokens without a page are reported and not part of their sequences; what comes after sees the others alone."""
+    n_pages = -(-10 // page) + -(-16 // page) + -(-22 // page) - -(-10 // page)
+    s = Sequences(oracle_lib, 2, n_pages, page, 100, 40)
+    s.step([10, 16])
+    s.step([12, 9], [12, -(-16 // page) * page - 16], status=BOUNDS)
+    room = -(-22 // page) * page - 22
+    s.step([min(room, 3), 0])
+    s.step([0, 9], [0, 0], status=BOUNDS)
+    s.step([0, 0])
+
+
+def test_steps_of_more_tokens_than_rows(lib, oracle_lib):
+    s = Sequences(oracle_lib, 3, 60, 16, 300, 40)
+    s.step([30, 200, 1], [30, 10, 0], status=BOUNDS)
+    s.step([1, 1, 1])
+    s.step([0, 41, 5], [0, 40, 0], status=BOUNDS)
+    s.step([20, 10, 10])
+
+
+def test_a_sequence_beyond_its_row_of_the_table(lib, oracle_lib):
+    s = Sequences(oracle_lib, 2, 60, 16, 32, 40)
+    s.step([30, 5])
+    s.step([3, 5], [0, 5], [0, 0], BOUNDS)
+    s.step([2, 5])
+    s.step([1, 5], [0, 5], [0, 0], BOUNDS)
+
+

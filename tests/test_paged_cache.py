@@ -1,0 +1,48 @@
+"""PagedCache's own bookkeeping, on the CPU: what a step commits."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from tests import paged_reference as R
+
+
+@pytest.fixture(scope="module")
+def cache():
+    from compressed_sparse_attention_index_gb300.decode import PagedCache
+    return lambda *a, **k: PagedCache(*a, device="cpu", **k)
+
+
+@pytest.mark.parametrize("n_seq,n_pages,page,max_len,rows,seed", [(3, 20, 16, 100, 40, 0), (5, 9, 4, 60, 16, 1), (2, 30, 1, 50, 25, 2),
+                                                                  (1, 6, 7, 40, 8, 3), (9, 12, 8, 64, 64, 4)])
+def test_advance_by_what_was_written(cache, n_seq, n_pages, page, max_len, rows, seed):
+    """Steps that fit, run out of pages, of rows and of their table's row: lengths, pages and the free list's head."""
+    c = cache(n_seq, n_pages, page, max_len, rows)
+    r = np.random.default_rng(seed)
+    lens, head, table = np.zeros(n_seq, np.int64), 0, np.full(c.table.shape, -1)
+    reported = 0
+    for _ in range(60):
+        new = r.integers(0, 1 + 2 * rows // n_seq, n_seq) * (r.random(n_seq) < 0.6)
+        desc, first, totals, planned, fine = R.plan(lens, new, page, n_pages, np.arange(n_pages), head, table, c.swa_cap, rows)
+        c.desc.copy_(torch.from_numpy(desc.astype(np.int32)))
+        c.first.copy_(torch.from_numpy(first.astype(np.int32))), c.totals.copy_(torch.from_numpy(totals.astype(np.int32)))
+        c.advance()
+        reported += not fine
+        for b in range(n_seq):
+            kept = [t for t in range(first[b], min(first[b + 1], rows)) if desc[5][t] >= 0]
+            assert kept == list(range(first[b], first[b] + len(kept)))
+            before, lens[b] = lens[b], lens[b] + len(kept)
+            cols = range(-(-before // page), -(-lens[b] // page))
+            for col in cols:
+                assert planned[b, col] == head      # the free list names the pages in order
+                table[b, col] = head
+                head += 1
+        assert c.seq_len.tolist() == lens.tolist() and c.free_head.tolist() == [head]
+    assert 0 < reported < 60
+
+
+def test_a_cache_without_a_plan_holds_no_tokens(cache):
+    c = cache(3, 8, 1, 64, 5)
+    assert c.desc.tolist() == [[0] * 5] * 5 + [[-1] * 5] * 2 and c.first.tolist() == [0] * 4 and c.totals.tolist() == [0, 0]
+    c.advance()
+    assert c.seq_len.tolist() == [0, 0, 0] and c.free_head.tolist() == [0]
