@@ -159,7 +159,10 @@ class PagedCache:
     attend and advance, or step, which is all four.  Everything stays on the
     device and on one stream (the current one, or `stream`, a torch.cuda.Stream),
     so a step can be captured into a CUDA graph and replayed: new_len and the
-    inputs are read where they lie.
+    inputs are read where they lie.  A new cache is whole when its constructor returns
+    (it waits for its fills); from then on the order of calls on different streams is the
+    caller's, and so is the cache's life until work on other streams than the
+    constructor's is over.
 
     Tokens are numbered in sequence order.  Pages that run out, sequences beyond
     max_len and tokens beyond max_tokens are reported by csa2_get_device_status; a
@@ -203,6 +206,9 @@ class PagedCache:
         self.lse = torch.empty((max_tokens, 64), dtype=torch.float32, device=device)
         self.ws = torch.empty(L.csa2_workspace_size(L.CSA2_OP_PAGED_ATTN, max_tokens, 0), dtype=torch.uint8,
                               device=device)
+        # the fills above ran on the current stream, the steps may run on any
+        if self.pages.is_cuda and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self.pages.device).synchronize()
 
     def _want(self, name, x, rows, cols, dtype):
         """x: rows of `cols` elements (any stride between rows), on the cache's device."""

@@ -154,3 +154,21 @@ def test_a_sequence_beyond_its_row_of_the_table(lib, oracle_lib):
     s.step([1, 5], [0, 5], [0, 0], BOUNDS)
 
 
+# ------------------------------------------------------------------ streams
+def test_a_new_cache_is_whole_on_every_stream(lib):
+    """The constructor's fills, behind whatever its stream holds, are over when it returns."""
+    from compressed_sparse_attention_index_gb300.decode import PagedCache
+    a = torch.ones((8192, 8192), dtype=torch.bfloat16, device="cuda")
+    new, ins = _i32([3, 1]), _inputs(8, 1)
+    want = [x.clone() for x in PagedCache(2, 30, 16, 200, 8).step(new, *ins)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        a @ a
+    c = PagedCache(2, 200_000, 16, 200, 8)                            # 0.9 GB of pages
+    assert torch.cuda.current_stream().query()
+    s = torch.cuda.Stream()
+    got = c.step(new, *ins, stream=s)
+    s.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want, got)) and lib.csa2_get_device_status() == 0
+
+
