@@ -156,7 +156,9 @@ class DecoderStep:
 class PagedCache:
     """A main cache in pages and a window ring for n_seq sequences, with the
     buffers of a step of up to max_tokens new tokens.  A step is plan, write,
-    attend and advance, or step, which is all four.  Everything stays on the
+    attend and advance, or step, which is all four.  It works on as many rows as its
+    inputs have, or as plan is told (max_tokens otherwise): a step of a few tokens
+    costs that of a few rows, whatever max_tokens is.  Everything stays on the
     device and on one stream (the current one, or `stream`, a torch.cuda.Stream),
     so a step can be captured into a CUDA graph and replayed: new_len and the
     inputs are read where they lie.  A new cache is whole when its constructor returns
@@ -189,14 +191,12 @@ class PagedCache:
         self._state = torch.zeros(n_seq + 1, **i32)
         self.seq_len, self.free_head = self._state[:n_seq], self._state[n_seq:]
         self.free = torch.arange(n_pages, **i32)
-        # the descriptors' rows (no token anywhere before the first plan), and a row ahead of them that names free_head's
-        # place in the state as q_seq names seq_len's
-        self._desc = torch.zeros((8, max_tokens), **i32)
-        self._desc[0] = n_seq
-        self._desc[6:] = -1
-        self.desc = self._desc[1:]
-        added = torch.empty((2, max_tokens), **i32)
-        self._count = self._desc[:2].view(-1), added.view(-1), added[0], added[1], self.desc[5]
+        # the descriptors of a step of r rows, [7][r] (no token anywhere before the first plan), and ahead of them r
+        # entries that name free_head's place in the state as q_seq names seq_len's
+        self._desc = torch.full((8 * max_tokens,), n_seq, **i32)
+        self._desc[max_tokens:6 * max_tokens] = 0
+        self._desc[6 * max_tokens:] = -1
+        self._added = torch.empty(2 * max_tokens, **i32)
         self.first = torch.zeros(n_seq + 1, **i32)
         self.totals = torch.zeros(2, **i32)
         self.q = torch.empty((max_tokens, 64, 512), dtype=torch.bfloat16, device=device)
@@ -209,6 +209,19 @@ class PagedCache:
         # the fills above ran on the current stream, the steps may run on any
         if self.pages.is_cuda and not torch.cuda.is_current_stream_capturing():
             torch.cuda.current_stream(self.pages.device).synchronize()
+        self._views = {}
+        self._use_rows(max_tokens)
+
+    def _use_rows(self, rows):
+        """The descriptors, buffers and counters of a step of `rows` rows."""
+        v = self._views.get(rows)
+        if v is None:
+            at = self.max_tokens
+            desc, added = self._desc[at:at + 7 * rows].view(7, rows), self._added[:2 * rows].view(2, rows)
+            v = self._views[rows] = (desc, desc.unbind(), (self._desc[at - rows:at + rows], added.view(-1), *added.unbind()),
+                                     (self.out[:rows], self.lse[:rows]))
+        self.rows = rows
+        self.desc, self._d, self._count, self._rows = v
 
     def _want(self, name, x, rows, cols, dtype):
         """x: rows of `cols` elements (any stride between rows), on the cache's device."""
@@ -217,8 +230,12 @@ class PagedCache:
             raise ValueError(f"{name}: {rows} rows of {cols} contiguous {dtype} on {self.seq_len.device} expected, "
                              f"not {tuple(x.shape)} {x.dtype} on {x.device}")
 
-    def plan(self, new_len, stream=None):
-        """Pages, slots and descriptors for new_len (device int32 [n_seq]) new tokens per sequence."""
+    def plan(self, new_len, stream=None, rows=None):
+        """Pages, slots and descriptors for new_len (device int32 [n_seq]) new tokens per sequence, in a step of `rows`
+        rows (max_tokens at most, and by default)."""
+        rows = self.max_tokens if rows is None else rows
+        if not 0 <= rows <= self.max_tokens:
+            raise ValueError(f"rows: 0 .. {self.max_tokens} expected, not {rows}")
         if not new_len.is_contiguous():
             raise ValueError("new_len: contiguous int32 expected")
         self._want("new_len", new_len, self.n_seq, 1, torch.int32)
@@ -229,37 +246,39 @@ class PagedCache:
             # cannot be makes the plan report the sequence and give it no tokens
             with torch.cuda.stream(stream):
                 new_len = new_len.masked_fill(new_len > self.swa_cap - self.seq_len.clamp(0, win - 1), -1)
+        self._use_rows(rows)
         L.csa2_page_plan(self.seq_len, new_len, self.n_seq, self.page_size, self.n_pages, self.free, self.n_pages,
-                         self.free_head, self.table, self.table.shape[1], self.swa_cap, self.desc, self.max_tokens,
-                         self.first, self.totals, stream)
+                         self.free_head, self.table, self.table.shape[1], self.swa_cap, self.desc, rows, self.first,
+                         self.totals, stream)
 
     def write(self, q, latent, q_gain=None, latent_gain=None, eps=1e-6, params=None, stream=None):
-        """Norm and rotation of the planned tokens' queries (bf16 [max_tokens][64][512]) and latents
-        ([max_tokens][512]), into self.q and self.latent, and the latents' records into the caches."""
-        self._want("q", q, self.max_tokens, 64 * 512, torch.bfloat16)
-        self._want("latent", latent, self.max_tokens, 512, torch.bfloat16)
+        """Norm and rotation of the planned tokens' queries (bf16 [rows][64][512]) and latents
+        ([rows][512]), into self.q and self.latent, and the latents' records into the caches."""
+        self._want("q", q, self.rows, 64 * 512, torch.bfloat16)
+        self._want("latent", latent, self.rows, 512, torch.bfloat16)
         for gain in (q_gain, latent_gain):
             if gain is not None:
                 self._want("gain", gain.reshape(-1, 1), 512, 1, torch.float32)
                 if not gain.is_contiguous():
                     raise ValueError("gain: contiguous fp32 expected")
-        L.csa2_qk_norm_rope(q, q.stride(0), q_gain, self.q, latent, latent.stride(0), latent_gain, self.latent,
-                            self.desc[2], self.desc[5], self.desc[6], self.max_tokens, eps, self.pages,
-                            self.n_pages * self.page_size, self.swa, self.n_seq * self.swa_cap, params, stream)
+        d = self._d
+        L.csa2_qk_norm_rope(q, q.stride(0), q_gain, self.q, latent, latent.stride(0), latent_gain, self.latent, d[2],
+                            d[5], d[6], self.rows, eps, self.pages, self.n_pages * self.page_size, self.swa,
+                            self.n_seq * self.swa_cap, params, stream)
 
     def attend(self, sel=None, params=None, stream=None):
-        """(output [max_tokens][64][512], lse [max_tokens][64]) of the planned tokens, over all that they see
-        or over sel (device int32 [max_tokens][k]); places without a token get zeros and -inf."""
+        """(output [rows][64][512], lse [rows][64]) of the planned tokens, over all that they see or over sel (device
+        int32 [rows][k]); rows without a token get zeros and -inf, those behind the step's are left as they were."""
         if sel is not None:
             if not sel.is_contiguous():
                 raise ValueError("sel: contiguous int32 expected")
-            self._want("sel", sel, self.max_tokens, sel.shape[1], torch.int32)
-        d = self.desc
+            self._want("sel", sel, self.rows, sel.shape[1], torch.int32)
+        d = self._d
         L.csa2_paged_attn(self.q, self.pages, self.n_pages, self.page_size, self.table, self.table.shape[1],
                           self.n_seq, sel, 0 if sel is None else sel.shape[1], self.swa, self.swa_cap, d[0], d[1],
-                          d[2], d[3], d[4], self.max_tokens, self.out, self.out_dtype, self.lse, params, self.ws,
+                          d[2], d[3], d[4], self.rows, self.out, self.out_dtype, self.lse, params, self.ws,
                           self.ws.numel(), stream)
-        return self.out, self.lse
+        return self._rows
 
     def advance(self, stream=None):
         """The tokens that were written become part of the sequences, the pages that they are on are taken."""
@@ -268,7 +287,7 @@ class PagedCache:
                 return self.advance()
         # a token with a slot counts as one of its sequence; where the slot is a page's first, as a page.  (Slots end
         # within a sequence, pages of the free list within a step, so what is counted comes first in both.)
-        place, add, pages, tokens, slot = self._count
+        (place, add, pages, tokens), slot = self._count, self._d[5]
         torch.ge(slot, 0, out=tokens)
         if self.page_size > 1:
             torch.remainder(slot, self.page_size, out=pages)           # (-1: a page's last place)
@@ -278,7 +297,8 @@ class PagedCache:
         self._state.index_add_(0, place, add)
 
     def step(self, new_len, q, latent, q_gain=None, latent_gain=None, eps=1e-6, sel=None, params=None, stream=None):
-        self.plan(new_len, stream)
+        """plan, write, attend and advance on as many rows as q and latent have."""
+        self.plan(new_len, stream, q.shape[0])
         self.write(q, latent, q_gain, latent_gain, eps, params, stream)
         out = self.attend(sel, params, stream)
         self.advance(stream)

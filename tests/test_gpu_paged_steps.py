@@ -172,3 +172,49 @@ def test_a_new_cache_is_whole_on_every_stream(lib):
     assert all(torch.equal(x, y) for x, y in zip(want, got)) and lib.csa2_get_device_status() == 0
 
 
+# ------------------------------------------------------------------ rows
+def test_a_step_works_on_the_rows_it_is_given(lib, oracle_lib):
+    """A cache for long prompts steps a few tokens on a few rows: the bits of a small cache, the rows behind untouched."""
+    from compressed_sparse_attention_index_gb300.decode import PagedCache
+    big, small = PagedCache(4, 60, 16, 300, 512, 640), PagedCache(4, 60, 16, 300, 8, 640)
+    for k, new in enumerate([[2, 1, 4, 1], [1, 1, 1, 1], [0, 3, 0, 0]]):
+        for x in (big.out, big.lse, big.q, big.latent):
+            x.fill_(7.0)
+        q, lat = _inputs(8, k)
+        got, want = big.step(_i32(new), q, lat), small.step(_i32(new), q, lat)
+        for x, y in zip(got, want):
+            assert x.shape == y.shape and torch.equal(x, y)
+        assert torch.equal(big.desc, small.desc) and torch.equal(big.first, small.first)
+        for x in (big.out, big.lse, big.q, big.latent):
+            assert bool((x[8:] == 7.0).all())
+    # a step of another number of rows, a captured one, a longer one again
+    s = Sequences(oracle_lib, 3, 60, 16, 300, 200)
+    s.step([40, 1, 100], rows=150)
+    s.step([1, 1, 1], rows=3)
+    s.step([5, 0, 60])
+    s.step([1, 3, 1], [1, 2, 0], status=BOUNDS, rows=3)
+    assert torch.equal(big.seq_len, small.seq_len) and torch.equal(big.pages, small.pages)
+
+
+def test_a_step_of_a_few_rows_captured(lib):
+    from compressed_sparse_attention_index_gb300.decode import PagedCache
+    a, b = PagedCache(3, 60, 16, 300, 64), PagedCache(3, 60, 16, 300, 64)
+    x, y = _inputs(64, 5)
+    for c in (a, b):
+        c.step(_i32([40, 3, 20]), x, y)
+    new, q, lat = _i32([0, 0, 0]), *_inputs(3, 6)
+    b.step(new, q, lat)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.step(new, q, lat)
+    for k in range(3):
+        n, (u, v) = _i32([1, k % 2, 1]), _inputs(3, 10 + k)
+        want = a.step(n, u, v)
+        new.copy_(n), q.copy_(u), lat.copy_(v)
+        graph.replay()
+        assert torch.equal(want[0], b.out[:3]) and torch.equal(want[1], b.lse[:3])
+    torch.cuda.synchronize()
+    assert torch.equal(a.seq_len, b.seq_len) and torch.equal(a.pages, b.pages) and lib.csa2_get_device_status() == 0
+
+

@@ -46,3 +46,25 @@ def test_a_cache_without_a_plan_holds_no_tokens(cache):
     assert c.desc.tolist() == [[0] * 5] * 5 + [[-1] * 5] * 2 and c.first.tolist() == [0] * 4 and c.totals.tolist() == [0, 0]
     c.advance()
     assert c.seq_len.tolist() == [0, 0, 0] and c.free_head.tolist() == [0]
+
+
+def test_rows_of_a_step(cache):
+    """Inputs have as many rows as the step was planned for; the views of a step of r rows are those of a cache of r."""
+    c, d = cache(3, 8, 16, 64, 5), cache(3, 8, 16, 64, 2)
+    with pytest.raises(ValueError):
+        c.plan(torch.zeros(3, dtype=torch.int32), rows=6)
+    with pytest.raises(ValueError):
+        c.plan(torch.zeros(3, dtype=torch.int32), rows=-1)
+    with pytest.raises(ValueError):
+        c.step(torch.zeros(3, dtype=torch.int32), torch.zeros((6, 64, 512), dtype=torch.bfloat16), torch.zeros((6, 512), dtype=torch.bfloat16))
+    c._use_rows(2)                                        # (as plan does)
+    assert c.desc.shape == (7, 2) and c.desc.is_contiguous()
+    desc = torch.tensor([[0, 2], [1, 1], [0, 0], [0, 0], [1, 1], [0, 16], [0, 256]], dtype=torch.int32)
+    for x in (c, d):
+        x.desc.copy_(desc)
+        x.advance()
+        assert x.seq_len.tolist() == [1, 0, 1] and x.free_head.tolist() == [2]
+    with pytest.raises(ValueError):
+        c.write(torch.zeros((5, 64, 512), dtype=torch.bfloat16), torch.zeros((5, 512), dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        c.attend(torch.zeros((5, 8), dtype=torch.int32))
