@@ -306,9 +306,9 @@ class PagedCache:
 
     def read(self, slots, out, stream=None):
         """Latents of the main cache's records `slots` (device int32, as in desc[5]) into out, bf16 or fp32 [n][512]."""
-        if not slots.is_contiguous() or slots.dtype != torch.int32 or not out.is_contiguous() or \
-                out.dtype not in (torch.bfloat16, torch.float32):
-            raise ValueError("read: contiguous int32 slots and contiguous bf16 or fp32 out expected")
+        if not slots.is_contiguous() or slots.dtype != torch.int32 or slots.device != self.seq_len.device or \
+                not out.is_contiguous() or out.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("read: contiguous int32 slots on the cache's device and contiguous bf16 or fp32 out expected")
         self._want("out", out, slots.numel(), 512, out.dtype)
         L.csa2_cache_read(L.CSA2_KV_NVFP4, self.pages, self.n_pages * self.page_size, slots, slots.numel(), out,
                           L.CSA2_OUT_F32 if out.dtype == torch.float32 else L.CSA2_OUT_BF16, stream)

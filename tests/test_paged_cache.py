@@ -68,3 +68,12 @@ def test_rows_of_a_step(cache):
         c.write(torch.zeros((5, 64, 512), dtype=torch.bfloat16), torch.zeros((5, 512), dtype=torch.bfloat16))
     with pytest.raises(ValueError):
         c.attend(torch.zeros((5, 8), dtype=torch.int32))
+
+
+def test_slots_elsewhere_are_refused(cache):
+    """Slots have to lie on the cache's device: the kernel reads them there."""
+    c = cache(3, 8, 16, 64, 5)
+    with pytest.raises(ValueError):
+        c.read(torch.zeros(6, dtype=torch.int32, device="meta"), torch.zeros((6, 512)))
+    with pytest.raises(ValueError):
+        c.read(torch.zeros(6, dtype=torch.int32), torch.zeros((6, 512), device="meta"))
