@@ -261,10 +261,12 @@ class PagedCache:
                 self._want("gain", gain.reshape(-1, 1), 512, 1, torch.float32)
                 if not gain.is_contiguous():
                     raise ValueError("gain: contiguous fp32 expected")
+        # (a single row's stride may be anything)
+        q_stride, stride = (q.stride(0), latent.stride(0)) if self.rows > 1 else (64 * 512, 512)
         d = self._d
-        L.csa2_qk_norm_rope(q, q.stride(0), q_gain, self.q, latent, latent.stride(0), latent_gain, self.latent, d[2],
-                            d[5], d[6], self.rows, eps, self.pages, self.n_pages * self.page_size, self.swa,
-                            self.n_seq * self.swa_cap, params, stream)
+        L.csa2_qk_norm_rope(q, q_stride, q_gain, self.q, latent, stride, latent_gain, self.latent, d[2], d[5], d[6],
+                            self.rows, eps, self.pages, self.n_pages * self.page_size, self.swa, self.n_seq * self.swa_cap,
+                            params, stream)
 
     def attend(self, sel=None, params=None, stream=None):
         """(output [rows][64][512], lse [rows][64]) of the planned tokens, over all that they see or over sel (device

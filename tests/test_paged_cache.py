@@ -77,3 +77,15 @@ def test_slots_elsewhere_are_refused(cache):
         c.read(torch.zeros(6, dtype=torch.int32, device="meta"), torch.zeros((6, 512)))
     with pytest.raises(ValueError):
         c.read(torch.zeros(6, dtype=torch.int32), torch.zeros((6, 512), device="meta"))
+
+
+def test_a_single_row_of_any_stride(cache, monkeypatch):
+    """A step of one row: the stride to a next row, which there is not, may be anything."""
+    from compressed_sparse_attention_index_gb300 import decode
+    seen = []
+    monkeypatch.setattr(decode.L, "csa2_qk_norm_rope", lambda *a: seen.append((a[1], a[5])))
+    c = cache(1, 8, 16, 64, 1)
+    q, lat = torch.zeros((64, 1, 512), dtype=torch.bfloat16).transpose(0, 1), torch.zeros((512, 1), dtype=torch.bfloat16).t()
+    assert q.stride(0) == 512 and lat.stride(0) == 1
+    c.write(q, lat)
+    assert seen == [(64 * 512, 512)]
