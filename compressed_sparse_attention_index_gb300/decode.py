@@ -182,6 +182,8 @@ class PagedCache:
                  out_dtype=L.CSA2_OUT_BF16, device="cuda"):
         self.n_seq, self.n_pages, self.page_size, self.max_tokens = n_seq, n_pages, page_size, max_tokens
         swa_cap = SWA - 1 + max_tokens if swa_cap is None else swa_cap
+        if not 1 <= max_tokens <= 65535 or swa_cap < 0 or n_seq * swa_cap >= 2**31:
+            raise ValueError(f"max_tokens 1 .. 65535 and n_seq x swa_cap below 2^31 expected, not {max_tokens}, {n_seq} x {swa_cap}")
         self.swa_cap, self.out_dtype = swa_cap, out_dtype
         i32 = dict(dtype=torch.int32, device=device)
         self.pages = torch.zeros((n_pages, page_size, 288), dtype=torch.uint8, device=device)

@@ -89,3 +89,12 @@ def test_a_single_row_of_any_stride(cache, monkeypatch):
     assert q.stride(0) == 512 and lat.stride(0) == 1
     c.write(q, lat)
     assert seen == [(64 * 512, 512)]
+
+
+def test_limits(cache):
+    for rows in (0, 65_536):
+        with pytest.raises(ValueError):
+            cache(3, 8, 16, 64, rows)
+    for cap in (-1, 2**30):
+        with pytest.raises(ValueError):
+            cache(3, 8, 16, 64, 5, swa_cap=cap)
