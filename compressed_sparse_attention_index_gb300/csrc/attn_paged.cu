@@ -29,8 +29,8 @@
 // Window records (E4M3 x 2^e) are exact in f16 where -15 <= e <= 7; otherwise
 // the window is scaled by 2^kx, kx = 7 - (the largest e): exact but for values
 // below 2^-31 of the window's largest, and undone on its logits and, being the
-// first chunk, on O before the next one.  Q out of f16's range goes to f16 under a
-// power of two, undone on the logits.
+// first chunk, on O before the next one.  A head of Q out of f16's range goes to f16
+// under a power of two of its own, undone on its logits.
 //
 // Warps, with their own barriers between them: two fetch records into shared memory;
 // eight (K) dequantise them, a row per thread, into slabs of 128 dims in tensor memory,
@@ -45,8 +45,8 @@
 // conflicts: 4,700 of the 5,000 to 5,300 cycles that a chunk takes.  That is why K goes
 // through tensor memory (both operands in shared memory took 512 cycles more), and why
 // its rows are dequantised once (a second time for V cost more arithmetic than
-// everything else together).  8 x 1,048,576 entries: 1,200 us, 0.92 PFLOP/s; 32 x 65,536:
-// 331 us; 33 sequences of up to 40,001: 147 us; 40 queries x 512 selected: 35 us.
+// everything else together).  8 x 1,048,576 entries: 1,220 us, 0.90 PFLOP/s; 32 x 65,536:
+// 334 us; 33 sequences of up to 40,001: 147 us; 40 queries x 512 selected: 35 us.
 // A few short rows are a chain of latencies: 18 us for one chunk each, the join included.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -75,7 +75,7 @@ constexpr int kPgSmP = kPgSmQ + 64 * 1024;         // 128 entries x 64 heads f16
 constexpr int kPgSmRaw = kPgSmP + 16 * 1024;       // a chunk's records
 constexpr int kPgSmEnd = kPgSmRaw + kPgRaw;
 constexpr int kPgSmAlloc = kPgSmEnd + 1024;
-static_assert(kPgSmAlloc + 4608 <= 227 * 1024, "shared memory");
+static_assert(kPgSmAlloc + 5120 <= 227 * 1024, "shared memory");
 // tensor memory: S^T, O^T, the ring of K
 constexpr uint32_t kPgColS = 0, kPgColO = 64, kPgColK = 320, kPgTmemCols = 512;
 constexpr float kPgRaise = 8.f, kPgShift = 7.f, kPgNoRef = 3e38f;   // (kPgNoRef: no entry met yet)
@@ -175,7 +175,8 @@ struct PagedInfo {
   int4 at;                      // query, place in it, its chunks, its first chunk
   uint32_t valid[4];            // rows that hold an entry
   int seq, win, first;          // sequence; window entries (0: entries of the cache), the oldest one's place
-  float f;                      // of a query's first chunk here: logits in log2 units per unit of Q K^T
+  float f;                      // of a query's first chunk here: logits in log2 units per unit of S, negative where
+  int units;                    // its heads have units, which stand there
   int kx;                       // a window's scale (its tile holds 2^kx times its values)
 };
 
@@ -190,8 +191,9 @@ struct PagedShared {
   __align__(16) float less[kHeads];    // minus a head's reference, which is kPgShift below a maximum
   float alpha[kHeads];
   float l[4][kHeads], red[4][kHeads];
-  uint32_t tmem, qmax[8];
-  int emin, emax;
+  float unit[2][kHeads];               // minus the heads' powers of two, for queries that have others than 1, by turns
+  uint32_t tmem, hmax[8][16], v_met[8];   // a V warp's largest |q| of its heads; its parities (see stage_q)
+  int emin, emax, units;               // (units: of the softmax's query)
   int scan[kPgThreads / 32], end[2], start, off, T, G;      // the run's ends; its first query, that one's first chunk; all chunks, their CTAs
   PagedQuery Q;
   volatile int bad;
@@ -512,6 +514,82 @@ __device__ __forceinline__ void paged_load(const PagedArgs &A, PagedShared &S, u
   }
 }
 
+// 16-B chunk lt % 64 of head lt / 64 + 4 i of Q, times `by`, into shared memory as f16,
+// K-major, 128B swizzle; returns the warp's largest |q|.
+__device__ __forceinline__ uint32_t put_q(unsigned char *sm, int lt, const uint4 &x, int i, float by) {
+  uint32_t w[4] = {x.x, x.y, x.z, x.w}, m = 0u;
+#pragma unroll
+  for (int u = 0; u < 4; u++) {
+    m = __vmaxu2(m, w[u] & 0x7FFF7FFFu);
+    const __half2 h2 = __floats2half2_rn(bf16_lo(w[u]) * by, bf16_hi(w[u]) * by);
+    w[u] = *reinterpret_cast<const uint32_t *>(&h2);
+  }
+  const int h = (lt >> 6) + 4 * i;
+  unsigned char *dst = sm + kPgSmQ + ((lt & 63) >> 3) * 1024 + (h >> 3) * 8192;
+  *reinterpret_cast<uint4 *>(dst + sw128(h & 7, lt & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
+  return __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
+}
+__device__ __forceinline__ uint32_t head_max(const PagedShared &S, int g, int i) {       // of head g + 4 i
+  return max(S.hmax[2 * g][i], S.hmax[2 * g + 1][i]);
+}
+__device__ __forceinline__ int head_power(uint32_t m) {
+  const int ex = (int)(m >> 7) - 127;                // max |q| in [2^ex, 2^(ex + 1)) if normal
+  return m == 0u || m >= 0x7F80u || (ex >= -4 && ex < 15) ? 0 : max(ex - 14, -126);
+}
+__device__ __forceinline__ float power_of_2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// The V group brings Q of a query into shared memory.  One pass as it is where every head's
+// max |q| lies in [2^-4, 2^15), or is zero or not finite: f16 holds a bf16 value exactly down
+// to 2^-17 and to 2^-25 below; else a second one, each head that does not under the power of
+// two that brings it into [2^14, 2^15).  By heads, as one of them may be 2^40 times another:
+// under one power for all the smaller would become zero.  (The parities, 1 of the group's
+// meetings, 2 of q_done, 4 of the queries, rest in shared memory between queries: the copying
+// loop has no register for them.)
+__device__ __forceinline__ void stage_q(const PagedArgs &A, PagedShared &S, unsigned char *sm, int qi, int k) {
+  const int lt = (int)threadIdx.x - kPgSoft - kPgLoad, lane = lt & 31;
+  uint32_t met = S.v_met[lt >> 5];
+  const uint4 *src = reinterpret_cast<const uint4 *>(A.q + (int64_t)qi * kHeads * kDim) + lt;
+#pragma unroll 1
+  for (int i0 = 0; i0 < 16; i0 += 8) {
+    uint4 x[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) x[i] = __ldg(src + (i0 + i) * kPgLoad);
+    if (i0 == 0 && k > 0) {                          // (the query before is multiplied)
+      paged_wait(A, S, &S.q_done, (met >> 1) & 1);
+      met ^= 2;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const uint32_t m = put_q(sm, lt, x[i], i0 + i, 1.f);
+      if (lane == 0) S.hmax[lt >> 5][i0 + i] = m;
+    }
+  }
+  // (the maxima are read before q_full, and written again after the next q_done)
+  paged_meet(A, S, 2, met);
+  const bool scaled = __any_sync(0xFFFFFFFFu, head_power(head_max(S, lane >> 4, lane & 15)) != 0 ||
+                                                  head_power(head_max(S, 2 + (lane >> 4), lane & 15)) != 0);
+  // (of the two places for units, the softmax may still read the other for the query before)
+  const int place = (int)(met >> 2) & 1;
+  met ^= 4;
+  if (__builtin_expect(scaled, 0)) {
+#pragma unroll 1
+    for (int i = 0; i < 16; i++) put_q(sm, lt, __ldg(src + i * kPgLoad), i, power_of_2(-head_power(head_max(S, lt >> 6, i))));
+    if (lt < kHeads) S.unit[place][lt] = -power_of_2(head_power(head_max(S, lt & 3, lt >> 2)));
+  }
+  if (lt == 0) {
+    PagedInfo &I = S.info[k & (kPgInfo - 1)];
+    I.f = A.scale * (scaled ? -1.4426950408889634f : 1.4426950408889634f);
+    I.units = place;
+  }
+  ptx::fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    S.v_met[lt >> 5] = met;
+    ptx::mbar_arrive(&S.q_full);
+  }
+  __syncwarp();
+}
+
 // The V group copies the slabs from tensor memory into a ring in shared memory, where
 // PV reads them MN-major, in two teams as the K group: a thread per row, holding a slab
 // in registers until PV has freed its slot.  (Dequantising them a second time cost more
@@ -524,82 +602,17 @@ __device__ __forceinline__ void paged_copy(const PagedArgs &A, PagedShared &S, u
   const uintptr_t tile = reinterpret_cast<uintptr_t>(sm + kPgSmV + (e >> 3) * 2048 + (e & 7) * 128 + (e & 7) * 16);
   static_assert(kPgVRing == kPgKRing, "one slot number for both rings");
   PagedSlab<2> n((unsigned)team);
-  // Q of a query to f16, K-major, 128B swizzle.  One pass as they are where max |q| lies
-  // in [2^-4, 2^15): f16 holds a bf16 value exactly down to 2^-17 and to 2^-25 below; else
-  // a second one under the power of two that brings it into [2^14, 2^15)
-  uint32_t met = 0;                                  // parities: 1 of the group's meetings, 2 of q_done
-  auto q_max = [&](uint32_t m) {                     // of the group, from two halves each
-    m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
-    if (lane == 0) S.qmax[lt >> 5] = m;
-    paged_meet(A, S, 2, met);
-#pragma unroll
-    for (int w = 0; w < 8; w++) m = max(m, S.qmax[w]);
-    paged_meet(A, S, 2, met);                        // (before the next one)
-    return m;
-  };
-  auto stage_q = [&](int qi, int k) {
-    const uint4 *src = reinterpret_cast<const uint4 *>(A.q + (int64_t)qi * kHeads * kDim) + lt;
-    unsigned char *dst = sm + kPgSmQ + ((lt & 63) >> 3) * 1024;
-    int qs = 0;
-    for (int pass = 0;; pass++) {
-      const float inv = ldexpf(1.f, -qs);
-      uint32_t m = 0u;
-#pragma unroll 1
-      for (int i0 = 0; i0 < 16; i0 += 8) {
-        uint4 x[8];
-#pragma unroll
-        for (int i = 0; i < 8; i++) x[i] = __ldg(src + (i0 + i) * kPgLoad);
-        if (pass == 0 && i0 == 0 && k > 0) {         // (the query before is multiplied)
-          paged_wait(A, S, &S.q_done, met >> 1);
-          met ^= 2;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; i++) {                // 16-B chunk lt % 64 of head lt / 64 + 4 (i0 + i)
-          uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-          for (int u = 0; u < 4; u++) {
-            m = __vmaxu2(m, w[u] & 0x7FFF7FFFu);
-            const __half2 h2 = __floats2half2_rn(bf16_lo(w[u]) * inv, bf16_hi(w[u]) * inv);
-            w[u] = *reinterpret_cast<const uint32_t *>(&h2);
-          }
-          const int h = (lt >> 6) + 4 * (i0 + i);
-          *reinterpret_cast<uint4 *>(dst + (h >> 3) * 8192 + sw128(h & 7, lt & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-      if (pass == 1) break;
-      m = q_max(m);
-      if (m >= 0x7F80u) {                            // a head that is not finite spoils its own output alone
-        m = 0u;
-#pragma unroll 1
-        for (int i = 0; i < 16; i++) {
-          const uint4 x = __ldg(src + i * kPgLoad);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int u = 0; u < 8; u++) {
-            const uint32_t v = (w[u >> 1] >> (16 * (u & 1))) & 0x7FFFu;
-            if (v < 0x7F80u) m = max(m, v);
-          }
-        }
-        m = q_max(m);
-      }
-      const int ex = (int)(m >> 7) - 127;            // max |q| in [2^ex, 2^(ex + 1)) if normal
-      if (m == 0u || (ex >= -4 && ex < 15)) break;
-      qs = max(ex - 14, -100);
-    }
-    if (lt == 0) S.info[k & (kPgInfo - 1)].f = A.scale * 1.4426950408889634f * ldexpf(1.f, qs);
-    ptx::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(&S.q_full);
-  };
-  // (the first query's while its records are looked up)
-  if (n_run > 0) stage_q(S.start, 0);
-  bool last = false;                                 // the chunk is its query's last
+  bool last = true;                                  // the chunk before was its query's last
 #pragma unroll 1
   for (int i = 0; i < 2 * n_run; i++, n.next()) {
     if (last && (i & 1) == 0) {                      // the next query's, before its first slab
-      paged_wait(A, S, &S.raw_full[(i >> 1) & 1], (i >> 2) & 1);
-      if (paged_bad(S)) break;
-      stage_q(S.info[(i >> 1) & (kPgInfo - 1)].at.x, i >> 1);
+      int qi = S.start;                              // (the first one's while its records are looked up)
+      if (i > 0) {
+        paged_wait(A, S, &S.raw_full[(i >> 1) & 1], (i >> 2) & 1);
+        if (paged_bad(S)) break;
+        qi = S.info[(i >> 1) & (kPgInfo - 1)].at.x;
+      }
+      stage_q(A, S, sm, qi, i >> 1);
     }
     uint32_t r[2][32];
     paged_wait(A, S, &S.k_full[n.bar], n.phase);
@@ -683,6 +696,21 @@ __device__ __forceinline__ bool paged_numerators(uint64_t (&s)[16]) {
   return top > 32768.f;
 }
 
+// This lane's entry: S of 32 heads times their units, in place (and for the whole query, so
+// that nothing else has to know of them; a factor in the logits took 8 % of every row's time).
+__device__ __noinline__ void paged_units(uint32_t ta, const float *unit) {
+#pragma unroll 1
+  for (int h = 0; h < 32; h += 16) {
+    uint32_t a[16];
+    ptx::tmem_ld_32x32b_x16(ta + h, a);
+    ptx::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; i++) a[i] = __float_as_uint(__uint_as_float(a[i]) * unit[h + i]);
+    ptx::tmem_st_32x32b_x16(ta + h, a);
+  }
+  ptx::tmem_wait_st();
+}
+
 // Warp w has TMEM lane quarter w % 4 (S: entries, O: dims) and heads 32 (w / 4) ..
 __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S, unsigned char *sm, int n_run,
                                               uint32_t tmem) {
@@ -690,7 +718,7 @@ __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S
   const int quarter = warp & 3, hb = (warp >> 2) * 32, e_row = quarter * 32 + lane;
   const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16);
   uint64_t l_acc[16];                                // 32 heads' denominators
-  float q_f = 0.f;                                   // logits in log2 units per unit of S
+  float q_f = 0.f;                                   // logits in log2 units per unit of S; negative: S still lacks its units
   uint32_t met = 0;
   float o_scale = 1.f;                               // what O still has to be multiplied by
   bool acc = false;                                  // O holds something of this query
@@ -707,6 +735,7 @@ __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S
       for (int i = 0; i < 16; i++) l_acc[i] = 0ull;
       if (t < kHeads) S.less[t] = kPgNoRef;
       q_f = info.f;
+      if (t == 0) S.units = info.units;
       paged_meet(A, S, 0, met);
     }
     const int kx = info.kx;
@@ -716,8 +745,9 @@ __device__ __forceinline__ void paged_softmax(const PagedArgs &A, PagedShared &S
     uint64_t s[16];
     paged_logits(ta, f, none, &S.less[hb], s);
     const bool over = paged_numerators(s);
-    // (a window's 2^-kx is undone before the next chunk)
-    if (soft_any(over || (acc && o_scale != 1.f))) {
+    // (a window's 2^-kx is undone before the next chunk; heads with units are always dealt with here)
+    if (__builtin_expect(soft_any(over || q_f < 0.f || (acc && o_scale != 1.f)), 0)) {
+      if (__builtin_expect(q_f < 0.f, 0)) paged_units(ta, &S.unit[S.units & 1][hb]);
       // the chunk's maximum of every head, 16 at a time: lanes L and L + 16 end with head L
 #pragma unroll 1
       for (int h = 0; h < 32; h += 16) {
@@ -993,6 +1023,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     ptx::mbar_init(&S.o_done, 1);
     ptx::mbar_init(&S.drain, 2);
     S.bad = 0;
+    for (int i = 0; i < 8; i++) S.v_met[i] = 0u;
     S.start = S.off = 0;
     ptx::fence_mbar_init();
   }

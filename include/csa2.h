@@ -582,8 +582,8 @@ csa2_status csa2_cache_read(int kind, const void *cache, int64_t n_slots, const 
  *                bytes, 256-B aligned; no initialisation.  Calls that may run at
  *                the same time need one each.
  *   Limits: n_q <= 65535; n_pages * page_size below 2^31; n_q * (row / 128 + 1) up to 2^30, row = sel_stride or
- *   table_stride * page_size.  A head of a query that holds an infinity or NaN
- *   leaves the query's other heads as they are.
+ *   table_stride * page_size.  Each head of a query has its own scale: whatever it
+ *   holds, an infinity or NaN among it, the query's other heads stay as they are.
  */
 csa2_status csa2_paged_attn(const void *q, const void *pages, int n_pages, int page_size, const int32_t *block_table,
                             int64_t table_stride, int n_seq, const int32_t *sel, int sel_stride, const void *swa_cache,

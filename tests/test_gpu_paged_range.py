@@ -1,0 +1,111 @@
+"""The paged-cache operators at the ends of their numeric range, against the
+64-bit restatements: heads of unlike size, long rows and their log-sum-exp,
+query rows that fp32 squares cannot hold, angles of far positions."""
+from decimal import Decimal, getcontext
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from gen import inputs as G  # noqa: E402
+import paged_reference as R  # noqa: E402
+from parity import ATTN_TOL_F32, row_norm_err  # noqa: E402
+from test_gpu_pack_topk import _edge_rows  # noqa: E402
+from test_gpu_paged import Case, _bf16, _bits, _decode_queries, _i32  # noqa: E402
+from test_gpu_paged_run import _attend_rows  # noqa: E402
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import compressed_sparse_attention_index_gb300 as c
+    return c
+
+
+# ------------------------------------------------------------------ heads of unlike size
+def _scaled(bits, power):
+    """bf16 rows times 2^power (a power a row): exact."""
+    return R.round_bf16_bits(R.bf16_values(bits).astype(np.float64) * 2.0 ** np.asarray(power, np.float64)[..., None])
+
+
+def _logit_room(q, k, scale=512**-0.5):
+    """How far each head's logits may be off.  A logit is 32 products of 16 dims added up in fp32: each addition is off by
+    a step (2^-23) of the larger of the sum so far and what is added, taken twice for products that are aligned
+    before they are added."""
+    a, b = torch.from_numpy(q).cuda().view(64, 32, 16), torch.from_numpy(k).cuda()
+    top = torch.zeros(64, dtype=torch.float64, device="cuda")
+    for c in b.split(2000):
+        part = torch.einsum("hsd,nsd->hns", a, c.view(-1, 32, 16)).cumsum(-1).abs().amax((1, 2))
+        step = torch.einsum("hsd,nsd->hns", a.abs(), c.view(-1, 32, 16).abs()).amax((1, 2))
+        top = torch.maximum(top, torch.maximum(part, step))
+    return scale * 32 * 2.0**-22 * top.cpu().numpy()
+
+
+def _check_heads(c, x, out, lse, queries, rows):
+    for i in rows:
+        b, vis, pos, first, cnt = queries[i]
+        k = R.kv_values(R.paged_rows(c.pages, c.table[b], c.page, range(vis)))
+        if cnt:
+            k = np.concatenate([k, R.swa_values(c.swa[b][(first + np.arange(cnt)) % c.swa_cap])])
+        v = R.bf16_values(x[i]).astype(np.float64)
+        o, le = R.attention(v, k, pos)
+        room = _logit_room(v, k)
+        # what the weights of all entries but the largest can change by: to first order where the logits are known to
+        # 1/20, else by all that they may weigh
+        logit = 512**-0.5 * (v @ k.T)
+        logit -= logit.max(1, keepdims=True)
+        w = np.exp(logit - np.log(np.exp(logit).sum(1, keepdims=True)))
+        rest = np.exp(np.minimum(logit + 2 * room[:, None], 0)).sum(1) - 1
+        moved = np.where(room <= 0.05, 4 * room * (w * (1 - w)).sum(1), 2 * rest)
+        size = np.abs(o).max(1)
+        assert np.all(np.abs(out[i] - o).max(1) <= ATTN_TOL_F32 * size + moved * np.abs(k).max()), i
+        assert np.all(np.abs(lse[i] - le) <= room + 1e-5 + 2.0**-22 * np.abs(le)), i
+
+
+@pytest.mark.parametrize("power", [60, 100, -60, 14])
+def test_a_head_leaves_the_others_as_they_are(lib, oracle_lib, power):
+    """One large or small head: the other heads keep their bits, and it has its own answer."""
+    c = Case(oracle_lib, [700, 40], 64, seed=110)
+    q = _decode_queries([700, 40]) + [(0, 650, 649, 0, 128)]
+    want, want_l = c.run(lib, q)
+    p = np.zeros((3, 64))
+    p[0, 7] = p[2, 0] = p[2, 63] = power
+    x = _scaled(c.q, p)
+    out, lse = _attend_rows(lib, c, x, q)
+    assert np.array_equal(out[p == 0], want[p == 0]) and np.array_equal(lse[p == 0], want_l[p == 0])
+    _check_heads(c, x, out, lse, q, range(3))
+
+
+@pytest.mark.parametrize("latent_scale,swa_scale", [(1.0, 1.0), (50.0, 1.0), (1.0, 2.0**25)])
+def test_heads_of_every_size(lib, oracle_lib, latent_scale, swa_scale):
+    """Heads from 2^-70 to 2^70 and a head of zeros in one query; a query of equal heads beside it."""
+    c = Case(oracle_lib, [900, 300], 48, seed=111, latent_scale=latent_scale, swa_scale=swa_scale)
+    q = _decode_queries([900, 300]) + [(0, 5, 4, 0, 0), (1, 299, 298, 0, 128)]
+    c.run(lib, q)
+    r = np.random.default_rng(5)
+    x = _scaled(c.q, np.where(np.arange(4)[:, None] == 1, 0, r.integers(-70, 71, (4, 64))))
+    x[0, 17] = 0
+    x[3, 1], x[3, 2, 5] = 0x8000, 0x7F80               # zeros, and a head that is not finite beside the rest
+    out, lse = _attend_rows(lib, c, x, q)
+    assert not np.isfinite(out[3, 2]).any()
+    out[3, 2], x[3, 2] = 0, 0
+    o, le = _attend_rows(lib, c, x, q)
+    out[3, 2], lse[3, 2] = o[3, 2], le[3, 2]
+    assert np.array_equal(out, o) and np.array_equal(lse, le)
+    _check_heads(c, x, out, lse, q, range(4))
+
+
+def test_heads_of_unlike_size_in_many_short_rows(lib, oracle_lib):
+    """Queries one after another on an SM, every third one with heads of its own sizes."""
+    lens = [int(v) for v in np.random.default_rng(12).integers(1, 300, 400)]
+    c = Case(oracle_lib, lens, 16, seed=112)
+    q = _decode_queries(lens)
+    want, want_l = c.run(lib, q)
+    p = np.where(np.arange(400)[:, None] % 3 == 1, np.random.default_rng(6).integers(-40, 41, (400, 64)), 0)
+    x = _scaled(c.q, p)
+    out, lse = _attend_rows(lib, c, x, q)
+    assert np.array_equal(out[p == 0], want[p == 0]) and np.array_equal(lse[p == 0], want_l[p == 0])
+    _check_heads(c, x, out, lse, q, range(1, 400, 21))
+
+
