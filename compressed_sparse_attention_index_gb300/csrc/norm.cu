@@ -16,7 +16,8 @@
 // lane holds channels [8 lane, 8 lane + 8) and 256 + that, so every access of a
 // warp is 512 contiguous bytes; a CTA's 8 warps take the heads of one token and
 // share its 32 angles.  Sums are fp32 (32 terms of a lane's row at most, then a
-// shuffle tree), the result is rounded once.
+// shuffle tree), the result is rounded once; a row whose mean square is out of
+// [2^-100, 2^100], or not a number, goes to fp64.
 //
 // Latent rows, one warp per token, feed cache records, whose codes hang on
 // which side of a rounding border a value falls.  So that the records do not
@@ -65,7 +66,51 @@ __device__ __forceinline__ void load_gain(const float *gain, int lane, float *g)
   }
 }
 
+// fp64 to bf16, any value
+__device__ __forceinline__ uint32_t bf16_of_f64(double v) {
+  if (isnan(v)) return 0x7FFFu;
+  if (fabs(v) >= 0x1.FFp127) return v > 0 ? 0x7F80u : 0xFF80u;      // half a step above the largest: infinity
+  return bf16_from_f64(v);
+}
+
+// A row in fp64 (warp-wide): y[i] = bf16 bits of the lane's 16 channels.
+__device__ __noinline__ void row_f64(const float *x, const float *g, double eps, uint64_t turn, int lane,
+                                            uint32_t *y) {
+  double ss = 0.0;
+  for (int i = 0; i < 16; i++) ss = fma((double)x[i], (double)x[i], ss);
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+  const double inv = 1.0 / sqrt(ss / kDim + eps);
+  double c, s;
+  sincospi((double)(int64_t)turn * 0x1p-63, &s, &c);                 // pair `lane`
+  for (int i = 0; i < 8; i++) y[i] = bf16_of_f64((double)x[i] * (double)g[i] * inv);
+  for (int k = 0; k < 4; k++) {
+    const double ck = __shfl_sync(0xFFFFFFFFu, c, (lane & 7) * 4 + k);
+    const double sk = __shfl_sync(0xFFFFFFFFu, s, (lane & 7) * 4 + k);
+    double a = (double)x[8 + 2 * k] * (double)g[8 + 2 * k] * inv;
+    double b = (double)x[9 + 2 * k] * (double)g[9 + 2 * k] * inv;
+    if (lane >= (kRopeOff - 256) / 8) {
+      const double a0 = a;
+      a = a0 * ck - b * sk;
+      b = a0 * sk + b * ck;
+    }
+    y[8 + 2 * k] = bf16_of_f64(a);
+    y[9 + 2 * k] = bf16_of_f64(b);
+  }
+}
+
 // ------------------------------------------------------------------ queries
+// A query row whose mean square (plus eps) fp32 does not hold well: in fp64.
+__device__ __noinline__ void query_row_f64(const NormArgs &A, int64_t tok, const uint16_t *row, int lane, uint4 *out) {
+  float x[16], g[16];
+  uint32_t y[16];
+  unpack8(*reinterpret_cast<const uint4 *>(row), x);
+  unpack8(*reinterpret_cast<const uint4 *>(row + 256), x + 8);
+  load_gain(A.q_gain, lane, g);
+  row_f64(x, g, A.eps, (uint64_t)(int64_t)__ldg(A.pos + tok) * A.turn[lane], lane, y);
+  out[0] = make_uint4(y[0] | y[1] << 16, y[2] | y[3] << 16, y[4] | y[5] << 16, y[6] | y[7] << 16);
+  out[32] = make_uint4(y[8] | y[9] << 16, y[10] | y[11] << 16, y[12] | y[13] << 16, y[14] | y[15] << 16);
+}
+
 template <int HPW>
 __device__ __forceinline__ void query_rows(const NormArgs &A, int idx, float2 *cs_sh) {
   constexpr int B = HPW < 2 ? HPW : 2;              // rows of a warp in flight
@@ -76,6 +121,7 @@ __device__ __forceinline__ void query_rows(const NormArgs &A, int idx, float2 *c
   const uint16_t *src = A.q + tok * A.q_stride + lane * 8;
   uint16_t *dst = A.q_out + tok * (kHeads * kDim) + lane * 8;
   uint4 r[B][2];
+  uint32_t again = 0u;                              // rows left to fp64
   auto load = [&](int j0) {
 #pragma unroll
     for (int j = 0; j < B; j++) {
@@ -115,7 +161,10 @@ __device__ __forceinline__ void query_rows(const NormArgs &A, int idx, float2 *c
       for (int j = 0; j < B; j++) ss[j] += __shfl_xor_sync(0xFFFFFFFFu, ss[j], o);
 #pragma unroll
     for (int j = 0; j < B; j++) {
-      const float inv = rsqrtf(fmaf(ss[j], 1.f / kDim, A.eps_hi));
+      const float ms = fmaf(ss[j], 1.f / kDim, A.eps_hi), inv = rsqrtf(ms);
+      uint4 *p = reinterpret_cast<uint4 *>(dst + (h0 + 8 * (j0 + j)) * kDim);
+      const bool held = ms > 0x1p-100f && ms < 0x1p100f;      // (the same for all lanes; false for NaN)
+      if (!held) again |= 1u << (j0 + j);
       float x[16];
       unpack8(r[j][0], x);
       unpack8(r[j][1], x + 8);
@@ -129,12 +178,21 @@ __device__ __forceinline__ void query_rows(const NormArgs &A, int idx, float2 *c
           x[9 + 2 * k] = a * cs[k].y + b * cs[k].x;
         }
       }
-      uint4 *p = reinterpret_cast<uint4 *>(dst + (h0 + 8 * (j0 + j)) * kDim);
-      p[0] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                        pack_bf16x2(x[6], x[7]));
-      p[32] = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]), pack_bf16x2(x[12], x[13]),
-                         pack_bf16x2(x[14], x[15]));
+      const uint4 lo = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                  pack_bf16x2(x[6], x[7]));
+      const uint4 hi = make_uint4(pack_bf16x2(x[8], x[9]), pack_bf16x2(x[10], x[11]), pack_bf16x2(x[12], x[13]),
+                                  pack_bf16x2(x[14], x[15]));
+      if (held) {
+        p[0] = lo;
+        p[32] = hi;
+      }
     }
+  }
+  // (read again, behind all others: a call among them costs the loop 33 us of 8,192 tokens' 184 in spills)
+  while (__builtin_expect(again != 0u, 0)) {
+    const int h = h0 + 8 * (__ffs((int)again) - 1);
+    query_row_f64(A, tok, src + h * kDim, lane, reinterpret_cast<uint4 *>(dst + h * kDim));
+    again &= again - 1u;
   }
 }
 
@@ -153,38 +211,6 @@ __device__ __forceinline__ uint32_t bf16_of_pair(float h, float l) {
   // a tie of the rounded sum is decided by what it left out
   if ((u & 0xFFFFu) == 0x8000u && t != 0.f) return (u >> 16) + ((t > 0.f) == (s > 0.f) ? 1u : 0u);
   return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-}
-
-// fp64 to bf16, any value
-__device__ __forceinline__ uint32_t bf16_of_f64(double v) {
-  if (isnan(v)) return 0x7FFFu;
-  if (fabs(v) >= 0x1.FFp127) return v > 0 ? 0x7F80u : 0xFF80u;      // half a step above the largest: infinity
-  return bf16_from_f64(v);
-}
-
-// The row in fp64 (warp-wide): y[i] = bf16 bits of the lane's 16 channels.
-__device__ __noinline__ void latent_row_f64(const float *x, const float *g, double eps, uint64_t turn, int lane,
-                                            uint32_t *y) {
-  double ss = 0.0;
-  for (int i = 0; i < 16; i++) ss = fma((double)x[i], (double)x[i], ss);
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-  const double inv = 1.0 / sqrt(ss / kDim + eps);
-  double c, s;
-  sincospi((double)(int64_t)turn * 0x1p-63, &s, &c);                 // pair `lane`
-  for (int i = 0; i < 8; i++) y[i] = bf16_of_f64((double)x[i] * (double)g[i] * inv);
-  for (int k = 0; k < 4; k++) {
-    const double ck = __shfl_sync(0xFFFFFFFFu, c, (lane & 7) * 4 + k);
-    const double sk = __shfl_sync(0xFFFFFFFFu, s, (lane & 7) * 4 + k);
-    double a = (double)x[8 + 2 * k] * (double)g[8 + 2 * k] * inv;
-    double b = (double)x[9 + 2 * k] * (double)g[9 + 2 * k] * inv;
-    if (lane >= (kRopeOff - 256) / 8) {
-      const double a0 = a;
-      a = a0 * ck - b * sk;
-      b = a0 * sk + b * ck;
-    }
-    y[8 + 2 * k] = bf16_of_f64(a);
-    y[9 + 2 * k] = bf16_of_f64(b);
-  }
 }
 
 // A rotated pair in fp64: its bf16 bits, the first channel's in the lower half.
@@ -271,7 +297,7 @@ __device__ __forceinline__ void latent_row(const NormArgs &A, int tok, int lane)
     }
   }
   if (__any_sync(0xFFFFFFFFu, again)) {
-    latent_row_f64(x, g, A.eps, turn, lane, y);
+    row_f64(x, g, A.eps, turn, lane, y);
   } else if (__any_sync(0xFFFFFFFFu, close != 0u)) {
 #pragma unroll
     for (int k = 0; k < 4; k++) {
@@ -370,7 +396,7 @@ cudaError_t launch_qk_norm_rope(NormArgs A, double eps, double rope_base, cudaSt
   rope_turns(rope_base, A.turn);
   A.lat_ctas = A.lat != nullptr ? (A.n + kNormThreads / 32 - 1) / (kNormThreads / 32) : 0;
   // heads per warp: one CTA per token once that fills the SMs four times over
-  // (a warp then has four rows in flight); fewer heads per warp below that
+  // (a warp then has eight rows, two in flight); fewer heads per warp below that
   const int64_t want = 4 * (int64_t)device_sm_count(current_device());
   const int hpw = A.q == nullptr || A.n >= want ? 8 : 2 * (int64_t)A.n >= want ? 4 : 4 * (int64_t)A.n >= want ? 2 : 1;
   const unsigned grid = (unsigned)A.lat_ctas + (A.q != nullptr ? (unsigned)A.n * (8 / hpw) : 0u);

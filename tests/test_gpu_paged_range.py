@@ -109,3 +109,40 @@ def test_heads_of_unlike_size_in_many_short_rows(lib, oracle_lib):
     _check_heads(c, x, out, lse, q, range(1, 400, 21))
 
 
+# ------------------------------------------------------------------ query rows
+@pytest.mark.parametrize("eps", [1e-6, 1e-12, 1e-60])
+@pytest.mark.parametrize("gains", [False, True])
+def test_query_rows_at_the_edges_of_their_range(lib, eps, gains):
+    """Zero rows under an eps that fp32 does not hold, subnormal and huge rows, infinities and NaN, beside ordinary heads."""
+    n = 5
+    x = G.normal_block_bf16(130, G.S_Q, 0, 0, n * 64, 512).reshape(n, 64, 512)
+    edge = _edge_rows(512)
+    x[1, 3:15] = edge
+    x[4, ::5][:12] = edge
+    x[2, 0, 9], x[2, 1, 500], x[2, 2, 450] = 0x7F80, 0x7FC0, 0xFF80
+    r = np.random.default_rng(7)
+    gain = (1 + 0.2 * r.normal(size=512)).astype(np.float32)
+    pos = np.array([0, 1 << 20, 77, 5, 123_457])
+    out = torch.empty((n, 64, 512), dtype=torch.bfloat16, device="cuda")
+    lib.csa2_qk_norm_rope(_bf16(x), 32768, torch.from_numpy(gain).cuda() if gains else None, out, None, 0, None, None, _i32(pos),
+                          None, None, n, eps, None, 0, None, 0)
+    there = _bf16(x)                                       # in place, the same
+    lib.csa2_qk_norm_rope(there, 32768, torch.from_numpy(gain).cuda() if gains else None, there, None, 0, None, None, _i32(pos),
+                          None, None, n, eps, None, 0, None, 0)
+    assert np.array_equal(_bits(there), _bits(out))
+    got = R.bf16_values(_bits(out)).astype(np.float64)
+    ref = R.norm_rope(R.bf16_values(x), gain if gains else None, pos[:, None], eps)
+    odd = np.zeros((n, 64), bool)
+    odd[2, :3] = True
+    # one bf16 rounding (two where a value of bf16's subnormals goes through fp32's), and fp32 arithmetic: 16 terms and 5 joins of
+    # the sum (2^-20), the quotient and products (2^-22), cos and sin (2^-22) of a pair's |a| + |b|
+    room = np.abs(ref)
+    room[..., 448::2] += np.abs(ref[..., 449::2])
+    room[..., 449::2] += np.abs(ref[..., 448::2])
+    fine = np.abs(got - ref) <= 2.0**-8 * np.abs(ref) + 2.0**-18 * room + 2.0**-133
+    assert fine[~odd].all()
+    # a head that is not finite: NaN where it stood (and where the rotation takes it), zeros beside an infinity
+    want = np.isnan(ref[odd])
+    assert np.array_equal(np.isnan(got[odd]), want) and np.all(got[odd][~want] == 0)
+
+
