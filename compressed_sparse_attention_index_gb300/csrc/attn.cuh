@@ -53,17 +53,48 @@ __device__ __forceinline__ void rope_cs(double inv_freq, int pos, float &c, floa
   sincosf((float)r, &s, &c);
 }
 
+// Sums h + l of two fp64 numbers, |l| at most half an ulp of h (host; about 104 bits).
+struct Double2 {
+  double h, l;
+};
+inline Double2 sum2(double h, double l) {             // |l| below |h|
+  const double s = h + l;
+  return {s, l - (s - h)};
+}
+inline Double2 mul2(const Double2 &a, const Double2 &b) {
+  volatile double p = a.h * b.h;                      // (rounded here, whatever the compiler contracts)
+  return sum2(p, fma(a.h, b.h, -p) + (a.h * b.l + a.l * b.h));
+}
+inline Double2 sqrt2(const Double2 &a) {
+  const double x = sqrt(a.h);
+  return sum2(x, (fma(-x, x, a.h) + a.l) / (2.0 * x));
+}
+inline Double2 inverse2(const Double2 &a) {
+  const double x = 1.0 / a.h;
+  return sum2(x, (fma(-x, a.h, 1.0) - x * a.l) * x);
+}
+
 // The same angles in turns, as 64-bit fixed-point fractions: one position's
 // turns modulo one in 2^-64ths, so that pos * turn (wrapping) drops whole turns
-// exactly; the fraction (53 bits) goes to fp32 for the sine and cosine.
+// exactly and is off by half a 2^-64th a position, 2^-31 rad at the farthest; the
+// fraction (53 bits) goes to fp32 for the sine and cosine.  The powers
+// rope_base^(-i/32) come from five square roots, an inverse and products, all in
+// pairs of fp64 (pow's 53 bits left 2^-24 rad there, and the ulps differ between machines).
 // (A host thread's last base is kept: 32 powers are a microsecond or two.)
 inline void rope_turns(double rope_base, uint64_t (&turn)[kRopeDim / 2]) {
   static thread_local double base = 0.0;           // (not a base)
   static thread_local uint64_t last[kRopeDim / 2];
   if (base != rope_base) {
-    for (int i = 0; i < kRopeDim / 2; i++) {
-      const double t = pow(rope_base, -2.0 * i / (double)kRopeDim) / 6.283185307179586;
-      last[i] = (uint64_t)ldexp(t - floor(t), 64);
+    Double2 step = {rope_base, 0.0};
+    for (int i = 0; i < 5; i++) step = sqrt2(step);   // (kRopeDim / 2 is 2^5)
+    step = inverse2(step);
+    Double2 t = inverse2({6.283185307179586, 2.4492935982947064e-16});       // 1 / (2 pi)
+    for (int i = 0; i < kRopeDim / 2; i++, t = mul2(t, step)) {
+      // (beyond 2^53 turns a position, of a base near zero, nothing is left of the fraction)
+      const bool some = fabs(t.h) < 0x1p53;
+      const double h = some ? t.h - floor(t.h) : 0.0, a = floor(h * 0x1p32);
+      const double rest = some ? ((h * 0x1p32 - a) + t.l * 0x1p32) * 0x1p32 : 0.0;
+      last[i] = ((uint64_t)a << 32) + (uint64_t)(int64_t)rint(rest);
     }
     base = rope_base;
   }

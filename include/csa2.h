@@ -510,11 +510,11 @@ csa2_status csa2_page_plan(const int32_t *seq_len, const int32_t *new_len, int n
  *     y_c = g_c x_c / sqrt(mean_c(x_c^2) + eps)
  * then the pairs (rope_off + 2i, rope_off + 2i + 1), i < 32, are rotated by
  * +pos:  (a, b) <- (a cos t - b sin t, a sin t + b cos t),
- * t = pos * rope_base^(-2i/64).  Queries are computed in fp32 (rows that
- * fp32 squares do not hold in fp64) and rounded once;
- * the latent is the exact value rounded once to bf16 (to 2^-32 of it, or of the
- * pair that it was rotated from), and its records are those csa2_fp4_pack makes
- * of that bf16 row, byte for byte.
+ * t = pos * rope_base^(-2i/64).  Queries are computed in fp32 (rows that fp32
+ * squares do not hold in fp64) and rounded once; the latent is the exact value
+ * rounded once to bf16 (to 2^-30 of it, or of the pair that it was rotated from, at
+ * any position), and its records are those csa2_fp4_pack makes of that bf16 row,
+ * byte for byte.
  *
  *   q            (device) bf16, token t's 64 heads at q + t * q_stride elements
  *                ([64][512] each; q_stride >= 32768, a multiple of 8); NULL: no

@@ -146,3 +146,34 @@ def test_query_rows_at_the_edges_of_their_range(lib, eps, gains):
     assert np.array_equal(np.isnan(got[odd]), want) and np.all(got[odd][~want] == 0)
 
 
+# ------------------------------------------------------------------ angles
+def _far_rotation(y, pos, base):
+    """fp64 rows rotated forward by pos, the angles to 60 digits before they are reduced; and |a| + |b| of every pair."""
+    getcontext().prec = 60
+    two_pi = Decimal("6.28318530717958647692528676655900576839433879875021164194988918461563281257241799725606965068423413596")
+    t = np.array([float((Decimal(int(pos)) * Decimal(base) ** (Decimal(-2 * i) / 64)) % two_pi) for i in range(32)])
+    a, b = y[:, 448::2].copy(), y[:, 449::2].copy()
+    y[:, 448::2], y[:, 449::2] = a * np.cos(t) - b * np.sin(t), a * np.sin(t) + b * np.cos(t)
+    size = np.zeros_like(y)
+    size[:, 448::2] = size[:, 449::2] = np.abs(a) + np.abs(b)
+    return y, size
+
+
+@pytest.mark.parametrize("base", [10000.0, 500000.0, 1.0])
+@pytest.mark.parametrize("pos", [2**31 - 1, 2**30 + 12345, 2**27 - 3, -(2**31)])
+def test_latents_of_far_positions(lib, pos, base):
+    """The exact value's rounding at any position: 8,192 rows have half a million rotated values, a few of which
+    fall on the other side of a border with angles from a frequency of 53 bits (2^-24 at the farthest positions)."""
+    n = 8192
+    x = G.normal_block_bf16(140, G.S_MISC, 0, 0, n, 512)
+    p = lib.default_params()
+    p.rope_base = base
+    out = torch.empty((n, 512), dtype=torch.bfloat16, device="cuda")
+    lib.csa2_qk_norm_rope(None, 0, None, None, _bf16(x), 512, None, out, torch.full((n,), pos, dtype=torch.int32, device="cuda"), None,
+                          None, n, 1e-6, None, 0, None, 0, p)
+    v = R.bf16_values(x).astype(np.float64)
+    ref, size = _far_rotation(v / np.sqrt((v * v).mean(1, keepdims=True) + 1e-6), pos, base)
+    # a turn in 2^-64ths is off by half of one, 2^31 times at most: 2^-34 turns, 2^-31 rad; fp64's own roundings are 2^-50
+    got, room = _bits(out), 2.0**-30 * size + 2.0**-48 * np.abs(ref)
+    assert np.all((got == R.round_bf16_bits(ref - room)) | (got == R.round_bf16_bits(ref + room)))
+    assert np.count_nonzero(got != R.round_bf16_bits(ref)) <= 8          # (as good as none: 2^-22 of the values lie so close)
