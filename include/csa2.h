@@ -226,7 +226,8 @@ csa2_status csa2_topk(const float *scores, int64_t score_stride, int n_q, const 
  * entries only, bf16 for chunks holding window entries), products accumulate
  * in fp32, and the softmax numerators are rounded to f16 (11 bits) or kept as
  * bf16 hi + lo parts; the row-normalised error against an fp64 evaluation is
- * about 2e-4 (under 2e-3).
+ * about 2e-4 (under 2e-3).  A query's heads share one power of two in f16, so this
+ * holds for heads within about 2^24 of its largest (csa2_paged_attn scales each).
  *
  *   q            (device) bf16 [n_q][64][512] (already rotated by upstream).
  *   kv_cache     (device) KV records [n_seq][n_max][288].
@@ -549,6 +550,9 @@ csa2_status csa2_qk_norm_rope(const void *q, int64_t q_stride, const float *q_ga
  *   slots     (device) int32 [n]; a negative slot gives zeros, one at or above
  *             n_slots zeros and CSA2_ERR_BOUNDS.
  *   out       (device) [n][512], bf16 or fp32 per out_dtype, 16-B aligned.
+ * Codes that no packer writes are not read alike: a KV scale of 0x7F is 480 here and
+ * NaN in the attention, a window scale of byte 0 with codes other than zero counts
+ * as 2^-127 here and as zero there.
  */
 csa2_status csa2_cache_read(int kind, const void *cache, int64_t n_slots, const int32_t *slots, int64_t n, void *out,
                             int out_dtype, csa2_stream_t stream);
@@ -563,7 +567,9 @@ csa2_status csa2_cache_read(int kind, const void *cache, int64_t n_slots, const 
  * rows' lengths; the same inputs give the same bits on every call.
  * Arithmetic as csa2_sparse_attn on FP4 latents (f16 products of exact
  * dequantised latents, fp32 sums, numerators rounded to 11 bits): row-normalised
- * error against an fp64 evaluation about 2e-4 (under 2e-3), lse to about 1e-6.
+ * error against an fp64 evaluation about 2e-4 (under 2e-3); lse to about 1e-6
+ * where the logits are of unit size (and within 1e-4: fp32 sums of 512 products).
+ * out and lse must not overlap any input.
  *
  *   q            (device) bf16 [n_q][64][512], rotated (csa2_qk_norm_rope).
  *   pages .. n_seq   the paged cache and its block table (above).  A table entry

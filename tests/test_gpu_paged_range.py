@@ -177,3 +177,59 @@ def test_latents_of_far_positions(lib, pos, base):
     got, room = _bits(out), 2.0**-30 * size + 2.0**-48 * np.abs(ref)
     assert np.all((got == R.round_bf16_bits(ref - room)) | (got == R.round_bf16_bits(ref + room)))
     assert np.count_nonzero(got != R.round_bf16_bits(ref)) <= 8          # (as good as none: 2^-22 of the values lie so close)
+# ------------------------------------------------------------------ long rows, and the log-sum-exp to its figure
+def _lse_room(q, k):
+    """A bound of the log-sum-exp's error, over the heads of q: that of the logits; the softmax's own sums, 2^-24 an
+    addition, of which an entry's numerator goes through one a chunk of 128 and 16 more; 2^-22 each for the
+    exponential and the logarithm."""
+    return _logit_room(q, k).max() + (len(k) / 128 + 16) * 2.0**-24 + 2 * 2.0**-22
+
+
+@pytest.mark.parametrize("lens,sel", [([5000], 0), ([4000, 17, 900], 0), ([3000, 700], 500)])
+def test_lse_to_its_figure(lib, oracle_lib, lens, sel):
+    """Tight enough to see one entry of 5,000 missing (2e-4) or a denominator summed from rounded numerators."""
+    c = Case(oracle_lib, lens, 64, seed=120)
+    q = _decode_queries(lens)
+    r = np.random.default_rng(2)
+    pick = np.stack([np.sort(r.permutation(n)[:sel]) for n in lens]) if sel else None
+    out, lse = c.run(lib, q, sel=pick)
+    for i, (b, vis, pos, first, cnt) in enumerate(q):
+        idx = range(vis) if pick is None else pick[i]
+        k = np.concatenate([R.kv_values(R.paged_rows(c.pages, c.table[b], 64, idx)), R.swa_values(c.swa[b][(first + np.arange(cnt)) % 128])])
+        v = R.bf16_values(c.q[i]).astype(np.float64)
+        o, le = R.attention(v, k, pos)
+        room = _lse_room(v, k) + 3 * 2.0**-24 * np.abs(le).max()          # (the result is rounded after three operations)
+        assert room < 1e-4
+        err = np.abs(lse[i] - le).max()
+        assert err <= room, (err, room)
+        assert row_norm_err(out[i], o) <= ATTN_TOL_F32
+
+
+def test_a_long_row(lib):
+    """100,003 entries of random records against the 64-bit form, one query of 64 heads and a short one beside it."""
+    r = np.random.default_rng(121)
+    n, page = 100_003, 48
+    n_pages = -(-n // page) + 2
+    rec = r.integers(0, 256, (n_pages * page, 288), dtype=np.uint8)
+    rec[:, 256:] = r.integers(0x28, 0x38, (n_pages * page, 32))           # scales of 1/4 .. 1: latents of unit size
+    table = np.stack([r.permutation(n_pages)] * 2)
+    x = r.normal(size=(2, 64, 512))
+    x[:, 5] *= 4.0                                                       # (a head with peaks)
+    bits = R.round_bf16_bits(x)
+    wsb = lib.csa2_workspace_size(lib.CSA2_OP_PAGED_ATTN, 2, 0)
+    ws = torch.empty(wsb, dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty((2, 64, 512), device="cuda"), torch.empty((2, 64), device="cuda")
+    lib.csa2_paged_attn(_bf16(bits), torch.from_numpy(rec).cuda(), n_pages, page, _i32(table), n_pages, 2, None, 0, None, 0,
+                        _i32([0, 1]), _i32([n, 300]), _i32([n - 1, 299]), _i32([0, 0]), _i32([0, 0]), 2, out, lib.CSA2_OUT_F32,
+                        lse, None, ws, wsb)
+    assert lib.csa2_get_device_status() == 0
+    for i, vis in enumerate((n, 300)):
+        j = np.arange(vis)
+        k = R.kv_values(rec[table[i][j // page] * page + j % page])
+        v = R.bf16_values(bits[i]).astype(np.float64)
+        o, le = R.attention(v, k, vis - 1)
+        assert row_norm_err(out[i].cpu().numpy(), o) <= ATTN_TOL_F32
+        room = _lse_room(v, k) + 3 * 2.0**-24 * np.abs(le).max()
+        assert np.abs(lse[i].cpu().numpy() - le).max() <= room
+
+
