@@ -225,6 +225,11 @@ class PagedCache:
         self.rows = rows
         self.desc, self._d, self._count, self._rows = v
 
+    def _here(self):
+        """The kernels run on the current device, and read the cache there."""
+        if self.pages.is_cuda and self.pages.get_device() != torch.cuda.current_device():
+            raise ValueError(f"the cache is on {self.pages.device}, the current device is {torch.cuda.current_device()}")
+
     def _want(self, name, x, rows, cols, dtype):
         """x: rows of `cols` elements (any stride between rows), on the cache's device."""
         if x.dtype != dtype or x.device != self.seq_len.device or x.shape[0] != rows or x.numel() != rows * cols or \
@@ -235,6 +240,7 @@ class PagedCache:
     def plan(self, new_len, stream=None, rows=None):
         """Pages, slots and descriptors for new_len (device int32 [n_seq]) new tokens per sequence, in a step of `rows`
         rows (max_tokens at most, and by default)."""
+        self._here()
         rows = self.max_tokens if rows is None else rows
         if not 0 <= rows <= self.max_tokens:
             raise ValueError(f"rows: 0 .. {self.max_tokens} expected, not {rows}")
@@ -256,6 +262,7 @@ class PagedCache:
     def write(self, q, latent, q_gain=None, latent_gain=None, eps=1e-6, params=None, stream=None):
         """Norm and rotation of the planned tokens' queries (bf16 [rows][64][512]) and latents
         ([rows][512]), into self.q and self.latent, and the latents' records into the caches."""
+        self._here()
         self._want("q", q, self.rows, 64 * 512, torch.bfloat16)
         self._want("latent", latent, self.rows, 512, torch.bfloat16)
         for gain in (q_gain, latent_gain):
@@ -273,6 +280,7 @@ class PagedCache:
     def attend(self, sel=None, params=None, stream=None):
         """(output [rows][64][512], lse [rows][64]) of the planned tokens, over all that they see or over sel (device
         int32 [rows][k]); rows without a token get zeros and -inf, those behind the step's are left as they were."""
+        self._here()
         if sel is not None:
             if not sel.is_contiguous():
                 raise ValueError("sel: contiguous int32 expected")
@@ -310,6 +318,7 @@ class PagedCache:
 
     def read(self, slots, out, stream=None):
         """Latents of the main cache's records `slots` (device int32, as in desc[5]) into out, bf16 or fp32 [n][512]."""
+        self._here()
         if not slots.is_contiguous() or slots.dtype != torch.int32 or slots.device != self.seq_len.device or \
                 not out.is_contiguous() or out.dtype not in (torch.bfloat16, torch.float32):
             raise ValueError("read: contiguous int32 slots on the cache's device and contiguous bf16 or fp32 out expected")

@@ -218,3 +218,16 @@ def test_a_step_of_a_few_rows_captured(lib):
     assert torch.equal(a.seq_len, b.seq_len) and torch.equal(a.pages, b.pages) and lib.csa2_get_device_status() == 0
 
 
+def test_another_current_device(lib, monkeypatch):
+    """The kernels would read the cache of this device from that one."""
+    from compressed_sparse_attention_index_gb300.decode import PagedCache
+    c, new, ins = PagedCache(2, 30, 16, 200, 8), _i32([3, 1]), _inputs(8, 1)
+    want = [x.clone() for x in c.step(new, *ins)]
+    here = torch.cuda.current_device()
+    slots, out = _i32([0]), torch.empty((1, 512), device="cuda")
+    with monkeypatch.context() as m:
+        m.setattr(torch.cuda, "current_device", lambda: here + 1)
+        for call in (lambda: c.plan(new), lambda: c.write(*ins), c.attend, lambda: c.read(slots, out), lambda: c.step(new, *ins)):
+            with pytest.raises(ValueError):
+                call()
+    assert torch.equal(c.attend()[0], want[0])
