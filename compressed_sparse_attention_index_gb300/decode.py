@@ -173,9 +173,10 @@ class PagedCache:
     A token's window holds the last min(128, swa_cap) positions, and a step writes
     the window records of all its tokens before it attends: the ring has to hold the
     windows of all of them, 127 + the longest new_len records.  The default,
-    127 + max_tokens, holds those of any step; of a shorter ring (128 for single
-    tokens) a sequence whose new tokens would overwrite their own windows gets none,
-    which is reported as CSA2_ERR_BOUNDS (four small launches more in each plan).
+    127 + max_tokens, holds those of any step.  In a step of more rows than a shorter
+    ring is sure to hold (swa_cap - 127), a sequence whose new tokens would overwrite
+    their own windows gets none, which is reported as CSA2_ERR_BOUNDS; finding them takes
+    four small launches more.
     max_tokens is at most 65,535."""
 
     def __init__(self, n_seq: int, n_pages: int, page_size: int, max_len: int, max_tokens: int, swa_cap: int = None,
@@ -199,6 +200,8 @@ class PagedCache:
         self._desc[max_tokens:6 * max_tokens] = 0
         self._desc[6 * max_tokens:] = -1
         self._added = torch.empty(2 * max_tokens, **i32)
+        self._fit = (torch.empty(n_seq, **i32), torch.empty(n_seq, dtype=torch.bool, device=device),
+                     torch.empty(n_seq, **i32), torch.full((n_seq,), -1, **i32), torch.full((n_seq,), swa_cap, **i32))
         self.first = torch.zeros(n_seq + 1, **i32)
         self.totals = torch.zeros(2, **i32)
         self.q = torch.empty((max_tokens, 64, 512), dtype=torch.bfloat16, device=device)
@@ -247,17 +250,24 @@ class PagedCache:
         if not new_len.is_contiguous():
             raise ValueError("new_len: contiguous int32 expected")
         self._want("new_len", new_len, self.n_seq, 1, torch.int32)
-        win = min(SWA, self.swa_cap)
-        if 0 < self.swa_cap < win - 1 + self.max_tokens:
-            # the first new token's window reaches back to min(win - 1, seq_len) positions before it, and its records
-            # are there when it is read where the ring has room for them and for all new tokens; a length that
-            # cannot be makes the plan report the sequence and give it no tokens
-            with torch.cuda.stream(stream):
-                new_len = new_len.masked_fill(new_len > self.swa_cap - self.seq_len.clamp(0, win - 1), -1)
+        if 0 < self.swa_cap < min(SWA, self.swa_cap) - 1 + rows:
+            new_len = self._that_fit(new_len, stream)
         self._use_rows(rows)
         L.csa2_page_plan(self.seq_len, new_len, self.n_seq, self.page_size, self.n_pages, self.free, self.n_pages,
                          self.free_head, self.table, self.table.shape[1], self.swa_cap, self.desc, rows, self.first,
                          self.totals, stream)
+
+    def _that_fit(self, new_len, stream):
+        """new_len, and -1, which the plan reports and gives no tokens, where the ring does not hold the records of the
+        new tokens beside the first one's window, which reaches back to min(window - 1, seq_len) positions before it."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self._that_fit(new_len, None)
+        room, over, fit, none, cap = self._fit
+        torch.clamp(self.seq_len, 0, min(SWA, self.swa_cap) - 1, out=room)
+        torch.sub(cap, room, out=room)
+        torch.gt(new_len, room, out=over)
+        return torch.where(over, none, new_len, out=fit)
 
     def write(self, q, latent, q_gain=None, latent_gain=None, eps=1e-6, params=None, stream=None):
         """Norm and rotation of the planned tokens' queries (bf16 [rows][64][512]) and latents
