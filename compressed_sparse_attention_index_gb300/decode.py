@@ -194,11 +194,11 @@ class PagedCache:
         self._state = torch.zeros(n_seq + 1, **i32)
         self.seq_len, self.free_head = self._state[:n_seq], self._state[n_seq:]
         self.free = torch.arange(n_pages, **i32)
-        # the descriptors of a step of r rows, [7][r] (no token anywhere before the first plan), and ahead of them r
-        # entries that name free_head's place in the state as q_seq names seq_len's
-        self._desc = torch.full((8 * max_tokens,), n_seq, **i32)
-        self._desc[max_tokens:6 * max_tokens] = 0
-        self._desc[6 * max_tokens:] = -1
+        # the descriptors of a step of r rows, [7][r] (no token anywhere before the first plan); ahead of them r
+        # entries that name free_head's place in the state as q_seq names seq_len's, and r that advance computes
+        self._desc = torch.full((9 * max_tokens,), n_seq, **i32)
+        self._desc[2 * max_tokens:7 * max_tokens] = 0
+        self._desc[7 * max_tokens:] = -1
         self._added = torch.empty(2 * max_tokens, **i32)
         self._fit = (torch.empty(n_seq, **i32), torch.empty(n_seq, dtype=torch.bool, device=device),
                      torch.empty(n_seq, **i32), torch.full((n_seq,), -1, **i32), torch.full((n_seq,), swa_cap, **i32))
@@ -221,9 +221,10 @@ class PagedCache:
         """The descriptors, buffers and counters of a step of `rows` rows."""
         v = self._views.get(rows)
         if v is None:
-            at = self.max_tokens
-            desc, added = self._desc[at:at + 7 * rows].view(7, rows), self._added[:2 * rows].view(2, rows)
-            v = self._views[rows] = (desc, desc.unbind(), (self._desc[at - rows:at + rows], added.view(-1), *added.unbind()),
+            at = 2 * self.max_tokens
+            desc, added = self._desc[at:at + 7 * rows].view(7, rows), self._added[:2 * rows]
+            counted = self._desc.as_strided((2, rows), (at + 5 * rows, 1))       # what advance computes, and the slots
+            v = self._views[rows] = (desc, desc.unbind(), (self._desc[at - rows:at + rows], counted, counted[0], added.view(2, rows), added),
                                      (self.out[:rows], self.lse[:rows]))
         self.rows = rows
         self.desc, self._d, self._count, self._rows = v
@@ -309,13 +310,12 @@ class PagedCache:
                 return self.advance()
         # a token with a slot counts as one of its sequence; where the slot is a page's first, as a page.  (Slots end
         # within a sequence, pages of the free list within a step, so what is counted comes first in both.)
-        (place, add, pages, tokens), slot = self._count, self._d[5]
-        torch.ge(slot, 0, out=tokens)
+        place, counted, first, added, add = self._count
         if self.page_size > 1:
-            torch.remainder(slot, self.page_size, out=pages)           # (-1: a page's last place)
-            torch.eq(pages, 0, out=pages)
+            torch.remainder(self._d[5], -self.page_size, out=first)    # 0 at a page's first place, else below
         else:
-            pages.copy_(tokens)
+            first.copy_(self._d[5])
+        torch.ge(counted, 0, out=added)
         self._state.index_add_(0, place, add)
 
     def step(self, new_len, q, latent, q_gain=None, latent_gain=None, eps=1e-6, sel=None, params=None, stream=None):
