@@ -41,12 +41,13 @@
 // What bounds it: the heads fill half of an MMA's width, so the tensor cores' 2,600
 // cycles a chunk are far from the peak rate by themselves, and shared memory moves more:
 // V's slabs 1,024 cycles to write and as much for PV to read, Q 512, P 128 to write and
-// 512 to read, the records 288 in and 320 out, and some 800 of waits, descriptions and
-// conflicts: 4,700 of the 5,000 to 5,300 cycles that a chunk takes.  That is why K goes
-// through tensor memory (both operands in shared memory took 512 cycles more), and why
-// its rows are dequantised once (a second time for V cost more arithmetic than
-// everything else together).  8 x 1,048,576 entries: 1,220 us, 0.90 PFLOP/s; 32 x 65,536:
-// 334 us; 33 sequences of up to 40,001: 147 us; 40 queries x 512 selected: 35 us.
+// 512 to read, the records 288 in and 320 out, and (counted) 1,330 of barriers, waits,
+// descriptions, the softmax's exchanges, global accesses and conflicts: 5,140 of the 5,100
+// to 5,400 cycles that a chunk takes.  That is why K goes through tensor memory (both
+// operands in shared memory took 512 cycles more), and why its rows are dequantised once (a
+// second time for V cost more arithmetic than everything else together).  8 x 1,048,576
+// entries: 1,220 us, 0.90 PFLOP/s; 32 x 65,536: 334 us; 33 sequences of up to 40,001: 147 us;
+// 40 queries x 512 selected: 35 us.
 // A few short rows are a chain of latencies: 18 us for one chunk each, the join included.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -167,10 +168,10 @@ struct PagedCursor {
   __device__ __forceinline__ bool window() const { return Q.win > 0 && c == off; }
 };
 
-// What the roles need to know of a chunk (kPgInfo of them, by chunk number).
 // j / page
 __device__ __forceinline__ unsigned paged_col(unsigned j, const PagedArgs &A) { return magic_div(j, A.page_mul, A.page_shift); }
 
+// What the roles need to know of a chunk (kPgInfo of them, by chunk number).
 struct PagedInfo {
   int4 at;                      // query, place in it, its chunks, its first chunk
   uint32_t valid[4];            // rows that hold an entry

@@ -373,8 +373,8 @@ __device__ __forceinline__ void latent_row(const NormArgs &A, int tok, int lane)
 
 // Grid: lat_ctas CTAs of eight latent rows (first: their rare fp64 rows take
 // longest), then 8 / HPW CTAs per token of 8 HPW query heads each.  Two rows of a warp
-// in flight and four CTAs an SM: of 8,192 tokens the queries take 162 us, as a copy of
-// their bytes does (163), the latents alone 23 (their arithmetic), both together 176; four
+// in flight and four CTAs an SM: of 8,192 tokens the queries take 158 us (a copy of
+// their bytes 163), the latents alone 19 (their arithmetic), both together 171; four
 // rows in flight, or what registers the compiler likes, took 14 and 4 us more.
 template <int HPW>
 __global__ void __launch_bounds__(kNormThreads, 4) qk_norm_rope_kernel(const __grid_constant__ NormArgs A) {
