@@ -161,7 +161,8 @@ class PagedCache:
     costs that of a few rows, whatever max_tokens is.  Everything stays on the
     device and on one stream (the current one, or `stream`, a torch.cuda.Stream),
     so a step can be captured into a CUDA graph and replayed: new_len and the
-    inputs are read where they lie.  A new cache is whole when its constructor returns
+    inputs are read where they lie.  (write, attend and advance go with the last plan that
+    the host made: a graph that plans should hold the whole step.)  A new cache is whole when its constructor returns
     (it waits for its fills); from then on the order of calls on different streams is the
     caller's, and so is the cache's life until work on other streams than the
     constructor's is over.
@@ -194,11 +195,12 @@ class PagedCache:
         self._state = torch.zeros(n_seq + 1, **i32)
         self.seq_len, self.free_head = self._state[:n_seq], self._state[n_seq:]
         self.free = torch.arange(n_pages, **i32)
-        # the descriptors of a step of r rows, [7][r] (no token anywhere before the first plan); ahead of them r
-        # entries that name free_head's place in the state as q_seq names seq_len's, and r that advance computes
-        self._desc = torch.full((9 * max_tokens,), n_seq, **i32)
-        self._desc[2 * max_tokens:7 * max_tokens] = 0
-        self._desc[7 * max_tokens:] = -1
+        # the descriptors of a step of r rows, [7][r] (no token anywhere before the first plan), and ahead of them a row
+        # that advance computes
+        self._desc = torch.zeros(8 * max_tokens, **i32)
+        self._desc[6 * max_tokens:] = -1
+        # what advance adds to: r times free_head's place in the state, then the tokens' sequences
+        self._place = torch.full((2 * max_tokens,), n_seq, **i32)
         self._added = torch.empty(2 * max_tokens, **i32)
         self._fit = (torch.empty(n_seq, **i32), torch.empty(n_seq, dtype=torch.bool, device=device),
                      torch.empty(n_seq, **i32), torch.full((n_seq,), -1, **i32), torch.full((n_seq,), swa_cap, **i32))
@@ -221,10 +223,11 @@ class PagedCache:
         """The descriptors, buffers and counters of a step of `rows` rows."""
         v = self._views.get(rows)
         if v is None:
-            at = 2 * self.max_tokens
-            desc, added = self._desc[at:at + 7 * rows].view(7, rows), self._added[:2 * rows]
-            counted = self._desc.as_strided((2, rows), (at + 5 * rows, 1))       # what advance computes, and the slots
-            v = self._views[rows] = (desc, desc.unbind(), (self._desc[at - rows:at + rows], counted, counted[0], added.view(2, rows), added),
+            at = self.max_tokens
+            desc, place = self._desc[at:at + 7 * rows].view(7, rows), self._place[at - rows:at + rows]
+            counted = self._desc.as_strided((2, rows), (at + 5 * rows, 1))       # the row ahead, and the slots
+            added = self._added[:2 * rows]
+            v = self._views[rows] = (desc, desc.unbind(), (place, place[rows:], counted, counted[0], added.view(2, rows), added),
                                      (self.out[:rows], self.lse[:rows]))
         self.rows = rows
         self.desc, self._d, self._count, self._rows = v
@@ -310,7 +313,8 @@ class PagedCache:
                 return self.advance()
         # a token with a slot counts as one of its sequence; where the slot is a page's first, as a page.  (Slots end
         # within a sequence, pages of the free list within a step, so what is counted comes first in both.)
-        place, counted, first, added, add = self._count
+        place, seq, counted, first, added, add = self._count
+        torch.clamp(self._d[0], 0, self.n_seq - 1, out=seq)            # (whatever a step of other rows has left there)
         if self.page_size > 1:
             torch.remainder(self._d[5], -self.page_size, out=first)    # 0 at a page's first place, else below
         else:

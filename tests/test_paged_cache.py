@@ -98,3 +98,13 @@ def test_limits(cache):
     for cap in (-1, 2**30):
         with pytest.raises(ValueError):
             cache(3, 8, 16, 64, 5, swa_cap=cap)
+
+
+def test_advance_after_a_step_of_other_rows(cache):
+    """Descriptors read with other rows than they were planned for name no place outside the state."""
+    c = cache(2, 8, 16, 64, 40)
+    c._use_rows(4)
+    c.desc.copy_(torch.tensor([[0, 0, 1, 1], [1, 2, 60, 61], [0, 1, 59, 60], [0] * 4, [1] * 4, [100, 101, 102, 103], [5] * 4]))
+    c._use_rows(40)
+    c.advance()                                          # (index_add_ would raise)
+    assert c.seq_len.shape == (2,)
