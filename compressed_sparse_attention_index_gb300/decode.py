@@ -178,7 +178,8 @@ class PagedCache:
     ring is sure to hold (swa_cap - 127), a sequence whose new tokens would overwrite
     their own windows gets none, which is reported as CSA2_ERR_BOUNDS; finding them takes
     four small launches more.
-    max_tokens is at most 65,535."""
+    max_tokens is at most 65,535.  Pages are taken and not returned: what ends a
+    sequence, and gives its pages to others, is the caller's."""
 
     def __init__(self, n_seq: int, n_pages: int, page_size: int, max_len: int, max_tokens: int, swa_cap: int = None,
                  out_dtype=L.CSA2_OUT_BF16, device="cuda"):

@@ -463,7 +463,8 @@ csa2_status csa2_profile_events(void *begin, void *end);
  * numbered in sequence order, and so are the pages it needs: columns
  * ceil(seq_len / page_size) .. ceil((seq_len + new_len) / page_size) - 1 of row b
  * of the block table are written with the next pages of the free list; no other
- * column is written.  One launch; the host reads nothing.
+ * column is written.  One launch; the host reads nothing.  An entry is a token
+ * (m = 1): caches that pool two tokens into an entry need descriptors of their own.
  *
  *   seq_len, new_len  (device) int32 [n_seq]; n_seq in 0 .. 16384.  A sequence
  *                with a negative length, or with more entries than its row of
@@ -494,7 +495,9 @@ csa2_status csa2_profile_events(void *begin, void *end);
  *                then the number of tokens (sums beyond 2^31 - 1 stay there).
  *   totals       (device) int32 [2]: the tokens, and the pages the step needs
  *                (advance free_head by as many).
- *   Limits: n_pages * page_size and n_seq * swa_cap below 2^31.
+ *   Limits: n_pages * page_size and n_seq * swa_cap below 2^31.  (A step of more
+ *   tokens than csa2_paged_attn's 65,535 is attended to in parts: rows of desc from
+ *   a column on.)
  */
 csa2_status csa2_page_plan(const int32_t *seq_len, const int32_t *new_len, int n_seq, int page_size, int n_pages,
                            const int32_t *free_pages, int n_free, const int32_t *free_head, int32_t *block_table,
@@ -520,7 +523,8 @@ csa2_status csa2_page_plan(const int32_t *seq_len, const int32_t *new_len, int n
  *   q            (device) bf16, token t's 64 heads at q + t * q_stride elements
  *                ([64][512] each; q_stride >= 32768, a multiple of 8); NULL: no
  *                queries.  q_out (device) bf16 [n][64][512]; it may be q itself
- *                where q_stride is 32768, and must not overlap q otherwise.
+ *                where q_stride is 32768, and must not overlap q otherwise (nor may
+ *                any output overlap another input).
  *   latent       (device) bf16, row t at latent + t * latent_stride elements
  *                (>= 512, a multiple of 8); NULL: none.  latent_out (device) bf16
  *                [n][512] or NULL: the normed, rotated latents (the input of
