@@ -541,9 +541,11 @@ __device__ __forceinline__ float power_of_2(int e) { return __uint_as_float((uin
 
 // The V group brings Q of a query into shared memory.  One pass as it is where every head's
 // max |q| lies in [2^-4, 2^15), or is zero or not finite: f16 holds a bf16 value exactly down
-// to 2^-17 and to 2^-25 below; else a second one, each head that does not under the power of
-// two that brings it into [2^14, 2^15).  By heads, as one of them may be 2^40 times another:
-// under one power for all the smaller would become zero.  (The parities, 1 of the group's
+// to 2^-17 and to 2^-25 below; else a second one.  Heads of about one size (2^18) that are too
+// small, or all too large, go under one power of two that brings the largest into [2^14, 2^15)
+// and counts as part of the scale.  Else each head that needs it has its own, a unit, as one of
+// them may be 2^40 times another, and under one power the smaller would become zero: that is
+// slower (see paged_units), so it is not for queries that are small as a whole.  (The parities, 1 of the group's
 // meetings, 2 of q_done, 4 of the queries, rest in shared memory between queries: the copying
 // loop has no register for them.)
 __device__ __forceinline__ void stage_q(const PagedArgs &A, PagedShared &S, unsigned char *sm, int qi, int k) {
@@ -567,19 +569,32 @@ __device__ __forceinline__ void stage_q(const PagedArgs &A, PagedShared &S, unsi
   }
   // (the maxima are read before q_full, and written again after the next q_done)
   paged_meet(A, S, 2, met);
-  const bool scaled = __any_sync(0xFFFFFFFFu, head_power(head_max(S, lane >> 4, lane & 15)) != 0 ||
-                                                  head_power(head_max(S, 2 + (lane >> 4), lane & 15)) != 0);
+  const uint32_t m0 = head_max(S, lane >> 4, lane & 15), m1 = head_max(S, 2 + (lane >> 4), lane & 15);
+  const bool scaled = __any_sync(0xFFFFFFFFu, head_power(m0) != 0 || head_power(m1) != 0);
   // (of the two places for units, the softmax may still read the other for the query before)
   const int place = (int)(met >> 2) & 1;
   met ^= 4;
+  float f = A.scale * 1.4426950408889634f;
   if (__builtin_expect(scaled, 0)) {
+    const bool h0 = m0 != 0u && m0 < 0x7F80u, h1 = m1 != 0u && m1 < 0x7F80u;
+    const int hi = (int)__reduce_max_sync(0xFFFFFFFFu, max(h0 ? m0 : 0u, h1 ? m1 : 0u) >> 7) - 127;
+    const int lo = (int)__reduce_min_sync(0xFFFFFFFFu, min(h0 ? m0 : 0x7F80u, h1 ? m1 : 0x7F80u) >> 7) - 127;
+    const bool units = hi - lo > 18 || (hi >= 15 && lo < 15) || hi < -86;
 #pragma unroll 1
-    for (int i = 0; i < 16; i++) put_q(sm, lt, __ldg(src + i * kPgLoad), i, power_of_2(-head_power(head_max(S, lt >> 6, i))));
-    if (lt < kHeads) S.unit[place][lt] = -power_of_2(head_power(head_max(S, lt & 3, lt >> 2)));
+    for (int i0 = 0; i0 < 16; i0 += 4) {
+      uint4 x[4];
+#pragma unroll
+      for (int i = 0; i < 4; i++) x[i] = __ldg(src + (i0 + i) * kPgLoad);
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        put_q(sm, lt, x[i], i0 + i, power_of_2(-(units ? head_power(head_max(S, lt >> 6, i0 + i)) : hi - 14)));
+    }
+    if (units && lt < kHeads) S.unit[place][lt] = -power_of_2(head_power(head_max(S, lt & 3, lt >> 2)));
+    f *= units ? -1.f : power_of_2(hi - 14);
   }
   if (lt == 0) {
     PagedInfo &I = S.info[k & (kPgInfo - 1)];
-    I.f = A.scale * (scaled ? -1.4426950408889634f : 1.4426950408889634f);
+    I.f = f;
     I.units = place;
   }
   ptx::fence_proxy_async_smem();

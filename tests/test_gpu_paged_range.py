@@ -177,6 +177,22 @@ def test_latents_of_far_positions(lib, pos, base):
     got, room = _bits(out), 2.0**-30 * size + 2.0**-48 * np.abs(ref)
     assert np.all((got == R.round_bf16_bits(ref - room)) | (got == R.round_bf16_bits(ref + room)))
     assert np.count_nonzero(got != R.round_bf16_bits(ref)) <= 8          # (as good as none: 2^-22 of the values lie so close)
+@pytest.mark.parametrize("low,high", [(-5, -5), (-7, -7), (-30, -30), (20, 20), (-12, -2), (-12, 0), (-16, -2), (-25, -2), (10, 16), (15, 25),
+                                      (-95, -92), (-110, -96)])
+def test_queries_small_or_large_as_a_whole(lib, oracle_lib, low, high):
+    """Heads of about one size, out of f16's comfortable range or on its border, beside an ordinary query."""
+    c = Case(oracle_lib, [700, 300], 64, seed=113)
+    q = _decode_queries([700, 300]) + [(0, 130, 129, 0, 100)]
+    want, want_l = c.run(lib, q)
+    p = np.random.default_rng(3).integers(low, high + 1, (3, 64))
+    p[1] = 0
+    x = _scaled(c.q, p)
+    x[2, 8] = 0
+    out, lse = _attend_rows(lib, c, x, q)
+    assert np.array_equal(out[1], want[1]) and np.array_equal(lse[1], want_l[1])
+    _check_heads(c, x, out, lse, q, range(3))
+
+
 # ------------------------------------------------------------------ long rows, and the log-sum-exp to its figure
 def _lse_room(q, k):
     """A bound of the log-sum-exp's error, over the heads of q: that of the logits; the softmax's own sums, 2^-24 an
