@@ -18,6 +18,9 @@ CSA2_KV_NVFP4, CSA2_IDX_MXFP4, CSA2_SWA_MXFP8 = 0, 1, 2
 CSA2_OUT_BF16, CSA2_OUT_F32 = 0, 1
 CSA2_OP_TOPK, CSA2_OP_SPARSE_ATTN, CSA2_OP_DECODE, CSA2_OP_DECODE_HOST, CSA2_OP_DECODE_MQ = 0, 1, 2, 3, 4
 CSA2_OP_BUILD_CACHE, CSA2_OP_DECODE_REINDEX, CSA2_OP_PAGED_ATTN = 5, 6, 7
+CSA2_OP_ATTN_WEIGHT, CSA2_OP_EVICT, CSA2_OP_VERIFY = 8, 9, 10
+CSA2_VERIFY_SAMPLE, CSA2_VERIFY_GREEDY = 0, 1
+CSA2_PROB_BF16, CSA2_PROB_F32, CSA2_PROB_F16 = 0, 1, 2
 STATUS = {0: "CSA2_OK", 1: "CSA2_ERR_INVALID_ARG", 2: "CSA2_ERR_UNSUPPORTED", 3: "CSA2_ERR_CUDA",
           4: "CSA2_ERR_BOUNDS", 5: "CSA2_ERR_TIMEOUT", 6: "CSA2_ERR_WORKSPACE"}
 
@@ -26,7 +29,8 @@ EXPORTS = ["csa2_default_params", "csa2_entry_bytes", "csa2_status_string", "csa
            "csa2_get_device_status", "csa2_topk_noalloc", "csa2_decode", "csa2_decode_host",
            "csa2_index_score_mq", "csa2_decode_mq", "csa2_check_bounded_wait", "csa2_index_key_proj",
            "csa2_build_cache", "csa2_decode_reindex", "csa2_profile_events", "csa2_page_plan", "csa2_qk_norm_rope",
-           "csa2_cache_read", "csa2_paged_attn"]
+           "csa2_cache_read", "csa2_paged_attn", "csa2_page_plan_at", "csa2_attn_weight", "csa2_evict", "csa2_page_trim",
+           "csa2_verify_drafts"]
 
 
 class CSA2Error(RuntimeError):
@@ -53,7 +57,7 @@ def load(path: str = LIB_PATH):
     if not os.path.exists(path):
         raise ImportError(f"libcsa2.so not built at {path}: run __graft_entry__.build()")
     L = ctypes.CDLL(path)
-    P, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+    P, i64, i32, sz, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
     PP = ctypes.POINTER(csa2_params)
     sig = {
         "csa2_default_params": (i32, [PP]),
@@ -82,6 +86,11 @@ def load(path: str = LIB_PATH):
         "csa2_cache_read": (i32, [i32, P, i64, P, i64, P, i32, P]),
         "csa2_paged_attn": (i32, [P, P, i32, i32, P, i64, i32, P, i32, P, i32, P, P, P, P, P, i32, P, i32, P, PP, P, sz,
                                   P]),
+        "csa2_page_plan_at": (i32, [P, P, P, i32, i32, i32, P, i32, P, P, i64, i32, P, i32, P, P, P]),
+        "csa2_attn_weight": (i32, [P, P, i32, i32, P, i64, P, i32, P, i32, P, P, i32, f32, P, P, PP, P, sz, P]),
+        "csa2_evict": (i32, [P, P, i32, i32, P, i64, P, P, i32, i32, P, P, i32, P, i64, P, P, i64, P, sz, P]),
+        "csa2_page_trim": (i32, [P, P, i32, i32, i32, P, i32, P, P, i64, P]),
+        "csa2_verify_drafts": (i32, [i32, P, i64, P, i64, i32, i32, P, P, i32, i32, P, P, P, P, P, sz, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -297,3 +306,45 @@ def csa2_paged_attn(q, pages, n_pages, page_size, block_table, table_stride, n_s
         _ptr(sel), int(sel_stride), _ptr(swa_cache), int(swa_cap), _ptr(q_seq), _ptr(n_vis), _ptr(pos),
         _ptr(swa_first), _ptr(swa_cnt), int(n_q), _ptr(out), int(out_dtype), _ptr(lse), pp, _ptr(workspace),
         int(workspace_bytes), _stream(stream)))
+
+
+def csa2_page_plan_at(seq_len, new_len, gone, n_seq, page_size, n_pages, free_pages, n_free, free_head, block_table,
+                      table_stride, swa_cap, desc, max_tokens, first, totals, stream=None):
+    _check("csa2_page_plan_at", load().csa2_page_plan_at(
+        _ptr(seq_len), _ptr(new_len), _ptr(gone), int(n_seq), int(page_size), int(n_pages), _ptr(free_pages),
+        int(n_free), _ptr(free_head), _ptr(block_table), int(table_stride), int(swa_cap), _ptr(desc), int(max_tokens),
+        _ptr(first), _ptr(totals), _stream(stream)))
+
+
+def csa2_attn_weight(q, pages, n_pages, page_size, block_table, table_stride, first, n_seq, sel, sel_stride, n_vis,
+                     lse, n_q, decay, prior, weight, params=None, workspace=None, workspace_bytes=0, stream=None):
+    pp = ctypes.byref(params) if params is not None else None
+    _check("csa2_attn_weight", load().csa2_attn_weight(
+        _ptr(q), _ptr(pages), int(n_pages), int(page_size), _ptr(block_table), int(table_stride), _ptr(first),
+        int(n_seq), _ptr(sel), int(sel_stride), _ptr(n_vis), _ptr(lse), int(n_q), float(decay), _ptr(prior),
+        _ptr(weight), pp, _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def csa2_evict(pages, weight, n_pages, page_size, block_table, table_stride, seq_len, keep, n_seq, recent, dst_pages,
+               dst_weight, n_dst_pages, dst_table, dst_stride, new_len, from_=None, from_stride=0, workspace=None,
+               workspace_bytes=0, stream=None):
+    _check("csa2_evict", load().csa2_evict(
+        _ptr(pages), _ptr(weight), int(n_pages), int(page_size), _ptr(block_table), int(table_stride), _ptr(seq_len),
+        _ptr(keep), int(n_seq), int(recent), _ptr(dst_pages), _ptr(dst_weight), int(n_dst_pages), _ptr(dst_table),
+        int(dst_stride), _ptr(new_len), _ptr(from_), int(from_stride), _ptr(workspace), int(workspace_bytes),
+        _stream(stream)))
+
+
+def csa2_page_trim(len_, new_len, n_seq, page_size, n_pages, free_pages, n_free, free_head, block_table, table_stride,
+                   stream=None):
+    _check("csa2_page_trim", load().csa2_page_trim(
+        _ptr(len_), _ptr(new_len), int(n_seq), int(page_size), int(n_pages), _ptr(free_pages), int(n_free),
+        _ptr(free_head), _ptr(block_table), int(table_stride), _stream(stream)))
+
+
+def csa2_verify_drafts(mode, target, target_stride, draft, draft_stride, dtype, vocab, tokens, first, n_seq, n_rows, u,
+                       v, kept, next_, workspace=None, workspace_bytes=0, stream=None):
+    _check("csa2_verify_drafts", load().csa2_verify_drafts(
+        int(mode), _ptr(target), int(target_stride), _ptr(draft), int(draft_stride), int(dtype), int(vocab),
+        _ptr(tokens), _ptr(first), int(n_seq), int(n_rows), _ptr(u), _ptr(v), _ptr(kept), _ptr(next_),
+        _ptr(workspace), int(workspace_bytes), _stream(stream)))

@@ -1,6 +1,7 @@
 // C ABI of the CSA2 library: argument checks, workspace sizing, launches.
 // The declarations and the contract of every entry point are in include/csa2.h.
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <math.h>
 #include <string.h>
 
@@ -216,6 +217,21 @@ csa2_status csa2_workspace_size(int op, int n_q, int64_t n_items, int k, size_t 
   }
   if (op == CSA2_OP_PAGED_ATTN) {
     *bytes = paged_attn_workspace_bytes();
+    return CSA2_OK;
+  }
+  if (op == CSA2_OP_ATTN_WEIGHT) {
+    if (k < 0 || k > kTopK || n_q > 65535 || n_items > kPlanMaxSeq) return CSA2_ERR_INVALID_ARG;
+    *bytes = weigh_workspace_bytes(n_q, n_items, k);
+    return CSA2_OK;
+  }
+  if (op == CSA2_OP_EVICT) {
+    if (n_q > kPlanMaxSeq || n_items > INT_MAX) return CSA2_ERR_INVALID_ARG;
+    *bytes = evict_workspace_bytes(n_q, n_items);
+    return CSA2_OK;
+  }
+  if (op == CSA2_OP_VERIFY) {
+    if (n_q > 65535) return CSA2_ERR_INVALID_ARG;
+    *bytes = verify_workspace_bytes(n_q);
     return CSA2_OK;
   }
   if (op == CSA2_OP_DECODE_MQ) {

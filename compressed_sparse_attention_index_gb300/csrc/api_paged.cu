@@ -23,20 +23,21 @@ using namespace csa2;
 
 extern "C" {
 
-csa2_status csa2_page_plan(const int32_t *seq_len, const int32_t *new_len, int n_seq, int page_size, int n_pages,
-                           const int32_t *free_pages, int n_free, const int32_t *free_head, int32_t *block_table,
-                           int64_t table_stride, int swa_cap, int32_t *desc, int max_tokens, int32_t *first,
-                           int32_t *totals, csa2_stream_t stream) {
+csa2_status csa2_page_plan_at(const int32_t *seq_len, const int32_t *new_len, const int32_t *gone, int n_seq,
+                              int page_size, int n_pages, const int32_t *free_pages, int n_free,
+                              const int32_t *free_head, int32_t *block_table, int64_t table_stride, int swa_cap,
+                              int32_t *desc, int max_tokens, int32_t *first, int32_t *totals, csa2_stream_t stream) {
   if (n_seq < 0 || page_size < 1 || n_pages < 1 || n_free < 0 || table_stride < 1 || swa_cap < 0 || max_tokens < 0)
     return CSA2_ERR_INVALID_ARG;
   if ((int64_t)n_pages * page_size > INT_MAX || (int64_t)n_seq * swa_cap > INT_MAX) return CSA2_ERR_UNSUPPORTED;
   if (n_seq > kPlanMaxSeq || table_stride > INT_MAX) return CSA2_ERR_UNSUPPORTED;
   if (!on(first, 4) || !on(totals, 4) || (max_tokens > 0 && !on(desc, 4))) return CSA2_ERR_INVALID_ARG;
   if (n_seq > 0 && (!on(seq_len, 4) || !on(new_len, 4) || !on(block_table, 4))) return CSA2_ERR_INVALID_ARG;
-  if ((n_free > 0 && !on(free_pages, 4)) || !off_or_on(free_head, 4)) return CSA2_ERR_INVALID_ARG;
+  if ((n_free > 0 && !on(free_pages, 4)) || !off_or_on(free_head, 4) || !off_or_on(gone, 4)) return CSA2_ERR_INVALID_ARG;
   PlanArgs P;
   P.seq_len = seq_len;
   P.new_len = new_len;
+  P.gone = gone;
   P.n_seq = n_seq;
   P.page = page_size;
   P.n_pages = n_pages;
@@ -55,6 +56,14 @@ csa2_status csa2_page_plan(const int32_t *seq_len, const int32_t *new_len, int n
   P.status = status_word_ptr();
   if (P.status == nullptr) return CSA2_ERR_CUDA;
   return launch_page_plan(P, (cudaStream_t)stream) == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
+}
+
+csa2_status csa2_page_plan(const int32_t *seq_len, const int32_t *new_len, int n_seq, int page_size, int n_pages,
+                           const int32_t *free_pages, int n_free, const int32_t *free_head, int32_t *block_table,
+                           int64_t table_stride, int swa_cap, int32_t *desc, int max_tokens, int32_t *first,
+                           int32_t *totals, csa2_stream_t stream) {
+  return csa2_page_plan_at(seq_len, new_len, nullptr, n_seq, page_size, n_pages, free_pages, n_free, free_head,
+                           block_table, table_stride, swa_cap, desc, max_tokens, first, totals, stream);
 }
 
 csa2_status csa2_qk_norm_rope(const void *q, int64_t q_stride, const float *q_gain, void *q_out, const void *latent,

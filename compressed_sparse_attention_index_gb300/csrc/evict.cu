@@ -1,0 +1,570 @@
+// Eviction from paged caches by accumulated attention weight (csa2_evict), and giving pages
+// behind a new length back (csa2_page_trim).
+//
+// Of a sequence's n entries the last min(recent, k) stay, and of the others the heaviest, k in
+// all; they move together, in order, to places 0 .. k - 1.  Two launches:
+//
+// evict_select_kernel: a cluster per sequence finds the smallest weight that stays, as an order key,
+// by histograms of up to 11 bits at a time below the bits that all keys share (at most three, of one
+// pass each; the keys stay in shared memory where a CTA's part of the row fits).  Each warp has a
+// contiguous part of the row, so that one count of every part gives every kept entry its rank, and
+// writes which entry each new place comes from.
+//
+// evict_move_kernel: tiles of kMvTile new places, read whole and then written.  In place, a tile's
+// places may hold entries that are still to be moved, but only those of its own and of earlier tiles
+// (an entry never moves behind its place, so ranks are not above places): tiles are handed out in order, each
+// raises a flag when it has read, and before it writes waits for the at most two tiles that its places'
+// entries belong to.  A tile that is waited for has been handed out, and reads without waiting for any.
+//
+// What bounds it: 288 B read and written for each entry that stays (HBM).
+#include <limits.h>
+
+#include "common.cuh"
+#include "launch.cuh"
+#include "tc_ptx.cuh"
+
+namespace csa2 {
+
+constexpr int kEvThreads = 1024, kEvWarps = kEvThreads / 32, kEvBits = 11, kEvBins = 1 << kEvBits;
+constexpr int kEvMaxCtas = 16;
+constexpr int kMvTile = 128, kMvThreads = 288, kMvUnits = 8;     // a record is 18 units of 16 B
+static_assert(kMvThreads / 18 * kMvUnits == kMvTile, "a tile's units");
+
+// ------------------------------------------------------------------ workspace
+// per sequence: {n, k, entries of the row it reads, -}; the ticket; then from, before, flags
+struct EvictWs {
+  int4 *meta;
+  uint32_t *ticket;
+  int32_t *from;
+  int64_t from_stride;
+  int32_t *before;            // kept entries ahead of every kMvTile-th place
+  uint32_t *flag;             // of each tile: read
+  int64_t tile_stride;
+};
+static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+size_t evict_workspace_bytes(int n_seq, int64_t row) {
+  const size_t tiles = (size_t)(row / kMvTile + 2);
+  return 256 + up256((size_t)n_seq * sizeof(int4)) + up256((size_t)n_seq * (size_t)row * 4) + 2 * up256((size_t)n_seq * tiles * 4);
+}
+static EvictWs evict_ws(void *ws, int n_seq, int64_t row) {
+  char *p = static_cast<char *>(ws);
+  EvictWs W;
+  W.ticket = reinterpret_cast<uint32_t *>(p);
+  p += 256;
+  W.meta = reinterpret_cast<int4 *>(p);
+  p += up256((size_t)n_seq * sizeof(int4));
+  W.from = reinterpret_cast<int32_t *>(p);
+  W.from_stride = row;
+  p += up256((size_t)n_seq * (size_t)row * 4);
+  W.tile_stride = row / kMvTile + 2;
+  W.before = reinterpret_cast<int32_t *>(p);
+  p += up256((size_t)n_seq * (size_t)W.tile_stride * 4);
+  W.flag = reinterpret_cast<uint32_t *>(p);
+  return W;
+}
+
+// ------------------------------------------------------------------ select
+__device__ __forceinline__ void ev_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t ev_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The word at the place of p (this CTA's shared memory) in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t ev_get(const uint32_t *p, uint32_t rank) {
+  uint32_t a, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+struct EvictShared {
+  uint32_t hist[kEvBins];
+  uint32_t lo[kEvWarps], hi[kEvWarps], gt[kEvWarps], eq[kEvWarps];
+  uint32_t minmax[2], count[2], found[3];
+};
+
+// Order key of entry j's weight, larger is heavier (NaN: 0, below everything).
+struct EvictRow {
+  const float *weight;
+  const int32_t *table;
+  int page, n_pages;
+  uint64_t mul;
+  int shift;
+  int *status;
+  __device__ __forceinline__ int col(int j) const { return (int)(((uint64_t)(unsigned)j * mul) >> shift); }
+  __device__ __forceinline__ int64_t slot(int j, int c) const {
+    const int id = __ldg(table + c);
+    return id >= 0 && id < n_pages ? (int64_t)id * page + (j - c * page) : -1;
+  }
+  __device__ __forceinline__ uint32_t key(float w) const { return w == w ? order_key(w) : 0u; }
+  // four entries from j on, those below n (0 elsewhere)
+  __device__ __forceinline__ void keys(int j, int n, bool report, uint32_t (&x)[4]) const {
+    if ((page & 3) == 0 && j + 3 < n) {              // (one page holds them, on a 16-byte boundary)
+      const int64_t s = slot(j, col(j));
+      if (s >= 0) {
+        const float4 w = __ldg(reinterpret_cast<const float4 *>(weight + s));
+        x[0] = key(w.x);
+        x[1] = key(w.y);
+        x[2] = key(w.z);
+        x[3] = key(w.w);
+      } else {
+        x[0] = x[1] = x[2] = x[3] = 0u;
+        if (report) record_error(status, CSA2_ERR_BOUNDS);
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      x[i] = 0u;
+      if (j + i < n) {
+        const int64_t s = slot(j + i, col(j + i));
+        if (s >= 0) x[i] = key(__ldg(weight + s));
+        else if (report) record_error(status, CSA2_ERR_BOUNDS);
+      }
+    }
+  }
+};
+
+__global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_constant__ EvictArgs A, EvictWs W, int cache_keys) {
+  extern __shared__ __align__(16) uint32_t ev_keys[];          // the CTA's keys, if they fit
+  __shared__ EvictShared S;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, ctas = gridDim.x, b = blockIdx.y;
+  const uint32_t rank = ev_rank();
+  griddep_wait();
+  griddep_launch();
+  const int64_t row = A.table_stride * A.page, dst_row = A.dst_stride * A.page;
+  int n = __ldg(A.seq_len + b), k = __ldg(A.keep + b);
+  const bool bad = n < 0 || k < 0 || n > row || min(n, k) > dst_row || (A.from != nullptr && min(n, k) > A.from_stride);
+  if (bad) {
+    if (t == 0 && rank == 0) record_error(A.status, CSA2_ERR_BOUNDS);
+    if (!A.in_place) n = 0;
+    k = 0;
+  }
+  k = min(n, k);
+  if (t == 0 && rank == 0) {
+    // (a sequence that is out of range keeps its length and moves nothing)
+    W.meta[b] = make_int4(n, k, bad ? n : k, 0);
+    if (b == 0) *W.ticket = 0u;
+  }
+  const int last = min(A.recent, k), m = n - last, kk = k - last;        // candidates, those of them that stay
+  const int tiles = (n + kMvTile - 1) / kMvTile;
+  // contiguous parts of whole tiles: of the CTAs, of their warps
+  const int per_cta = (tiles + ctas - 1) / ctas, t0 = min((int)rank * per_cta, tiles), t1 = min(t0 + per_cta, tiles);
+  const int per_warp = (t1 - t0 + kEvWarps - 1) / kEvWarps;
+  const int w0 = min(t0 + warp * per_warp, t1), w1 = min(w0 + per_warp, t1);
+  for (int i = t0 + t; i < t1; i += kEvThreads) W.flag[(int64_t)b * W.tile_stride + i] = 0u;
+  if (bad || k == 0) return;                         // (the whole cluster)
+  EvictRow R;
+  R.weight = A.weight;
+  R.table = A.table + (int64_t)b * A.table_stride;
+  R.page = A.page;
+  R.n_pages = A.n_pages;
+  R.mul = A.page_mul;
+  R.shift = A.page_shift;
+  R.status = A.status;
+  const bool cached = (t1 - t0) * kMvTile <= cache_keys;
+  uint32_t *mine = ev_keys + (size_t)(w0 - t0) * kMvTile;      // this warp's part
+  auto keys_of = [&](int tile, uint32_t (&x)[4]) {
+    if (cached) {
+      const uint4 y = *reinterpret_cast<const uint4 *>(mine + (tile - w0) * kMvTile + lane * 4);
+      x[0] = y.x;
+      x[1] = y.y;
+      x[2] = y.z;
+      x[3] = y.w;
+    } else {
+      R.keys(tile * kMvTile + lane * 4, n, false, x);
+    }
+  };
+  // ---------------------------------------------------- the bits that all candidates share
+  uint32_t lo = 0xFFFFFFFFu, hi = 0u;
+#pragma unroll 4
+  for (int tile = w0; tile < w1; tile++) {
+    const int j = tile * kMvTile + lane * 4;
+    uint32_t x[4];
+    R.keys(j, n, true, x);
+    if (cached) *reinterpret_cast<uint4 *>(mine + (tile - w0) * kMvTile + lane * 4) = make_uint4(x[0], x[1], x[2], x[3]);
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      if (j + i < m) {
+        lo = min(lo, x[i]);
+        hi = max(hi, x[i]);
+      }
+  }
+  uint32_t T = 0u, ties = 0u;                        // stay: keys above T, and the first `ties` of those at T
+  if (kk > 0 && kk < m) {
+    lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+    hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+    if (lane == 0) {
+      S.lo[warp] = lo;
+      S.hi[warp] = hi;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      lo = __reduce_min_sync(0xFFFFFFFFu, S.lo[lane]);
+      hi = __reduce_max_sync(0xFFFFFFFFu, S.hi[lane]);
+      if (lane == 0) {
+        S.minmax[0] = lo;
+        S.minmax[1] = hi;
+      }
+    }
+    __syncthreads();
+    ev_cluster_sync();
+    lo = lane < ctas ? ev_get(&S.minmax[0], (uint32_t)lane) : 0xFFFFFFFFu;
+    hi = lane < ctas ? ev_get(&S.minmax[1], (uint32_t)lane) : 0u;
+    lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+    hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+    int low = 32 - __clz((int)(lo ^ hi));            // bits that are not known yet (0: all keys are one)
+    uint32_t known = low == 32 ? 0u : hi >> low, need = (uint32_t)kk;
+    while (low > 0) {
+      const int w = min(kEvBits, low);
+      for (int i = t; i < kEvBins; i += kEvThreads) S.hist[i] = 0u;
+      __syncthreads();
+      const uint32_t mask = (1u << w) - 1u;
+      for (int tile = w0; tile < w1; tile++) {
+        const int j = tile * kMvTile + lane * 4;
+        uint32_t x[4];
+        keys_of(tile, x);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          if (j + i < m && (low == 32 || x[i] >> low == known)) atomicAdd(&S.hist[(x[i] >> (low - w)) & mask], 1u);
+      }
+      __syncthreads();
+      ev_cluster_sync();
+      // the digit at which the count from the top passes `need`: thread t has bins 2 t and 2 t + 1
+      static_assert(kEvBins == 2 * kEvThreads, "two bins a thread");
+      uint32_t h0 = 0u, h1 = 0u;
+      for (int c = 0; c < ctas; c++) {
+        h0 += ev_get(&S.hist[2 * t], (uint32_t)c);
+        h1 += ev_get(&S.hist[2 * t + 1], (uint32_t)c);
+      }
+      uint32_t above = h0 + h1;                      // of this thread's bins and all above them
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_down_sync(0xFFFFFFFFu, above, o);
+        if (lane + o < 32) above += y;
+      }
+      if (lane == 0) S.lo[warp] = above;
+      __syncthreads();
+      for (int i = warp + 1; i < kEvWarps; i++) above += S.lo[i];
+      const uint32_t top1 = above - h0 - h1, top0 = above - h0;          // above bin 2 t + 1, above bin 2 t
+      if (top1 < need && need <= top1 + h1) {
+        S.found[0] = (uint32_t)(2 * t + 1);
+        S.found[1] = need - top1;
+      } else if (top0 < need && need <= above) {
+        S.found[0] = (uint32_t)(2 * t);
+        S.found[1] = need - top0;
+      }
+      __syncthreads();
+      known = known << w | S.found[0];
+      need = S.found[1];
+      low -= w;
+      ev_cluster_sync();                             // (the histograms are read, everywhere)
+    }
+    T = known;
+    ties = need;
+  } else if (kk == 0) {
+    T = 0xFFFFFFFFu;                                 // (none: no key is above, and no tie stays)
+  }
+  const bool all = kk == m;
+  // ---------------------------------------------------- ranks
+  uint32_t gt = 0u, eq = 0u;
+  for (int tile = w0; tile < w1; tile++) {
+    const int j = tile * kMvTile + lane * 4;
+    uint32_t x[4];
+    keys_of(tile, x);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      gt += (j + i < n && (j + i >= m || all || x[i] > T)) ? 1u : 0u;
+      eq += (j + i < m && !all && x[i] == T) ? 1u : 0u;
+    }
+  }
+  gt = __reduce_add_sync(0xFFFFFFFFu, gt);
+  eq = __reduce_add_sync(0xFFFFFFFFu, eq);
+  if (lane == 0) {
+    S.gt[warp] = gt;
+    S.eq[warp] = eq;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const uint32_t a = __reduce_add_sync(0xFFFFFFFFu, S.gt[lane]), c = __reduce_add_sync(0xFFFFFFFFu, S.eq[lane]);
+    if (lane == 0) {
+      S.count[0] = a;
+      S.count[1] = c;
+    }
+  }
+  __syncthreads();
+  ev_cluster_sync();
+  gt = lane < (int)rank ? ev_get(&S.count[0], (uint32_t)lane) : 0u;
+  eq = lane < (int)rank ? ev_get(&S.count[1], (uint32_t)lane) : 0u;
+  gt += lane < warp ? S.gt[lane] : 0u;
+  eq += lane < warp ? S.eq[lane] : 0u;
+  gt = __reduce_add_sync(0xFFFFFFFFu, gt);           // ahead of this warp's part
+  eq = __reduce_add_sync(0xFFFFFFFFu, eq);
+  ev_cluster_sync();                                 // (nothing of this CTA is read from here on)
+  int32_t *from = W.from + (int64_t)b * W.from_stride, *before = W.before + (int64_t)b * W.tile_stride;
+  int32_t *out = A.from != nullptr ? A.from + (int64_t)b * A.from_stride : nullptr;
+  for (int tile = w0; tile < w1; tile++) {
+    const int j = tile * kMvTile + lane * 4;
+    uint32_t x[4];
+    keys_of(tile, x);
+    if (lane == 0) before[tile] = (int32_t)(gt + min(eq, ties));
+    uint32_t g = 0u, e = 0u;                         // bits of the lane's entries that stay for sure, that tie
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      if (j + i < n && (j + i >= m || all || x[i] > T)) g |= 1u << i;
+      if (j + i < m && !all && x[i] == T) e |= 1u << i;
+    }
+    uint32_t sum = (uint32_t)__popc(g) | (uint32_t)__popc(e) << 16;      // (at most 128 each)
+    const uint32_t own = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    uint32_t a = gt + ((sum - own) & 0xFFFFu), c = eq + ((sum - own) >> 16);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const bool tie = (e >> i) & 1u;
+      if (((g >> i) & 1u) || (tie && c < ties)) {
+        const uint32_t r = a + min(c, ties);
+        from[r] = j + i;
+        if (out != nullptr) out[r] = j + i;
+      }
+      a += (g >> i) & 1u;
+      c += tie ? 1u : 0u;
+    }
+    const uint32_t all_sum = __shfl_sync(0xFFFFFFFFu, sum, 31);
+    gt += all_sum & 0xFFFFu;
+    eq += all_sum >> 16;
+  }
+  if (w1 == tiles && w0 < w1 && lane == 0) before[tiles] = k;
+}
+
+// ------------------------------------------------------------------ move
+// Loads that stay where they stand between barriers (what they read is written by other CTAs of the
+// same launch once this one has said that it has read it).
+__device__ __forceinline__ uint4 mv_load16(const uint8_t *p) {
+  uint4 v;
+  asm volatile("ld.relaxed.gpu.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float mv_load4(const float *p) {
+  float v;
+  asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(kMvThreads, 4) evict_move_kernel(const __grid_constant__ EvictArgs A, EvictWs W) {
+  __shared__ int64_t src_sh[kMvTile], dst_sh[kMvTile];
+  __shared__ uint32_t next_sh;
+  const int t = threadIdx.x, lane = t & 31;
+  griddep_wait();
+  griddep_launch();
+  if (blockIdx.x == 0)
+    for (int b = t; b < A.n_seq; b += kMvThreads) A.new_len[b] = W.meta[b].z;
+  // tiles of all sequences are numbered in order; the cursor moves on with the tile number
+  int b0 = 0;                                        // 32 sequences from b0 on have tiles from base on
+  int64_t base = 0;
+  uint32_t tile = blockIdx.x;
+  for (;; tile += gridDim.x) {
+    if (A.in_place) {
+      if (t == 0) next_sh = atomicAdd(W.ticket, 1u);
+      __syncthreads();
+      tile = next_sh;
+    }
+    // (every warp finds the sequence for itself)
+    int b = -1, i = 0, k = 0, n = 0;
+    while (b0 < A.n_seq) {
+      const int4 M = b0 + lane < A.n_seq ? W.meta[b0 + lane] : make_int4(0, 0, 0, 0);
+      const int own = (M.y + kMvTile - 1) / kMvTile;
+      int64_t inc = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      const uint32_t past = __ballot_sync(0xFFFFFFFFu, (int64_t)tile < base + inc);
+      if (past != 0u) {
+        const int from = __ffs((int)past) - 1;
+        b = b0 + from;
+        i = (int)((int64_t)tile - (base + __shfl_sync(0xFFFFFFFFu, inc - own, from)));
+        n = __shfl_sync(0xFFFFFFFFu, M.x, from);
+        k = __shfl_sync(0xFFFFFFFFu, M.y, from);
+        break;
+      }
+      base += __shfl_sync(0xFFFFFFFFu, inc, 31);
+      b0 += 32;
+    }
+    if (b < 0) return;                               // (no tile is left: the whole CTA)
+    const int r0 = i * kMvTile, rows = min(kMvTile, k - r0);
+    const int32_t *table = A.table + (int64_t)b * A.table_stride, *dst_table = A.dst_table + (int64_t)b * A.dst_stride;
+    bool there = true;                               // the entry is where it goes
+    if (t < rows) {
+      const int j = __ldg(W.from + (int64_t)b * W.from_stride + r0 + t), r = r0 + t;
+      const int cs = (int)(((uint64_t)(unsigned)j * A.page_mul) >> A.page_shift), cd = (int)(((uint64_t)(unsigned)r * A.page_mul) >> A.page_shift);
+      const int ps = __ldg(table + cs), pd = __ldg(dst_table + cd);
+      there = A.in_place && j == r;
+      const bool ok = ps >= 0 && ps < A.n_pages && pd >= 0 && pd < A.n_dst;
+      if (!ok) record_error(A.status, CSA2_ERR_BOUNDS);
+      src_sh[t] = ok ? (int64_t)ps * A.page + (j - cs * A.page) : -1;
+      dst_sh[t] = ok ? (int64_t)pd * A.page + (r - cd * A.page) : -1;
+    }
+    const bool still = __syncthreads_and(there) != 0;
+    uint32_t *flag = W.flag + (int64_t)b * W.tile_stride;
+    if (still) {
+      if (A.in_place && t == 0) ptx::st_release_u32(flag + i, 1u);
+      __syncthreads();
+      continue;
+    }
+    uint4 x[kMvUnits];
+    float w = 0.f;
+    const int unit = t % 18, sub = t / 18;
+#pragma unroll
+    for (int u = 0; u < kMvUnits; u++) {
+      const int r = u * (kMvThreads / 18) + sub;
+      x[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rows && src_sh[r] >= 0) x[u] = mv_load16(A.pages + src_sh[r] * kKvBytes + unit * 16);
+    }
+    if (t < rows && src_sh[t] >= 0) w = mv_load4(A.weight + src_sh[t]);
+    if (A.in_place) {
+      __threadfence();
+      __syncthreads();                               // (all of the tile is read)
+      if (t == 0) {
+        ptx::st_release_u32(flag + i, 1u);
+        // the entries at places r0 .. r0 + 127 (those below n) have ranks [lo, hi): one tile or two, none behind this one
+        const int32_t *before = W.before + (int64_t)b * W.tile_stride;
+        const int lo = __ldcg(before + i), hi = r0 + kMvTile <= n ? __ldcg(before + i + 1) : k;
+        for (int x = lo / kMvTile; x <= (hi - 1) / kMvTile && lo < hi; x++)
+          if (x != i && !ptx::poll_at_least_u32(flag + x, 1u)) {
+            record_error(A.status, CSA2_ERR_TIMEOUT);
+            break;
+          }
+        __threadfence();
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int u = 0; u < kMvUnits; u++) {
+      const int r = u * (kMvThreads / 18) + sub;
+      if (r < rows && dst_sh[r] >= 0) __stcs(reinterpret_cast<uint4 *>(A.dst_pages + dst_sh[r] * kKvBytes + unit * 16), x[u]);
+    }
+    if (t < rows && dst_sh[t] >= 0) A.dst_weight[dst_sh[t]] = w;
+    __syncthreads();                                 // (the slots are read)
+  }
+}
+
+// j / n by a multiplication, exact for j below 2^31
+static void evict_magic(unsigned n, uint64_t &mul, int &shift) {
+  int s = 0;
+  while (((int64_t)1 << s) < (int64_t)n) s++;
+  shift = 31 + s;
+  mul = (uint64_t)((((unsigned __int128)1 << shift) + n - 1) / n);
+}
+
+cudaError_t launch_evict(EvictArgs A, void *ws, cudaStream_t st) {
+  const int dev = current_device();
+  constexpr int kKeys = 49152;                       // 192 KB of them
+  static std::atomic<int> attr_done[kMaxDevices];
+  cudaError_t e = once_per_device(attr_done, dev, [&] {
+    const cudaError_t f = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeys * 4);
+    return f != cudaSuccess ? f : cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  });
+  if (e != cudaSuccess) return e;
+  const int64_t sms = device_sm_count(dev), row = A.table_stride * A.page;
+  evict_magic((unsigned)A.page, A.page_mul, A.page_shift);
+  const EvictWs W = evict_ws(ws, A.n_seq, row);
+  // CTAs of a row: one for each 8,192 entries, up to 16, while the sequences leave SMs for more
+  int ctas = 1;
+  while (ctas < kEvMaxCtas && (int64_t)ctas * 8192 < row && (int64_t)A.n_seq * ctas * 2 <= sms) ctas *= 2;
+  const int64_t share = ((row + kMvTile - 1) / kMvTile + ctas - 1) / ctas * kMvTile;
+  const int keys = share <= kKeys ? (int)share : 0;
+  e = launch_pdl(evict_select_kernel, dim3((unsigned)ctas, (unsigned)A.n_seq), dim3(kEvThreads), (size_t)keys * 4, st, (unsigned)ctas, A, W, keys);
+  if (e != cudaSuccess) return e;
+  // no more CTAs than there can be tiles
+  const int64_t dst_row = A.dst_stride * A.page, most = dst_row < row ? dst_row : row;
+  const int64_t tiles = A.n_seq * ((most + kMvTile - 1) / kMvTile), grid = tiles < 4 * sms ? tiles : 4 * sms;
+  return launch_pdl(evict_move_kernel, dim3((unsigned)grid), dim3(kMvThreads), 0, st, 1u, A, W);
+}
+
+// ------------------------------------------------------------------ trim
+// One CTA: pages behind the new lengths, counted by a prefix sum over the sequences, found by a
+// binary search each.  (One, because the list's head is read by all and written at the end.)
+__global__ void __launch_bounds__(kPlanThreads) page_trim_kernel(const __grid_constant__ TrimArgs A) {
+  extern __shared__ int trim_sh[];                   // pages given back ahead of each sequence, [n_seq + 1]
+  __shared__ int wt[kPlanThreads / 32];
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  griddep_wait();
+  griddep_launch();
+  const int per = (A.n_seq + kPlanThreads - 1) / kPlanThreads, b0 = min(t * per, A.n_seq), b1 = min(b0 + per, A.n_seq);
+  auto columns = [&](int b, int &c0) -> int {        // -1: out of range
+    const int len = __ldg(A.len + b), to = __ldg(A.new_len + b);
+    if (len < 0 || to < 0 || to > len || len > A.row_cap) return -1;
+    c0 = (int)(((unsigned)to + (unsigned)A.page - 1u) / (unsigned)A.page);
+    return (int)(((unsigned)len + (unsigned)A.page - 1u) / (unsigned)A.page) - c0;
+  };
+  int sum = 0, c0 = 0;
+  bool err = false;
+  for (int b = b0; b < b1; b++) {
+    const int c = columns(b, c0);
+    err |= c < 0;
+    sum = (int)min((unsigned)sum + (unsigned)max(c, 0), (unsigned)INT_MAX);
+  }
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc = (int)min((unsigned)inc + (unsigned)y, (unsigned)INT_MAX);
+  }
+  if (lane == 31) wt[warp] = inc;
+  int ahead = __shfl_up_sync(0xFFFFFFFFu, inc, 1);
+  if (lane == 0) ahead = 0;
+  __syncthreads();
+  for (int w = 0; w < warp; w++) ahead = (int)min((unsigned)ahead + (unsigned)wt[w], (unsigned)INT_MAX);
+  for (int b = b0; b < b1; b++) {
+    trim_sh[b] = ahead;
+    ahead = (int)min((unsigned)ahead + (unsigned)max(columns(b, c0), 0), (unsigned)INT_MAX);
+  }
+  if (t == kPlanThreads - 1) trim_sh[A.n_seq] = ahead;
+  const int head = *A.free_head;
+  __syncthreads();
+  const int total = trim_sh[A.n_seq];
+  // more pages than were taken from the list, or a head outside it: nothing is given back
+  const bool fits = head >= 0 && head <= A.n_free && total <= head;
+  err |= !fits;
+  if (fits) {
+    for (int i = t; i < total; i += kPlanThreads) {
+      int lo = 0, hi = A.n_seq;                      // the last sequence with trim_sh <= i
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (trim_sh[mid] <= i) lo = mid;
+        else hi = mid;
+      }
+      columns(lo, c0);
+      int32_t *at = A.table + (int64_t)lo * A.table_stride + c0 + (i - trim_sh[lo]);
+      const int id = *at;
+      err |= id < 0 || id >= A.n_pages;
+      A.free_pages[head - total + i] = id;
+      *at = -1;
+    }
+    if (t == 0) *A.free_head = head - total;
+  }
+  if (err) record_error(A.status, CSA2_ERR_BOUNDS);
+}
+
+cudaError_t launch_page_trim(const TrimArgs &A, cudaStream_t st) {
+  const int dev = current_device();
+  static std::atomic<int> attr_done[kMaxDevices];
+  const cudaError_t e = once_per_device(attr_done, dev, [&] {
+    return cudaFuncSetAttribute(page_trim_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kPlanMaxSeq + 1) * (int)sizeof(int));
+  });
+  if (e != cudaSuccess) return e;
+  return launch_pdl(page_trim_kernel, dim3(1), dim3(kPlanThreads), (size_t)(A.n_seq + 1) * sizeof(int), st, 1u, A);
+}
+
+}  // namespace csa2

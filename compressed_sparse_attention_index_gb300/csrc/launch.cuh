@@ -255,6 +255,7 @@ cudaError_t launch_qk_norm_rope(NormArgs A, double eps, double rope_base, cudaSt
 constexpr int kPlanThreads = 1024, kPlanMaxSeq = 16384;
 struct PlanArgs {
   const int32_t *seq_len, *new_len;
+  const int32_t *gone;        // null: none
   int n_seq, page, n_pages;
   const int32_t *free_pages;
   int n_free;
@@ -301,6 +302,85 @@ struct PagedArgs {
 };
 size_t paged_attn_workspace_bytes();
 cudaError_t launch_paged_attn(PagedArgs A, double rope_base, void *ws, cudaStream_t st);
+
+// csa2_attn_weight (see csa2.h).
+struct WeighArgs {
+  const uint16_t *q;
+  const uint8_t *pages;
+  int n_pages, page;
+  const int32_t *table;
+  int64_t table_stride;
+  const int32_t *first;
+  int n_seq;
+  const int32_t *sel;         // null: every visible entry
+  int sel_stride;
+  const int32_t *n_vis;
+  const float *lse;
+  int n_q;
+  float decay;
+  const float *prior;         // null: zeros
+  float *weight;
+  int *status;
+  float scale;
+  uint64_t page_mul;          // j / page as (j * page_mul) >> page_shift
+  int page_shift;
+};
+size_t weigh_workspace_bytes(int n_q, int64_t n_seq, int sel_stride);
+cudaError_t launch_weigh(WeighArgs A, void *ws, cudaStream_t st);
+
+// csa2_evict (see csa2.h).
+struct EvictArgs {
+  const uint8_t *pages;
+  const float *weight;
+  int n_pages, page;
+  const int32_t *table;
+  int64_t table_stride;
+  const int32_t *seq_len, *keep;
+  int n_seq, recent;
+  uint8_t *dst_pages;
+  float *dst_weight;
+  int n_dst;
+  const int32_t *dst_table;
+  int64_t dst_stride;
+  int in_place;               // the destination is the source
+  int32_t *new_len;
+  int32_t *from;              // null: not wanted
+  int64_t from_stride;
+  int *status;
+  uint64_t page_mul;          // j / page as (j * page_mul) >> page_shift
+  int page_shift;
+};
+size_t evict_workspace_bytes(int n_seq, int64_t row);
+cudaError_t launch_evict(EvictArgs A, void *ws, cudaStream_t st);
+
+// csa2_page_trim (see csa2.h).
+struct TrimArgs {
+  const int32_t *len, *new_len;
+  int n_seq, page, n_pages;
+  int32_t *free_pages;
+  int n_free;
+  int32_t *free_head, *table;
+  int64_t table_stride, row_cap;
+  int *status;
+};
+cudaError_t launch_page_trim(const TrimArgs &A, cudaStream_t st);
+
+// csa2_verify_drafts (see csa2.h).
+struct VerifyArgs {
+  const void *target;
+  int64_t target_stride;
+  const void *draft;          // null: drafts were not drawn
+  int64_t draft_stride;
+  int vocab;
+  const int32_t *tokens, *first;
+  int n_seq, n_rows;
+  const float *u, *v;
+  int32_t *kept, *next;
+  unsigned long long *best;   // greedy: scratch
+  int *status;
+};
+size_t verify_workspace_bytes(int n_rows);
+cudaError_t launch_verify(const VerifyArgs &A, int dtype, bool greedy, cudaStream_t st);
 
 cudaError_t launch_bounded_wait_check(int *status, unsigned long long limit_ns, cudaStream_t st);
 

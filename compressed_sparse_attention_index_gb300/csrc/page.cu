@@ -19,6 +19,7 @@ namespace csa2 {
 // itself in shared memory (8 B a sequence from L2, cheaper than a grid-wide
 // barrier or a second launch).  Latency-bound for a decode step; for a prompt
 // the 28 B written per token.
+// Places and positions are the same until a sequence loses entries (gone of them).
 struct PlanSeq {
   int len, add, have, need;
 };
@@ -32,7 +33,8 @@ __device__ __forceinline__ PlanSeq plan_seq(const PlanArgs &P, int b, bool &bad)
   s.len = __ldg(P.seq_len + b);
   s.add = __ldg(P.new_len + b);
   // a sequence that cannot be: it takes no part in the step
-  bad = s.len < 0 || s.add < 0 || (int64_t)s.len + s.add > P.row_cap;
+  const int gone = P.gone != nullptr ? __ldg(P.gone + b) : 0;
+  bad = s.len < 0 || s.add < 0 || (int64_t)s.len + s.add > P.row_cap || gone < 0 || (int64_t)s.len + s.add + gone > INT_MAX;
   if (bad) s.len = s.add = 0;
   s.have = (int)(((unsigned)s.len + (unsigned)P.page - 1u) / (unsigned)P.page);
   s.need = (int)(((unsigned)(s.len + s.add) + (unsigned)P.page - 1u) / (unsigned)P.page);
@@ -114,7 +116,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
       const int b = seq_of(tok, P.n_seq, (int)i);              // (has tokens, so its lengths are sound)
       const int len = __ldg(P.seq_len + b), add = __ldg(P.new_len + b);
       const int have = (int)(((unsigned)len + (unsigned)P.page - 1u) / (unsigned)P.page);
-      const int pos = len + ((int)i - tok[b]), col = (int)((unsigned)pos / (unsigned)P.page);
+      const int place = len + ((int)i - tok[b]), col = (int)((unsigned)place / (unsigned)P.page);
+      const int gone = P.gone != nullptr ? __ldg(P.gone + b) : 0, pos = place + gone;
       int id;
       if (col < have) {                                      // (columns that this step does not write)
         id = P.block_table[(int64_t)b * P.table_stride + col];
@@ -125,15 +128,15 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
       err |= id < 0;
       const int cnt = min(min(kSwa, P.swa_cap), pos + 1);
       v[0] = b;
-      v[1] = pos + 1;
+      v[1] = place + 1;
       v[2] = pos;
       v[3] = P.swa_cap > 0 ? (int)((unsigned)(pos + 1 - cnt) % (unsigned)P.swa_cap) : 0;
       v[4] = cnt;
-      v[5] = id < 0 ? -1 : id * P.page + (pos - col * P.page);
+      v[5] = id < 0 ? -1 : id * P.page + (place - col * P.page);
       // a ring slot that a later token of this step takes again is not written (a token
       // without a descriptor takes none)
       const int kept = min(add, P.max_tokens - tok[b]);
-      v[6] = P.swa_cap > 0 && (int64_t)pos + P.swa_cap >= (int64_t)len + kept
+      v[6] = P.swa_cap > 0 && (int64_t)place + P.swa_cap >= (int64_t)len + kept
                  ? b * P.swa_cap + (int)((unsigned)pos % (unsigned)P.swa_cap)
                  : -1;
     }

@@ -13,7 +13,9 @@
  * sequences' lengths (csa2_page_plan), the norm, rotation and cache write of its
  * tokens (csa2_qk_norm_rope), reading records back (csa2_cache_read), and
  * attention over paged latents, all visible ones or a selection
- * (csa2_paged_attn).
+ * (csa2_paged_attn); and what such a cache keeps: the attention weight that its
+ * entries get (csa2_attn_weight), eviction by it (csa2_evict), the verification
+ * of drafted tokens (csa2_verify_drafts), pages given back (csa2_page_trim).
  *
  * Conventions (every entry point):
  *   - Returns a csa2_status.  Nothing aborts, prints or allocates device memory.
@@ -86,7 +88,11 @@ enum { CSA2_KV_NVFP4 = 0, CSA2_IDX_MXFP4 = 1, CSA2_SWA_MXFP8 = 2 };
 enum { CSA2_OUT_BF16 = 0, CSA2_OUT_F32 = 1 };
 /* Operations for csa2_workspace_size. */
 enum { CSA2_OP_TOPK = 0, CSA2_OP_SPARSE_ATTN = 1, CSA2_OP_DECODE = 2, CSA2_OP_DECODE_HOST = 3, CSA2_OP_DECODE_MQ = 4,
-       CSA2_OP_BUILD_CACHE = 5, CSA2_OP_DECODE_REINDEX = 6, CSA2_OP_PAGED_ATTN = 7 };
+       CSA2_OP_BUILD_CACHE = 5, CSA2_OP_DECODE_REINDEX = 6, CSA2_OP_PAGED_ATTN = 7, CSA2_OP_ATTN_WEIGHT = 8,
+       CSA2_OP_EVICT = 9, CSA2_OP_VERIFY = 10 };
+/* Modes and types of csa2_verify_drafts. */
+enum { CSA2_VERIFY_SAMPLE = 0, CSA2_VERIFY_GREEDY = 1 };
+enum { CSA2_PROB_BF16 = 0, CSA2_PROB_F32 = 1, CSA2_PROB_F16 = 2 };
 
 /* Model constants.  The kernels are built for the pages' values only
  * (study, reading notes: 64 heads, 512-wide latent, RoPE on 64 of the 512
@@ -604,6 +610,158 @@ csa2_status csa2_paged_attn(const void *q, const void *pages, int n_pages, int p
                             csa2_stream_t stream);
 
 /*
+ * What a paged cache keeps.  A cache that loses entries has places that are no
+ * positions any more: entry j of a sequence is its j-th one still there, and
+ * gone[b] counts those that were lost.  (A latent carries its position's rotation,
+ * and attention does not depend on the entries' order.)
+ *
+ * csa2_page_plan_at -- csa2_page_plan for such caches: the new tokens of sequence
+ * b take places seq_len[b], seq_len[b] + 1, .. (block tables, slots, n_vis = place +
+ * 1) at positions gone[b] + seq_len[b], .. (pos, the window and its ring).
+ *
+ *   gone         NULL (none: csa2_page_plan), or (device) int32 [n_seq].  A
+ *                negative one, or positions beyond 2^31 - 1, record
+ *                CSA2_ERR_BOUNDS, and the sequence gets no tokens.
+ */
+csa2_status csa2_page_plan_at(const int32_t *seq_len, const int32_t *new_len, const int32_t *gone, int n_seq,
+                              int page_size, int n_pages, const int32_t *free_pages, int n_free,
+                              const int32_t *free_head, int32_t *block_table, int64_t table_stride, int swa_cap,
+                              int32_t *desc, int max_tokens, int32_t *first, int32_t *totals, csa2_stream_t stream);
+
+/*
+ * csa2_attn_weight -- the attention weight that the main cache's entries get from
+ * a step's queries, added to what they had:
+ *     weight[s] = decay * prior[s] + sum_q sum_h exp(sm_scale q_h . k_j - lse[q][h])
+ * for the slot s of every entry j that a query of its sequence sees (j below the
+ * largest n_vis), the sum over the sequence's queries that see j and their 64
+ * heads.  With the lse of csa2_paged_attn over the same entries these are the
+ * softmax weights with which the queries attended to j (the window's entries have
+ * the rest).  Queries of one sequence are neighbours.  fp32 sums in a fixed order:
+ * the same inputs give the same bits.  A head whose lse or query is not finite adds
+ * nothing (and one that attended to nothing, with an lse of -inf).
+ *
+ *   q            (device) bf16 [n_q][64][512], as csa2_paged_attn's.
+ *   pages .. table_stride   the paged cache and its block table.  A table entry
+ *                outside [0, n_pages): its entries are skipped and CSA2_ERR_BOUNDS
+ *                is recorded.  Sequences may not share pages here.
+ *   first        (device) int32 [n_seq + 1]: sequence b's queries are first[b] ..
+ *                first[b + 1] - 1 (csa2_page_plan's); out of range of n_q: recorded, the
+ *                sequence is skipped.  A sequence without queries is left as it is.
+ *   sel          NULL, or (device) int32 [n_q][sel_stride], as csa2_paged_attn's: a
+ *                query sees the entries sel[q] only; one named twice counts twice.
+ *                decay still takes all entries below the largest n_vis.
+ *   n_vis        (device) int32 [n_q]; outside [0, table_stride * page_size]:
+ *                recorded, the query adds nothing.
+ *   lse          (device) fp32 [n_q][64].
+ *   prior        NULL (zeros), or (device) fp32 [n_pages * page_size], by slot; it
+ *                may be weight itself, and may not overlap it otherwise.
+ *   weight       (device) fp32 [n_pages * page_size].  Slots of other entries are
+ *                left as they are.
+ *   workspace    (device) >= csa2_workspace_size(CSA2_OP_ATTN_WEIGHT, n_q, n_seq,
+ *                sel_stride or 0) bytes, 256-B aligned; no initialisation.
+ *   Limits: n_q <= 65535; n_seq <= 16384; n_pages * page_size and table_stride *
+ *   page_size below 2^31; n_q * (row / 128 + 1) up to 2^30, row = sel_stride or table_stride * page_size.
+ */
+csa2_status csa2_attn_weight(const void *q, const void *pages, int n_pages, int page_size, const int32_t *block_table,
+                             int64_t table_stride, const int32_t *first, int n_seq, const int32_t *sel, int sel_stride,
+                             const int32_t *n_vis, const float *lse, int n_q, float decay, const float *prior,
+                             float *weight, const csa2_params *params, void *workspace, size_t workspace_bytes,
+                             csa2_stream_t stream);
+
+/*
+ * csa2_evict -- cuts sequences down to their heaviest entries.  Of the seq_len[b]
+ * entries of sequence b, k = min(keep[b], seq_len[b]) stay: the last min(recent, k),
+ * and of the others those of largest weight (of equal ones those at the lowest
+ * places; -0 equals 0; NaN is lighter than everything).  They keep their order, and
+ * their records and weights go to places 0 .. k - 1 of row b of the destination.
+ * Records and weights of no other slot are written.
+ *
+ *   pages .. table_stride, seq_len   the paged cache; weight (device) fp32
+ *                [n_pages * page_size] by slot, 16-B aligned.  An entry on a column
+ *                that names no page is taken for the lightest, recorded as
+ *                CSA2_ERR_BOUNDS and, where it stays all the same, not copied.
+ *                Sequences may not share pages here.
+ *   keep         (device) int32 [n_seq].  recent >= 0.
+ *   dst_pages .. dst_stride   the destination, of the same page_size: other pages, of
+ *                the same cache (another table) or of another one, none of which is
+ *                read here or named twice, with their weights; or the source itself (the same
+ *                pointers): then the entries move in place.  (The pages behind
+ *                them: csa2_page_trim.)
+ *   new_len      (device) int32 [n_seq]: k.  May be seq_len itself.
+ *   from         NULL, or (device) int32 [n_seq][from_stride]: the places that the
+ *                kept entries come from, in order; what is behind them is left as
+ *                it is.  (For what else a caller keeps of an entry.)
+ *   A negative length or keep, a length that the block table cannot hold, or more
+ *   kept entries than the destination or from can: CSA2_ERR_BOUNDS is recorded,
+ *   nothing of the sequence moves, and new_len is seq_len in place, else 0.
+ *   workspace    (device) >= csa2_workspace_size(CSA2_OP_EVICT, n_seq, table_stride
+ *                * page_size, 0) bytes, 256-B aligned; no initialisation.
+ *   Limits: n_seq <= 16384; pages and rows of fewer than 2^31 entries.
+ */
+csa2_status csa2_evict(const void *pages, const float *weight, int n_pages, int page_size, const int32_t *block_table,
+                       int64_t table_stride, const int32_t *seq_len, const int32_t *keep, int n_seq, int recent,
+                       void *dst_pages, float *dst_weight, int n_dst_pages, const int32_t *dst_table,
+                       int64_t dst_stride, int32_t *new_len, int32_t *from, int64_t from_stride, void *workspace,
+                       size_t workspace_bytes, csa2_stream_t stream);
+
+/*
+ * csa2_page_trim -- gives the pages behind new lengths back to the free list:
+ * columns ceil(new_len / page_size) .. ceil(len / page_size) - 1 of every sequence's
+ * row of the block table go to the places ahead of free_head, in sequence order,
+ * and get -1 in the table; free_head moves back by as many.
+ *
+ *   len, new_len (device) int32 [n_seq], 0 <= new_len <= len, len within its row:
+ *                else CSA2_ERR_BOUNDS is recorded and the sequence's pages stay.
+ *   free_pages, n_free, free_head   as csa2_page_plan's, here written.  More pages
+ *                than were taken (free_head), or a free_head outside the list: recorded,
+ *                and nothing is given back.  A column that names no page goes to the
+ *                list as it is, and is recorded.
+ */
+csa2_status csa2_page_trim(const int32_t *len, const int32_t *new_len, int n_seq, int page_size, int n_pages,
+                           int32_t *free_pages, int n_free, int32_t *free_head, int32_t *block_table,
+                           int64_t table_stride, csa2_stream_t stream);
+
+/*
+ * csa2_verify_drafts -- which drafted tokens stay, and the token that follows.
+ * Rows first[b] .. first[b + 1] - 1 are the tokens of sequence b's step: the last
+ * sampled one, then drafts.  Row r of target is the target model's distribution of
+ * the token after tokens[r], so draft tokens[r + 1] is judged by row r.
+ *   CSA2_VERIFY_SAMPLE: in order, draft x = tokens[r + 1] stays while
+ *     u[r] * draft[r][x] < target[r][x].  At the first one that does not, next is
+ *     drawn from max(target[r] - draft[r], 0); if all stay, from the last row of
+ *     target: the lowest index whose running sum is above v[b] times the total (where
+ *     rounding leaves none, the last index of any weight).  If nothing is above zero
+ *     there, next is drawn from target[r].  Decided as by exact arithmetic (sums to
+ *     about 2^-46 of the total).
+ *   draft NULL: the drafts were not drawn (a lookup): draft[r] is 1 at x, 0 elsewhere.
+ *   CSA2_VERIFY_GREEDY: x stays while it is the index of row r's largest entry (the
+ *     lowest of equal ones; -0 equals 0; NaN is none), which is next otherwise;
+ *     target may hold logits; draft NULL; u and v are not read.
+ *
+ *   target       (device) [n_rows][target_stride] of type dtype, vocab entries a row;
+ *                draft likewise.  Element alignment will do; 16-B aligned rows are
+ *                read faster.  An entry that is negative, NaN or above 2^96 is
+ *                no probability and counts as 0 (SAMPLE).
+ *   tokens       (device) int32 [n_rows].  A draft outside [0, vocab) is refused and
+ *                recorded as CSA2_ERR_BOUNDS.
+ *   first        (device) int32 [n_seq + 1], as csa2_page_plan's; out of range of
+ *                n_rows: recorded, the sequence gets 0 and -1.  Rows from
+ *                first[n_seq] on are not read.
+ *   u, v         (device) fp32 [n_rows], [n_seq]: random numbers in [0, 1).
+ *   kept         (device) int32 [n_seq]: the step's tokens that stay, the accepted
+ *                drafts and the one before them; 0 for a sequence without rows.
+ *   next         (device) int32 [n_seq]; -1 for a sequence without rows, and, recorded,
+ *                where target[r] has no entry above zero (GREEDY: nothing but NaN).
+ *   workspace    GREEDY: (device) >= csa2_workspace_size(CSA2_OP_VERIFY, n_rows, 0, 0)
+ *                bytes, 256-B aligned; no initialisation.  SAMPLE: NULL will do.
+ *   Limits: n_seq <= 16384; n_rows <= 65535; vocab <= 2^28.
+ */
+csa2_status csa2_verify_drafts(int mode, const void *target, int64_t target_stride, const void *draft,
+                               int64_t draft_stride, int dtype, int vocab, const int32_t *tokens, const int32_t *first,
+                               int n_seq, int n_rows, const float *u, const float *v, int32_t *kept, int32_t *next,
+                               void *workspace, size_t workspace_bytes, csa2_stream_t stream);
+
+/*
  * csa2_workspace_size -- scratch bytes needed by an operation.
  *   op = CSA2_OP_TOPK:        n_q queries, n_items = items per row (entries,
  *                             blocks, or 16384 pool slots), k.
@@ -616,6 +774,10 @@ csa2_status csa2_paged_attn(const void *q, const void *pages, int n_pages, int p
  *   op = CSA2_OP_DECODE_REINDEX: n_q queries, n_items = n_max, k unused (512).
  *   op = CSA2_OP_PAGED_ATTN:  n_q, n_items and k unused: the same for every call
  *                             (two partial outputs per SM, 40 MB).
+ *   op = CSA2_OP_ATTN_WEIGHT: n_q queries, n_items = n_seq, k = sel_stride (0 without sel).
+ *   op = CSA2_OP_EVICT:       n_q = n_seq, n_items = entries of a row (table_stride *
+ *                             page_size), k unused.
+ *   op = CSA2_OP_VERIFY:      n_q = n_rows, n_items and k unused.
  * Sizes are for the current device (the attention's split plan follows its
  * SM count).
  */
