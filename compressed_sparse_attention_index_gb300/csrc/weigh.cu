@@ -2,17 +2,93 @@
 //
 //     w_j = decay prior_j + sum over the queries that see j, and their heads, of
 //           exp(scale q_h . k_j - lse_h)
+//
+// Work: the entries that a sequence's queries see form chunks of 128, its queries groups
+// of NQ.  All sequences' (chunk, group) products are dealt to the CTAs (one an SM) in contiguous runs of equal
+// numbers, cut between chunks, so that one CTA has all of an entry's queries and sums them in a fixed order.
+// With several groups a CTA takes 16 chunks at a time (one query a group: 8), group by group: Q stays in shared memory
+// for them, their records in L2 for the groups, and their sums in shared memory.  A selection is a
+// sequence of its own: its chunks' weights go to scratch, and are added query by query.
+//
+// Per chunk and group, on the 5th-generation tensor cores:
+//   S^T[entry][head] = K . Q^T     tcgen05 kind::f16, M = 128, N = 64 NQ, K = 512
+//   w[entry] += sum over heads of 2^(f_h S - lse_h log2 e)
+// An entry's heads lie in one row of tensor memory, so the sum is a thread's own.  K (E2M1 x E4M3) is exact
+// in f16; every head of Q goes to f16 under a power of two that brings its largest value into [2^14, 2^15),
+// so a bf16 value 2^-29 of that and above is exact; f_h = scale log2(e) over that power.  (A first launch does
+// that, and lays Q out as the tensor cores read it.)
+//
+// Warps, with their own barriers between them: one fetches records and Q by bulk copies; sixteen dequantise,
+// a row per thread and 128 dims a team, into tensor memory, where the MMAs read K as their A operand;
+// eight sum S; one thread issues the MMAs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <limits.h>
 #include <math.h>
 
 #include "attn.cuh"
 #include "common.cuh"
 #include "launch.cuh"
+#include "tc_ptx.cuh"
 
 namespace csa2 {
 
-constexpr int kWgTile = 32, kWgThreads = 256, kWgDims = 64;
+constexpr int kWgChunk = 128;                      // entries
+constexpr int kWgSumWarps = 8, kWgKWarps = 16, kWgWarps = 28;
+constexpr int kWgThreads = kWgWarps * 32;
+constexpr int kWgRaw = kWgChunk * kKvBytes;        // one chunk's records
+constexpr int kWgQBlock = 64 * 128;                // 64 heads x 64 dims f16: [h/8][h%8][128 B]
+constexpr int kWgImage = 8 * kWgQBlock;            // a query as the tensor cores read it
+constexpr int kWgMeta = 2 * kHeads * 4;            // its heads' f, then their -lse log2(e)
+constexpr int kWgMetas = 4;                        // groups whose f and lse are in shared memory
+constexpr int kWgScatter = 8;                      // pages of fewer entries are fetched as scattered records
+
+template <int NQ>
+struct WgSmem {
+  static constexpr int kStages = NQ == 1 ? 4 : 2;  // records of as many chunks
+  static constexpr int kBlock = NQ == 1 ? 8 : 16;  // chunks that take turns at several groups
+  static constexpr int kQ = 0;                     // [dims / 64][query][heads]
+  static constexpr int kRaw = kQ + NQ * kWgImage;
+  static constexpr int kAcc = kRaw + kStages * kWgRaw;         // [2][kBlock chunks][128]
+  static constexpr int kMeta = kAcc + 2 * kBlock * kWgChunk * 4;
+  static constexpr int kEnd = kMeta + kWgMetas * NQ * kWgMeta;
+  static constexpr int kAlloc = kEnd + 1024;
+  static_assert(kAlloc + 512 <= 227 * 1024, "shared memory");
+};
+constexpr uint32_t kWgColK = 0, kWgColS = 256, kWgTmemCols = 512;
+
+// What a sequence (a query, for selections) takes: entries, groups, its first query, its queries.
+struct WgWs {
+  int4 *item;
+  int32_t *off;                 // products ahead of it; [items] all of them
+  int32_t *q_seq;               // of each query (selections), -1: none
+  unsigned char *image;         // [n_q][kWgImage]
+  unsigned char *meta;          // [n_q][kWgMeta]
+  float *part;                  // [n_q][sel_stride]
+};
+static size_t wg_up(size_t x) { return (x + 255) / 256 * 256; }
+static size_t wg_layout(WgWs *W, void *ws, int n_q, int64_t n_seq, int sel_stride) {
+  const size_t items = (size_t)(n_q > n_seq ? n_q : n_seq);
+  char *p = static_cast<char *>(ws);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char *r = p == nullptr ? nullptr : p + at;
+    at += wg_up(bytes);
+    return r;
+  };
+  char *item = take(items * sizeof(int4)), *off = take((items + 1) * 4), *q_seq = take((size_t)n_q * 4);
+  char *image = take((size_t)n_q * kWgImage), *meta = take((size_t)n_q * kWgMeta), *part = take((size_t)n_q * (size_t)sel_stride * 4);
+  if (W != nullptr) {
+    W->item = reinterpret_cast<int4 *>(item);
+    W->off = reinterpret_cast<int32_t *>(off);
+    W->q_seq = reinterpret_cast<int32_t *>(q_seq);
+    W->image = reinterpret_cast<unsigned char *>(image);
+    W->meta = reinterpret_cast<unsigned char *>(meta);
+    W->part = reinterpret_cast<float *>(part);
+  }
+  return at;
+}
+size_t weigh_workspace_bytes(int n_q, int64_t n_seq, int sel_stride) { return wg_layout(nullptr, nullptr, n_q, n_seq, sel_stride); }
 
 // A sequence's queries, or none where that is out of range.
 __device__ __forceinline__ bool weigh_queries(const WeighArgs &A, int b, int &c0, int &c1) {
@@ -27,123 +103,640 @@ __device__ __forceinline__ int weigh_vis(const WeighArgs &A, int q) {
   const int v = __ldg(A.n_vis + q);
   return v < 0 || (int64_t)v > A.table_stride * A.page ? -1 : v;
 }
+__device__ __forceinline__ int weigh_col(const WeighArgs &A, int j) { return (int)(((uint64_t)(unsigned)j * A.page_mul) >> A.page_shift); }
 __device__ __forceinline__ int64_t weigh_slot(const WeighArgs &A, int b, int j) {
-  const int c = (int)(((uint64_t)(unsigned)j * A.page_mul) >> A.page_shift);
+  const int c = weigh_col(A, j);
   const int id = __ldg(A.table + (int64_t)b * A.table_stride + c);
   return id >= 0 && id < A.n_pages ? (int64_t)id * A.page + (j - c * A.page) : -1;
 }
 
-// 32 entries of a sequence (SEL: of a query's selection) against its queries, 64 dims at a time.
-template <bool SEL>
-__global__ void __launch_bounds__(kWgThreads) weigh_kernel(const __grid_constant__ WeighArgs A, float *part) {
-  __shared__ float ks[kWgTile][kWgDims + 1], qs[kHeads][kWgDims + 1];
-  __shared__ int64_t slot_sh[kWgTile];
-  const int t = threadIdx.x, e = t >> 3, hg = t & 7;
+// ------------------------------------------------------------------ what the products need
+constexpr int kPrepThreads = 256;
+__device__ __forceinline__ float wg_power(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// The first CTA: the items and the products ahead of each.  One for each query behind it: its
+// heads' powers of two, f16 image and constants.
+__global__ void __launch_bounds__(kPrepThreads) weigh_prep_kernel(const __grid_constant__ WeighArgs A, WgWs W, int nq) {
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   griddep_wait();
   griddep_launch();
-  int b = blockIdx.y, c0, c1;
-  if (SEL) {                                         // the sequence that has this query
-    const int q = blockIdx.y;
-    int lo = 0, hi = A.n_seq;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(A.first + mid) <= q) lo = mid;
-      else hi = mid;
+  if (blockIdx.x > 0) {
+    const int q = (int)blockIdx.x - 1;
+    if (A.sel != nullptr && t == 0) {
+      int lo = 0, hi = A.n_seq;                      // the last sequence with first <= q
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(A.first + mid) <= q) lo = mid;
+        else hi = mid;
+      }
+      int c0, c1;
+      W.q_seq[q] = weigh_queries(A, lo, c0, c1) && q >= c0 && q < c1 ? lo : -1;
     }
-    b = lo;
-    if (!weigh_queries(A, b, c0, c1) || q < c0 || q >= c1) return;
-    c0 = q;
-    c1 = q + 1;
-  } else if (!weigh_queries(A, b, c0, c1) && t == 0) {
-    record_error(A.status, CSA2_ERR_BOUNDS);
-  }
-  int most = 0;
-  for (int q = c0 + t; q < c1; q += kWgThreads) {
-    const int v = weigh_vis(A, q);
-    if (v < 0) record_error(A.status, CSA2_ERR_BOUNDS);
-    most = max(most, v);
-  }
-  __shared__ int most_sh;
-  if (t == 0) most_sh = 0;
-  __syncthreads();
-  atomicMax(&most_sh, most);
-  __syncthreads();
-  most = most_sh;
-  const int n = SEL ? A.sel_stride : most;
-  for (int j0 = blockIdx.x * kWgTile; j0 < n; j0 += gridDim.x * kWgTile) {
-    int j = j0 + e;
-    if (j >= n) j = -1;
-    if (SEL && j >= 0) {
-      j = __ldg(A.sel + (int64_t)c0 * A.sel_stride + j);
-      if (j >= most) {
-        if (hg == 0) record_error(A.status, CSA2_ERR_BOUNDS);
-        j = -1;
+    // eight heads a warp, 16 dims a lane
+#pragma unroll 2
+    for (int i = 0; i < 8; i++) {
+      const int h = warp * 8 + i;
+      const uint4 *src = reinterpret_cast<const uint4 *>(A.q + ((int64_t)q * kHeads + h) * kDim) + lane * 2;
+      const uint4 x = __ldg(src), y = __ldg(src + 1);
+      const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      uint32_t m = 0u;
+#pragma unroll
+      for (int u = 0; u < 8; u++) m = __vmaxu2(m, w[u] & 0x7FFF7FFFu);
+      m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
+      const float lse = __ldg(A.lse + (int64_t)q * kHeads + h);
+      const bool none = m >= 0x7F80u || !(fabsf(lse) < INFINITY);      // not finite: adds nothing
+      // max |q| in [2^e, 2^(e + 1)) (below 2^-126 its place among the subnormals)
+      const int e = m == 0u ? 14 : m < 0x80u ? -134 + 31 - __clz((int)m) + 1 : (int)(m >> 7) - 127;
+      const int by = none ? 0 : 14 - e, b0 = by / 2, b1 = by - b0;      // (2^by itself may be beyond fp32)
+      const float s0 = none ? 0.f : wg_power(b0), s1 = wg_power(b1);
+      uint32_t o[8];
+#pragma unroll
+      for (int u = 0; u < 8; u++) {
+        const float a = none ? 0.f : bf16_lo(w[u]) * s0 * s1, c = none ? 0.f : bf16_hi(w[u]) * s0 * s1;
+        const __half2 p = __floats2half2_rn(a, c);
+        o[u] = *reinterpret_cast<const uint32_t *>(&p);
+      }
+      // dims 16 lane ..: block of 64 dims lane / 4, 16-byte chunks 2 (lane % 4) and the next
+      unsigned char *dst = W.image + (int64_t)q * kWgImage + (lane >> 2) * kWgQBlock + (h >> 3) * 1024;
+      *reinterpret_cast<uint4 *>(dst + sw128(h & 7, (lane & 3) * 2)) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4 *>(dst + sw128(h & 7, (lane & 3) * 2 + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+      if (lane == 0) {
+        float *meta = reinterpret_cast<float *>(W.meta + (int64_t)q * kWgMeta);
+        meta[h] = none ? 0.f : A.scale * 1.4426950408889634f * wg_power(-b0) * wg_power(-b1);
+        meta[kHeads + h] = none ? -INFINITY : -lse * 1.4426950408889634f;
       }
     }
-    int64_t slot = -1;
-    if (j >= 0) {
-      slot = weigh_slot(A, b, j);
-      if (slot < 0 && hg == 0) record_error(A.status, CSA2_ERR_BOUNDS);
-    }
-    if (hg == 0) slot_sh[e] = slot;
-    float sum = 0.f;
-    for (int q = c0; q < c1; q++) {
-      const int vis = weigh_vis(A, q);
-      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      for (int d0 = 0; d0 < kDim; d0 += kWgDims) {
-        __syncthreads();
-        for (int i = t; i < kWgTile * kWgDims; i += kWgThreads) {
-          const int r = i / kWgDims, d = d0 + i % kWgDims;
-          float x = 0.f;
-          if (slot_sh[r] >= 0) {
-            const uint8_t *rec = A.pages + slot_sh[r] * kKvBytes;
-            x = 0.5f * (float)e2m1_x2((rec[d >> 1] >> (4 * (d & 1))) & 15u) * e4m3_to_float(rec[256 + (d >> 4)]);
-          }
-          ks[r][i % kWgDims] = x;
+    return;
+  }
+  // ---------------------------------------------------- items
+  const bool sel = A.sel != nullptr;
+  const int items = sel ? A.n_q : A.n_seq;
+  __shared__ int wt[kPrepThreads / 32], base_sh;
+  if (t == 0) base_sh = 0;
+  for (int i0 = 0; i0 < items; i0 += kPrepThreads) {
+    const int i = i0 + t;
+    int groups = 0, c0 = i, cnt = 0, most = 0;
+    if (sel) {
+      if (i < items) {
+        if (weigh_vis(A, i) < 0) record_error(A.status, CSA2_ERR_BOUNDS);
+        most = A.sel_stride;
+        cnt = 1;
+      }
+    } else {
+      int c1 = 0;
+      if (i < items && !weigh_queries(A, i, c0, c1)) record_error(A.status, CSA2_ERR_BOUNDS);
+      if (i < items) cnt = c1 - c0;
+      if (cnt <= 16)
+#pragma unroll 4
+        for (int q = c0; q < c0 + cnt; q++) {
+          const int v = weigh_vis(A, q);
+          if (v < 0) record_error(A.status, CSA2_ERR_BOUNDS);
+          most = max(most, v);
         }
-        for (int i = t; i < kHeads * kWgDims; i += kWgThreads)
-          qs[i / kWgDims][i % kWgDims] = __uint_as_float((uint32_t)A.q[((int64_t)q * kHeads + i / kWgDims) * kDim + d0 + i % kWgDims] << 16);
-        __syncthreads();
-        for (int d = 0; d < kWgDims; d++)
-#pragma unroll
-          for (int h = 0; h < 8; h++) acc[h] = fmaf(ks[e][d], qs[hg * 8 + h][d], acc[h]);
+      // sequences of many queries, one after another, by the whole warp
+      uint32_t many = __ballot_sync(0xFFFFFFFFu, cnt > 16);
+      while (many != 0u) {
+        const int from = __ffs((int)many) - 1;
+        many &= many - 1u;
+        const int a = __shfl_sync(0xFFFFFFFFu, c0, from), n = __shfl_sync(0xFFFFFFFFu, cnt, from);
+        int m = 0;
+        bool out = false;
+        for (int q = a + lane; q < a + n; q += 32) {
+          const int v = weigh_vis(A, q);
+          out |= v < 0;
+          m = max(m, v);
+        }
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+        if (__any_sync(0xFFFFFFFFu, out) && lane == 0) record_error(A.status, CSA2_ERR_BOUNDS);
+        if (lane == from) most = m;
       }
-      float p = 0.f;
-#pragma unroll
-      for (int h = 0; h < 8; h++) {
-        const float l = __ldg(A.lse + (int64_t)q * kHeads + hg * 8 + h);
-        if (fabsf(l) < INFINITY && fabsf(acc[h]) < INFINITY) p += exp2f((acc[h] * A.scale - l) * 1.4426950408889634f);
-      }
-      if (j < vis) sum += p;
     }
+    groups = most > 0 ? (cnt + nq - 1) / nq : 0;
+    const int own = (int)(((unsigned)most + kWgChunk - 1u) / kWgChunk) * groups;
+    int inc = own;
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (hg == 0) {
-      if (SEL) {
-        if (j0 + e < n) part[(int64_t)c0 * A.sel_stride + j0 + e] = slot >= 0 ? sum : 0.f;
-      } else if (slot >= 0) {
-        A.weight[slot] = (A.prior != nullptr ? A.decay * A.prior[slot] : 0.f) + sum;
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) wt[warp] = inc;
+    __syncthreads();
+    int ahead = base_sh + inc - own;
+    for (int w = 0; w < warp; w++) ahead += wt[w];
+    if (i < items) {
+      W.item[i] = make_int4(most, groups, c0, cnt);
+      W.off[i] = ahead;
     }
     __syncthreads();
+    if (t == kPrepThreads - 1) base_sh = ahead + own;
+    __syncthreads();
+  }
+  if (t == 0) W.off[items] = base_sh;
+}
+
+// ------------------------------------------------------------------ a CTA's run
+// Its products in order: item by item, block of chunks by block, group by group, chunk by chunk.
+__device__ __forceinline__ int wg_chunks(int n) { return (int)(((unsigned)n + kWgChunk - 1u) / kWgChunk); }
+template <int NQ>
+struct WgWalk {
+  int b, end_b, end_c;          // the item; the run's end: chunk end_c of item end_b
+  int4 I;
+  int lo, hi, seq_hi;           // the block's chunks; the item's end in this run
+  int g, c;
+  __device__ __forceinline__ void block() {
+    hi = I.y > 1 ? min(lo + WgSmem<NQ>::kBlock, seq_hi) : seq_hi;
+    g = 0;
+    c = lo;
+  }
+  // the next item that has a chunk in the run (false: the run is over)
+  __device__ __forceinline__ bool settle(const WgWs &W, int from) {
+    lo = from;
+    for (;; b++, lo = 0) {
+      if (b > end_b || (b == end_b && lo >= end_c)) return false;
+      I = __ldg(W.item + b);
+      seq_hi = b == end_b ? end_c : wg_chunks(I.x);
+      if (I.y > 0 && lo < seq_hi) break;
+    }
+    block();
+    return true;
+  }
+  __device__ __forceinline__ bool next(const WgWs &W) {
+    if (++c < hi) return true;
+    if (++g < I.y) {
+      c = lo;
+      return true;
+    }
+    lo = hi;
+    if (lo < seq_hi) {
+      block();
+      return true;
+    }
+    b++;
+    return settle(W, 0);
+  }
+  __device__ __forceinline__ bool group_begins() const { return c == lo; }
+  __device__ __forceinline__ bool group_ends() const { return c + 1 == hi; }
+  __device__ __forceinline__ bool last_group() const { return g + 1 == I.y; }
+};
+
+struct WgShared {
+  uint64_t raw_full[4], raw_free[4], k_full[4], k_free[4], q_full[4], q_free[4], s_full[2], s_free[2], m_full[kWgMetas], drain;
+  uint32_t tmem;
+  int begin_b, begin_c, end_b, end_c, steps;
+  volatile int bad;
+};
+
+// A wait that runs out marks the CTA bad; from then on no role waits, so that all of them run out
+// of products in bounded time.
+__device__ __forceinline__ void wg_wait(const WeighArgs &A, WgShared &S, uint64_t *bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (int i = 0; !ptx::mbar_try_wait_sleep(bar, parity, 1000000u); i++) {
+    if (S.bad) return;
+    if (i < 64) {
+      t0 = ptx::globaltimer();
+    } else if (ptx::globaltimer() - t0 > 2000000000ull) {
+      record_error(A.status, CSA2_ERR_TIMEOUT);
+      S.bad = 1;
+      return;
+    }
+  }
+}
+__device__ __forceinline__ bool wg_bad(const WgShared &S) { return __any_sync(0xFFFFFFFFu, S.bad); }
+
+// ------------------------------------------------------------------ records and Q
+template <int NQ, bool SEL>
+__device__ __forceinline__ void wg_fetch(const WeighArgs &A, const WgWs &W, WgShared &S, unsigned char *sm, WgWalk<NQ> C, bool more) {
+  using M = WgSmem<NQ>;
+  const int lane = threadIdx.x & 31;
+  const bool scattered = SEL || A.page < kWgScatter;
+  int rec[4];                                        // rows 32 g + lane: the record, -1: none
+  int rows[4];                                       // of the run that this lane leads, 0: none
+  int all_rows = 0;
+  auto look_up = [&]() {
+    int j[4], id[4], off[4];
+    int seq = C.b, vis = 0;
+    if (SEL) {
+      seq = __ldg(W.q_seq + C.b);
+      vis = seq >= 0 ? weigh_vis(A, C.b) : 0;
+    }
+    bool out = false;
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+      const int i = C.c * kWgChunk + 32 * g + lane;
+      j[g] = i;
+      if (SEL) {
+        j[g] = i < A.sel_stride && seq >= 0 ? __ldg(A.sel + (int64_t)C.b * A.sel_stride + i) : -1;
+        if (j[g] >= vis) {
+          out |= vis >= 0;                           // (a query that is out of range itself is recorded already)
+          j[g] = -1;
+        }
+      } else if (i >= C.I.x) {
+        j[g] = -1;
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+      const int col = j[g] >= 0 ? weigh_col(A, j[g]) : 0;
+      off[g] = j[g] - col * A.page;
+      id[g] = j[g] >= 0 ? __ldg(A.table + (int64_t)seq * A.table_stride + col) : -1;
+    }
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+      const bool ok = id[g] >= 0 && id[g] < A.n_pages;
+      if (SEL) out |= j[g] >= 0 && !ok;              // (dense rows are checked where they are written)
+      if (!ok) id[g] = -1;
+      rec[g] = ok ? id[g] * A.page + off[g] : -1;
+      const int pid = __shfl_up_sync(0xFFFFFFFFu, id[g], 1), poff = __shfl_up_sync(0xFFFFFFFFu, off[g], 1);
+      const bool leads = ok && (lane == 0 || pid != id[g] || poff + 1 != off[g]);
+      const uint32_t valid = __ballot_sync(0xFFFFFFFFu, ok), lead = __ballot_sync(0xFFFFFFFFu, leads);
+      const uint32_t stop = (lead | ~valid) & ~((2u << lane) - 1u);        // (lane 31: 2 << 31 is 0)
+      rows[g] = leads ? (stop != 0u ? __ffs(stop) - 1 : 32) - lane : 0;
+      all_rows = g == 0 ? __popc(valid) : all_rows + __popc(valid);
+    }
+    if (out) record_error(A.status, CSA2_ERR_BOUNDS);
+  };
+  if (more) look_up();
+  int groups = 0, slabs = 0, k = 0;                  // begun, asked for, fetched
+#pragma unroll 1
+  for (; more; k++) {
+    const int stage = k % M::kStages;
+    if (C.group_begins()) {
+      // Q slab by slab, as the group before lets go of it, and beside the first of them f and lse (their place
+      // was used four groups ago: the sums have left it once the group before is at its last product)
+      const int q0 = C.I.z + C.g * NQ, n = min(NQ, C.I.w - C.g * NQ), place = groups % kWgMetas;
+#pragma unroll 1
+      for (int s = 0; s < 4; s++) {
+        if (groups > 0) wg_wait(A, S, &S.q_free[s], (uint32_t)(groups - 1) & 1u);
+        if (wg_bad(S)) break;
+        if (lane == 0) {
+          if (s == 0) {
+            ptx::mbar_arrive_expect_tx(&S.m_full[place], (uint32_t)(n * kWgMeta));
+            ptx::bulk_load(sm + M::kMeta + place * NQ * kWgMeta, W.meta + (int64_t)q0 * kWgMeta, (uint32_t)(n * kWgMeta), &S.m_full[place]);
+          }
+          ptx::mbar_arrive_expect_tx(&S.q_full[s], (uint32_t)(n * 2 * kWgQBlock));
+          for (int i = 0; i < 2; i++)
+            for (int x = 0; x < n; x++)
+              ptx::bulk_load(sm + M::kQ + ((2 * s + i) * NQ + x) * kWgQBlock, W.image + (int64_t)(q0 + x) * kWgImage + (2 * s + i) * kWgQBlock, kWgQBlock, &S.q_full[s]);
+        }
+        slabs++;
+        __syncwarp();
+      }
+      groups++;
+    }
+    if (k >= M::kStages) wg_wait(A, S, &S.raw_free[stage], (uint32_t)(k / M::kStages - 1) & 1u);
+    if (wg_bad(S)) break;                            // no copy is started any more
+    uint64_t *full = &S.raw_full[stage];
+    unsigned char *to = sm + M::kRaw + stage * kWgRaw;
+    if (scattered) {
+#pragma unroll
+      for (int g = 0; g < 8; g++) {                  // two lanes to a record, 16 records at a time
+        const int from = (g & 1) * 16 + (lane >> 1);
+        const int r = __shfl_sync(0xFFFFFFFFu, rec[g >> 1], from);
+        const uint8_t *src = A.pages + (int64_t)r * kKvBytes + (lane & 1) * 16;
+        unsigned char *dst = to + ((g >> 1) * 32 + from) * kKvBytes + (lane & 1) * 16;
+        if (r >= 0)
+#pragma unroll
+          for (int i = 0; i < kKvBytes; i += 32) ptx::cp_async16(dst + i, src + i);
+      }
+      ptx::cp_async_arrive(full);                    // (each lane's copies, pending from here on)
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive_expect_tx(full, scattered ? 0u : (uint32_t)(all_rows * kKvBytes));
+    __syncwarp();
+    if (!scattered)
+#pragma unroll
+      for (int g = 0; g < 4; g++)
+        if (rows[g] > 0) ptx::bulk_load(to + (32 * g + lane) * kKvBytes, A.pages + (int64_t)rec[g] * kKvBytes, (uint32_t)(rows[g] * kKvBytes), full);
+    more = C.next(W);
+    if (more) look_up();
+  }
+  // its last copies have landed before the CTA may leave (bounded)
+  for (int i = max(0, k - M::kStages); i < k; i++) ptx::mbar_wait(&S.raw_full[i % M::kStages], (uint32_t)(i / M::kStages) & 1u);
+  for (int i = max(0, slabs - 4); i < slabs; i++) ptx::mbar_wait(&S.q_full[i & 3], (uint32_t)(i >> 2) & 1u);
+  for (int i = max(0, (slabs + 3) / 4 - kWgMetas); i < (slabs + 3) / 4; i++) ptx::mbar_wait(&S.m_full[i % kWgMetas], (uint32_t)(i / kWgMetas) & 1u);
+}
+
+// ------------------------------------------------------------------ dequantisation
+// Sixteen warps in four teams, a team a slab of 128 dims of every chunk, a row per thread.
+template <int NQ>
+__device__ __forceinline__ void wg_load(const WeighArgs &A, WgShared &S, const unsigned char *sm, int steps, uint32_t tmem) {
+  using M = WgSmem<NQ>;
+  const int lt = (int)threadIdx.x - kWgSumWarps * 32, lane = lt & 31;
+  const int e = lt & 127, team = lt >> 7;            // row
+  const uint32_t kcol = tmem + ((uint32_t)(e & 96) << 16) + kWgColK + (uint32_t)team * 64u;
+  // Records are 18 16-B units apart, so rows r and r + 4 of a unit share their banks: every
+  // other four rows read the units of a pair the other way round.
+  const bool flip = (e & 4) != 0;
+  const int other = flip ? -16 : 16;
+  int stage = 0;
+  uint32_t turn = 0u;
+  for (int k = 0; k < steps; k++) {
+    wg_wait(A, S, &S.raw_full[stage], turn);
+    const unsigned char *row = sm + M::kRaw + stage * kWgRaw + e * kKvBytes;
+    const uint2 sc = *reinterpret_cast<const uint2 *>(row + 256 + team * 8);
+    const unsigned char *raw = row + team * 64 + (flip ? 16 : 0);
+    uint4 code[4];
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      const uint4 x = *reinterpret_cast<const uint4 *>(raw + j * 16), y = *reinterpret_cast<const uint4 *>(raw + j * 16 + other);
+      code[j] = flip ? y : x;
+      code[j + 1] = flip ? x : y;
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&S.raw_free[stage]);
+    if (++stage == M::kStages) {
+      stage = 0;
+      turn ^= 1u;
+    }
+    if (k > 0) wg_wait(A, S, &S.k_free[team], (uint32_t)(k - 1) & 1u);
+    ptx::tc_fence_after();
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const uint32_t w[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
+      const uint32_t two = e4m3x2_to_f16x2((j < 2 ? sc.x : sc.y) >> (16 * (j & 1)));
+      const uint32_t s2[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
+      uint32_t o[16];
+#pragma unroll
+      for (int u = 0; u < 4; u++) {
+        uint32_t x[4];
+        e2m1x8_to_f16(w[u], x);
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+          const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x[q]), *reinterpret_cast<const __half2 *>(&s2[u >> 1]));
+          o[4 * u + q] = *reinterpret_cast<const uint32_t *>(&y);
+        }
+      }
+      ptx::tmem_st_32x32b_x16(kcol + j * 16, o);
+    }
+    ptx::tmem_wait_st();
+    ptx::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&S.k_full[team]);
   }
 }
 
+// ------------------------------------------------------------------ MMAs
+template <int NQ>
+__device__ __forceinline__ void wg_issue(const WeighArgs &A, const WgWs &W, WgShared &S, unsigned char *sm, WgWalk<NQ> C, bool more, uint32_t tmem) {
+  const uint64_t d_q = ptx::smem_desc(ptx::smem_u32(sm + WgSmem<NQ>::kQ), 16, 1024, 2);
+  int groups = 0;
+  for (int k = 0; more && !S.bad; k++) {
+    const bool begins = C.group_begins(), ends = C.group_ends();
+    if (begins) groups++;
+    const uint32_t id = NQ == 2 && C.I.w - C.g * NQ >= 2 ? idesc_m128(0, true, 2 * kHeads) : idesc_m128(0, true, kHeads);
+    const uint32_t d = tmem + kWgColS + (uint32_t)(k & 1) * 128u;
+    if (k >= 2) wg_wait(A, S, &S.s_free[k & 1], (uint32_t)((k >> 1) - 1) & 1u);
+#pragma unroll 1
+    for (int s = 0; s < 4; s++) {
+      wg_wait(A, S, &S.k_full[s], (uint32_t)k & 1u);
+      if (begins) wg_wait(A, S, &S.q_full[s], (uint32_t)(groups - 1) & 1u);
+      ptx::tc_fence_after();
+      const uint32_t ka = tmem + kWgColK + (uint32_t)s * 64u;
+      const uint64_t qa = d_q + (uint64_t)(s * 2 * NQ * (kWgQBlock >> 4));
+#pragma unroll
+      for (int kk = 0; kk < 8; kk++)
+        ptx::tc_mma_f16_ts(d, ka + kk * 8, qa + (kk >> 2) * (NQ * (kWgQBlock >> 4)) + (kk & 3) * 2, id, kk > 0 ? 1u : (uint32_t)(s > 0));
+      ptx::tc_commit(&S.k_free[s]);
+      if (ends) ptx::tc_commit(&S.q_free[s]);
+    }
+    ptx::tc_commit(&S.s_full[k & 1]);
+    more = C.next(W);
+  }
+  ptx::tc_commit(&S.drain);
+}
+
+// ------------------------------------------------------------------ sums
+__device__ __forceinline__ uint64_t wg_pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t wg_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t wg_add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float2 wg_unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ float wg_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Warp w has entries 32 (w % 4) .. of a chunk and, by w / 4, one of the group's two queries, or half of
+// the heads of its only one.
+template <int NQ, bool SEL>
+__device__ __forceinline__ void wg_sum(const WeighArgs &A, const WgWs &W, WgShared &S, unsigned char *sm, WgWalk<NQ> C, bool more, uint32_t tmem) {
+  using M = WgSmem<NQ>;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
+  const uint32_t ts = tmem + ((uint32_t)(quarter * 32) << 16) + kWgColS;
+  float *acc = reinterpret_cast<float *>(sm + M::kAcc);
+  int groups = 0, vis = 0;
+  bool two = false;
+  for (int k = 0; more; k++) {
+    if (C.group_begins()) {
+      wg_wait(A, S, &S.m_full[groups % kWgMetas], (uint32_t)(groups / kWgMetas) & 1u);
+      groups++;
+      two = NQ == 2 && C.I.w - C.g * NQ >= 2;
+      if (!SEL) vis = weigh_vis(A, C.I.z + C.g * NQ + (two ? half : 0));
+      // (the halves' sums of the chunks before are read)
+      if (C.g == 0) asm volatile("bar.sync %0, 64;" ::"r"(quarter + 1) : "memory");
+    }
+    // where the chunk's weights go, looked up ahead of the products
+    const bool last = C.last_group();
+    int64_t slot = -1;
+    float before = 0.f;
+    if (!SEL && last && half == 0) {
+      const int j = C.c * kWgChunk + row;
+      if (j < C.I.x) {
+        slot = weigh_slot(A, C.b, j);
+        if (slot < 0) record_error(A.status, CSA2_ERR_BOUNDS);
+        else if (A.prior != nullptr) before = A.decay * A.prior[slot];
+      }
+    }
+    const float *f = reinterpret_cast<const float *>(sm + M::kMeta + ((groups - 1) % kWgMetas) * NQ * kWgMeta) + (two ? half * 2 * kHeads : half * 32);
+    const float *nl = f + kHeads;
+    wg_wait(A, S, &S.s_full[k & 1], (uint32_t)(k >> 1) & 1u);
+    ptx::tc_fence_after();
+    const uint32_t ta = ts + (uint32_t)(k & 1) * 128u + (two ? (uint32_t)half * 64u : (uint32_t)half * 32u);
+    uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+    const int cols = two ? 64 : 32;
+#pragma unroll 1
+    for (int h = 0; h < cols; h += 32) {
+      uint32_t a[32];
+      ptx::tmem_ld_32x32b_x32(ta + h, a);
+      ptx::tmem_wait_ld();
+      if (h + 32 == cols) {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&S.s_free[k & 1]);
+      }
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(f + h + i), y = *reinterpret_cast<const ulonglong2 *>(nl + h + i);
+        const float2 u = wg_unpair(wg_fma2(wg_pair(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), x.x, y.x));
+        const float2 v = wg_unpair(wg_fma2(wg_pair(__uint_as_float(a[i + 2]), __uint_as_float(a[i + 3])), x.y, y.y));
+        sum[(i >> 1) & 2] = wg_add2(sum[(i >> 1) & 2], wg_pair(wg_ex2(u.x), wg_ex2(u.y)));
+        sum[((i >> 1) & 2) + 1] = wg_add2(sum[((i >> 1) & 2) + 1], wg_pair(wg_ex2(v.x), wg_ex2(v.y)));
+      }
+    }
+    const float2 all = wg_unpair(wg_add2(wg_add2(sum[0], sum[1]), wg_add2(sum[2], sum[3])));
+    float w = all.x + all.y;
+    if (!SEL && C.c * kWgChunk + row >= vis) w = 0.f;
+    // both halves' sums meet (one group: in two places by turns)
+    float *mine = acc + half * (M::kBlock * kWgChunk) + (C.I.y > 1 ? C.c - C.lo : k & 1) * kWgChunk + row;
+    if (C.g > 0) w += *mine;
+    if (!last || half == 1) *mine = w;
+    if (last) {
+      asm volatile("bar.sync %0, 64;" ::"r"(quarter + 1) : "memory");
+      if (half == 0) {
+        w += mine[M::kBlock * kWgChunk];
+        if (SEL) {
+          const int i = C.c * kWgChunk + row;
+          if (i < A.sel_stride) W.part[(int64_t)C.b * A.sel_stride + i] = w;
+        } else if (slot >= 0) {
+          A.weight[slot] = before + w;
+        }
+      }
+    }
+    more = C.next(W);
+  }
+}
+
+// The last b with off[b] <= x, by the whole warp (off ascending, off[0] = 0; x < off[items]).
+__device__ __forceinline__ int wg_find(const int32_t *off, int items, int x) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = items;                             // the answer is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const bool ok = at < lo + n && __ldg(off + at) <= x;
+    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, ok);       // lanes 0 .. some lane
+    const int last = 31 - __clz((int)hit);
+    const int end = lo + n;
+    lo += last * step;
+    n = min(step, end - lo);
+  }
+  return lo;
+}
+
+template <int NQ, bool SEL>
+__global__ void __launch_bounds__(kWgThreads, 1) weigh_kernel(const __grid_constant__ WeighArgs A, WgWs W) {
+  using M = WgSmem<NQ>;
+  extern __shared__ __align__(1024) unsigned char wg_smem_raw[];
+  unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(wg_smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ __align__(16) WgShared S;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  if (t == 0) {
+    for (int i = 0; i < 4; i++) {
+      ptx::mbar_init(&S.raw_full[i], 1);
+      ptx::mbar_init(&S.raw_free[i], kWgKWarps);
+      ptx::mbar_init(&S.k_full[i], kWgKWarps / 4);
+      ptx::mbar_init(&S.k_free[i], 1);
+      ptx::mbar_init(&S.q_full[i], 1);
+      ptx::mbar_init(&S.q_free[i], 1);
+    }
+    for (int i = 0; i < 2; i++) {
+      ptx::mbar_init(&S.s_full[i], 1);
+      ptx::mbar_init(&S.s_free[i], kWgSumWarps);
+    }
+    for (int i = 0; i < kWgMetas; i++) ptx::mbar_init(&S.m_full[i], 1);
+    ptx::mbar_init(&S.drain, 1);
+    S.bad = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 0) ptx::tmem_alloc(&S.tmem, kWgTmemCols);
+  griddep_wait();
+  griddep_launch();
+  // ---------------------------------------------------------- this CTA's run
+  const int items = SEL ? A.n_q : A.n_seq;
+  if (warp == 1 || warp == 2) {
+    const int T = __ldg(W.off + items), G = min((int)gridDim.x, max(T, 1));
+    const int i = min((int)blockIdx.x + warp - 1, G);
+    const int x = (int)((int64_t)T * i / G);
+    int b = items, c = 0;
+    if (x < T) {
+      b = wg_find(W.off, items, x);
+      // (items without products share their place with the one behind them: the last of them has it)
+      c = (x - __ldg(W.off + b)) / __ldg(&W.item[b].y);
+    }
+    if (lane == 0) {
+      if (warp == 1) {
+        S.begin_b = b;
+        S.begin_c = c;
+      } else {
+        S.end_b = b;
+        S.end_c = c;
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = S.tmem;
+  WgWalk<NQ> C;
+  C.b = S.begin_b;
+  C.end_b = min(S.end_b, items - 1);
+  C.end_c = S.end_c;
+  if (S.end_b >= items) C.end_c = wg_chunks(__ldg(&W.item[items - 1].x));
+  const bool more = C.b < items && C.settle(W, S.begin_c);
+  if (warp >= kWgSumWarps && warp < kWgSumWarps + kWgKWarps) {
+    // products of the run (the team needs no more of it)
+    int steps = 0;
+    WgWalk<NQ> D = C;
+    for (bool m = more; m; m = D.settle(W, 0)) {
+      steps += (D.seq_hi - D.lo) * D.I.y;
+      D.b++;
+    }
+    wg_load<NQ>(A, S, sm, steps, tmem);
+  } else if (warp < kWgSumWarps) {
+    wg_sum<NQ, SEL>(A, W, S, sm, C, more, tmem);
+  } else if (warp == kWgSumWarps + kWgKWarps) {
+    wg_fetch<NQ, SEL>(A, W, S, sm, C, more);
+  } else if (warp == kWgSumWarps + kWgKWarps + 1) {
+    if (ptx::elect_one()) wg_issue<NQ>(A, W, S, sm, C, more, tmem);
+  }
+  __syncwarp();
+  __syncthreads();
+  if (S.bad) {
+    // a wait ran out: every MMA issued here finishes before the tensor memory goes back (bounded)
+    ptx::mbar_wait(&S.drain, 0);
+    ptx::tc_fence_after();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kWgTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------ selections
 // What selections start from: decay prior, of every entry that a query of the sequence sees.
-__global__ void __launch_bounds__(kWgThreads) weigh_decay_kernel(const __grid_constant__ WeighArgs A) {
+constexpr int kDecayThreads = 256;
+__global__ void __launch_bounds__(kDecayThreads) weigh_decay_kernel(const __grid_constant__ WeighArgs A) {
   const int t = threadIdx.x, b = blockIdx.y;
   griddep_wait();
   griddep_launch();
   int c0, c1, most = 0;
   weigh_queries(A, b, c0, c1);
-  for (int q = c0 + t; q < c1; q += kWgThreads) most = max(most, weigh_vis(A, q));
+  for (int q = c0 + t; q < c1; q += kDecayThreads) most = max(most, weigh_vis(A, q));
   __shared__ int most_sh;
   if (t == 0) most_sh = 0;
   __syncthreads();
   atomicMax(&most_sh, most);
   __syncthreads();
   most = most_sh;
-  for (int64_t j = (int64_t)blockIdx.x * kWgThreads + t; j < most; j += (int64_t)gridDim.x * kWgThreads) {
+  for (int64_t j = (int64_t)blockIdx.x * kDecayThreads + t; j < most; j += (int64_t)gridDim.x * kDecayThreads) {
     const int64_t s = weigh_slot(A, b, (int)j);
     if (s >= 0) A.weight[s] = A.prior != nullptr ? A.decay * A.prior[s] : 0.f;
   }
@@ -177,28 +770,37 @@ static void weigh_magic(unsigned n, uint64_t &mul, int &shift) {      // j / n, 
   mul = (uint64_t)((((unsigned __int128)1 << shift) + n - 1) / n);
 }
 
-size_t weigh_workspace_bytes(int n_q, int64_t n_seq, int sel_stride) {
-  (void)n_seq;
-  return (size_t)n_q * (size_t)sel_stride * sizeof(float) + 256;
+template <int NQ, bool SEL>
+static cudaError_t launch_products(const WeighArgs &A, const WgWs &W, int dev, cudaStream_t st) {
+  static std::atomic<int> attr_done[kMaxDevices];
+  cudaError_t e = once_per_device(attr_done, dev, [&] {
+    return cudaFuncSetAttribute(weigh_kernel<NQ, SEL>, cudaFuncAttributeMaxDynamicSharedMemorySize, WgSmem<NQ>::kAlloc);
+  });
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(weigh_prep_kernel, dim3((unsigned)A.n_q + 1), dim3(kPrepThreads), 0, st, 1u, A, W, NQ);
+  if (e != cudaSuccess) return e;
+  // no more CTAs than there can be chunks
+  const int64_t sms = device_sm_count(dev), row = SEL ? A.sel_stride : A.table_stride * A.page;
+  const int64_t chunks = (SEL ? A.n_q : A.n_seq) * ((row + kWgChunk - 1) / kWgChunk);
+  return launch_pdl(weigh_kernel<NQ, SEL>, dim3((unsigned)(chunks < sms ? chunks : sms)), dim3(kWgThreads), (size_t)WgSmem<NQ>::kAlloc, st, 1u, A, W);
 }
 
 cudaError_t launch_weigh(WeighArgs A, void *ws, cudaStream_t st) {
+  const int dev = current_device();
   weigh_magic((unsigned)A.page, A.page_mul, A.page_shift);
-  float *part = static_cast<float *>(ws);
-  const int64_t row = A.table_stride * A.page;
-  if (A.sel == nullptr) {
-    const int64_t tiles = (row + kWgTile - 1) / kWgTile;
-    return launch_pdl(weigh_kernel<false>, dim3((unsigned)(tiles < 8192 ? tiles : 8192), (unsigned)A.n_seq), dim3(kWgThreads), 0, st, 1u, A, part);
-  }
+  WgWs W;
+  wg_layout(&W, ws, A.n_q, A.n_seq, A.sel_stride);
+  if (A.sel == nullptr)                              // two queries at a time where a sequence can have two
+    return A.n_q > A.n_seq ? launch_products<2, false>(A, W, dev, st) : launch_products<1, false>(A, W, dev, st);
   cudaError_t e = cudaSuccess;
   if (A.prior != A.weight || A.decay != 1.f) {
-    const int64_t tiles = (row + 4 * kWgThreads - 1) / (4 * kWgThreads);
-    e = launch_pdl(weigh_decay_kernel, dim3((unsigned)(tiles < 512 ? tiles : 512), (unsigned)A.n_seq), dim3(kWgThreads), 0, st, 1u, A);
+    const int64_t tiles = (A.table_stride * A.page + 4 * kDecayThreads - 1) / (4 * kDecayThreads);
+    e = launch_pdl(weigh_decay_kernel, dim3((unsigned)(tiles < 512 ? tiles : 512), (unsigned)A.n_seq), dim3(kDecayThreads), 0, st, 1u, A);
     if (e != cudaSuccess) return e;
   }
-  e = launch_pdl(weigh_kernel<true>, dim3((unsigned)(A.sel_stride + kWgTile - 1) / kWgTile, (unsigned)A.n_q), dim3(kWgThreads), 0, st, 1u, A, part);
+  e = launch_products<1, true>(A, W, dev, st);
   if (e != cudaSuccess) return e;
-  return launch_pdl(weigh_add_kernel, dim3((unsigned)A.n_seq), dim3(kTopK), 0, st, 1u, A, (const float *)part);
+  return launch_pdl(weigh_add_kernel, dim3((unsigned)A.n_seq), dim3(kTopK), 0, st, 1u, A, (const float *)W.part);
 }
 
 }  // namespace csa2
