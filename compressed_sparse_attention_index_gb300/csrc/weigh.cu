@@ -6,7 +6,7 @@
 // Work: the entries that a sequence's queries see form chunks of 128, its queries groups
 // of NQ.  All sequences' (chunk, group) products are dealt to the CTAs (one an SM) in contiguous runs of equal
 // numbers, cut between chunks, so that one CTA has all of an entry's queries and sums them in a fixed order.
-// With several groups a CTA takes 16 chunks at a time (one query a group: 8), group by group: Q stays in shared memory
+// With several groups a CTA takes 24 chunks at a time (one query a group: 16), group by group: Q stays in shared memory
 // for them, their records in L2 for the groups, and their sums in shared memory.  A selection is a
 // sequence of its own: its chunks' weights go to scratch, and are added query by query.
 //
@@ -18,9 +18,9 @@
 // so a bf16 value 2^-29 of that and above is exact; f_h = scale log2(e) over that power.  (A first launch does
 // that, and lays Q out as the tensor cores read it.)
 //
-// Warps, with their own barriers between them: one fetches records and Q by bulk copies; sixteen dequantise,
+// Warps, with their own barriers between them: two fetch records and one Q by bulk copies; sixteen dequantise,
 // a row per thread and 128 dims a team, into tensor memory, where the MMAs read K as their A operand;
-// eight sum S; one thread issues the MMAs.
+// two threads issue the MMAs; eight sum S.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <limits.h>
@@ -34,24 +34,30 @@
 namespace csa2 {
 
 constexpr int kWgChunk = 128;                      // entries
-constexpr int kWgSumWarps = 8, kWgKWarps = 16, kWgWarps = 28;
+constexpr int kWgSumWarps = 8, kWgKWarps = 16, kWgWarps = 32;
 constexpr int kWgThreads = kWgWarps * 32;
+// Registers: 1,024 threads are launched with 64 each; the summing warps, which read tensor memory ahead of
+// their arithmetic, take what the others give up.
+constexpr int kWgRegsSum = 88, kWgRegsK = 56, kWgRegsRest = 56;
+static_assert(kWgSumWarps * kWgRegsSum + kWgKWarps * kWgRegsK + 8 * kWgRegsRest <= 64 * kWgWarps, "register split");
 constexpr int kWgRaw = kWgChunk * kKvBytes;        // one chunk's records
 constexpr int kWgQBlock = 64 * 128;                // 64 heads x 64 dims f16: [h/8][h%8][128 B]
 constexpr int kWgImage = 8 * kWgQBlock;            // a query as the tensor cores read it
 constexpr int kWgMeta = 2 * kHeads * 4;            // its heads' f, then their -lse log2(e)
-constexpr int kWgMetas = 4;                        // groups whose f and lse are in shared memory
+constexpr int kWgMetas = 8;                        // groups whose f and lse are in shared memory
+constexpr int kWgSlots = 8;                        // chunks whose slots are in shared memory
 constexpr int kWgScatter = 8;                      // pages of fewer entries are fetched as scattered records
 
 template <int NQ>
 struct WgSmem {
   static constexpr int kStages = NQ == 1 ? 4 : 2;  // records of as many chunks
-  static constexpr int kBlock = NQ == 1 ? 8 : 16;  // chunks that take turns at several groups
+  static constexpr int kBlock = NQ == 1 ? 16 : 24; // chunks that take turns at several groups
   static constexpr int kQ = 0;                     // [dims / 64][query][heads]
   static constexpr int kRaw = kQ + NQ * kWgImage;
-  static constexpr int kAcc = kRaw + kStages * kWgRaw;         // [2][kBlock chunks][128]
-  static constexpr int kMeta = kAcc + 2 * kBlock * kWgChunk * 4;
-  static constexpr int kEnd = kMeta + kWgMetas * NQ * kWgMeta;
+  static constexpr int kAcc = kRaw + kStages * kWgRaw;         // [kBlock chunks][128]
+  static constexpr int kMeta = kAcc + kBlock * kWgChunk * 4;
+  static constexpr int kSlot = kMeta + kWgMetas * NQ * kWgMeta;
+  static constexpr int kEnd = kSlot + kWgSlots * kWgChunk * 4;
   static constexpr int kAlloc = kEnd + 1024;
   static_assert(kAlloc + 512 <= 227 * 1024, "shared memory");
 };
@@ -111,18 +117,18 @@ __device__ __forceinline__ int64_t weigh_slot(const WeighArgs &A, int b, int j) 
 }
 
 // ------------------------------------------------------------------ what the products need
-constexpr int kPrepThreads = 256;
+constexpr int kPrepThreads = 256, kPrepCtas = 8;     // CTAs of a query
 __device__ __forceinline__ float wg_power(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
-// The first CTA: the items and the products ahead of each.  One for each query behind it: its
+// The first CTA: the items and the products ahead of each.  Eight for each query behind it: its
 // heads' powers of two, f16 image and constants.
 __global__ void __launch_bounds__(kPrepThreads) weigh_prep_kernel(const __grid_constant__ WeighArgs A, WgWs W, int nq) {
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   griddep_wait();
   griddep_launch();
   if (blockIdx.x > 0) {
-    const int q = (int)blockIdx.x - 1;
-    if (A.sel != nullptr && t == 0) {
+    const int q = ((int)blockIdx.x - 1) / kPrepCtas, part = ((int)blockIdx.x - 1) % kPrepCtas;
+    if (A.sel != nullptr && part == 0 && t == 0) {
       int lo = 0, hi = A.n_seq;                      // the last sequence with first <= q
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -132,10 +138,9 @@ __global__ void __launch_bounds__(kPrepThreads) weigh_prep_kernel(const __grid_c
       int c0, c1;
       W.q_seq[q] = weigh_queries(A, lo, c0, c1) && q >= c0 && q < c1 ? lo : -1;
     }
-    // eight heads a warp, 16 dims a lane
-#pragma unroll 2
-    for (int i = 0; i < 8; i++) {
-      const int h = warp * 8 + i;
+    // a head a warp, 16 dims a lane
+    {
+      const int h = part * (kPrepThreads / 32) + warp;
       const uint4 *src = reinterpret_cast<const uint4 *>(A.q + ((int64_t)q * kHeads + h) * kDim) + lane * 2;
       const uint4 x = __ldg(src), y = __ldg(src + 1);
       const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
@@ -243,10 +248,12 @@ struct WgWalk {
   int4 I;
   int lo, hi, seq_hi;           // the block's chunks; the item's end in this run
   int g, c;
+  int group;                    // groups of the run that have begun, less one
   __device__ __forceinline__ void block() {
     hi = I.y > 1 ? min(lo + WgSmem<NQ>::kBlock, seq_hi) : seq_hi;
     g = 0;
     c = lo;
+    group++;
   }
   // the next item that has a chunk in the run (false: the run is over)
   __device__ __forceinline__ bool settle(const WgWs &W, int from) {
@@ -264,6 +271,7 @@ struct WgWalk {
     if (++c < hi) return true;
     if (++g < I.y) {
       c = lo;
+      group++;
       return true;
     }
     lo = hi;
@@ -274,13 +282,12 @@ struct WgWalk {
     b++;
     return settle(W, 0);
   }
-  __device__ __forceinline__ bool group_begins() const { return c == lo; }
   __device__ __forceinline__ bool group_ends() const { return c + 1 == hi; }
   __device__ __forceinline__ bool last_group() const { return g + 1 == I.y; }
 };
 
 struct WgShared {
-  uint64_t raw_full[4], raw_free[4], k_full[4], k_free[4], q_full[4], q_free[4], s_full[2], s_free[2], m_full[kWgMetas], drain;
+  uint64_t raw_full[4], raw_free[4], k_full[2][4], k_free[4], q_full[4], q_free[4], s_full[2], s_free[2], m_full[kWgMetas], drain;
   uint32_t tmem;
   int begin_b, begin_c, end_b, end_c, steps;
   volatile int bad;
@@ -288,103 +295,101 @@ struct WgShared {
 
 // A wait that runs out marks the CTA bad; from then on no role waits, so that all of them run out
 // of products in bounded time.
-__device__ __forceinline__ void wg_wait(const WeighArgs &A, WgShared &S, uint64_t *bar, uint32_t parity) {
+__device__ __forceinline__ void wg_wait_long(int *status, volatile int *bad, uint64_t *bar, uint32_t parity) {
   uint64_t t0 = 0;
   for (int i = 0; !ptx::mbar_try_wait_sleep(bar, parity, 1000000u); i++) {
-    if (S.bad) return;
+    if (*bad) return;
     if (i < 64) {
       t0 = ptx::globaltimer();
     } else if (ptx::globaltimer() - t0 > 2000000000ull) {
-      record_error(A.status, CSA2_ERR_TIMEOUT);
-      S.bad = 1;
+      record_error(status, CSA2_ERR_TIMEOUT);
+      *bad = 1;
       return;
     }
   }
 }
+__device__ __forceinline__ void wg_wait(const WeighArgs &A, WgShared &S, uint64_t *bar, uint32_t parity) {
+  if (!ptx::mbar_try_wait(bar, parity)) wg_wait_long(A.status, &S.bad, bar, parity);
+}
 __device__ __forceinline__ bool wg_bad(const WgShared &S) { return __any_sync(0xFFFFFFFFu, S.bad); }
 
 // ------------------------------------------------------------------ records and Q
+// Two warps take turns at the chunks (one took longer over a chunk than the MMAs): a lane finds the
+// records of four rows, and asks for the places of its next chunk's before it waits for a buffer.
 template <int NQ, bool SEL>
-__device__ __forceinline__ void wg_fetch(const WeighArgs &A, const WgWs &W, WgShared &S, unsigned char *sm, WgWalk<NQ> C, bool more) {
+__device__ __forceinline__ void wg_fetch(const WeighArgs &A, const WgWs &W, WgShared &S, unsigned char *sm, WgWalk<NQ> C, bool more, int turn) {
   using M = WgSmem<NQ>;
   const int lane = threadIdx.x & 31;
   const bool scattered = SEL || A.page < kWgScatter;
-  int rec[4];                                        // rows 32 g + lane: the record, -1: none
-  int rows[4];                                       // of the run that this lane leads, 0: none
-  int all_rows = 0;
-  auto look_up = [&]() {
-    int j[4], id[4], off[4];
-    int seq = C.b, vis = 0;
+  int id[4], off[4];                                 // rows 32 g + lane: the page (-1: none), the place in it
+  bool out = false;
+  auto ask = [&]() {
+    int j[4], seq = C.b;
     if (SEL) {
       seq = __ldg(W.q_seq + C.b);
-      vis = seq >= 0 ? weigh_vis(A, C.b) : 0;
-    }
-    bool out = false;
+      const int vis = seq >= 0 ? weigh_vis(A, C.b) : 0;
 #pragma unroll
-    for (int g = 0; g < 4; g++) {
-      const int i = C.c * kWgChunk + 32 * g + lane;
-      j[g] = i;
-      if (SEL) {
+      for (int g = 0; g < 4; g++) {
+        const int i = C.c * kWgChunk + 32 * g + lane;
         j[g] = i < A.sel_stride && seq >= 0 ? __ldg(A.sel + (int64_t)C.b * A.sel_stride + i) : -1;
         if (j[g] >= vis) {
           out |= vis >= 0;                           // (a query that is out of range itself is recorded already)
           j[g] = -1;
         }
-      } else if (i >= C.I.x) {
-        j[g] = -1;
+      }
+    } else {
+#pragma unroll
+      for (int g = 0; g < 4; g++) {
+        const int i = C.c * kWgChunk + 32 * g + lane;
+        j[g] = i < C.I.x ? i : -1;
       }
     }
 #pragma unroll
     for (int g = 0; g < 4; g++) {
       const int col = j[g] >= 0 ? weigh_col(A, j[g]) : 0;
       off[g] = j[g] - col * A.page;
-      id[g] = j[g] >= 0 ? __ldg(A.table + (int64_t)seq * A.table_stride + col) : -1;
+      id[g] = -1;
+      if (j[g] >= 0) {
+        id[g] = __ldg(A.table + (int64_t)seq * A.table_stride + col);
+        if (id[g] < 0) id[g] = INT_MIN;              // (an entry without a page)
+      }
     }
+  };
+  if (more && turn > 0) more = C.next(W);
+  if (more) ask();
+  int k = turn;
+#pragma unroll 1
+  for (; more; k += 2) {
+    const int stage = k % M::kStages;
+    int rec[4], rows[4], all_rows = 0;               // the record, -1: none; rows of the run that this lane leads, 0: none
 #pragma unroll
     for (int g = 0; g < 4; g++) {
       const bool ok = id[g] >= 0 && id[g] < A.n_pages;
-      if (SEL) out |= j[g] >= 0 && !ok;              // (dense rows are checked where they are written)
-      if (!ok) id[g] = -1;
-      rec[g] = ok ? id[g] * A.page + off[g] : -1;
-      const int pid = __shfl_up_sync(0xFFFFFFFFu, id[g], 1), poff = __shfl_up_sync(0xFFFFFFFFu, off[g], 1);
-      const bool leads = ok && (lane == 0 || pid != id[g] || poff + 1 != off[g]);
+      out |= !ok && id[g] != -1;
+      const int here = ok ? id[g] : -1;
+      rec[g] = ok ? here * A.page + off[g] : -1;
+      const int pid = __shfl_up_sync(0xFFFFFFFFu, here, 1), poff = __shfl_up_sync(0xFFFFFFFFu, off[g], 1);
+      const bool leads = ok && (lane == 0 || pid != here || poff + 1 != off[g]);
       const uint32_t valid = __ballot_sync(0xFFFFFFFFu, ok), lead = __ballot_sync(0xFFFFFFFFu, leads);
       const uint32_t stop = (lead | ~valid) & ~((2u << lane) - 1u);        // (lane 31: 2 << 31 is 0)
       rows[g] = leads ? (stop != 0u ? __ffs(stop) - 1 : 32) - lane : 0;
-      all_rows = g == 0 ? __popc(valid) : all_rows + __popc(valid);
+      all_rows += __popc(valid);
     }
-    if (out) record_error(A.status, CSA2_ERR_BOUNDS);
-  };
-  if (more) look_up();
-  int groups = 0, slabs = 0, k = 0;                  // begun, asked for, fetched
-#pragma unroll 1
-  for (; more; k++) {
-    const int stage = k % M::kStages;
-    if (C.group_begins()) {
-      // Q slab by slab, as the group before lets go of it, and beside the first of them f and lse (their place
-      // was used four groups ago: the sums have left it once the group before is at its last product)
-      const int q0 = C.I.z + C.g * NQ, n = min(NQ, C.I.w - C.g * NQ), place = groups % kWgMetas;
-#pragma unroll 1
-      for (int s = 0; s < 4; s++) {
-        if (groups > 0) wg_wait(A, S, &S.q_free[s], (uint32_t)(groups - 1) & 1u);
-        if (wg_bad(S)) break;
-        if (lane == 0) {
-          if (s == 0) {
-            ptx::mbar_arrive_expect_tx(&S.m_full[place], (uint32_t)(n * kWgMeta));
-            ptx::bulk_load(sm + M::kMeta + place * NQ * kWgMeta, W.meta + (int64_t)q0 * kWgMeta, (uint32_t)(n * kWgMeta), &S.m_full[place]);
-          }
-          ptx::mbar_arrive_expect_tx(&S.q_full[s], (uint32_t)(n * 2 * kWgQBlock));
-          for (int i = 0; i < 2; i++)
-            for (int x = 0; x < n; x++)
-              ptx::bulk_load(sm + M::kQ + ((2 * s + i) * NQ + x) * kWgQBlock, W.image + (int64_t)(q0 + x) * kWgImage + (2 * s + i) * kWgQBlock, kWgQBlock, &S.q_full[s]);
-        }
-        slabs++;
-        __syncwarp();
-      }
-      groups++;
-    }
+    const bool last = C.last_group();
+    more = C.next(W);
+    if (more) more = C.next(W);
+    if (more) ask();
     if (k >= M::kStages) wg_wait(A, S, &S.raw_free[stage], (uint32_t)(k / M::kStages - 1) & 1u);
     if (wg_bad(S)) break;                            // no copy is started any more
+    if (!SEL && last) {
+      // (its place was used eight products ago: the sums have read it before the products that freed the buffer)
+      int *slot = reinterpret_cast<int *>(sm + M::kSlot) + (k % kWgSlots) * kWgChunk + lane;
+#pragma unroll
+      for (int g = 0; g < 4; g++) {
+        slot[32 * g] = rec[g];
+        if (A.prior != nullptr && rec[g] >= 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(A.prior + rec[g]));
+      }
+    }
     uint64_t *full = &S.raw_full[stage];
     unsigned char *to = sm + M::kRaw + stage * kWgRaw;
     if (scattered) {
@@ -407,13 +412,42 @@ __device__ __forceinline__ void wg_fetch(const WeighArgs &A, const WgWs &W, WgSh
 #pragma unroll
       for (int g = 0; g < 4; g++)
         if (rows[g] > 0) ptx::bulk_load(to + (32 * g + lane) * kKvBytes, A.pages + (int64_t)rec[g] * kKvBytes, (uint32_t)(rows[g] * kKvBytes), full);
-    more = C.next(W);
-    if (more) look_up();
+  }
+  if (out) record_error(A.status, CSA2_ERR_BOUNDS);
+  // its last copies have landed before the CTA may leave (bounded)
+  for (int i = k - 2; i >= 0 && i >= k - M::kStages; i -= 2) ptx::mbar_wait(&S.raw_full[i % M::kStages], (uint32_t)(i / M::kStages) & 1u);
+}
+
+// Q of a group slab by slab, as the group before lets go of it, and beside the first of them f and lse
+// (their place was used eight groups ago: the sums have left it once the group before is at its last product).
+template <int NQ>
+__device__ __forceinline__ void wg_fetch_q(const WeighArgs &A, const WgWs &W, WgShared &S, unsigned char *sm, WgWalk<NQ> C, bool more) {
+  using M = WgSmem<NQ>;
+  int slabs = 0;
+#pragma unroll 1
+  for (int group = 0; more; group++) {
+    const int q0 = C.I.z + C.g * NQ, n = min(NQ, C.I.w - C.g * NQ), place = group % kWgMetas;
+#pragma unroll 1
+    for (int s = 0; s < 4; s++) {
+      if (group > 0) wg_wait(A, S, &S.q_free[s], (uint32_t)(group - 1) & 1u);
+      if (S.bad) break;
+      if (s == 0) {
+        ptx::mbar_arrive_expect_tx(&S.m_full[place], (uint32_t)(n * kWgMeta));
+        ptx::bulk_load(sm + M::kMeta + place * NQ * kWgMeta, W.meta + (int64_t)q0 * kWgMeta, (uint32_t)(n * kWgMeta), &S.m_full[place]);
+      }
+      ptx::mbar_arrive_expect_tx(&S.q_full[s], (uint32_t)(n * 2 * kWgQBlock));
+      for (int i = 0; i < 2; i++)
+        for (int x = 0; x < n; x++)
+          ptx::bulk_load(sm + M::kQ + ((2 * s + i) * NQ + x) * kWgQBlock, W.image + (int64_t)(q0 + x) * kWgImage + (2 * s + i) * kWgQBlock, kWgQBlock, &S.q_full[s]);
+      slabs++;
+    }
+    C.c = C.hi - 1;
+    more = C.next(W) && !S.bad;
   }
   // its last copies have landed before the CTA may leave (bounded)
-  for (int i = max(0, k - M::kStages); i < k; i++) ptx::mbar_wait(&S.raw_full[i % M::kStages], (uint32_t)(i / M::kStages) & 1u);
   for (int i = max(0, slabs - 4); i < slabs; i++) ptx::mbar_wait(&S.q_full[i & 3], (uint32_t)(i >> 2) & 1u);
-  for (int i = max(0, (slabs + 3) / 4 - kWgMetas); i < (slabs + 3) / 4; i++) ptx::mbar_wait(&S.m_full[i % kWgMetas], (uint32_t)(i / kWgMetas) & 1u);
+  const int metas = (slabs + 3) / 4;
+  for (int i = max(0, metas - kWgMetas); i < metas; i++) ptx::mbar_wait(&S.m_full[i % kWgMetas], (uint32_t)(i / kWgMetas) & 1u);
 }
 
 // ------------------------------------------------------------------ dequantisation
@@ -430,6 +464,7 @@ __device__ __forceinline__ void wg_load(const WeighArgs &A, WgShared &S, const u
   const int other = flip ? -16 : 16;
   int stage = 0;
   uint32_t turn = 0u;
+#pragma unroll 1
   for (int k = 0; k < steps; k++) {
     wg_wait(A, S, &S.raw_full[stage], turn);
     const unsigned char *row = sm + M::kRaw + stage * kWgRaw + e * kKvBytes;
@@ -448,48 +483,63 @@ __device__ __forceinline__ void wg_load(const WeighArgs &A, WgShared &S, const u
       stage = 0;
       turn ^= 1u;
     }
-    if (k > 0) wg_wait(A, S, &S.k_free[team], (uint32_t)(k - 1) & 1u);
-    ptx::tc_fence_after();
+    // half of the slab is converted before the wait for its place, beside the MMAs of the chunk before
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const uint32_t w[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
-      const uint32_t two = e4m3x2_to_f16x2((j < 2 ? sc.x : sc.y) >> (16 * (j & 1)));
-      const uint32_t s2[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
-      uint32_t o[16];
+    for (int hf = 0; hf < 2; hf++) {
+      uint32_t o[2][16];
 #pragma unroll
-      for (int u = 0; u < 4; u++) {
-        uint32_t x[4];
-        e2m1x8_to_f16(w[u], x);
+      for (int i = 0; i < 2; i++) {
+        const int j = 2 * hf + i;
+        const uint32_t w[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
+        const uint32_t two = e4m3x2_to_f16x2((hf == 0 ? sc.x : sc.y) >> (16 * i));
+        const uint32_t s2[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
 #pragma unroll
-        for (int q = 0; q < 4; q++) {
-          const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x[q]), *reinterpret_cast<const __half2 *>(&s2[u >> 1]));
-          o[4 * u + q] = *reinterpret_cast<const uint32_t *>(&y);
+        for (int u = 0; u < 4; u++) {
+          uint32_t x[4];
+          e2m1x8_to_f16(w[u], x);
+#pragma unroll
+          for (int q = 0; q < 4; q++) {
+            const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x[q]), *reinterpret_cast<const __half2 *>(&s2[u >> 1]));
+            o[i][4 * u + q] = *reinterpret_cast<const uint32_t *>(&y);
+          }
         }
       }
-      ptx::tmem_st_32x32b_x16(kcol + j * 16, o);
+      if (hf == 0) {
+        if (k > 0) wg_wait(A, S, &S.k_free[team], (uint32_t)(k - 1) & 1u);
+        ptx::tc_fence_after();
+      }
+#pragma unroll
+      for (int i = 0; i < 2; i++) ptx::tmem_st_32x32b_x16(kcol + (2 * hf + i) * 16, o[i]);
     }
     ptx::tmem_wait_st();
     ptx::tc_fence_before();
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(&S.k_full[team]);
+    if (lane == 0) ptx::mbar_arrive(&S.k_full[k & 1][team]);
   }
 }
 
 // ------------------------------------------------------------------ MMAs
+// Two threads take turns at the chunks (one took longer to issue a chunk's than they take to run).  A slab of K is
+// written again only when the MMAs that read it are complete, so a chunk's MMAs on a slab follow the chunk's before.
+// (A wait by parity holds only for who has seen the phase before, or knows of it: each thread has K's barriers of its own,
+// and once a slab of K is there the group before has had its Q.)
 template <int NQ>
-__device__ __forceinline__ void wg_issue(const WeighArgs &A, const WgWs &W, WgShared &S, unsigned char *sm, WgWalk<NQ> C, bool more, uint32_t tmem) {
+__device__ __forceinline__ void wg_issue(const WeighArgs &A, const WgWs &W, WgShared &S, unsigned char *sm, WgWalk<NQ> C, bool more, int turn, uint32_t tmem) {
   const uint64_t d_q = ptx::smem_desc(ptx::smem_u32(sm + WgSmem<NQ>::kQ), 16, 1024, 2);
-  int groups = 0;
-  for (int k = 0; more && !S.bad; k++) {
-    const bool begins = C.group_begins(), ends = C.group_ends();
-    if (begins) groups++;
+  const uint32_t d = tmem + kWgColS + (uint32_t)turn * 128u;
+  int seen = -1;                                     // the group whose Q this thread has waited for
+  if (more && turn > 0) more = C.next(W);
+#pragma unroll 1
+  for (int k = turn; more && !S.bad; k += 2) {
+    const bool fresh = C.group != seen, ends = C.group_ends();
+    const uint32_t q_parity = (uint32_t)C.group & 1u;
+    seen = C.group;
     const uint32_t id = NQ == 2 && C.I.w - C.g * NQ >= 2 ? idesc_m128(0, true, 2 * kHeads) : idesc_m128(0, true, kHeads);
-    const uint32_t d = tmem + kWgColS + (uint32_t)(k & 1) * 128u;
-    if (k >= 2) wg_wait(A, S, &S.s_free[k & 1], (uint32_t)((k >> 1) - 1) & 1u);
+    if (k >= 2) wg_wait(A, S, &S.s_free[turn], (uint32_t)((k >> 1) - 1) & 1u);
 #pragma unroll 1
     for (int s = 0; s < 4; s++) {
-      wg_wait(A, S, &S.k_full[s], (uint32_t)k & 1u);
-      if (begins) wg_wait(A, S, &S.q_full[s], (uint32_t)(groups - 1) & 1u);
+      wg_wait(A, S, &S.k_full[turn][s], (uint32_t)(k >> 1) & 1u);
+      if (fresh) wg_wait(A, S, &S.q_full[s], q_parity);
       ptx::tc_fence_after();
       const uint32_t ka = tmem + kWgColK + (uint32_t)s * 64u;
       const uint64_t qa = d_q + (uint64_t)(s * 2 * NQ * (kWgQBlock >> 4));
@@ -499,8 +549,9 @@ __device__ __forceinline__ void wg_issue(const WeighArgs &A, const WgWs &W, WgSh
       ptx::tc_commit(&S.k_free[s]);
       if (ends) ptx::tc_commit(&S.q_free[s]);
     }
-    ptx::tc_commit(&S.s_full[k & 1]);
+    ptx::tc_commit(&S.s_full[turn]);
     more = C.next(W);
+    if (more) more = C.next(W);
   }
   ptx::tc_commit(&S.drain);
 }
@@ -532,84 +583,87 @@ __device__ __forceinline__ float wg_ex2(float x) {
   return y;
 }
 
-// Warp w has entries 32 (w % 4) .. of a chunk and, by w / 4, one of the group's two queries, or half of
-// the heads of its only one.
+// Adds 32 heads' numerators of this lane's entry to sum.
+__device__ __forceinline__ void wg_add_heads(const uint32_t (&a)[32], const float *f, const float *nl, uint64_t (&sum)[4]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(f + i), y = *reinterpret_cast<const ulonglong2 *>(nl + i);
+    const float2 u = wg_unpair(wg_fma2(wg_pair(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), x.x, y.x));
+    const float2 v = wg_unpair(wg_fma2(wg_pair(__uint_as_float(a[i + 2]), __uint_as_float(a[i + 3])), x.y, y.y));
+    sum[(i >> 1) & 2] = wg_add2(sum[(i >> 1) & 2], wg_pair(wg_ex2(u.x), wg_ex2(u.y)));
+    sum[((i >> 1) & 2) + 1] = wg_add2(sum[((i >> 1) & 2) + 1], wg_pair(wg_ex2(v.x), wg_ex2(v.y)));
+  }
+}
+__device__ __forceinline__ float wg_total(const uint64_t (&sum)[4]) {
+  const float2 all = wg_unpair(wg_add2(wg_add2(sum[0], sum[1]), wg_add2(sum[2], sum[3])));
+  return all.x + all.y;
+}
+
+// Warps 0 .. 3 and 4 .. 7 take turns at the chunks, each with 32 of its entries over all of the
+// group's heads.  Tensor memory is read 32 heads ahead of the arithmetic.
 template <int NQ, bool SEL>
 __device__ __forceinline__ void wg_sum(const WeighArgs &A, const WgWs &W, WgShared &S, unsigned char *sm, WgWalk<NQ> C, bool more, uint32_t tmem) {
   using M = WgSmem<NQ>;
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
-  const uint32_t ts = tmem + ((uint32_t)(quarter * 32) << 16) + kWgColS;
-  float *acc = reinterpret_cast<float *>(sm + M::kAcc);
-  int groups = 0, vis = 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quarter = warp & 3, turn = warp >> 2, row = quarter * 32 + lane;
+  const uint32_t ts = tmem + ((uint32_t)(quarter * 32) << 16) + kWgColS + (uint32_t)turn * 128u;
+  float *acc = reinterpret_cast<float *>(sm + M::kAcc) + row;
+  int seen = -1, vis0 = 0, vis1 = 0;
   bool two = false;
-  for (int k = 0; more; k++) {
-    if (C.group_begins()) {
-      wg_wait(A, S, &S.m_full[groups % kWgMetas], (uint32_t)(groups / kWgMetas) & 1u);
-      groups++;
+#pragma unroll 1
+  for (int k = 0; more; k++, more = C.next(W)) {
+    if (C.group != seen) {
+      seen = C.group;
+      // (a chunk's sums of the group before may be the other four warps')
+      if (!SEL) asm volatile("bar.sync %0, 64;" ::"r"(quarter + 1) : "memory");
+      const int q = C.I.z + C.g * NQ;
       two = NQ == 2 && C.I.w - C.g * NQ >= 2;
-      if (!SEL) vis = weigh_vis(A, C.I.z + C.g * NQ + (two ? half : 0));
-      // (the halves' sums of the chunks before are read)
-      if (C.g == 0) asm volatile("bar.sync %0, 64;" ::"r"(quarter + 1) : "memory");
-    }
-    // where the chunk's weights go, looked up ahead of the products
-    const bool last = C.last_group();
-    int64_t slot = -1;
-    float before = 0.f;
-    if (!SEL && last && half == 0) {
-      const int j = C.c * kWgChunk + row;
-      if (j < C.I.x) {
-        slot = weigh_slot(A, C.b, j);
-        if (slot < 0) record_error(A.status, CSA2_ERR_BOUNDS);
-        else if (A.prior != nullptr) before = A.decay * A.prior[slot];
+      if (!SEL) {
+        vis0 = weigh_vis(A, q);
+        if (two) vis1 = weigh_vis(A, q + 1);
       }
     }
-    const float *f = reinterpret_cast<const float *>(sm + M::kMeta + ((groups - 1) % kWgMetas) * NQ * kWgMeta) + (two ? half * 2 * kHeads : half * 32);
-    const float *nl = f + kHeads;
-    wg_wait(A, S, &S.s_full[k & 1], (uint32_t)(k >> 1) & 1u);
+    if ((k & 1) != turn) continue;
+    const bool last = C.last_group();
+    const float *f = reinterpret_cast<const float *>(sm + M::kMeta + (seen % kWgMetas) * NQ * kWgMeta);
+    wg_wait(A, S, &S.s_full[turn], (uint32_t)(k >> 1) & 1u);
+    // (f and lse: as the group's products, or later; those of the groups before are there)
+    wg_wait(A, S, &S.m_full[seen % kWgMetas], (uint32_t)(seen / kWgMetas) & 1u);
     ptx::tc_fence_after();
-    const uint32_t ta = ts + (uint32_t)(k & 1) * 128u + (two ? (uint32_t)half * 64u : (uint32_t)half * 32u);
-    uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
-    const int cols = two ? 64 : 32;
+    int slot = -1;
+    float before = 0.f, w = 0.f;
+    if (!SEL && last) {                              // where the entry's weight is, asked for ahead of the sum
+      slot = reinterpret_cast<const int *>(sm + M::kSlot)[(k % kWgSlots) * kWgChunk + row];
+      if (S.bad) slot = -1;                          // (a place left from before, once a wait has run out)
+      if (slot >= 0 && A.prior != nullptr) before = A.prior[slot];
+    }
+    const int j = C.c * kWgChunk + row, n = NQ == 2 && two ? 2 : 1;
 #pragma unroll 1
-    for (int h = 0; h < cols; h += 32) {
-      uint32_t a[32];
-      ptx::tmem_ld_32x32b_x32(ta + h, a);
+    for (int x = 0; x < n; x++, f += 2 * kHeads) {
+      uint32_t a0[32], a1[32];
+      ptx::tmem_ld_32x32b_x32(ts + x * kHeads, a0);
+      uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
       ptx::tmem_wait_ld();
-      if (h + 32 == cols) {
+      ptx::tmem_ld_32x32b_x32(ts + x * kHeads + 32, a1);
+      wg_add_heads(a0, f, f + kHeads, sum);
+      ptx::tmem_wait_ld();
+      if (x + 1 == n) {
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&S.s_free[k & 1]);
+        if (lane == 0) ptx::mbar_arrive(&S.s_free[turn]);
       }
-#pragma unroll
-      for (int i = 0; i < 32; i += 4) {
-        const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(f + h + i), y = *reinterpret_cast<const ulonglong2 *>(nl + h + i);
-        const float2 u = wg_unpair(wg_fma2(wg_pair(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), x.x, y.x));
-        const float2 v = wg_unpair(wg_fma2(wg_pair(__uint_as_float(a[i + 2]), __uint_as_float(a[i + 3])), x.y, y.y));
-        sum[(i >> 1) & 2] = wg_add2(sum[(i >> 1) & 2], wg_pair(wg_ex2(u.x), wg_ex2(u.y)));
-        sum[((i >> 1) & 2) + 1] = wg_add2(sum[((i >> 1) & 2) + 1], wg_pair(wg_ex2(v.x), wg_ex2(v.y)));
-      }
+      wg_add_heads(a1, f + 32, f + kHeads + 32, sum);
+      if (SEL || j < (x == 0 ? vis0 : vis1)) w += wg_total(sum);
     }
-    const float2 all = wg_unpair(wg_add2(wg_add2(sum[0], sum[1]), wg_add2(sum[2], sum[3])));
-    float w = all.x + all.y;
-    if (!SEL && C.c * kWgChunk + row >= vis) w = 0.f;
-    // both halves' sums meet (one group: in two places by turns)
-    float *mine = acc + half * (M::kBlock * kWgChunk) + (C.I.y > 1 ? C.c - C.lo : k & 1) * kWgChunk + row;
+    float *mine = acc + (C.c - C.lo) * kWgChunk;     // (of several groups)
     if (C.g > 0) w += *mine;
-    if (!last || half == 1) *mine = w;
-    if (last) {
-      asm volatile("bar.sync %0, 64;" ::"r"(quarter + 1) : "memory");
-      if (half == 0) {
-        w += mine[M::kBlock * kWgChunk];
-        if (SEL) {
-          const int i = C.c * kWgChunk + row;
-          if (i < A.sel_stride) W.part[(int64_t)C.b * A.sel_stride + i] = w;
-        } else if (slot >= 0) {
-          A.weight[slot] = before + w;
-        }
-      }
+    if (!last) {
+      *mine = w;
+    } else if (SEL) {
+      if (j < A.sel_stride) W.part[(int64_t)C.b * A.sel_stride + j] = w;
+    } else if (slot >= 0) {
+      A.weight[slot] = A.decay * before + w;
     }
-    more = C.next(W);
   }
 }
 
@@ -640,17 +694,18 @@ __global__ void __launch_bounds__(kWgThreads, 1) weigh_kernel(const __grid_const
     for (int i = 0; i < 4; i++) {
       ptx::mbar_init(&S.raw_full[i], 1);
       ptx::mbar_init(&S.raw_free[i], kWgKWarps);
-      ptx::mbar_init(&S.k_full[i], kWgKWarps / 4);
+      ptx::mbar_init(&S.k_full[0][i], kWgKWarps / 4);
+      ptx::mbar_init(&S.k_full[1][i], kWgKWarps / 4);
       ptx::mbar_init(&S.k_free[i], 1);
       ptx::mbar_init(&S.q_full[i], 1);
       ptx::mbar_init(&S.q_free[i], 1);
     }
     for (int i = 0; i < 2; i++) {
       ptx::mbar_init(&S.s_full[i], 1);
-      ptx::mbar_init(&S.s_free[i], kWgSumWarps);
+      ptx::mbar_init(&S.s_free[i], kWgSumWarps / 2);
     }
     for (int i = 0; i < kWgMetas; i++) ptx::mbar_init(&S.m_full[i], 1);
-    ptx::mbar_init(&S.drain, 1);
+    ptx::mbar_init(&S.drain, 2);
     S.bad = 0;
     ptx::fence_mbar_init();
   }
@@ -688,8 +743,10 @@ __global__ void __launch_bounds__(kWgThreads, 1) weigh_kernel(const __grid_const
   C.end_b = min(S.end_b, items - 1);
   C.end_c = S.end_c;
   if (S.end_b >= items) C.end_c = wg_chunks(__ldg(&W.item[items - 1].x));
+  C.group = -1;
   const bool more = C.b < items && C.settle(W, S.begin_c);
   if (warp >= kWgSumWarps && warp < kWgSumWarps + kWgKWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWgRegsK));
     // products of the run (the team needs no more of it)
     int steps = 0;
     WgWalk<NQ> D = C;
@@ -699,11 +756,18 @@ __global__ void __launch_bounds__(kWgThreads, 1) weigh_kernel(const __grid_const
     }
     wg_load<NQ>(A, S, sm, steps, tmem);
   } else if (warp < kWgSumWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWgRegsSum));
     wg_sum<NQ, SEL>(A, W, S, sm, C, more, tmem);
-  } else if (warp == kWgSumWarps + kWgKWarps) {
-    wg_fetch<NQ, SEL>(A, W, S, sm, C, more);
-  } else if (warp == kWgSumWarps + kWgKWarps + 1) {
-    if (ptx::elect_one()) wg_issue<NQ>(A, W, S, sm, C, more, tmem);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWgRegsRest));
+    const int role = warp - kWgSumWarps - kWgKWarps;
+    if (role < 2) {
+      wg_fetch<NQ, SEL>(A, W, S, sm, C, more, role);
+    } else if (role < 4) {
+      if (ptx::elect_one()) wg_issue<NQ>(A, W, S, sm, C, more, role - 2, tmem);
+    } else if (role == 4) {
+      if (ptx::elect_one()) wg_fetch_q<NQ>(A, W, S, sm, C, more);
+    }
   }
   __syncwarp();
   __syncthreads();
@@ -777,7 +841,7 @@ static cudaError_t launch_products(const WeighArgs &A, const WgWs &W, int dev, c
     return cudaFuncSetAttribute(weigh_kernel<NQ, SEL>, cudaFuncAttributeMaxDynamicSharedMemorySize, WgSmem<NQ>::kAlloc);
   });
   if (e != cudaSuccess) return e;
-  e = launch_pdl(weigh_prep_kernel, dim3((unsigned)A.n_q + 1), dim3(kPrepThreads), 0, st, 1u, A, W, NQ);
+  e = launch_pdl(weigh_prep_kernel, dim3((unsigned)A.n_q * kPrepCtas + 1), dim3(kPrepThreads), 0, st, 1u, A, W, NQ);
   if (e != cudaSuccess) return e;
   // no more CTAs than there can be chunks
   const int64_t sms = device_sm_count(dev), row = SEL ? A.sel_stride : A.table_stride * A.page;
