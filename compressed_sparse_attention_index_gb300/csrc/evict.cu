@@ -6,8 +6,8 @@
 //
 // evict_select_kernel: a cluster per sequence finds the smallest weight that stays, as an order key,
 // by histograms of up to 11 bits at a time below the bits that all keys share (at most three, of one
-// pass each; the keys stay in shared memory where a CTA's part of the row fits).  Each warp has a
-// contiguous part of the row, so that one count of every part gives every kept entry its rank, and
+// pass each; keys stay in shared memory, 53,248 of a CTA's part of the row, and are read again behind
+// that).  Each warp has a contiguous part of the row, four tiles of it in flight, so that one count of every part gives every kept entry its rank, and
 // writes which entry each new place comes from.
 //
 // evict_move_kernel: tiles of kMvTile new places, read whole and then written.  In place, a tile's
@@ -27,6 +27,7 @@ namespace csa2 {
 
 constexpr int kEvThreads = 1024, kEvWarps = kEvThreads / 32, kEvBits = 11, kEvBins = 1 << kEvBits;
 constexpr int kEvMaxCtas = 16;
+constexpr int kEvKeyTiles = 13;                     // tiles of a warp's part whose keys fit shared memory (208 KB)
 constexpr int kMvTile = 128, kMvThreads = 288, kMvUnits = 8;     // a record is 18 units of 16 B
 static_assert(kMvThreads / 18 * kMvUnits == kMvTile, "a tile's units");
 
@@ -80,6 +81,14 @@ __device__ __forceinline__ uint32_t ev_get(const uint32_t *p, uint32_t rank) {
   return v;
 }
 
+__device__ __forceinline__ uint2 ev_get2(const uint32_t *p, uint32_t rank) {
+  uint32_t a;
+  uint2 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
 struct EvictShared {
   uint32_t hist[kEvBins];
   uint32_t lo[kEvWarps], hi[kEvWarps], gt[kEvWarps], eq[kEvWarps];
@@ -100,35 +109,47 @@ struct EvictRow {
     return id >= 0 && id < n_pages ? (int64_t)id * page + (j - c * page) : -1;
   }
   __device__ __forceinline__ uint32_t key(float w) const { return w == w ? order_key(w) : 0u; }
-  // four entries from j on, those below n (0 elsewhere)
-  __device__ __forceinline__ void keys(int j, int n, bool report, uint32_t (&x)[4]) const {
-    if ((page & 3) == 0 && j + 3 < n) {              // (one page holds them, on a 16-byte boundary)
-      const int64_t s = slot(j, col(j));
-      if (s >= 0) {
-        const float4 w = __ldg(reinterpret_cast<const float4 *>(weight + s));
-        x[0] = key(w.x);
-        x[1] = key(w.y);
-        x[2] = key(w.z);
-        x[3] = key(w.w);
-      } else {
-        x[0] = x[1] = x[2] = x[3] = 0u;
-        if (report) record_error(status, CSA2_ERR_BOUNDS);
-      }
-      return;
-    }
+  // keys of four tiles from `tile` on, four entries from j on of each for this lane: those below n (0 elsewhere)
+  __device__ __forceinline__ void keys(int tile, int lane, int n, bool report, uint32_t (&x)[4][4]) const {
+    const int j0 = tile * kMvTile + lane * 4;
+    bool out = false;
+    if ((page & 3) == 0) {                           // (one page holds the lane's four, on a 16-byte boundary)
+      int64_t s[4];
+      float4 w[4];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      x[i] = 0u;
-      if (j + i < n) {
-        const int64_t s = slot(j + i, col(j + i));
-        if (s >= 0) x[i] = key(__ldg(weight + s));
-        else if (report) record_error(status, CSA2_ERR_BOUNDS);
+      for (int u = 0; u < 4; u++) s[u] = j0 + u * kMvTile < n ? slot(j0 + u * kMvTile, col(j0 + u * kMvTile)) : -1;
+#pragma unroll
+      for (int u = 0; u < 4; u++) {
+        out |= s[u] < 0 && j0 + u * kMvTile < n;
+        w[u] = s[u] >= 0 ? __ldg(reinterpret_cast<const float4 *>(weight + s[u])) : make_float4(NAN, NAN, NAN, NAN);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; u++) {
+        const int left = n - (j0 + u * kMvTile);
+        x[u][0] = left > 0 ? key(w[u].x) : 0u;
+        x[u][1] = left > 1 ? key(w[u].y) : 0u;
+        x[u][2] = left > 2 ? key(w[u].z) : 0u;
+        x[u][3] = left > 3 ? key(w[u].w) : 0u;
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4; u++) {
+        int64_t s[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const int j = j0 + u * kMvTile + i;
+          s[i] = j < n ? slot(j, col(j)) : -1;
+          out |= s[i] < 0 && j < n;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) x[u][i] = s[i] >= 0 ? key(__ldg(weight + s[i])) : 0u;
       }
     }
+    if (report && out) record_error(status, CSA2_ERR_BOUNDS);
   }
 };
 
-__global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_constant__ EvictArgs A, EvictWs W, int cache_keys) {
+__global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_constant__ EvictArgs A, EvictWs W, int cache_tiles) {
   extern __shared__ __align__(16) uint32_t ev_keys[];          // the CTA's keys, if they fit
   __shared__ EvictShared S;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, ctas = gridDim.x, b = blockIdx.y;
@@ -165,33 +186,41 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
   R.mul = A.page_mul;
   R.shift = A.page_shift;
   R.status = A.status;
-  const bool cached = (t1 - t0) * kMvTile <= cache_keys;
-  uint32_t *mine = ev_keys + (size_t)(w0 - t0) * kMvTile;      // this warp's part
-  auto keys_of = [&](int tile, uint32_t (&x)[4]) {
-    if (cached) {
-      const uint4 y = *reinterpret_cast<const uint4 *>(mine + (tile - w0) * kMvTile + lane * 4);
-      x[0] = y.x;
-      x[1] = y.y;
-      x[2] = y.z;
-      x[3] = y.w;
+  // (the first cache_tiles of this warp's part stay in shared memory, a multiple of four, or all of them)
+  uint32_t *mine = ev_keys + (size_t)warp * cache_tiles * kMvTile + lane * 4;
+  const int kept_tiles = per_warp <= cache_tiles ? per_warp : cache_tiles & ~3;
+  // four tiles' keys
+  auto keys_of = [&](int tile, uint32_t (&x)[4][4]) {
+    if (tile - w0 < kept_tiles) {
+#pragma unroll
+      for (int u = 0; u < 4; u++) {
+        const uint4 y = tile + u < w1 ? *reinterpret_cast<const uint4 *>(mine + (tile - w0 + u) * kMvTile) : make_uint4(0u, 0u, 0u, 0u);
+        x[u][0] = y.x;
+        x[u][1] = y.y;
+        x[u][2] = y.z;
+        x[u][3] = y.w;
+      }
     } else {
-      R.keys(tile * kMvTile + lane * 4, n, false, x);
+      R.keys(tile, lane, min(n, w1 * kMvTile), false, x);
     }
   };
   // ---------------------------------------------------- the bits that all candidates share
   uint32_t lo = 0xFFFFFFFFu, hi = 0u;
-#pragma unroll 4
-  for (int tile = w0; tile < w1; tile++) {
-    const int j = tile * kMvTile + lane * 4;
-    uint32_t x[4];
-    R.keys(j, n, true, x);
-    if (cached) *reinterpret_cast<uint4 *>(mine + (tile - w0) * kMvTile + lane * 4) = make_uint4(x[0], x[1], x[2], x[3]);
+  for (int tile = w0; tile < w1; tile += 4) {
+    uint32_t x[4][4];
+    R.keys(tile, lane, min(n, w1 * kMvTile), true, x);
 #pragma unroll
-    for (int i = 0; i < 4; i++)
-      if (j + i < m) {
-        lo = min(lo, x[i]);
-        hi = max(hi, x[i]);
-      }
+    for (int u = 0; u < 4; u++) {
+      const int j = (tile + u) * kMvTile + lane * 4;
+      if (tile + u < w1 && tile - w0 < kept_tiles)
+        *reinterpret_cast<uint4 *>(mine + (tile - w0 + u) * kMvTile) = make_uint4(x[u][0], x[u][1], x[u][2], x[u][3]);
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        if (j + i < m && tile + u < w1) {
+          lo = min(lo, x[u][i]);
+          hi = max(hi, x[u][i]);
+        }
+    }
   }
   uint32_t T = 0u, ties = 0u;                        // stay: keys above T, and the first `ties` of those at T
   if (kk > 0 && kk < m) {
@@ -223,22 +252,32 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
       for (int i = t; i < kEvBins; i += kEvThreads) S.hist[i] = 0u;
       __syncthreads();
       const uint32_t mask = (1u << w) - 1u;
-      for (int tile = w0; tile < w1; tile++) {
-        const int j = tile * kMvTile + lane * 4;
-        uint32_t x[4];
+      for (int tile = w0; tile < w1; tile += 4) {
+        uint32_t x[4][4];
         keys_of(tile, x);
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-          if (j + i < m && (low == 32 || x[i] >> low == known)) atomicAdd(&S.hist[(x[i] >> (low - w)) & mask], 1u);
+        for (int u = 0; u < 4; u++) {
+          const int j = (tile + u) * kMvTile + lane * 4;
+#pragma unroll
+          for (int i = 0; i < 4; i++)
+            if (tile + u < w1 && j + i < m && (low == 32 || x[u][i] >> low == known)) atomicAdd(&S.hist[(x[u][i] >> (low - w)) & mask], 1u);
+        }
       }
       __syncthreads();
       ev_cluster_sync();
       // the digit at which the count from the top passes `need`: thread t has bins 2 t and 2 t + 1
       static_assert(kEvBins == 2 * kEvThreads, "two bins a thread");
       uint32_t h0 = 0u, h1 = 0u;
-      for (int c = 0; c < ctas; c++) {
-        h0 += ev_get(&S.hist[2 * t], (uint32_t)c);
-        h1 += ev_get(&S.hist[2 * t + 1], (uint32_t)c);
+#pragma unroll 1
+      for (int c = 0; c < ctas; c += 8) {            // (eight loads in flight)
+        uint2 y[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) y[i] = c + i < ctas ? ev_get2(&S.hist[2 * t], (uint32_t)(c + i)) : make_uint2(0u, 0u);
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          h0 += y[i].x;
+          h1 += y[i].y;
+        }
       }
       uint32_t above = h0 + h1;                      // of this thread's bins and all above them
 #pragma unroll
@@ -271,14 +310,17 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
   const bool all = kk == m;
   // ---------------------------------------------------- ranks
   uint32_t gt = 0u, eq = 0u;
-  for (int tile = w0; tile < w1; tile++) {
-    const int j = tile * kMvTile + lane * 4;
-    uint32_t x[4];
+  for (int tile = w0; tile < w1; tile += 4) {
+    uint32_t x[4][4];
     keys_of(tile, x);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      gt += (j + i < n && (j + i >= m || all || x[i] > T)) ? 1u : 0u;
-      eq += (j + i < m && !all && x[i] == T) ? 1u : 0u;
+    for (int u = 0; u < 4; u++) {
+      const int j = (tile + u) * kMvTile + lane * 4;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        gt += (tile + u < w1 && j + i < n && (j + i >= m || all || x[u][i] > T)) ? 1u : 0u;
+        eq += (tile + u < w1 && j + i < m && !all && x[u][i] == T) ? 1u : 0u;
+      }
     }
   }
   gt = __reduce_add_sync(0xFFFFFFFFu, gt);
@@ -306,39 +348,44 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
   ev_cluster_sync();                                 // (nothing of this CTA is read from here on)
   int32_t *from = W.from + (int64_t)b * W.from_stride, *before = W.before + (int64_t)b * W.tile_stride;
   int32_t *out = A.from != nullptr ? A.from + (int64_t)b * A.from_stride : nullptr;
-  for (int tile = w0; tile < w1; tile++) {
-    const int j = tile * kMvTile + lane * 4;
-    uint32_t x[4];
-    keys_of(tile, x);
-    if (lane == 0) before[tile] = (int32_t)(gt + min(eq, ties));
-    uint32_t g = 0u, e = 0u;                         // bits of the lane's entries that stay for sure, that tie
+  for (int tile4 = w0; tile4 < w1; tile4 += 4) {
+    uint32_t y[4][4];
+    keys_of(tile4, y);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      if (j + i < n && (j + i >= m || all || x[i] > T)) g |= 1u << i;
-      if (j + i < m && !all && x[i] == T) e |= 1u << i;
-    }
-    uint32_t sum = (uint32_t)__popc(g) | (uint32_t)__popc(e) << 16;      // (at most 128 each)
-    const uint32_t own = sum;
+    for (int v = 0; v < 4; v++) {
+      const int tile = tile4 + v, j = tile * kMvTile + lane * 4;
+      const uint32_t(&x)[4] = y[v];
+      if (tile >= w1) break;
+      if (lane == 0) before[tile] = (int32_t)(gt + min(eq, ties));
+      uint32_t g = 0u, e = 0u;                       // bits of the lane's entries that stay for sure, that tie
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-      if (lane >= o) sum += y;
-    }
-    uint32_t a = gt + ((sum - own) & 0xFFFFu), c = eq + ((sum - own) >> 16);
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const bool tie = (e >> i) & 1u;
-      if (((g >> i) & 1u) || (tie && c < ties)) {
-        const uint32_t r = a + min(c, ties);
-        from[r] = j + i;
-        if (out != nullptr) out[r] = j + i;
+      for (int i = 0; i < 4; i++) {
+        if (j + i < n && (j + i >= m || all || x[i] > T)) g |= 1u << i;
+        if (j + i < m && !all && x[i] == T) e |= 1u << i;
       }
-      a += (g >> i) & 1u;
-      c += tie ? 1u : 0u;
+      uint32_t sum = (uint32_t)__popc(g) | (uint32_t)__popc(e) << 16;      // (at most 128 each)
+      const uint32_t own = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t z = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        if (lane >= o) sum += z;
+      }
+      uint32_t a = gt + ((sum - own) & 0xFFFFu), c = eq + ((sum - own) >> 16);
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const bool tie = (e >> i) & 1u;
+        if (((g >> i) & 1u) || (tie && c < ties)) {
+          const uint32_t r = a + min(c, ties);
+          from[r] = j + i;
+          if (out != nullptr) out[r] = j + i;
+        }
+        a += (g >> i) & 1u;
+        c += tie ? 1u : 0u;
+      }
+      const uint32_t all_sum = __shfl_sync(0xFFFFFFFFu, sum, 31);
+      gt += all_sum & 0xFFFFu;
+      eq += all_sum >> 16;
     }
-    const uint32_t all_sum = __shfl_sync(0xFFFFFFFFu, sum, 31);
-    gt += all_sum & 0xFFFFu;
-    eq += all_sum >> 16;
   }
   if (w1 == tiles && w0 < w1 && lane == 0) before[tiles] = k;
 }
@@ -469,10 +516,10 @@ static void evict_magic(unsigned n, uint64_t &mul, int &shift) {
 
 cudaError_t launch_evict(EvictArgs A, void *ws, cudaStream_t st) {
   const int dev = current_device();
-  constexpr int kKeys = 49152;                       // 192 KB of them
+  constexpr size_t kTileBytes = (size_t)kEvWarps * kMvTile * 4;
   static std::atomic<int> attr_done[kMaxDevices];
   cudaError_t e = once_per_device(attr_done, dev, [&] {
-    const cudaError_t f = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeys * 4);
+    const cudaError_t f = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kEvKeyTiles * kTileBytes));
     return f != cudaSuccess ? f : cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   });
   if (e != cudaSuccess) return e;
@@ -482,9 +529,9 @@ cudaError_t launch_evict(EvictArgs A, void *ws, cudaStream_t st) {
   // CTAs of a row: one for each 8,192 entries, up to 16, while the sequences leave SMs for more
   int ctas = 1;
   while (ctas < kEvMaxCtas && (int64_t)ctas * 8192 < row && (int64_t)A.n_seq * ctas * 2 <= sms) ctas *= 2;
-  const int64_t share = ((row + kMvTile - 1) / kMvTile + ctas - 1) / ctas * kMvTile;
-  const int keys = share <= kKeys ? (int)share : 0;
-  e = launch_pdl(evict_select_kernel, dim3((unsigned)ctas, (unsigned)A.n_seq), dim3(kEvThreads), (size_t)keys * 4, st, (unsigned)ctas, A, W, keys);
+  const int64_t share = ((row + kMvTile - 1) / kMvTile + ctas - 1) / ctas, warp_share = (share + kEvWarps - 1) / kEvWarps;
+  const int cache = (int)(warp_share < kEvKeyTiles ? warp_share : kEvKeyTiles);
+  e = launch_pdl(evict_select_kernel, dim3((unsigned)ctas, (unsigned)A.n_seq), dim3(kEvThreads), cache * kTileBytes, st, (unsigned)ctas, A, W, cache);
   if (e != cudaSuccess) return e;
   // no more CTAs than there can be tiles
   const int64_t dst_row = A.dst_stride * A.page, most = dst_row < row ? dst_row : row;

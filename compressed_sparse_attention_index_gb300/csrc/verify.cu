@@ -7,13 +7,15 @@
 // stays while it is the largest entry of row t.
 //
 // A token is a whole number, so which side of a border a sum falls on has to be that of the exact
-// one: u q is a product of two fp32 in fp64 (exact), p - q and the running sums are pairs of fp32
+// one: u q is a product of two fp32 in fp64 (exact), and p - q and the running sums are pairs of fp32
 // (an fp32 sum of 131,072 probabilities picks another token in a call of a few hundred; fp64 has a
-// sixtieth of fp32's rate here, and 64 rows would take 55 us of it), and the last few sums are fp64.
+// sixtieth of fp32's rate here, and a few sums of it in every warp took half of the kernel's time).
 //
 // What bounds it: one row of p, and of q where a draft was refused, for each sequence (HBM; a few
-// sequences: a chain of loads).  A sequence's row is dealt to the CTAs of a cluster, whose sums meet
-// in each of them through distributed shared memory.
+// sequences: a chain of loads).  A sequence's row is dealt to the warps of a cluster in
+// contiguous segments, whose sums meet in each CTA through distributed shared memory; the CTA that has the
+// segment where the running sum passes looks through it with all its threads (one warp, 32 groups at a
+// time, took 25 us of a 4,096-entry segment).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -30,10 +32,35 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162flo
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
 
 // What is no probability (negative, NaN, above 2^96) counts as none.
-__device__ __forceinline__ float probability(float x) { return x >= 0.f && x <= 0x1p96f ? x : 0.f; }
+__device__ __forceinline__ float probability(float x) { return __float_as_uint(x) <= 0x6F800000u ? x : 0.f; }
 
-// A row of `n` elements in groups that start on 16-byte boundaries: group k has elements
-// [k VEC - skew, .. + VEC), the first and the last one's may lie outside the row.
+// Four words of a row: 16 / sizeof(T) elements as fp32.
+__device__ __forceinline__ void widen(const uint4 &w, float (&x)[4], float) {
+  x[0] = __uint_as_float(w.x);
+  x[1] = __uint_as_float(w.y);
+  x[2] = __uint_as_float(w.z);
+  x[3] = __uint_as_float(w.w);
+}
+__device__ __forceinline__ void widen(const uint4 &w, float (&x)[8], __nv_bfloat16) {
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    x[2 * i] = bf16_lo(v[i]);
+    x[2 * i + 1] = bf16_hi(v[i]);
+  }
+}
+__device__ __forceinline__ void widen(const uint4 &w, float (&x)[8], __half) {
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v[i]));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+// A row of n elements in groups of VEC that start on 16-byte boundaries: group k has elements
+// k VEC - skew .. + VEC; the first and the last one's may lie outside the row (`none` there).
 template <class T>
 struct ProbRow {
   static constexpr int kVec = 16 / sizeof(T);
@@ -41,54 +68,149 @@ struct ProbRow {
   int n, skew;
   __device__ __forceinline__ ProbRow(const T *r, int n_) : row(r), n(n_), skew((int)(((uintptr_t)r / sizeof(T)) % kVec)) {}
   __device__ __forceinline__ int groups() const { return (n + skew + kVec - 1) / kVec; }
-};
-// Elements e0 .. e0 + VEC of a row, as they are; `none` outside.  wide: e0 is on a 16-byte boundary.
-template <class T>
-__device__ __forceinline__ void load_group(const T *row, int n, int e0, bool wide, float none, float (&x)[16 / sizeof(T)]) {
-  constexpr int V = 16 / sizeof(T);
-  if (wide && e0 >= 0 && e0 + V <= n) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(row + e0));
-    const T *y = reinterpret_cast<const T *>(&w);
+  __device__ __forceinline__ int first(int k) const { return k * kVec - skew; }
+  __device__ __forceinline__ bool inside(int k) const { return first(k) >= 0 && first(k) + kVec <= n; }
+  __device__ __forceinline__ uint4 wide(int k) const { return __ldg(reinterpret_cast<const uint4 *>(row + first(k))); }
+  // element by element
+  __device__ __forceinline__ void edge(int k, float none, float (&x)[kVec]) const {
 #pragma unroll
-    for (int i = 0; i < V; i++) x[i] = to_f32(y[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; i++) x[i] = e0 + i >= 0 && e0 + i < n ? to_f32(row[e0 + i]) : none;
+    for (int i = 0; i < kVec; i++) {
+      const int e = first(k) + i;
+      x[i] = e >= 0 && e < n ? to_f32(row[e]) : none;
+    }
   }
-}
+  __device__ __forceinline__ void get(int k, float none, float (&x)[kVec]) const {
+    if (inside(k)) widen(wide(k), x, T());
+    else edge(k, none, x);
+  }
+};
 
-// h + l: a sum of fp32 numbers to twice fp32's precision
+// h + l: a sum to twice fp32's precision
 struct Pair32 {
   float h, l;
-  __device__ __forceinline__ void add(float x, float rest) {
+  __device__ __forceinline__ void add(float x) {
     const float s = h + x, b = s - h;
-    l += (h - (s - b)) + (x - b) + rest;
+    l += (h - (s - b)) + (x - b);
     h = s;
   }
-  __device__ __forceinline__ double f64() const { return (double)h + (double)l; }
+  __device__ __forceinline__ void add(const Pair32 &y) {
+    add(y.h);
+    l += y.l;
+  }
+  __device__ __forceinline__ Pair32 up(int o) const { return {__shfl_up_sync(0xFFFFFFFFu, h, o), __shfl_up_sync(0xFFFFFFFFu, l, o)}; }
+  __device__ __forceinline__ Pair32 from(int lane) const { return {__shfl_sync(0xFFFFFFFFu, h, lane), __shfl_sync(0xFFFFFFFFu, l, lane)}; }
 };
+__device__ __forceinline__ bool above(const Pair32 &a, const Pair32 &b) { return (a.h - b.h) + (a.l - b.l) > 0.f; }
+// sum over the warp's lanes up to this one
+__device__ __forceinline__ Pair32 warp_scan(Pair32 x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Pair32 y = x.up(o);
+    if (lane >= o) x.add(y);
+  }
+  return x;
+}
 
-// What the sampled token is drawn from: weights w_e of a row's elements.
+// What the sampled token is drawn from: the weights max(p - q, 0) of a row's elements.
 template <class T>
 struct Weights {
-  const T *p, *q;               // q: null, none
-  int n, skew, out;             // out: an element of weight 0, or -1
-  bool q_wide;
-  // the group's weights, as value and what its rounding left
-  __device__ __forceinline__ void get(int k, float (&w)[16 / sizeof(T)], float (&rest)[16 / sizeof(T)]) const {
-    constexpr int V = 16 / sizeof(T);
-    const int e0 = k * V - skew;
-    load_group(p, n, e0, true, 0.f, w);
-    float y[V];
-    if (q != nullptr) load_group(q, n, e0, q_wide, 0.f, y);
+  static constexpr int V = 16 / sizeof(T);
+  ProbRow<T> p, q;              // q.row null: none
+  int out;                      // an element of weight 0, or -1
+  bool wide;                    // q's groups are p's
+  // a group's weights, as value and what its rounding left
+  __device__ __forceinline__ void weigh(int k, float (&w)[V], const float (&y)[V], float (&rest)[V]) const {
 #pragma unroll
     for (int i = 0; i < V; i++) {
-      const float a = probability(w[i]), b = q != nullptr ? probability(y[i]) : 0.f;
-      const float d = a - b;
-      const bool some = d > 0.f && e0 + i != out;
-      w[i] = some ? d : 0.f;
-      rest[i] = some ? (a - d) - b : 0.f;          // exact, as a >= b >= 0
+      const float a = probability(w[i]), b = probability(y[i]), d = a - b;
+      w[i] = fmaxf(d, 0.f);
+      rest[i] = d > 0.f ? (a - d) - b : 0.f;         // exact, as a >= b >= 0
     }
+  }
+  __device__ __forceinline__ void plain(int k, float (&w)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V; i++) w[i] = probability(w[i]);
+    const int x = out - p.first(k);
+    if ((unsigned)x < (unsigned)V && out >= 0) {
+#pragma unroll
+      for (int i = 0; i < V; i++)
+        if (i == x) w[i] = 0.f;
+    }
+  }
+  __device__ __forceinline__ void get_q(int k, float (&y)[V]) const {
+    if (wide && p.inside(k)) {
+      widen(__ldg(reinterpret_cast<const uint4 *>(q.row + p.first(k))), y, T());
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; i++) {
+        const int e = p.first(k) + i;
+        y[i] = e >= 0 && e < p.n ? to_f32(q.row[e]) : 0.f;
+      }
+    }
+  }
+  __device__ __forceinline__ void get(int k, float (&w)[V], float (&rest)[V]) const {
+    p.get(k, 0.f, w);
+    if (q.row != nullptr) {
+      float y[V];
+      get_q(k, y);
+      weigh(k, w, y, rest);
+    } else {
+      plain(k, w);
+#pragma unroll
+      for (int i = 0; i < V; i++) rest[i] = 0.f;
+    }
+  }
+  // this lane's part of groups [g0, g1): every 32nd, four rows of loads in flight
+  __device__ __forceinline__ Pair32 sum(int g0, int g1, int lane) const {
+    Pair32 s = {0.f, 0.f};
+    int k = g0 + lane;
+    if (q.row != nullptr) {
+      if (wide)
+        for (; k + 96 < g1 && p.inside(k) && p.inside(k + 96); k += 128) {
+          uint4 a[4], b[4];
+#pragma unroll
+          for (int u = 0; u < 4; u++) {
+            a[u] = p.wide(k + 32 * u);
+            b[u] = __ldg(reinterpret_cast<const uint4 *>(q.row + p.first(k + 32 * u)));
+          }
+#pragma unroll
+          for (int u = 0; u < 4; u++) {
+            float w[V], y[V], rest[V];
+            widen(a[u], w, T());
+            widen(b[u], y, T());
+            weigh(k + 32 * u, w, y, rest);
+#pragma unroll
+            for (int i = 0; i < V; i++) {
+              s.add(w[i]);
+              s.l += rest[i];
+            }
+          }
+        }
+    } else {
+      for (; k + 96 < g1 && p.inside(k) && p.inside(k + 96); k += 128) {
+        uint4 a[4];
+#pragma unroll
+        for (int u = 0; u < 4; u++) a[u] = p.wide(k + 32 * u);
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+          float w[V];
+          widen(a[u], w, T());
+          plain(k + 32 * u, w);
+#pragma unroll
+          for (int i = 0; i < V; i++) s.add(w[i]);
+        }
+      }
+    }
+    for (; k < g1; k += 32) {
+      float w[V], rest[V];
+      get(k, w, rest);
+#pragma unroll
+      for (int i = 0; i < V; i++) {
+        s.add(w[i]);
+        s.l += rest[i];
+      }
+    }
+    return s;
   }
 };
 
@@ -101,16 +223,46 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 // Stores v at the place of p (this CTA's shared memory) in CTA `rank` of the cluster.
-__device__ __forceinline__ void put_f64(const double *p, uint32_t rank, double v) {
+__device__ __forceinline__ void put_pair(const float2 *p, uint32_t rank, const Pair32 &v) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_u32(p)), "r"(rank));
-  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(a), "d"(v) : "memory");
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.h), "f"(v.l) : "memory");
+}
+
+// The place in an ascending list of sums (32 SLOTS of them, lane and slot c: number 32 c + lane, x[c] the sum
+// of its own) where the running sum first passes goal: its number, -1 where none does, the sum ahead of it, and
+// the last number that adds anything.
+template <int SLOTS>
+__device__ __forceinline__ int find_pass(const Pair32 (&x)[SLOTS], const Pair32 &goal, int lane, Pair32 &ahead, int &some) {
+  int hit = -1;
+  Pair32 run = {0.f, 0.f};
+  some = -1;
+#pragma unroll
+  for (int c = 0; c < SLOTS; c++) {
+    const Pair32 in = warp_scan(x[c], lane);
+    Pair32 at = run, before = in.up(1);
+    at.add(in);
+    if (lane == 0) before = {0.f, 0.f};
+    Pair32 b = run;
+    b.add(before);
+    const uint32_t past = __ballot_sync(0xFFFFFFFFu, above(at, goal) && x[c].h > 0.f);
+    const uint32_t any = __ballot_sync(0xFFFFFFFFu, x[c].h > 0.f);
+    if (any != 0u) some = c * 32 + 31 - __clz((int)any);
+    if (hit < 0 && past != 0u) {
+      const int from = __ffs((int)past) - 1;
+      hit = c * 32 + from;
+      ahead = b.from(from);
+    }
+    run = at.from(31);
+  }
+  return hit;
 }
 
 template <class T>
 __global__ void __launch_bounds__(kVfThreads) verify_sample_kernel(const __grid_constant__ VerifyArgs A) {
-  constexpr int V = 16 / sizeof(T);
-  __shared__ double sums[2][kVfMaxParts * kVfWarps];
+  constexpr int V = 16 / sizeof(T), kSlots = kVfMaxParts * kVfWarps / 32;
+  __shared__ float2 sums[2][kVfMaxParts * kVfWarps], inner[kVfWarps];
+  __shared__ int accepted_sh, refused_sh;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, parts = gridDim.x;
   const int b = blockIdx.y;
   const uint32_t rank = cluster_rank();
@@ -127,148 +279,136 @@ __global__ void __launch_bounds__(kVfThreads) verify_sample_kernel(const __grid_
     return;
   }
   const T *target = static_cast<const T *>(A.target), *draft = static_cast<const T *>(A.draft);
-  // the first refused draft: every warp for itself, a lane to a draft
+  // the first refused draft, a lane to a draft
   const int drafts = c1 - c0 - 1;
-  int accepted = drafts, refused_token = -1;
-  for (int i0 = 0; i0 < drafts; i0 += 32) {
-    const int i = i0 + lane;
-    bool ok = true;
-    int x = -1;
-    if (i < drafts) {
-      const int64_t r = c0 + i;
-      x = __ldg(A.tokens + r + 1);
-      ok = x >= 0 && x < A.vocab;
-      if (ok) {
-        const float p = probability(to_f32(target[r * A.target_stride + x]));
-        const float q = draft != nullptr ? probability(to_f32(draft[r * A.draft_stride + x])) : 1.f;
-        ok = (double)__ldg(A.u + r) * (double)q < (double)p;
-      } else {
-        x = -1;
+  if (warp == 0) {
+    int accepted = drafts, refused = -1;
+    for (int i0 = 0; i0 < drafts; i0 += 32) {
+      const int i = i0 + lane;
+      bool ok = true;
+      int x = -1;
+      if (i < drafts) {
+        const int64_t r = c0 + i;
+        x = __ldg(A.tokens + r + 1);
+        ok = x >= 0 && x < A.vocab;
+        if (ok) {
+          const float p = probability(to_f32(target[r * A.target_stride + x]));
+          const float q = draft != nullptr ? probability(to_f32(draft[r * A.draft_stride + x])) : 1.f;
+          ok = (double)__ldg(A.u + r) * (double)q < (double)p;
+        } else {
+          x = -1;
+        }
+      }
+      const uint32_t no = __ballot_sync(0xFFFFFFFFu, !ok);
+      if (no != 0u) {
+        const int from = __ffs((int)no) - 1;
+        accepted = i0 + from;
+        refused = __shfl_sync(0xFFFFFFFFu, x, from);
+        if (refused < 0 && lane == 0 && rank == 0) record_error(A.status, CSA2_ERR_BOUNDS);
+        break;
       }
     }
-    const uint32_t no = __ballot_sync(0xFFFFFFFFu, !ok);
-    if (no != 0u) {
-      const int from = __ffs((int)no) - 1;
-      accepted = i0 + from;
-      refused_token = __shfl_sync(0xFFFFFFFFu, x, from);
-      if (refused_token < 0 && t == 0 && rank == 0) record_error(A.status, CSA2_ERR_BOUNDS);
-      break;
+    if (lane == 0) {
+      accepted_sh = accepted;
+      refused_sh = refused;
     }
   }
-  const int64_t row = c0 + accepted;
-  Weights<T> W;
-  const ProbRow<T> P(target + row * A.target_stride, A.vocab);
-  W.p = P.row;
-  W.n = A.vocab;
-  W.skew = P.skew;
+  __syncthreads();
+  const int accepted = accepted_sh;
   const bool refused = accepted < drafts;
-  W.q = refused && draft != nullptr ? draft + row * A.draft_stride : nullptr;
-  W.q_wide = W.q != nullptr && ProbRow<T>(W.q, A.vocab).skew == W.skew;
-  W.out = refused && draft == nullptr ? refused_token : -1;
+  const int64_t row = c0 + accepted;
+  const ProbRow<T> P(target + row * A.target_stride, A.vocab);
+  const ProbRow<T> Q(refused && draft != nullptr ? draft + row * A.draft_stride : nullptr, A.vocab);
+  Weights<T> W = {P, Q, refused && draft == nullptr ? refused_sh : -1, Q.skew == P.skew};
   const int groups = P.groups(), segs = parts * kVfWarps;
   // this warp's segment of the row
   const int per = (groups + segs - 1) / segs, seg = (int)rank * kVfWarps + warp;
   const int g0 = min(seg * per, groups), g1 = min(g0 + per, groups);
-  const double v = (double)__ldg(A.v + b);
-  int next = -1;
+  const float v = __ldg(A.v + b);
 #pragma unroll 1
   for (int pass = 0; pass < 2; pass++) {
-    Pair32 s = {0.f, 0.f};
-#pragma unroll 2
-    for (int k = g0 + lane; k < g1; k += 32) {
-      float w[V], rest[V];
-      W.get(k, w, rest);
-#pragma unroll
-      for (int i = 0; i < V; i++) s.add(w[i], rest[i]);
-    }
-    double sum = s.f64();
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (lane < parts) put_f64(&sums[pass][seg], (uint32_t)lane, sum);
+    Pair32 s = warp_scan(W.sum(g0, g1, lane), lane).from(31);
+    if (lane < parts) put_pair(&sums[pass][seg], (uint32_t)lane, s);
     __syncwarp();
     cluster_sync();
-    // every warp: the segment in which the running sum passes v times the total
-    double run = 0.0, at[kVfMaxParts * kVfWarps / 32];
+    Pair32 x[kSlots], total = {0.f, 0.f}, ahead = {0.f, 0.f}, none = {0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < kVfMaxParts * kVfWarps / 32; c++) {
-      double x = c * 32 + lane < segs ? sums[pass][c * 32 + lane] : 0.0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-        if (lane >= o) x += y;
-      }
-      at[c] = run + x;
-      run = __shfl_sync(0xFFFFFFFFu, at[c], 31);
+    for (int c = 0; c < kSlots; c++) {
+      const float2 y = c * 32 + lane < segs ? sums[pass][c * 32 + lane] : make_float2(0.f, 0.f);
+      x[c] = {y.x, y.y};
+      total.add(x[c]);
     }
-    if (!(run > 0.0)) {                              // nothing is left of p - q: p itself, else no token
-      W.q = nullptr;
+    total = warp_scan(total, lane).from(31);
+    if (!(total.h > 0.f)) {                          // nothing is left of p - q: p itself, else no token
+      W.q.row = nullptr;
       W.out = -1;
       continue;
     }
-    const double goal = v * run;
-    int hit = -1, some = 0;
-    double before = 0.0, carry = 0.0;                // (carry: of the 32 segments before)
-#pragma unroll
-    for (int c = 0; c < kVfMaxParts * kVfWarps / 32; c++) {
-      const double left = __shfl_up_sync(0xFFFFFFFFu, at[c], 1);
-      const double ahead = lane > 0 ? left : carry;
-      carry = __shfl_sync(0xFFFFFFFFu, at[c], 31);
-      const uint32_t past = __ballot_sync(0xFFFFFFFFu, at[c] > goal);
-      const uint32_t any = __ballot_sync(0xFFFFFFFFu, at[c] > ahead);
-      if (any != 0u) some = c * 32 + 31 - __clz((int)any);
-      if (hit < 0 && past != 0u) {
-        hit = c * 32 + __ffs((int)past) - 1;
-        before = __shfl_sync(0xFFFFFFFFu, ahead, hit & 31);
-      }
-    }
+    // the segment in which the running sum passes v times the total
+    Pair32 goal = {v * total.h, 0.f};
+    goal.l = fmaf(v, total.h, -goal.h) + v * total.l;
+    int some;
+    int hit = find_pass<kSlots>(x, goal, lane, ahead, some);
     const bool end = hit < 0;                        // (v is not below 1: the last element that weighs anything)
     if (end) hit = some;
-    if (hit == seg) {
-      // ------------------------------------------------ inside the segment, 32 groups at a time
-      int last = -1;
-      for (int k0 = g0; k0 < g1 && next < 0; k0 += 32) {
-        float w[V], rest[V];
-        const bool in = k0 + lane < g1;
-        Pair32 y = {0.f, 0.f};
-        int mine = -1;
-        if (in) {
-          W.get(k0 + lane, w, rest);
-#pragma unroll
-          for (int i = 0; i < V; i++) {
-            y.add(w[i], rest[i]);
-            if (w[i] > 0.f) mine = (k0 + lane) * V - W.skew + i;
-          }
-        }
-        double x = y.f64();
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const double z = __shfl_up_sync(0xFFFFFFFFu, x, o);
-          if (lane >= o) x += z;
-        }
-        last = max(last, __reduce_max_sync(0xFFFFFFFFu, mine));
-        const uint32_t past = __ballot_sync(0xFFFFFFFFu, !end && in && before + x > goal);
-        if (past != 0u) {
-          const int from = __ffs((int)past) - 1;
-          const double left = __shfl_up_sync(0xFFFFFFFFu, x, 1);
-          const double z = lane > 0 ? before + left : before;
-          int e = mine;
-          if (lane == from) {
-#pragma unroll
-            for (int i = V - 1; i >= 0; i--) {       // (backwards: the first that passes stays)
-              double zi = z;
-              for (int j = 0; j <= i; j++) zi += (double)w[j] + (double)rest[j];
-              if (w[i] > 0.f && zi > goal) e = (k0 + lane) * V - W.skew + i;
-            }
-          }
-          next = __shfl_sync(0xFFFFFFFFu, e, from);
-        }
-        before += __shfl_sync(0xFFFFFFFFu, x, 31);
-      }
-      if (next < 0) next = last;
-      if (lane == 0) A.next[b] = next;
-    }
     if (t == 0 && rank == 0) A.kept[b] = 1 + accepted;
-    return;                                          // (the whole cluster: run is the same in all of it)
+    if (hit / kVfWarps != (int)rank) return;         // (another CTA of the cluster has it)
+    // ---------------------------------------------------- inside the segment: contiguous groups to every thread
+    const int h0 = min(hit * per, groups), h1 = min(h0 + per, groups), each = (h1 - h0 + kVfThreads - 1) / kVfThreads;
+    const int k0 = min(h0 + t * each, h1), k1 = min(k0 + each, h1);
+    Pair32 own = none;
+    for (int k = k0; k < k1; k++) {
+      float w[V], rest[V];
+      W.get(k, w, rest);
+#pragma unroll
+      for (int i = 0; i < V; i++) {
+        own.add(w[i]);
+        own.l += rest[i];
+      }
+    }
+    const Pair32 in = warp_scan(own, lane);
+    if (lane == 31) inner[warp] = make_float2(in.h, in.l);
+    __syncthreads();
+    const float2 y = lane < kVfWarps ? inner[lane] : make_float2(0.f, 0.f);
+    const Pair32 z[1] = {{y.x, y.y}};
+    // (rounding may leave the goal behind the last one: then the last that weighs anything)
+    Pair32 to = goal;
+    to.add(-ahead.h);
+    to.l -= ahead.l;
+    Pair32 ahead2 = none;
+    int warp_hit = end ? -1 : find_pass<1>(z, to, lane, ahead2, some);
+    const uint32_t any_warp = __ballot_sync(0xFFFFFFFFu, z[0].h > 0.f);
+    const bool last_warp = warp_hit < 0;
+    if (last_warp) warp_hit = 31 - __clz((int)any_warp);
+    if (warp != warp_hit) return;
+    const Pair32 o[1] = {own};
+    Pair32 to2 = to;
+    to2.add(-ahead2.h);
+    to2.l -= ahead2.l;
+    Pair32 ahead3 = none;
+    int lane_hit = last_warp ? -1 : find_pass<1>(o, to2, lane, ahead3, some);
+    const uint32_t any_lane = __ballot_sync(0xFFFFFFFFu, own.h > 0.f);
+    const bool last_lane = lane_hit < 0;
+    if (last_lane) lane_hit = 31 - __clz((int)any_lane);
+    if (lane != lane_hit) return;
+    Pair32 at = ahead3;
+    int next = -1;
+    bool passed = false;
+    for (int k = k0; k < k1 && !passed; k++) {
+      float w[V], rest[V];
+      W.get(k, w, rest);
+#pragma unroll
+      for (int i = 0; i < V; i++) {
+        at.add(w[i]);
+        at.l += rest[i];
+        if (w[i] > 0.f && !passed) {
+          next = W.p.first(k) + i;
+          passed = !last_lane && above(at, to2);
+        }
+      }
+    }
+    A.next[b] = next;
+    return;
   }
   if (t == 0 && rank == 0) {
     A.kept[b] = 1 + accepted;
@@ -280,6 +420,7 @@ __global__ void __launch_bounds__(kVfThreads) verify_sample_kernel(const __grid_
 // ------------------------------------------------------------------ greedy
 // The largest element of a part of a row: its order key above the complement of its index, so that
 // the largest word is the largest element, the lowest index among equals (0: nothing but NaN).
+// A lane's elements come in ascending order, so a comparison and two selections keep its largest.
 template <class T>
 __global__ void __launch_bounds__(kVfThreads) verify_best_kernel(const __grid_constant__ VerifyArgs A) {
   constexpr int V = 16 / sizeof(T);
@@ -292,19 +433,45 @@ __global__ void __launch_bounds__(kVfThreads) verify_best_kernel(const __grid_co
   const ProbRow<T> P(static_cast<const T *>(A.target) + row * A.target_stride, A.vocab);
   const int groups = P.groups(), per = (groups + parts - 1) / parts;
   const int g0 = min((int)blockIdx.x * per, groups), g1 = min(g0 + per, groups);
-  unsigned long long best = 0ull;
-#pragma unroll 4
-  for (int k = g0 + t; k < g1; k += kVfThreads) {
-    float x[V];
-    const int e0 = k * V - P.skew;
-    load_group(P.row, P.n, e0, true, __int_as_float(0x7FC00000), x);
+  float top = -INFINITY;
+  int at = -1;
+  auto take = [&](int k, const float (&x)[V]) {
+    const int e0 = P.first(k);
 #pragma unroll
     for (int i = 0; i < V; i++)
-      if (x[i] == x[i]) {
-        const unsigned long long w = (unsigned long long)order_key(x[i]) << 32 | (uint32_t) ~(uint32_t)(e0 + i);
-        best = w > best ? w : best;
+      if (x[i] > top) {
+        top = x[i];
+        at = e0 + i;
       }
+  };
+  int k = g0 + t;
+  for (; k + 3 * kVfThreads < g1 && P.inside(k) && P.inside(k + 3 * kVfThreads); k += 4 * kVfThreads) {
+    uint4 w[4];
+#pragma unroll
+    for (int u = 0; u < 4; u++) w[u] = P.wide(k + u * kVfThreads);
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+      float x[V];
+      widen(w[u], x, T());
+      take(k + u * kVfThreads, x);
+    }
   }
+  for (; k < g1; k += kVfThreads) {
+    float x[V];
+    P.get(k, -INFINITY, x);
+    take(k, x);
+  }
+  // nothing above -inf: the first -inf, if any
+  if (__syncthreads_or(at >= 0) == 0) {
+    for (k = g0 + t; k < g1 && at < 0; k += kVfThreads) {
+      float x[V];
+      P.get(k, __int_as_float(0x7FC00000), x);
+#pragma unroll
+      for (int i = V - 1; i >= 0; i--)
+        if (x[i] == -INFINITY) at = P.first(k) + i;
+    }
+  }
+  unsigned long long best = at >= 0 ? (unsigned long long)order_key(top) << 32 | (uint32_t) ~(uint32_t)at : 0ull;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const unsigned long long w = __shfl_xor_sync(0xFFFFFFFFu, best, o);
