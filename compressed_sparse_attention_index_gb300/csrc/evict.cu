@@ -5,10 +5,9 @@
 // all; they move together, in order, to places 0 .. k - 1.  Two launches:
 //
 // evict_select_kernel: a cluster per sequence finds the smallest weight that stays, as an order key,
-// by histograms of up to 11 bits at a time below the bits that all keys share (at most three, of one
-// pass each; keys stay in shared memory, 53,248 of a CTA's part of the row, and are read again behind
-// that).  Each warp has a contiguous part of the row, four tiles of it in flight, so that one count of every part gives every kept entry its rank, and
-// writes which entry each new place comes from.
+// by histograms of 11, 11 and 10 of its bits, one pass over the keys each (they stay in shared memory, 53,248 of a CTA's
+// part of the row; those behind are read again).  Each warp has a contiguous part of the row, so that
+// one count of every part gives every kept entry its rank, and writes which entry each new place comes from.
 //
 // evict_move_kernel: tiles of kMvTile new places, read whole and then written.  In place, a tile's
 // places may hold entries that are still to be moved, but only those of its own and of earlier tiles
@@ -91,8 +90,8 @@ __device__ __forceinline__ uint2 ev_get2(const uint32_t *p, uint32_t rank) {
 
 struct EvictShared {
   uint32_t hist[kEvBins];
-  uint32_t lo[kEvWarps], hi[kEvWarps], gt[kEvWarps], eq[kEvWarps];
-  uint32_t minmax[2], count[2], found[3];
+  uint32_t above[kEvWarps], gt[kEvWarps], eq[kEvWarps];
+  uint32_t count[2], found[2];
 };
 
 // Order key of entry j's weight, larger is heavier (NaN: 0, below everything).
@@ -194,59 +193,30 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
     if (tile - w0 < kept_tiles) {
 #pragma unroll
       for (int u = 0; u < 4; u++) {
-        const uint4 y = tile + u < w1 ? *reinterpret_cast<const uint4 *>(mine + (tile - w0 + u) * kMvTile) : make_uint4(0u, 0u, 0u, 0u);
+        if (tile + u >= w1) break;
+        const uint4 y = *reinterpret_cast<const uint4 *>(mine + (tile - w0 + u) * kMvTile);
         x[u][0] = y.x;
         x[u][1] = y.y;
         x[u][2] = y.z;
         x[u][3] = y.w;
       }
     } else {
-      R.keys(tile, lane, min(n, w1 * kMvTile), false, x);
+      R.keys(tile, lane, min(n, w1 * kMvTile), true, x);
     }
   };
-  // ---------------------------------------------------- the bits that all candidates share
-  uint32_t lo = 0xFFFFFFFFu, hi = 0u;
-  for (int tile = w0; tile < w1; tile += 4) {
-    uint32_t x[4][4];
-    R.keys(tile, lane, min(n, w1 * kMvTile), true, x);
+  // the row's keys, read once where they fit
+  if (kept_tiles > 0)
+    for (int tile = w0; tile < min(w1, w0 + kept_tiles); tile += 4) {
+      uint32_t x[4][4];
+      R.keys(tile, lane, min(n, w1 * kMvTile), true, x);
 #pragma unroll
-    for (int u = 0; u < 4; u++) {
-      const int j = (tile + u) * kMvTile + lane * 4;
-      if (tile + u < w1 && tile - w0 < kept_tiles)
-        *reinterpret_cast<uint4 *>(mine + (tile - w0 + u) * kMvTile) = make_uint4(x[u][0], x[u][1], x[u][2], x[u][3]);
-#pragma unroll
-      for (int i = 0; i < 4; i++)
-        if (j + i < m && tile + u < w1) {
-          lo = min(lo, x[u][i]);
-          hi = max(hi, x[u][i]);
-        }
+      for (int u = 0; u < 4; u++)
+        if (tile + u < w1) *reinterpret_cast<uint4 *>(mine + (tile - w0 + u) * kMvTile) = make_uint4(x[u][0], x[u][1], x[u][2], x[u][3]);
     }
-  }
   uint32_t T = 0u, ties = 0u;                        // stay: keys above T, and the first `ties` of those at T
   if (kk > 0 && kk < m) {
-    lo = __reduce_min_sync(0xFFFFFFFFu, lo);
-    hi = __reduce_max_sync(0xFFFFFFFFu, hi);
-    if (lane == 0) {
-      S.lo[warp] = lo;
-      S.hi[warp] = hi;
-    }
-    __syncthreads();
-    if (warp == 0) {
-      lo = __reduce_min_sync(0xFFFFFFFFu, S.lo[lane]);
-      hi = __reduce_max_sync(0xFFFFFFFFu, S.hi[lane]);
-      if (lane == 0) {
-        S.minmax[0] = lo;
-        S.minmax[1] = hi;
-      }
-    }
-    __syncthreads();
-    ev_cluster_sync();
-    lo = lane < ctas ? ev_get(&S.minmax[0], (uint32_t)lane) : 0xFFFFFFFFu;
-    hi = lane < ctas ? ev_get(&S.minmax[1], (uint32_t)lane) : 0u;
-    lo = __reduce_min_sync(0xFFFFFFFFu, lo);
-    hi = __reduce_max_sync(0xFFFFFFFFu, hi);
-    int low = 32 - __clz((int)(lo ^ hi));            // bits that are not known yet (0: all keys are one)
-    uint32_t known = low == 32 ? 0u : hi >> low, need = (uint32_t)kk;
+    int low = 32;                                    // bits that are not known yet
+    uint32_t known = 0u, need = (uint32_t)kk;
     while (low > 0) {
       const int w = min(kEvBits, low);
       for (int i = t; i < kEvBins; i += kEvThreads) S.hist[i] = 0u;
@@ -258,9 +228,20 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
 #pragma unroll
         for (int u = 0; u < 4; u++) {
           const int j = (tile + u) * kMvTile + lane * 4;
+          if (tile + u >= w1) break;
 #pragma unroll
-          for (int i = 0; i < 4; i++)
-            if (tile + u < w1 && j + i < m && (low == 32 || x[u][i] >> low == known)) atomicAdd(&S.hist[(x[u][i] >> (low - w)) & mask], 1u);
+          for (int i = 0; i < 4; i++) {
+            const bool in = j + i < m && (low == 32 || x[u][i] >> low == known);
+            const uint32_t digit = (x[u][i] >> (low - w)) & mask;
+            if (low == 32) {                         // (many equal weights: one of the warp counts for all)
+              const uint32_t one = __shfl_sync(0xFFFFFFFFu, digit, 0);
+              if (__all_sync(0xFFFFFFFFu, in && digit == one)) {
+                if (lane == 0) atomicAdd(&S.hist[digit], 32u);
+                continue;
+              }
+            }
+            if (in) atomicAdd(&S.hist[digit], 1u);
+          }
         }
       }
       __syncthreads();
@@ -285,9 +266,9 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
         const uint32_t y = __shfl_down_sync(0xFFFFFFFFu, above, o);
         if (lane + o < 32) above += y;
       }
-      if (lane == 0) S.lo[warp] = above;
+      if (lane == 0) S.above[warp] = above;
       __syncthreads();
-      for (int i = warp + 1; i < kEvWarps; i++) above += S.lo[i];
+      for (int i = warp + 1; i < kEvWarps; i++) above += S.above[i];
       const uint32_t top1 = above - h0 - h1, top0 = above - h0;          // above bin 2 t + 1, above bin 2 t
       if (top1 < need && need <= top1 + h1) {
         S.found[0] = (uint32_t)(2 * t + 1);
@@ -316,10 +297,11 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
 #pragma unroll
     for (int u = 0; u < 4; u++) {
       const int j = (tile + u) * kMvTile + lane * 4;
+      if (tile + u >= w1) break;
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        gt += (tile + u < w1 && j + i < n && (j + i >= m || all || x[u][i] > T)) ? 1u : 0u;
-        eq += (tile + u < w1 && j + i < m && !all && x[u][i] == T) ? 1u : 0u;
+        gt += (j + i < n && (j + i >= m || all || x[u][i] > T)) ? 1u : 0u;
+        eq += (j + i < m && !all && x[u][i] == T) ? 1u : 0u;
       }
     }
   }
