@@ -5,7 +5,7 @@
 // all; they move together, in order, to places 0 .. k - 1.  Two launches:
 //
 // evict_select_kernel: a cluster per sequence finds the smallest weight that stays, as an order key,
-// by histograms of 11, 11 and 10 of its bits, one pass over the keys each (they stay in shared memory, 53,248 of a CTA's
+// by histograms of 11, 11 and 10 of its bits, one pass over the keys each (they stay in shared memory, 49,152 of a CTA's
 // part of the row; those behind are read again).  Each warp has a contiguous part of the row, so that
 // one count of every part gives every kept entry its rank, and writes which entry each new place comes from.
 //
@@ -26,7 +26,7 @@ namespace csa2 {
 
 constexpr int kEvThreads = 1024, kEvWarps = kEvThreads / 32, kEvBits = 11, kEvBins = 1 << kEvBits;
 constexpr int kEvMaxCtas = 16;
-constexpr int kEvKeyTiles = 13;                     // tiles of a warp's part whose keys fit shared memory (208 KB)
+constexpr int kEvKeyTiles = 12;                     // tiles of a warp's part whose keys fit shared memory (192 KB)
 constexpr int kMvTile = 128, kMvThreads = 288, kMvUnits = 8;     // a record is 18 units of 16 B
 static_assert(kMvThreads / 18 * kMvUnits == kMvTile, "a tile's units");
 
@@ -72,14 +72,7 @@ __device__ __forceinline__ uint32_t ev_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-// The word at the place of p (this CTA's shared memory) in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t ev_get(const uint32_t *p, uint32_t rank) {
-  uint32_t a, v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-
+// Two words at the place of p (this CTA's shared memory) in CTA `rank` of the cluster, read and written.
 __device__ __forceinline__ uint2 ev_get2(const uint32_t *p, uint32_t rank) {
   uint32_t a;
   uint2 v;
@@ -87,11 +80,17 @@ __device__ __forceinline__ uint2 ev_get2(const uint32_t *p, uint32_t rank) {
   asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
   return v;
 }
+__device__ __forceinline__ void ev_put2(const uint32_t *p, uint32_t rank, uint32_t x, uint32_t y) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_u32(p)), "r"(rank));
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
 
-struct EvictShared {
+struct __align__(16) EvictShared {
   uint32_t hist[kEvBins];
+  uint32_t slice[kEvMaxCtas][2], found[2], count[kEvMaxCtas][2];       // by CTA of the cluster
   uint32_t above[kEvWarps], gt[kEvWarps], eq[kEvWarps];
-  uint32_t count[2], found[2];
+  int32_t stage[kEvWarps][kMvTile];
 };
 
 // Order key of entry j's weight, larger is heavier (NaN: 0, below everything).
@@ -213,10 +212,16 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
       for (int u = 0; u < 4; u++)
         if (tile + u < w1) *reinterpret_cast<uint4 *>(mine + (tile - w0 + u) * kMvTile) = make_uint4(x[u][0], x[u][1], x[u][2], x[u][3]);
     }
+  auto meet = [&]() {                                // all threads of the cluster
+    if (ctas > 1) ev_cluster_sync();
+    else __syncthreads();
+  };
   uint32_t T = 0u, ties = 0u;                        // stay: keys above T, and the first `ties` of those at T
   if (kk > 0 && kk < m) {
     int low = 32;                                    // bits that are not known yet
     uint32_t known = 0u, need = (uint32_t)kk;
+    // bins 2 t and 2 t + 1 of this CTA's slice of the histogram
+    const int bins = kEvBins / ctas, bin = (int)rank * bins + 2 * t, warps = max(1, bins / 64);
     while (low > 0) {
       const int w = min(kEvBits, low);
       for (int i = t; i < kEvBins; i += kEvThreads) S.hist[i] = 0u;
@@ -227,40 +232,50 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
         keys_of(tile, x);
 #pragma unroll
         for (int u = 0; u < 4; u++) {
-          const int j = (tile + u) * kMvTile + lane * 4;
           if (tile + u >= w1) break;
+          const int left = m - ((tile + u) * kMvTile + lane * 4);        // the lane's candidates
+          if (low == 32) {
+            uint32_t d[4];
 #pragma unroll
-          for (int i = 0; i < 4; i++) {
-            const bool in = j + i < m && (low == 32 || x[u][i] >> low == known);
-            const uint32_t digit = (x[u][i] >> (low - w)) & mask;
-            if (low == 32) {                         // (many equal weights: one of the warp counts for all)
-              const uint32_t one = __shfl_sync(0xFFFFFFFFu, digit, 0);
-              if (__all_sync(0xFFFFFFFFu, in && digit == one)) {
-                if (lane == 0) atomicAdd(&S.hist[digit], 32u);
-                continue;
-              }
+            for (int i = 0; i < 4; i++) d[i] = x[u][i] >> (32 - kEvBits);
+            // (many equal weights: one lane counts for all)
+            const uint32_t one = __shfl_sync(0xFFFFFFFFu, d[0], 0);
+            if (__all_sync(0xFFFFFFFFu, left >= 4 && d[0] == one && d[1] == one && d[2] == one && d[3] == one)) {
+              if (lane == 0) atomicAdd(&S.hist[one], (uint32_t)kMvTile);
+              continue;
             }
-            if (in) atomicAdd(&S.hist[digit], 1u);
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+              if (i < left) atomicAdd(&S.hist[d[i]], 1u);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+              if (x[u][i] >> low == known && i < left) atomicAdd(&S.hist[(x[u][i] >> (low - w)) & mask], 1u);
           }
         }
       }
-      __syncthreads();
-      ev_cluster_sync();
-      // the digit at which the count from the top passes `need`: thread t has bins 2 t and 2 t + 1
-      static_assert(kEvBins == 2 * kEvThreads, "two bins a thread");
-      uint32_t h0 = 0u, h1 = 0u;
+      meet();
+      // the digit at which the count from the top passes `need`: each CTA sums a slice of the histograms
+      uint32_t h0 = 0u, h1 = 0u, above = 0u;
+      if (2 * t < bins) {
+        if (ctas == 1) {
+          h0 = S.hist[bin];
+          h1 = S.hist[bin + 1];
+        } else {
 #pragma unroll 1
-      for (int c = 0; c < ctas; c += 8) {            // (eight loads in flight)
-        uint2 y[8];
+          for (int c = 0; c < ctas; c += 8) {        // (eight loads in flight)
+            uint2 y[8];
 #pragma unroll
-        for (int i = 0; i < 8; i++) y[i] = c + i < ctas ? ev_get2(&S.hist[2 * t], (uint32_t)(c + i)) : make_uint2(0u, 0u);
+            for (int i = 0; i < 8; i++) y[i] = c + i < ctas ? ev_get2(&S.hist[bin], (uint32_t)(c + i)) : make_uint2(0u, 0u);
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-          h0 += y[i].x;
-          h1 += y[i].y;
+            for (int i = 0; i < 8; i++) {
+              h0 += y[i].x;
+              h1 += y[i].y;
+            }
+          }
         }
       }
-      uint32_t above = h0 + h1;                      // of this thread's bins and all above them
+      above = h0 + h1;                               // of this thread's bins and those above them
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint32_t y = __shfl_down_sync(0xFFFFFFFFu, above, o);
@@ -268,20 +283,33 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
       }
       if (lane == 0) S.above[warp] = above;
       __syncthreads();
-      for (int i = warp + 1; i < kEvWarps; i++) above += S.above[i];
-      const uint32_t top1 = above - h0 - h1, top0 = above - h0;          // above bin 2 t + 1, above bin 2 t
-      if (top1 < need && need <= top1 + h1) {
-        S.found[0] = (uint32_t)(2 * t + 1);
-        S.found[1] = need - top1;
-      } else if (top0 < need && need <= above) {
-        S.found[0] = (uint32_t)(2 * t);
-        S.found[1] = need - top0;
+      const uint32_t part = lane < warps ? S.above[lane] : 0u;
+      above += __reduce_add_sync(0xFFFFFFFFu, lane > warp ? part : 0u);
+      if (ctas > 1) {
+        const uint32_t sum = __reduce_add_sync(0xFFFFFFFFu, part);
+        if (t < ctas) ev_put2(S.slice[rank], (uint32_t)t, sum, 0u);
+        __syncwarp();
+        ev_cluster_sync();
+        above += __reduce_add_sync(0xFFFFFFFFu, lane > (int)rank && lane < ctas ? S.slice[lane & (kEvMaxCtas - 1)][0] : 0u);
       }
-      __syncthreads();
+      if (2 * t < bins) {
+        const uint32_t top1 = above - h0 - h1, top0 = above - h0;        // above bin + 1, above bin
+        const bool hit1 = top1 < need && need <= top1 + h1, hit0 = top0 < need && need <= above;
+        if (hit0 || hit1) {                          // (one thread of the cluster)
+          const uint32_t digit = (uint32_t)bin + (hit1 ? 1u : 0u), rest = need - (hit1 ? top1 : top0);
+          if (ctas == 1) {
+            S.found[0] = digit;
+            S.found[1] = rest;
+          } else {
+            for (int c = 0; c < ctas; c++) ev_put2(S.found, (uint32_t)c, digit, rest);
+          }
+        }
+      }
+      __syncwarp();
+      meet();
       known = known << w | S.found[0];
       need = S.found[1];
       low -= w;
-      ev_cluster_sync();                             // (the histograms are read, everywhere)
     }
     T = known;
     ties = need;
@@ -290,19 +318,27 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
   }
   const bool all = kk == m;
   // ---------------------------------------------------- ranks
+  // bits of the lane's entries of a tile that stay for sure, that tie
+  auto stays = [&](int tile, const uint32_t (&x)[4], uint32_t &g, uint32_t &e) {
+    const int j = tile * kMvTile + lane * 4;
+    g = e = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      if (j + i >= m ? j + i < n : all || x[i] > T) g |= 1u << i;
+      if (j + i < m && !all && x[i] == T) e |= 1u << i;
+    }
+  };
   uint32_t gt = 0u, eq = 0u;
   for (int tile = w0; tile < w1; tile += 4) {
     uint32_t x[4][4];
     keys_of(tile, x);
 #pragma unroll
     for (int u = 0; u < 4; u++) {
-      const int j = (tile + u) * kMvTile + lane * 4;
       if (tile + u >= w1) break;
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        gt += (j + i < n && (j + i >= m || all || x[u][i] > T)) ? 1u : 0u;
-        eq += (j + i < m && !all && x[u][i] == T) ? 1u : 0u;
-      }
+      uint32_t g, e;
+      stays(tile + u, x[u], g, e);
+      gt += (uint32_t)__popc(g);
+      eq += (uint32_t)__popc(e);
     }
   }
   gt = __reduce_add_sync(0xFFFFFFFFu, gt);
@@ -312,39 +348,30 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
     S.eq[warp] = eq;
   }
   __syncthreads();
-  if (warp == 0) {
-    const uint32_t a = __reduce_add_sync(0xFFFFFFFFu, S.gt[lane]), c = __reduce_add_sync(0xFFFFFFFFu, S.eq[lane]);
-    if (lane == 0) {
-      S.count[0] = a;
-      S.count[1] = c;
+  gt = lane < warp ? S.gt[lane] : 0u;
+  eq = lane < warp ? S.eq[lane] : 0u;
+  if (ctas > 1) {
+    if (warp == 0) {
+      const uint32_t a = __reduce_add_sync(0xFFFFFFFFu, S.gt[lane]), c = __reduce_add_sync(0xFFFFFFFFu, S.eq[lane]);
+      if (lane < ctas) ev_put2(S.count[rank], (uint32_t)lane, a, c);
+      __syncwarp();
     }
+    ev_cluster_sync();                               // (nothing of another CTA is read or written from here on)
+    gt += lane < (int)rank ? S.count[lane & (kEvMaxCtas - 1)][0] : 0u;
+    eq += lane < (int)rank ? S.count[lane & (kEvMaxCtas - 1)][1] : 0u;
   }
-  __syncthreads();
-  ev_cluster_sync();
-  gt = lane < (int)rank ? ev_get(&S.count[0], (uint32_t)lane) : 0u;
-  eq = lane < (int)rank ? ev_get(&S.count[1], (uint32_t)lane) : 0u;
-  gt += lane < warp ? S.gt[lane] : 0u;
-  eq += lane < warp ? S.eq[lane] : 0u;
   gt = __reduce_add_sync(0xFFFFFFFFu, gt);           // ahead of this warp's part
   eq = __reduce_add_sync(0xFFFFFFFFu, eq);
-  ev_cluster_sync();                                 // (nothing of this CTA is read from here on)
   int32_t *from = W.from + (int64_t)b * W.from_stride, *before = W.before + (int64_t)b * W.tile_stride;
-  int32_t *out = A.from != nullptr ? A.from + (int64_t)b * A.from_stride : nullptr;
   for (int tile4 = w0; tile4 < w1; tile4 += 4) {
     uint32_t y[4][4];
     keys_of(tile4, y);
 #pragma unroll
     for (int v = 0; v < 4; v++) {
-      const int tile = tile4 + v, j = tile * kMvTile + lane * 4;
-      const uint32_t(&x)[4] = y[v];
+      const int tile = tile4 + v;
       if (tile >= w1) break;
-      if (lane == 0) before[tile] = (int32_t)(gt + min(eq, ties));
-      uint32_t g = 0u, e = 0u;                       // bits of the lane's entries that stay for sure, that tie
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        if (j + i < n && (j + i >= m || all || x[i] > T)) g |= 1u << i;
-        if (j + i < m && !all && x[i] == T) e |= 1u << i;
-      }
+      uint32_t g, e;
+      stays(tile, y[v], g, e);
       uint32_t sum = (uint32_t)__popc(g) | (uint32_t)__popc(e) << 16;      // (at most 128 each)
       const uint32_t own = sum;
 #pragma unroll
@@ -352,21 +379,23 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
         const uint32_t z = __shfl_up_sync(0xFFFFFFFFu, sum, o);
         if (lane >= o) sum += z;
       }
+      const uint32_t all_sum = __shfl_sync(0xFFFFFFFFu, sum, 31), r0 = gt + min(eq, ties);
       uint32_t a = gt + ((sum - own) & 0xFFFFu), c = eq + ((sum - own) >> 16);
+      // (through shared memory: the places of a tile's kept entries are neighbours)
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         const bool tie = (e >> i) & 1u;
-        if (((g >> i) & 1u) || (tie && c < ties)) {
-          const uint32_t r = a + min(c, ties);
-          from[r] = j + i;
-          if (out != nullptr) out[r] = j + i;
-        }
+        if (((g >> i) & 1u) || (tie && c < ties)) S.stage[warp][a + min(c, ties) - r0] = tile * kMvTile + lane * 4 + i;
         a += (g >> i) & 1u;
         c += tie ? 1u : 0u;
       }
-      const uint32_t all_sum = __shfl_sync(0xFFFFFFFFu, sum, 31);
+      __syncwarp();
       gt += all_sum & 0xFFFFu;
       eq += all_sum >> 16;
+      const uint32_t count = gt + min(eq, ties) - r0;
+      for (uint32_t i = lane; i < count; i += 32) from[r0 + i] = S.stage[warp][i];
+      if (lane == 0) before[tile] = (int32_t)r0;
+      __syncwarp();
     }
   }
   if (w1 == tiles && w0 < w1 && lane == 0) before[tiles] = k;
@@ -507,7 +536,11 @@ cudaError_t launch_evict(EvictArgs A, void *ws, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t sms = device_sm_count(dev), row = A.table_stride * A.page;
   evict_magic((unsigned)A.page, A.page_mul, A.page_shift);
-  const EvictWs W = evict_ws(ws, A.n_seq, row);
+  EvictWs W = evict_ws(ws, A.n_seq, row);
+  if (A.from != nullptr) {
+    W.from = A.from;
+    W.from_stride = A.from_stride;
+  }
   // CTAs of a row: one for each 8,192 entries, up to 16, while the sequences leave SMs for more
   int ctas = 1;
   while (ctas < kEvMaxCtas && (int64_t)ctas * 8192 < row && (int64_t)A.n_seq * ctas * 2 <= sms) ctas *= 2;
@@ -515,9 +548,10 @@ cudaError_t launch_evict(EvictArgs A, void *ws, cudaStream_t st) {
   const int cache = (int)(warp_share < kEvKeyTiles ? warp_share : kEvKeyTiles);
   e = launch_pdl(evict_select_kernel, dim3((unsigned)ctas, (unsigned)A.n_seq), dim3(kEvThreads), cache * kTileBytes, st, (unsigned)ctas, A, W, cache);
   if (e != cudaSuccess) return e;
-  // no more CTAs than there can be tiles
+  // no more CTAs than there can be tiles, and many more than run at a time: SMs differ in speed (8 x 1M entries cut to
+  // half: 720 us with four CTAs an SM that take equal shares)
   const int64_t dst_row = A.dst_stride * A.page, most = dst_row < row ? dst_row : row;
-  const int64_t tiles = A.n_seq * ((most + kMvTile - 1) / kMvTile), grid = tiles < 4 * sms ? tiles : 4 * sms;
+  const int64_t tiles = A.n_seq * ((most + kMvTile - 1) / kMvTile), grid = tiles < 64 * sms ? tiles : 64 * sms;
   return launch_pdl(evict_move_kernel, dim3((unsigned)grid), dim3(kMvThreads), 0, st, 1u, A, W);
 }
 
