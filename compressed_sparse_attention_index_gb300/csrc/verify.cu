@@ -160,37 +160,39 @@ struct Weights {
       for (int i = 0; i < V; i++) rest[i] = 0.f;
     }
   }
-  // this lane's part of groups [g0, g1): every 32nd, four rows of loads in flight
+  __device__ __forceinline__ void take(Pair32 &s, float (&w)[V], const float (&y)[V], int k) const {
+    float rest[V];
+    weigh(k, w, y, rest);
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+      s.add(w[i]);
+      s.l += rest[i];
+    }
+  }
+  // this lane's part of groups [g0, g1): every 32nd, four of them in flight (the row's first and last group, which may
+  // not be whole, on their own)
   __device__ __forceinline__ Pair32 sum(int g0, int g1, int lane) const {
     Pair32 s = {0.f, 0.f};
+    for (int side = 0; side < 2 && g0 < g1; side++) {
+      const int k = side == 0 ? g0 : g1 - 1;
+      if (p.inside(k)) continue;
+      if (side == 0) g0++;
+      else g1--;
+      if (lane > 0) continue;
+      float w[V], rest[V];
+      get(k, w, rest);
+#pragma unroll
+      for (int i = 0; i < V; i++) {
+        s.add(w[i]);
+        s.l += rest[i];
+      }
+    }
     int k = g0 + lane;
-    if (q.row != nullptr) {
-      if (wide)
-        for (; k + 96 < g1 && p.inside(k) && p.inside(k + 96); k += 128) {
-          uint4 a[4], b[4];
-#pragma unroll
-          for (int u = 0; u < 4; u++) {
-            a[u] = p.wide(k + 32 * u);
-            b[u] = __ldg(reinterpret_cast<const uint4 *>(q.row + p.first(k + 32 * u)));
-          }
-#pragma unroll
-          for (int u = 0; u < 4; u++) {
-            float w[V], y[V], rest[V];
-            widen(a[u], w, T());
-            widen(b[u], y, T());
-            weigh(k + 32 * u, w, y, rest);
-#pragma unroll
-            for (int i = 0; i < V; i++) {
-              s.add(w[i]);
-              s.l += rest[i];
-            }
-          }
-        }
-    } else {
-      for (; k + 96 < g1 && p.inside(k) && p.inside(k + 96); k += 128) {
+    if (q.row == nullptr) {
+      for (; k < g1; k += 128) {
         uint4 a[4];
 #pragma unroll
-        for (int u = 0; u < 4; u++) a[u] = p.wide(k + 32 * u);
+        for (int u = 0; u < 4; u++) a[u] = k + 32 * u < g1 ? p.wide(k + 32 * u) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int u = 0; u < 4; u++) {
           float w[V];
@@ -200,14 +202,29 @@ struct Weights {
           for (int i = 0; i < V; i++) s.add(w[i]);
         }
       }
-    }
-    for (; k < g1; k += 32) {
-      float w[V], rest[V];
-      get(k, w, rest);
+    } else if (wide) {
+      for (; k < g1; k += 64) {
+        uint4 a[2], b[2];
 #pragma unroll
-      for (int i = 0; i < V; i++) {
-        s.add(w[i]);
-        s.l += rest[i];
+        for (int u = 0; u < 2; u++) {
+          const bool in = k + 32 * u < g1;
+          a[u] = in ? p.wide(k + 32 * u) : make_uint4(0u, 0u, 0u, 0u);
+          b[u] = in ? __ldg(reinterpret_cast<const uint4 *>(q.row + p.first(k + 32 * u))) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+          float w[V], y[V];
+          widen(a[u], w, T());
+          widen(b[u], y, T());
+          take(s, w, y, k + 32 * u);
+        }
+      }
+    } else {
+      for (; k < g1; k += 32) {
+        float w[V], y[V];
+        widen(p.wide(k), w, T());
+        get_q(k, y);
+        take(s, w, y, k);
       }
     }
     return s;
@@ -444,8 +461,19 @@ __global__ void __launch_bounds__(kVfThreads) verify_best_kernel(const __grid_co
         at = e0 + i;
       }
   };
-  int k = g0 + t;
-  for (; k + 3 * kVfThreads < g1 && P.inside(k) && P.inside(k + 3 * kVfThreads); k += 4 * kVfThreads) {
+  // (the row's first and last group, which may not be whole, on their own; a lane's elements still ascend)
+  int a0 = g0, a1 = g1;
+  if (a0 < a1 && !P.inside(a0)) {
+    if (t == 0) {
+      float x[V];
+      P.edge(a0, -INFINITY, x);
+      take(a0, x);
+    }
+    a0++;
+  }
+  if (a0 < a1 && !P.inside(a1 - 1)) a1--;
+  int k = a0 + t;
+  for (; k + 3 * kVfThreads < a1; k += 4 * kVfThreads) {
     uint4 w[4];
 #pragma unroll
     for (int u = 0; u < 4; u++) w[u] = P.wide(k + u * kVfThreads);
@@ -456,14 +484,19 @@ __global__ void __launch_bounds__(kVfThreads) verify_best_kernel(const __grid_co
       take(k + u * kVfThreads, x);
     }
   }
-  for (; k < g1; k += kVfThreads) {
+  for (; k < a1; k += kVfThreads) {
     float x[V];
-    P.get(k, -INFINITY, x);
+    widen(P.wide(k), x, T());
     take(k, x);
+  }
+  if (a1 < g1 && a1 >= a0 && t == 0) {
+    float x[V];
+    P.edge(a1, -INFINITY, x);
+    take(a1, x);
   }
   // nothing above -inf: the first -inf, if any
   if (__syncthreads_or(at >= 0) == 0) {
-    for (k = g0 + t; k < g1 && at < 0; k += kVfThreads) {
+    for (int k = g0 + t; k < g1 && at < 0; k += kVfThreads) {
       float x[V];
       P.get(k, __int_as_float(0x7FC00000), x);
 #pragma unroll
