@@ -25,7 +25,8 @@
 
 namespace csa2 {
 
-constexpr int kVfThreads = 512, kVfWarps = kVfThreads / 32, kVfMaxParts = 8;
+constexpr int kVfThreads = 256, kVfWarps = kVfThreads / 32, kVfMaxParts = 16;
+constexpr int kVfCtas = 4, kVfBestCtas = 6;         // of an SM at a time (sampled, greedy)
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -203,16 +204,16 @@ struct Weights {
         }
       }
     } else if (wide) {
-      for (; k < g1; k += 64) {
-        uint4 a[2], b[2];
+      for (; k < g1; k += 128) {
+        uint4 a[4], b[4];
 #pragma unroll
-        for (int u = 0; u < 2; u++) {
+        for (int u = 0; u < 4; u++) {
           const bool in = k + 32 * u < g1;
           a[u] = in ? p.wide(k + 32 * u) : make_uint4(0u, 0u, 0u, 0u);
           b[u] = in ? __ldg(reinterpret_cast<const uint4 *>(q.row + p.first(k + 32 * u))) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
-        for (int u = 0; u < 2; u++) {
+        for (int u = 0; u < 4; u++) {
           float w[V], y[V];
           widen(a[u], w, T());
           widen(b[u], y, T());
@@ -251,32 +252,42 @@ __device__ __forceinline__ void put_pair(const float2 *p, uint32_t rank, const P
 // the last number that adds anything.
 template <int SLOTS>
 __device__ __forceinline__ int find_pass(const Pair32 (&x)[SLOTS], const Pair32 &goal, int lane, Pair32 &ahead, int &some) {
+  Pair32 in[SLOTS];
+#pragma unroll
+  for (int c = 0; c < SLOTS; c++) in[c] = x[c];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    Pair32 y[SLOTS];                                 // (the slots' scans beside one another)
+#pragma unroll
+    for (int c = 0; c < SLOTS; c++) y[c] = in[c].up(o);
+#pragma unroll
+    for (int c = 0; c < SLOTS; c++)
+      if (lane >= o) in[c].add(y[c]);
+  }
   int hit = -1;
   Pair32 run = {0.f, 0.f};
   some = -1;
 #pragma unroll
   for (int c = 0; c < SLOTS; c++) {
-    const Pair32 in = warp_scan(x[c], lane);
-    Pair32 at = run, before = in.up(1);
-    at.add(in);
+    Pair32 at = run, before = in[c].up(1);
+    at.add(in[c]);
     if (lane == 0) before = {0.f, 0.f};
-    Pair32 b = run;
-    b.add(before);
     const uint32_t past = __ballot_sync(0xFFFFFFFFu, above(at, goal) && x[c].h > 0.f);
     const uint32_t any = __ballot_sync(0xFFFFFFFFu, x[c].h > 0.f);
     if (any != 0u) some = c * 32 + 31 - __clz((int)any);
     if (hit < 0 && past != 0u) {
       const int from = __ffs((int)past) - 1;
       hit = c * 32 + from;
-      ahead = b.from(from);
+      ahead = run;
+      ahead.add(before.from(from));
     }
-    run = at.from(31);
+    run.add(in[c].from(31));
   }
   return hit;
 }
 
 template <class T>
-__global__ void __launch_bounds__(kVfThreads) verify_sample_kernel(const __grid_constant__ VerifyArgs A) {
+__global__ void __launch_bounds__(kVfThreads, kVfCtas) verify_sample_kernel(const __grid_constant__ VerifyArgs A) {
   constexpr int V = 16 / sizeof(T), kSlots = kVfMaxParts * kVfWarps / 32;
   __shared__ float2 sums[2][kVfMaxParts * kVfWarps], inner[kVfWarps];
   __shared__ int accepted_sh, refused_sh;
@@ -563,10 +574,19 @@ size_t verify_workspace_bytes(int n_rows) { return (size_t)n_rows * kVfMaxParts 
 template <class T>
 static cudaError_t launch_verify_as(VerifyArgs A, bool greedy, cudaStream_t st) {
   const int64_t sms = device_sm_count(current_device());
-  // parts of a row: about two CTAs an SM in all, and at least 16 KB of the row each
+  // parts of a row: as many as run at a time (256 rows of 131,072 in two waves took twice as long), of at
+  // least 16 KB of the row each; clusters of more than eight CTAs for a few rows only (32 rows: 9.4 us with eight, 13
+  // with sixteen; one row: 7.6, 6.6)
   const int64_t rows = greedy ? A.n_rows : A.n_seq, most = (int64_t)A.vocab * (int64_t)sizeof(T) / 16384;
   int parts = 1;
-  while (parts < kVfMaxParts && 2 * parts <= most && parts * rows < 2 * sms) parts *= 2;
+  while (parts < kVfMaxParts && 2 * parts <= most && 2 * parts * rows <= (greedy ? kVfBestCtas : kVfCtas) * sms &&
+         (greedy || parts < 8 || rows * 32 <= sms))
+    parts *= 2;
+  static std::atomic<int> attr_done[kMaxDevices];
+  const cudaError_t attr = once_per_device(attr_done, current_device(), [&] {
+    return cudaFuncSetAttribute(verify_sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  });
+  if (attr != cudaSuccess) return attr;
   if (!greedy) return launch_pdl(verify_sample_kernel<T>, dim3((unsigned)parts, (unsigned)A.n_seq), dim3(kVfThreads), 0, st, (unsigned)parts, A);
   if (A.n_rows > 0) {
     const cudaError_t e = launch_pdl(verify_best_kernel<T>, dim3((unsigned)parts, (unsigned)A.n_rows), dim3(kVfThreads), 0, st, 1u, A);
