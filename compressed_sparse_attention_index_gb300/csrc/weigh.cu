@@ -6,7 +6,7 @@
 // Work: the entries that a sequence's queries see form chunks of 128, its queries groups
 // of NQ.  All sequences' (chunk, group) products are dealt to the CTAs (one an SM) in contiguous runs of equal
 // numbers, cut between chunks, so that one CTA has all of an entry's queries and sums them in a fixed order.
-// With several groups a CTA takes 24 chunks at a time (one query a group: 16), group by group: Q stays in shared memory
+// With several groups a CTA takes 24 chunks at a time (one query a group: 8), group by group: Q stays in shared memory
 // for them, their records in L2 for the groups, and their sums in shared memory.  A selection is a
 // sequence of its own: its chunks' weights go to scratch, and are added query by query.
 //
@@ -45,19 +45,21 @@ constexpr int kWgQBlock = 64 * 128;                // 64 heads x 64 dims f16: [h
 constexpr int kWgImage = 8 * kWgQBlock;            // a query as the tensor cores read it
 constexpr int kWgMeta = 2 * kHeads * 4;            // its heads' f, then their -lse log2(e)
 constexpr int kWgMetas = 8;                        // groups whose f and lse are in shared memory
-constexpr int kWgSlots = 8;                        // chunks whose slots are in shared memory
 constexpr int kWgScatter = 8;                      // pages of fewer entries are fetched as scattered records
 
 template <int NQ>
 struct WgSmem {
   static constexpr int kStages = NQ == 1 ? 4 : 2;  // records of as many chunks
-  static constexpr int kBlock = NQ == 1 ? 16 : 24; // chunks that take turns at several groups
+  static constexpr int kBlock = NQ == 1 ? 8 : 24;  // chunks that take turns at several groups
+  static constexpr int kSums = NQ == 1 ? 4 : 2;    // accumulators of S in tensor memory
+  static constexpr int kSlots = NQ == 1 ? 16 : 8;  // chunks whose slots are in shared memory
   static constexpr int kQ = 0;                     // [dims / 64][query][heads]
   static constexpr int kRaw = kQ + NQ * kWgImage;
   static constexpr int kAcc = kRaw + kStages * kWgRaw;         // [kBlock chunks][128]
   static constexpr int kMeta = kAcc + kBlock * kWgChunk * 4;
   static constexpr int kSlot = kMeta + kWgMetas * NQ * kWgMeta;
-  static constexpr int kEnd = kSlot + kWgSlots * kWgChunk * 4;
+  static constexpr int kPart = kSlot + kSlots * kWgChunk * 4;  // [2][128]: the second query's sums (NQ = 2)
+  static constexpr int kEnd = kPart + (NQ == 2 ? 2 * kWgChunk * 4 : 0);
   static constexpr int kAlloc = kEnd + 1024;
   static_assert(kAlloc + 512 <= 227 * 1024, "shared memory");
 };
@@ -287,7 +289,7 @@ struct WgWalk {
 };
 
 struct WgShared {
-  uint64_t raw_full[4], raw_free[4], k_full[2][4], k_free[4], q_full[4], q_free[4], s_full[2], s_free[2], m_full[kWgMetas], drain;
+  uint64_t raw_full[4], raw_free[4], k_full[2][4], k_free[4], q_full[4], q_free[4], s_full[4], s_free[4], m_full[kWgMetas], drain;
   uint32_t tmem;
   int begin_b, begin_c, end_b, end_c, steps;
   volatile int bad;
@@ -382,8 +384,10 @@ __device__ __forceinline__ void wg_fetch(const WeighArgs &A, const WgWs &W, WgSh
     if (k >= M::kStages) wg_wait(A, S, &S.raw_free[stage], (uint32_t)(k / M::kStages - 1) & 1u);
     if (wg_bad(S)) break;                            // no copy is started any more
     if (!SEL && last) {
-      // (its place was used eight products ago: the sums have read it before the products that freed the buffer)
-      int *slot = reinterpret_cast<int *>(sm + M::kSlot) + (k % kWgSlots) * kWgChunk + lane;
+      // (its place was used kSlots products ago.  The buffer was freed by the rows of product k - kStages, which came after the
+      // MMAs of k - kStages - 2, which came after the sums of k - kStages - 2 - kSums had read theirs)
+      static_assert(M::kSlots >= M::kStages + 2 + M::kSums, "slots");
+      int *slot = reinterpret_cast<int *>(sm + M::kSlot) + (k % M::kSlots) * kWgChunk + lane;
 #pragma unroll
       for (int g = 0; g < 4; g++) {
         slot[32 * g] = rec[g];
@@ -526,7 +530,7 @@ __device__ __forceinline__ void wg_load(const WeighArgs &A, WgShared &S, const u
 template <int NQ>
 __device__ __forceinline__ void wg_issue(const WeighArgs &A, const WgWs &W, WgShared &S, unsigned char *sm, WgWalk<NQ> C, bool more, int turn, uint32_t tmem) {
   const uint64_t d_q = ptx::smem_desc(ptx::smem_u32(sm + WgSmem<NQ>::kQ), 16, 1024, 2);
-  const uint32_t d = tmem + kWgColS + (uint32_t)turn * 128u;
+  using M = WgSmem<NQ>;
   int seen = -1;                                     // the group whose Q this thread has waited for
   if (more && turn > 0) more = C.next(W);
 #pragma unroll 1
@@ -535,7 +539,9 @@ __device__ __forceinline__ void wg_issue(const WeighArgs &A, const WgWs &W, WgSh
     const uint32_t q_parity = (uint32_t)C.group & 1u;
     seen = C.group;
     const uint32_t id = NQ == 2 && C.I.w - C.g * NQ >= 2 ? idesc_m128(0, true, 2 * kHeads) : idesc_m128(0, true, kHeads);
-    if (k >= 2) wg_wait(A, S, &S.s_free[turn], (uint32_t)((k >> 1) - 1) & 1u);
+    const int place = k % M::kSums;
+    const uint32_t d = tmem + kWgColS + (uint32_t)place * (64u * NQ);
+    if (k >= M::kSums) wg_wait(A, S, &S.s_free[place], (uint32_t)(k / M::kSums - 1) & 1u);
 #pragma unroll 1
     for (int s = 0; s < 4; s++) {
       wg_wait(A, S, &S.k_full[turn][s], (uint32_t)(k >> 1) & 1u);
@@ -549,7 +555,7 @@ __device__ __forceinline__ void wg_issue(const WeighArgs &A, const WgWs &W, WgSh
       ptx::tc_commit(&S.k_free[s]);
       if (ends) ptx::tc_commit(&S.q_free[s]);
     }
-    ptx::tc_commit(&S.s_full[turn]);
+    ptx::tc_commit(&S.s_full[place]);
     more = C.next(W);
     if (more) more = C.next(W);
   }
@@ -599,62 +605,66 @@ __device__ __forceinline__ float wg_total(const uint64_t (&sum)[4]) {
   return all.x + all.y;
 }
 
-// Warps 0 .. 3 and 4 .. 7 take turns at the chunks, each with 32 of its entries over all of the
-// group's heads.  Tensor memory is read 32 heads ahead of the arithmetic.
+// Each warp has 32 of a chunk's entries and 64 heads: a query at a time, warps 0 .. 3 and 4 .. 7 take turns at the
+// chunks; of two queries the former have the first and the latter the second, whose sums go to the former
+// through shared memory.  Tensor memory is read 32 heads ahead of the arithmetic.
 template <int NQ, bool SEL>
 __device__ __forceinline__ void wg_sum(const WeighArgs &A, const WgWs &W, WgShared &S, unsigned char *sm, WgWalk<NQ> C, bool more, uint32_t tmem) {
   using M = WgSmem<NQ>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int quarter = warp & 3, turn = warp >> 2, row = quarter * 32 + lane;
-  const uint32_t ts = tmem + ((uint32_t)(quarter * 32) << 16) + kWgColS + (uint32_t)turn * 128u;
-  float *acc = reinterpret_cast<float *>(sm + M::kAcc) + row;
-  int seen = -1, vis0 = 0, vis1 = 0;
+  const int quarter = warp & 3, side = warp >> 2, row = quarter * 32 + lane;
+  const uint32_t ts = tmem + ((uint32_t)(quarter * 32) << 16) + kWgColS + (NQ == 2 ? (uint32_t)side * 64u : 0u);
+  float *acc = reinterpret_cast<float *>(sm + M::kAcc) + row, *part = reinterpret_cast<float *>(sm + M::kPart) + row;
+  int seen = -1, vis = 0;
   bool two = false;
 #pragma unroll 1
   for (int k = 0; more; k++, more = C.next(W)) {
     if (C.group != seen) {
       seen = C.group;
-      // (a chunk's sums of the group before may be the other four warps')
+      // (a chunk's sums of the group before may be the other four warps', or not be read yet)
       if (!SEL) asm volatile("bar.sync %0, 64;" ::"r"(quarter + 1) : "memory");
-      const int q = C.I.z + C.g * NQ;
       two = NQ == 2 && C.I.w - C.g * NQ >= 2;
-      if (!SEL) {
-        vis0 = weigh_vis(A, q);
-        if (two) vis1 = weigh_vis(A, q + 1);
-      }
+      if (!SEL) vis = weigh_vis(A, C.I.z + C.g * NQ + (two ? side : 0));
     }
-    if ((k & 1) != turn) continue;
-    const bool last = C.last_group();
-    const float *f = reinterpret_cast<const float *>(sm + M::kMeta + (seen % kWgMetas) * NQ * kWgMeta);
-    wg_wait(A, S, &S.s_full[turn], (uint32_t)(k >> 1) & 1u);
+    if (NQ == 1 && (k & 1) != side) continue;
+    const bool last = C.last_group(), works = NQ == 1 || side == 0 || two;
+    const int place = k % M::kSums;
+    wg_wait(A, S, &S.s_full[place], (uint32_t)(k / M::kSums) & 1u);
     // (f and lse: as the group's products, or later; those of the groups before are there)
     wg_wait(A, S, &S.m_full[seen % kWgMetas], (uint32_t)(seen / kWgMetas) & 1u);
     ptx::tc_fence_after();
     int slot = -1;
     float before = 0.f, w = 0.f;
-    if (!SEL && last) {                              // where the entry's weight is, asked for ahead of the sum
-      slot = reinterpret_cast<const int *>(sm + M::kSlot)[(k % kWgSlots) * kWgChunk + row];
+    if (!SEL && last && (NQ == 1 || side == 0)) {    // where the entry's weight is, asked for ahead of the sum
+      slot = reinterpret_cast<const int *>(sm + M::kSlot)[(k % M::kSlots) * kWgChunk + row];
       if (S.bad) slot = -1;                          // (a place left from before, once a wait has run out)
       if (slot >= 0 && A.prior != nullptr) before = A.prior[slot];
     }
-    const int j = C.c * kWgChunk + row, n = NQ == 2 && two ? 2 : 1;
-#pragma unroll 1
-    for (int x = 0; x < n; x++, f += 2 * kHeads) {
-      uint32_t a0[32], a1[32];
-      ptx::tmem_ld_32x32b_x32(ts + x * kHeads, a0);
-      uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+    const int j = C.c * kWgChunk + row;
+    const float *f = reinterpret_cast<const float *>(sm + M::kMeta + (seen % kWgMetas) * NQ * kWgMeta) + (NQ == 2 ? side * 2 * kHeads : 0);
+    uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+    uint32_t a1[32];
+    if (works) {
+      uint32_t a0[32];
+      ptx::tmem_ld_32x32b_x32(ts + place * (64 * NQ), a0);
       ptx::tmem_wait_ld();
-      ptx::tmem_ld_32x32b_x32(ts + x * kHeads + 32, a1);
+      ptx::tmem_ld_32x32b_x32(ts + place * (64 * NQ) + 32, a1);
       wg_add_heads(a0, f, f + kHeads, sum);
       ptx::tmem_wait_ld();
-      if (x + 1 == n) {
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&S.s_free[turn]);
-      }
-      wg_add_heads(a1, f + 32, f + kHeads + 32, sum);
-      if (SEL || j < (x == 0 ? vis0 : vis1)) w += wg_total(sum);
     }
+    ptx::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&S.s_free[place]);
+    if (works) {
+      wg_add_heads(a1, f + 32, f + kHeads + 32, sum);
+      if (SEL || j < vis) w = wg_total(sum);
+    }
+    if (NQ == 2 && two) {
+      if (side == 1) part[(k & 1) * kWgChunk] = w;
+      asm volatile("bar.sync %0, 64;" ::"r"(quarter + 1) : "memory");
+      if (side == 0) w += part[(k & 1) * kWgChunk];
+    }
+    if (NQ == 2 && side == 1) continue;
     float *mine = acc + (C.c - C.lo) * kWgChunk;     // (of several groups)
     if (C.g > 0) w += *mine;
     if (!last) {
@@ -700,9 +710,9 @@ __global__ void __launch_bounds__(kWgThreads, 1) weigh_kernel(const __grid_const
       ptx::mbar_init(&S.q_full[i], 1);
       ptx::mbar_init(&S.q_free[i], 1);
     }
-    for (int i = 0; i < 2; i++) {
+    for (int i = 0; i < 4; i++) {
       ptx::mbar_init(&S.s_full[i], 1);
-      ptx::mbar_init(&S.s_free[i], kWgSumWarps / 2);
+      ptx::mbar_init(&S.s_free[i], NQ == 1 ? kWgSumWarps / 2 : kWgSumWarps);
     }
     for (int i = 0; i < kWgMetas; i++) ptx::mbar_init(&S.m_full[i], 1);
     ptx::mbar_init(&S.drain, 2);
