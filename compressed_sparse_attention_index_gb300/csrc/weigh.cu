@@ -118,6 +118,31 @@ __device__ __forceinline__ int64_t weigh_slot(const WeighArgs &A, int b, int j) 
   return id >= 0 && id < A.n_pages ? (int64_t)id * A.page + (j - c * A.page) : -1;
 }
 
+// Shared memory by its own addresses (behind the base's alignment the compiler takes pointers for any memory's, and
+// loads through them cost half as many instructions again).
+__device__ __forceinline__ uint4 wg_lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 wg_lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ ulonglong2 wg_lds2x64(uint32_t a) {
+  ulonglong2 v;
+  asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t wg_lds4(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float wg_ldsf(uint32_t a) { return __uint_as_float(wg_lds4(a)); }
+__device__ __forceinline__ void wg_sts4(uint32_t a, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory"); }
+
 // ------------------------------------------------------------------ what the products need
 constexpr int kPrepThreads = 256, kPrepCtas = 8;     // CTAs of a query
 __device__ __forceinline__ float wg_power(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
@@ -323,6 +348,7 @@ __device__ __forceinline__ void wg_fetch(const WeighArgs &A, const WgWs &W, WgSh
   using M = WgSmem<NQ>;
   const int lane = threadIdx.x & 31;
   const bool scattered = SEL || A.page < kWgScatter;
+  const uint32_t smu = ptx::smem_u32(sm);
   int id[4], off[4];                                 // rows 32 g + lane: the page (-1: none), the place in it
   bool out = false;
   auto ask = [&]() {
@@ -387,10 +413,10 @@ __device__ __forceinline__ void wg_fetch(const WeighArgs &A, const WgWs &W, WgSh
       // (its place was used kSlots products ago.  The buffer was freed by the rows of product k - kStages, which came after the
       // MMAs of k - kStages - 2, which came after the sums of k - kStages - 2 - kSums had read theirs)
       static_assert(M::kSlots >= M::kStages + 2 + M::kSums, "slots");
-      int *slot = reinterpret_cast<int *>(sm + M::kSlot) + (k % M::kSlots) * kWgChunk + lane;
+      const uint32_t slot = smu + M::kSlot + (uint32_t)((k % M::kSlots) * kWgChunk + lane) * 4u;
 #pragma unroll
       for (int g = 0; g < 4; g++) {
-        slot[32 * g] = rec[g];
+        wg_sts4(slot + 128u * g, (uint32_t)rec[g]);
         if (A.prior != nullptr && rec[g] >= 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(A.prior + rec[g]));
       }
     }
@@ -465,19 +491,18 @@ __device__ __forceinline__ void wg_load(const WeighArgs &A, WgShared &S, const u
   // Records are 18 16-B units apart, so rows r and r + 4 of a unit share their banks: every
   // other four rows read the units of a pair the other way round.
   const bool flip = (e & 4) != 0;
-  const int other = flip ? -16 : 16;
+  const uint32_t rows = ptx::smem_u32(sm) + M::kRaw + (uint32_t)(e * kKvBytes), own = (uint32_t)(team * 64) + (flip ? 16u : 0u), other = flip ? 0u - 16u : 16u;
   int stage = 0;
   uint32_t turn = 0u;
 #pragma unroll 1
   for (int k = 0; k < steps; k++) {
     wg_wait(A, S, &S.raw_full[stage], turn);
-    const unsigned char *row = sm + M::kRaw + stage * kWgRaw + e * kKvBytes;
-    const uint2 sc = *reinterpret_cast<const uint2 *>(row + 256 + team * 8);
-    const unsigned char *raw = row + team * 64 + (flip ? 16 : 0);
+    const uint32_t row = rows + (uint32_t)(stage * kWgRaw), raw = row + own;
+    const uint2 sc = wg_lds8(row + 256u + (uint32_t)team * 8u);
     uint4 code[4];
 #pragma unroll
     for (int j = 0; j < 4; j += 2) {
-      const uint4 x = *reinterpret_cast<const uint4 *>(raw + j * 16), y = *reinterpret_cast<const uint4 *>(raw + j * 16 + other);
+      const uint4 x = wg_lds16(raw + j * 16u), y = wg_lds16(raw + j * 16u + other);
       code[j] = flip ? y : x;
       code[j + 1] = flip ? x : y;
     }
@@ -590,10 +615,10 @@ __device__ __forceinline__ float wg_ex2(float x) {
 }
 
 // Adds 32 heads' numerators of this lane's entry to sum.
-__device__ __forceinline__ void wg_add_heads(const uint32_t (&a)[32], const float *f, const float *nl, uint64_t (&sum)[4]) {
+__device__ __forceinline__ void wg_add_heads(const uint32_t (&a)[32], uint32_t f, uint64_t (&sum)[4]) {
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
-    const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(f + i), y = *reinterpret_cast<const ulonglong2 *>(nl + i);
+    const ulonglong2 x = wg_lds2x64(f + 4u * i), y = wg_lds2x64(f + 4u * (kHeads + i));
     const float2 u = wg_unpair(wg_fma2(wg_pair(__uint_as_float(a[i]), __uint_as_float(a[i + 1])), x.x, y.x));
     const float2 v = wg_unpair(wg_fma2(wg_pair(__uint_as_float(a[i + 2]), __uint_as_float(a[i + 3])), x.y, y.y));
     sum[(i >> 1) & 2] = wg_add2(sum[(i >> 1) & 2], wg_pair(wg_ex2(u.x), wg_ex2(u.y)));
@@ -614,7 +639,7 @@ __device__ __forceinline__ void wg_sum(const WeighArgs &A, const WgWs &W, WgShar
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3, side = warp >> 2, row = quarter * 32 + lane;
   const uint32_t ts = tmem + ((uint32_t)(quarter * 32) << 16) + kWgColS + (NQ == 2 ? (uint32_t)side * 64u : 0u);
-  float *acc = reinterpret_cast<float *>(sm + M::kAcc) + row, *part = reinterpret_cast<float *>(sm + M::kPart) + row;
+  const uint32_t smu = ptx::smem_u32(sm), acc = smu + M::kAcc + row * 4u, part = smu + M::kPart + row * 4u;
   int seen = -1, vis = 0;
   bool two = false;
 #pragma unroll 1
@@ -636,12 +661,12 @@ __device__ __forceinline__ void wg_sum(const WeighArgs &A, const WgWs &W, WgShar
     int slot = -1;
     float before = 0.f, w = 0.f;
     if (!SEL && last && (NQ == 1 || side == 0)) {    // where the entry's weight is, asked for ahead of the sum
-      slot = reinterpret_cast<const int *>(sm + M::kSlot)[(k % M::kSlots) * kWgChunk + row];
+      slot = (int)wg_lds4(smu + M::kSlot + (uint32_t)((k % M::kSlots) * kWgChunk + row) * 4u);
       if (S.bad) slot = -1;                          // (a place left from before, once a wait has run out)
       if (slot >= 0 && A.prior != nullptr) before = A.prior[slot];
     }
     const int j = C.c * kWgChunk + row;
-    const float *f = reinterpret_cast<const float *>(sm + M::kMeta + (seen % kWgMetas) * NQ * kWgMeta) + (NQ == 2 ? side * 2 * kHeads : 0);
+    const uint32_t f = smu + M::kMeta + (uint32_t)((seen % kWgMetas) * NQ * kWgMeta + (NQ == 2 ? side * kWgMeta : 0));
     uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
     uint32_t a1[32];
     if (works) {
@@ -649,26 +674,27 @@ __device__ __forceinline__ void wg_sum(const WeighArgs &A, const WgWs &W, WgShar
       ptx::tmem_ld_32x32b_x32(ts + place * (64 * NQ), a0);
       ptx::tmem_wait_ld();
       ptx::tmem_ld_32x32b_x32(ts + place * (64 * NQ) + 32, a1);
-      wg_add_heads(a0, f, f + kHeads, sum);
+      wg_add_heads(a0, f, sum);
       ptx::tmem_wait_ld();
     }
     ptx::tc_fence_before();
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&S.s_free[place]);
     if (works) {
-      wg_add_heads(a1, f + 32, f + kHeads + 32, sum);
+      wg_add_heads(a1, f + 128u, sum);
       if (SEL || j < vis) w = wg_total(sum);
     }
     if (NQ == 2 && two) {
-      if (side == 1) part[(k & 1) * kWgChunk] = w;
+      const uint32_t at = part + (uint32_t)(k & 1) * (kWgChunk * 4u);
+      if (side == 1) wg_sts4(at, __float_as_uint(w));
       asm volatile("bar.sync %0, 64;" ::"r"(quarter + 1) : "memory");
-      if (side == 0) w += part[(k & 1) * kWgChunk];
+      if (side == 0) w += wg_ldsf(at);
     }
     if (NQ == 2 && side == 1) continue;
-    float *mine = acc + (C.c - C.lo) * kWgChunk;     // (of several groups)
-    if (C.g > 0) w += *mine;
+    const uint32_t mine = acc + (uint32_t)(C.c - C.lo) * (kWgChunk * 4u);        // (of several groups)
+    if (C.g > 0) w += wg_ldsf(mine);
     if (!last) {
-      *mine = w;
+      wg_sts4(mine, __float_as_uint(w));
     } else if (SEL) {
       if (j < A.sel_stride) W.part[(int64_t)C.b * A.sel_stride + j] = w;
     } else if (slot >= 0) {
