@@ -341,13 +341,76 @@ __device__ __forceinline__ void wg_wait(const WeighArgs &A, WgShared &S, uint64_
 __device__ __forceinline__ bool wg_bad(const WgShared &S) { return __any_sync(0xFFFFFFFFu, S.bad); }
 
 // ------------------------------------------------------------------ records and Q
-// Two warps take turns at the chunks (one took longer over a chunk than the MMAs): a lane finds the
-// records of four rows, and asks for the places of its next chunk's before it waits for a buffer.
+// Two warps take turns at the chunks (one took longer over a chunk than the MMAs).
+//
+// Where pages hold at least kWgScatter entries a lane has one of the (at most 17) pages that a chunk touches, asks
+// for its number a chunk ahead, and copies what the chunk has of it in one piece.
+template <int NQ>
+__device__ __forceinline__ void wg_fetch_runs(const WeighArgs &A, const WgWs &W, WgShared &S, unsigned char *sm, WgWalk<NQ> C, bool more, int turn) {
+  using M = WgSmem<NQ>;
+  static_assert((kWgChunk + kWgScatter - 2) / kWgScatter + 1 <= 32, "a lane a page");
+  const int lane = threadIdx.x & 31;
+  const uint32_t smu = ptx::smem_u32(sm);
+  int id = -1, first = 0, rows = 0, off = 0;           // of this lane's page: its first row of the chunk, rows, place of the first
+  int j0 = 0, col0 = 0, end = 0;                       // the chunk: its first entry, that one's page, the end of its entries
+  bool out = false;
+  auto ask = [&]() {
+    j0 = C.c * kWgChunk;
+    end = min(j0 + kWgChunk, C.I.x);
+    col0 = weigh_col(A, j0);
+    const int64_t at = (int64_t)(col0 + lane) * A.page;        // the page's first entry
+    const int from = (int)(at > j0 ? (at < end ? at : end) : j0), to = (int)(at + A.page < end ? at + A.page : end);
+    rows = max(to - from, 0);
+    first = from - j0;
+    off = (int)(from - at);
+    if (rows > 0) id = __ldg(A.table + (int64_t)C.b * A.table_stride + col0 + lane);
+  };
+  if (more && turn > 0) more = C.next(W);
+  if (more) ask();
+  int k = turn;
+#pragma unroll 1
+  for (; more; k += 2) {
+    const int stage = k % M::kStages;
+    const bool ok = rows > 0 && id >= 0 && id < A.n_pages, last = C.last_group();
+    out |= rows > 0 && !ok;
+    const int copied = (int)__reduce_add_sync(0xFFFFFFFFu, ok ? (uint32_t)rows : 0u);
+    const int page = ok ? id : -1, to = first, n = rows, at = off, j = j0, c0 = col0, j_end = end;
+    more = C.next(W);
+    if (more) more = C.next(W);
+    if (more) ask();
+    if (k >= M::kStages) wg_wait(A, S, &S.raw_free[stage], (uint32_t)(k / M::kStages - 1) & 1u);
+    if (wg_bad(S)) break;                            // no copy is started any more
+    if (last) {
+      // (its place was used kSlots products ago.  The buffer was freed by the rows of product k - kStages, which came after the
+      // MMAs of k - kStages - 2, which came after the sums of k - kStages - 2 - kSums had read theirs)
+      static_assert(M::kSlots >= M::kStages + 2 + M::kSums, "slots");
+      const uint32_t slot = smu + M::kSlot + (uint32_t)((k % M::kSlots) * kWgChunk + lane) * 4u;
+#pragma unroll
+      for (int g = 0; g < 4; g++) {
+        const int e = j + 32 * g + lane, c = e < j_end ? weigh_col(A, e) : c0;
+        const int has = __shfl_sync(0xFFFFFFFFu, page, c - c0);
+        const int rec = e < j_end && has >= 0 ? has * A.page + (e - c * A.page) : -1;
+        wg_sts4(slot + 128u * g, (uint32_t)rec);
+        if (A.prior != nullptr && rec >= 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(A.prior + rec));
+      }
+    }
+    uint64_t *full = &S.raw_full[stage];
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive_expect_tx(full, (uint32_t)(copied * kKvBytes));
+    __syncwarp();
+    if (page >= 0)
+      ptx::bulk_load(sm + M::kRaw + stage * kWgRaw + to * kKvBytes, A.pages + ((int64_t)page * A.page + at) * kKvBytes, (uint32_t)(n * kKvBytes), full);
+  }
+  if (out) record_error(A.status, CSA2_ERR_BOUNDS);
+  // its last copies have landed before the CTA may leave (bounded)
+  for (int i = k - 2; i >= 0 && i >= k - M::kStages; i -= 2) ptx::mbar_wait(&S.raw_full[i % M::kStages], (uint32_t)(i / M::kStages) & 1u);
+}
+
+// A selection, and pages of a few entries: a lane finds the records of four rows, and two lanes copy a record by 16 B.
 template <int NQ, bool SEL>
-__device__ __forceinline__ void wg_fetch(const WeighArgs &A, const WgWs &W, WgShared &S, unsigned char *sm, WgWalk<NQ> C, bool more, int turn) {
+__device__ __forceinline__ void wg_fetch_rows(const WeighArgs &A, const WgWs &W, WgShared &S, unsigned char *sm, WgWalk<NQ> C, bool more, int turn) {
   using M = WgSmem<NQ>;
   const int lane = threadIdx.x & 31;
-  const bool scattered = SEL || A.page < kWgScatter;
   const uint32_t smu = ptx::smem_u32(sm);
   int id[4], off[4];                                 // rows 32 g + lane: the page (-1: none), the place in it
   bool out = false;
@@ -389,19 +452,12 @@ __device__ __forceinline__ void wg_fetch(const WeighArgs &A, const WgWs &W, WgSh
 #pragma unroll 1
   for (; more; k += 2) {
     const int stage = k % M::kStages;
-    int rec[4], rows[4], all_rows = 0;               // the record, -1: none; rows of the run that this lane leads, 0: none
+    int rec[4];                                      // the record, -1: none
 #pragma unroll
     for (int g = 0; g < 4; g++) {
       const bool ok = id[g] >= 0 && id[g] < A.n_pages;
       out |= !ok && id[g] != -1;
-      const int here = ok ? id[g] : -1;
-      rec[g] = ok ? here * A.page + off[g] : -1;
-      const int pid = __shfl_up_sync(0xFFFFFFFFu, here, 1), poff = __shfl_up_sync(0xFFFFFFFFu, off[g], 1);
-      const bool leads = ok && (lane == 0 || pid != here || poff + 1 != off[g]);
-      const uint32_t valid = __ballot_sync(0xFFFFFFFFu, ok), lead = __ballot_sync(0xFFFFFFFFu, leads);
-      const uint32_t stop = (lead | ~valid) & ~((2u << lane) - 1u);        // (lane 31: 2 << 31 is 0)
-      rows[g] = leads ? (stop != 0u ? __ffs(stop) - 1 : 32) - lane : 0;
-      all_rows += __popc(valid);
+      rec[g] = ok ? id[g] * A.page + off[g] : -1;
     }
     const bool last = C.last_group();
     more = C.next(W);
@@ -409,39 +465,27 @@ __device__ __forceinline__ void wg_fetch(const WeighArgs &A, const WgWs &W, WgSh
     if (more) ask();
     if (k >= M::kStages) wg_wait(A, S, &S.raw_free[stage], (uint32_t)(k / M::kStages - 1) & 1u);
     if (wg_bad(S)) break;                            // no copy is started any more
-    if (!SEL && last) {
-      // (its place was used kSlots products ago.  The buffer was freed by the rows of product k - kStages, which came after the
-      // MMAs of k - kStages - 2, which came after the sums of k - kStages - 2 - kSums had read theirs)
-      static_assert(M::kSlots >= M::kStages + 2 + M::kSums, "slots");
+    if (!SEL && last) {                              // (as in wg_fetch_runs)
       const uint32_t slot = smu + M::kSlot + (uint32_t)((k % M::kSlots) * kWgChunk + lane) * 4u;
 #pragma unroll
-      for (int g = 0; g < 4; g++) {
-        wg_sts4(slot + 128u * g, (uint32_t)rec[g]);
-        if (A.prior != nullptr && rec[g] >= 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(A.prior + rec[g]));
-      }
+      for (int g = 0; g < 4; g++) wg_sts4(slot + 128u * g, (uint32_t)rec[g]);
     }
     uint64_t *full = &S.raw_full[stage];
     unsigned char *to = sm + M::kRaw + stage * kWgRaw;
-    if (scattered) {
 #pragma unroll
-      for (int g = 0; g < 8; g++) {                  // two lanes to a record, 16 records at a time
-        const int from = (g & 1) * 16 + (lane >> 1);
-        const int r = __shfl_sync(0xFFFFFFFFu, rec[g >> 1], from);
-        const uint8_t *src = A.pages + (int64_t)r * kKvBytes + (lane & 1) * 16;
-        unsigned char *dst = to + ((g >> 1) * 32 + from) * kKvBytes + (lane & 1) * 16;
-        if (r >= 0)
+    for (int g = 0; g < 8; g++) {                    // 16 records at a time
+      const int from = (g & 1) * 16 + (lane >> 1);
+      const int r = __shfl_sync(0xFFFFFFFFu, rec[g >> 1], from);
+      const uint8_t *src = A.pages + (int64_t)r * kKvBytes + (lane & 1) * 16;
+      unsigned char *dst = to + ((g >> 1) * 32 + from) * kKvBytes + (lane & 1) * 16;
+      if (r >= 0)
 #pragma unroll
-          for (int i = 0; i < kKvBytes; i += 32) ptx::cp_async16(dst + i, src + i);
-      }
-      ptx::cp_async_arrive(full);                    // (each lane's copies, pending from here on)
+        for (int i = 0; i < kKvBytes; i += 32) ptx::cp_async16(dst + i, src + i);
     }
+    ptx::cp_async_arrive(full);                      // (each lane's copies, pending from here on)
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive_expect_tx(full, scattered ? 0u : (uint32_t)(all_rows * kKvBytes));
+    if (lane == 0) ptx::mbar_arrive(full);
     __syncwarp();
-    if (!scattered)
-#pragma unroll
-      for (int g = 0; g < 4; g++)
-        if (rows[g] > 0) ptx::bulk_load(to + (32 * g + lane) * kKvBytes, A.pages + (int64_t)rec[g] * kKvBytes, (uint32_t)(rows[g] * kKvBytes), full);
   }
   if (out) record_error(A.status, CSA2_ERR_BOUNDS);
   // its last copies have landed before the CTA may leave (bounded)
@@ -798,7 +842,8 @@ __global__ void __launch_bounds__(kWgThreads, 1) weigh_kernel(const __grid_const
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWgRegsRest));
     const int role = warp - kWgSumWarps - kWgKWarps;
     if (role < 2) {
-      wg_fetch<NQ, SEL>(A, W, S, sm, C, more, role);
+      if (SEL || A.page < kWgScatter) wg_fetch_rows<NQ, SEL>(A, W, S, sm, C, more, role);
+      else wg_fetch_runs<NQ>(A, W, S, sm, C, more, role);
     } else if (role < 4) {
       if (ptx::elect_one()) wg_issue<NQ>(A, W, S, sm, C, more, role - 2, tmem);
     } else if (role == 4) {
