@@ -147,12 +147,36 @@ __device__ __forceinline__ void wg_sts4(uint32_t a, uint32_t v) { asm volatile("
 constexpr int kPrepThreads = 256, kPrepCtas = 8;     // CTAs of a query
 __device__ __forceinline__ float wg_power(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
+// What selections start from: decay prior, of every entry that a query of the sequence sees.
+__device__ __forceinline__ void weigh_decay(const WeighArgs &A, int b, int part, int parts) {
+  __shared__ int most_sh;
+  const int t = threadIdx.x;
+  int c0, c1, most = 0;
+  weigh_queries(A, b, c0, c1);
+  for (int q = c0 + t; q < c1; q += kPrepThreads) most = max(most, weigh_vis(A, q));
+  if (t == 0) most_sh = 0;
+  __syncthreads();
+  atomicMax(&most_sh, most);
+  __syncthreads();
+  most = most_sh;
+  for (int64_t j = (int64_t)part * kPrepThreads + t; j < most; j += (int64_t)parts * kPrepThreads) {
+    const int64_t s = weigh_slot(A, b, (int)j);
+    if (s >= 0) A.weight[s] = A.prior != nullptr ? A.decay * A.prior[s] : 0.f;
+  }
+}
+
 // The first CTA: the items and the products ahead of each.  Eight for each query behind it: its
-// heads' powers of two, f16 image and constants.
-__global__ void __launch_bounds__(kPrepThreads) weigh_prep_kernel(const __grid_constant__ WeighArgs A, WgWs W, int nq) {
+// heads' powers of two, f16 image and constants.  For selections, where the weights change by more than what is added:
+// decay_parts for each sequence behind those.
+__global__ void __launch_bounds__(kPrepThreads) weigh_prep_kernel(const __grid_constant__ WeighArgs A, WgWs W, int nq, int decay_parts) {
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   griddep_wait();
   griddep_launch();
+  const int64_t behind = (int64_t)blockIdx.x - 1 - (int64_t)A.n_q * kPrepCtas;
+  if (behind >= 0) {
+    weigh_decay(A, (int)(behind / decay_parts), (int)(behind % decay_parts), decay_parts);
+    return;
+  }
   if (blockIdx.x > 0) {
     const int q = ((int)blockIdx.x - 1) / kPrepCtas, part = ((int)blockIdx.x - 1) % kPrepCtas;
     if (A.sel != nullptr && part == 0 && t == 0) {
@@ -866,45 +890,35 @@ __global__ void __launch_bounds__(kWgThreads, 1) weigh_kernel(const __grid_const
 }
 
 // ------------------------------------------------------------------ selections
-// What selections start from: decay prior, of every entry that a query of the sequence sees.
-constexpr int kDecayThreads = 256;
-__global__ void __launch_bounds__(kDecayThreads) weigh_decay_kernel(const __grid_constant__ WeighArgs A) {
-  const int t = threadIdx.x, b = blockIdx.y;
-  griddep_wait();
-  griddep_launch();
-  int c0, c1, most = 0;
-  weigh_queries(A, b, c0, c1);
-  for (int q = c0 + t; q < c1; q += kDecayThreads) most = max(most, weigh_vis(A, q));
-  __shared__ int most_sh;
-  if (t == 0) most_sh = 0;
-  __syncthreads();
-  atomicMax(&most_sh, most);
-  __syncthreads();
-  most = most_sh;
-  for (int64_t j = (int64_t)blockIdx.x * kDecayThreads + t; j < most; j += (int64_t)gridDim.x * kDecayThreads) {
-    const int64_t s = weigh_slot(A, b, (int)j);
-    if (s >= 0) A.weight[s] = A.prior != nullptr ? A.decay * A.prior[s] : 0.f;
-  }
-}
-
 // Adds the selections' weights, a CTA per sequence, query by query: entries that several queries
 // selected get their parts in the queries' order, so the sums are the same on every call.  (Within
 // a query an entry named twice gets the same part twice: their order does not matter.)
+// Slots and parts of kAddAhead queries are read at a time.
+constexpr int kAddAhead = 8;
 __global__ void __launch_bounds__(kTopK) weigh_add_kernel(const __grid_constant__ WeighArgs A, const float *part) {
   const int t = threadIdx.x, b = blockIdx.x;
   griddep_wait();
   griddep_launch();
   int c0, c1;
   if (!weigh_queries(A, b, c0, c1) && t == 0) record_error(A.status, CSA2_ERR_BOUNDS);
-  for (int q = c0; q < c1; q++) {
-    if (t < A.sel_stride) {
-      const int j = __ldg(A.sel + (int64_t)q * A.sel_stride + t);
-      if (j >= 0 && j < weigh_vis(A, q)) {
-        const int64_t s = weigh_slot(A, b, j);
-        if (s >= 0) atomicAdd(A.weight + s, __ldg(part + (int64_t)q * A.sel_stride + t));
-      }
+  for (int q0 = c0; q0 < c1; q0 += kAddAhead) {
+    int j[kAddAhead];
+    int64_t s[kAddAhead];
+    float w[kAddAhead];
+#pragma unroll
+    for (int i = 0; i < kAddAhead; i++) j[i] = q0 + i < c1 && t < A.sel_stride ? __ldg(A.sel + (int64_t)(q0 + i) * A.sel_stride + t) : -1;
+#pragma unroll
+    for (int i = 0; i < kAddAhead; i++) {
+      const bool in = j[i] >= 0 && j[i] < weigh_vis(A, q0 + i);
+      s[i] = in ? weigh_slot(A, b, j[i]) : -1;
+      w[i] = in ? __ldg(part + (int64_t)(q0 + i) * A.sel_stride + t) : 0.f;
     }
-    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kAddAhead; i++) {
+      if (q0 + i >= c1) break;
+      if (s[i] >= 0) atomicAdd(A.weight + s[i], w[i]);
+      __syncthreads();
+    }
   }
 }
 
@@ -916,13 +930,14 @@ static void weigh_magic(unsigned n, uint64_t &mul, int &shift) {      // j / n, 
 }
 
 template <int NQ, bool SEL>
-static cudaError_t launch_products(const WeighArgs &A, const WgWs &W, int dev, cudaStream_t st) {
+static cudaError_t launch_products(const WeighArgs &A, const WgWs &W, int decay_parts, int dev, cudaStream_t st) {
   static std::atomic<int> attr_done[kMaxDevices];
   cudaError_t e = once_per_device(attr_done, dev, [&] {
     return cudaFuncSetAttribute(weigh_kernel<NQ, SEL>, cudaFuncAttributeMaxDynamicSharedMemorySize, WgSmem<NQ>::kAlloc);
   });
   if (e != cudaSuccess) return e;
-  e = launch_pdl(weigh_prep_kernel, dim3((unsigned)A.n_q * kPrepCtas + 1), dim3(kPrepThreads), 0, st, 1u, A, W, NQ);
+  const unsigned ctas = 1u + (unsigned)A.n_q * kPrepCtas + (unsigned)A.n_seq * (unsigned)decay_parts;
+  e = launch_pdl(weigh_prep_kernel, dim3(ctas), dim3(kPrepThreads), 0, st, 1u, A, W, NQ, decay_parts);
   if (e != cudaSuccess) return e;
   // no more CTAs than there can be chunks
   const int64_t sms = device_sm_count(dev), row = SEL ? A.sel_stride : A.table_stride * A.page;
@@ -936,14 +951,11 @@ cudaError_t launch_weigh(WeighArgs A, void *ws, cudaStream_t st) {
   WgWs W;
   wg_layout(&W, ws, A.n_q, A.n_seq, A.sel_stride);
   if (A.sel == nullptr)                              // two queries at a time where a sequence can have two
-    return A.n_q > A.n_seq ? launch_products<2, false>(A, W, dev, st) : launch_products<1, false>(A, W, dev, st);
-  cudaError_t e = cudaSuccess;
-  if (A.prior != A.weight || A.decay != 1.f) {
-    const int64_t tiles = (A.table_stride * A.page + 4 * kDecayThreads - 1) / (4 * kDecayThreads);
-    e = launch_pdl(weigh_decay_kernel, dim3((unsigned)(tiles < 512 ? tiles : 512), (unsigned)A.n_seq), dim3(kDecayThreads), 0, st, 1u, A);
-    if (e != cudaSuccess) return e;
-  }
-  e = launch_products<1, true>(A, W, dev, st);
+    return A.n_q > A.n_seq ? launch_products<2, false>(A, W, 0, dev, st) : launch_products<1, false>(A, W, 0, dev, st);
+  // a CTA for each 1,024 places of a row, up to 512
+  const int64_t tiles = (A.table_stride * A.page + 4 * kPrepThreads - 1) / (4 * kPrepThreads);
+  const int decay_parts = A.prior == A.weight && A.decay == 1.f ? 0 : (int)(tiles < 512 ? tiles : 512);
+  const cudaError_t e = launch_products<1, true>(A, W, decay_parts, dev, st);
   if (e != cudaSuccess) return e;
   return launch_pdl(weigh_add_kernel, dim3((unsigned)A.n_seq), dim3(kTopK), 0, st, 1u, A, (const float *)W.part);
 }
