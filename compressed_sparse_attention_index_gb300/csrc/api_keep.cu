@@ -12,6 +12,9 @@ namespace csa2 {
 static bool on(const void *p, size_t a) { return p != nullptr && ((uintptr_t)p % a) == 0; }
 static bool off_or_on(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
+// Entries of a row: the end of the last tile of 128 is counted in 32 bits.
+constexpr int64_t kRowMax = INT_MAX - 255;
+
 }  // namespace csa2
 
 using namespace csa2;
@@ -28,7 +31,7 @@ csa2_status csa2_attn_weight(const void *q, const void *pages, int n_pages, int 
     return CSA2_ERR_INVALID_ARG;
   if (sel != nullptr && (sel_stride < 1 || sel_stride > kTopK)) return CSA2_ERR_INVALID_ARG;
   if (n_q > 65535 || n_seq > kPlanMaxSeq || table_stride > INT_MAX || (int64_t)n_pages * page_size > INT_MAX ||
-      table_stride * page_size > INT_MAX)
+      table_stride * page_size > kRowMax)
     return CSA2_ERR_UNSUPPORTED;
   // work is counted in chunks of 128 entries and queries, in 32 bits
   const int64_t row = sel != nullptr ? sel_stride : table_stride * page_size;
@@ -76,7 +79,7 @@ csa2_status csa2_evict(const void *pages, const float *weight, int n_pages, int 
   if (in_place && (dst_weight != weight || n_dst_pages != n_pages || dst_stride != table_stride)) return CSA2_ERR_INVALID_ARG;
   if (n_seq > kPlanMaxSeq || table_stride > INT_MAX || dst_stride > INT_MAX ||
       (int64_t)n_pages * page_size > INT_MAX || (int64_t)n_dst_pages * page_size > INT_MAX ||
-      table_stride * page_size > INT_MAX || dst_stride * page_size > INT_MAX)
+      table_stride * page_size > kRowMax || dst_stride * page_size > kRowMax)
     return CSA2_ERR_UNSUPPORTED;
   if (n_seq == 0) return CSA2_OK;
   if (!on(pages, 32) || !on(weight, 16) || !on(block_table, 4) || !on(seq_len, 4) || !on(keep, 4) ||

@@ -14,6 +14,7 @@
 // (an entry never moves behind its place, so ranks are not above places): tiles are handed out in order, each
 // raises a flag when it has read, and before it writes waits for the at most two tiles that its places'
 // entries belong to.  A tile that is waited for has been handed out, and reads without waiting for any.
+// The places behind the kept entries are tiles too, behind a sequence's others: their weights are cleared in the same way.
 //
 // What bounds it: 288 B read and written for each entry that stays (HBM).
 #include <limits.h>
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
   k = min(n, k);
   if (t == 0 && rank == 0) {
     // (a sequence that is out of range keeps its length and moves nothing)
-    W.meta[b] = make_int4(n, k, bad ? n : k, 0);
+    W.meta[b] = make_int4(bad ? 0 : n, k, bad ? n : k, 0);
     if (b == 0) *W.ticket = 0u;
   }
   const int last = min(A.recent, k), m = n - last, kk = k - last;        // candidates, those of them that stay
@@ -438,9 +439,12 @@ __global__ void __launch_bounds__(kMvThreads, 4) evict_move_kernel(const __grid_
     }
     // (every warp finds the sequence for itself)
     int b = -1, i = 0, k = 0, n = 0;
+    // tiles of k kept entries, and of the places behind them
+    auto moved = [](int k) { return (k + kMvTile - 1) / kMvTile; };
+    auto cleared = [&](int n, int k) { return A.in_place && k < n ? (n - 1) / kMvTile - k / kMvTile + 1 : 0; };
     while (b0 < A.n_seq) {
       const int4 M = b0 + lane < A.n_seq ? W.meta[b0 + lane] : make_int4(0, 0, 0, 0);
-      const int own = (M.y + kMvTile - 1) / kMvTile;
+      const int own = moved(M.y) + cleared(M.x, M.y);
       int64_t inc = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -460,8 +464,34 @@ __global__ void __launch_bounds__(kMvThreads, 4) evict_move_kernel(const __grid_
       b0 += 32;
     }
     if (b < 0) return;                               // (no tile is left: the whole CTA)
-    const int r0 = i * kMvTile, rows = min(kMvTile, k - r0);
     const int32_t *table = A.table + (int64_t)b * A.table_stride, *dst_table = A.dst_table + (int64_t)b * A.dst_stride;
+    uint32_t *flag = W.flag + (int64_t)b * W.tile_stride;
+    // waits until the entries at the places of tile p are read: those have ranks [lo, hi), of one tile or two, and none of a
+    // tile behind this one
+    auto wait_read = [&](int p, int self) {
+      const int32_t *before = W.before + (int64_t)b * W.tile_stride;
+      const int lo = __ldcg(before + p), hi = __ldcg(before + p + 1);
+      for (int x = lo / kMvTile; lo < hi && x <= (hi - 1) / kMvTile; x++)
+        if (x != self && !ptx::poll_at_least_u32(flag + x, 1u)) {
+          record_error(A.status, CSA2_ERR_TIMEOUT);
+          break;
+        }
+      __threadfence();
+    };
+    if (i >= moved(k)) {                             // places that nothing is at any more
+      const int p = k / kMvTile + (i - moved(k)), j = p * kMvTile + t;
+      if (k > 0) {
+        if (t == 0) wait_read(p, -1);
+        __syncthreads();
+      }
+      if (t < kMvTile && j >= k && j < n) {
+        const int c = (int)(((uint64_t)(unsigned)j * A.page_mul) >> A.page_shift), id = __ldg(table + c);
+        if (id >= 0 && id < A.n_pages) A.dst_weight[(int64_t)id * A.page + (j - c * A.page)] = 0.f;
+      }
+      __syncthreads();
+      continue;
+    }
+    const int r0 = i * kMvTile, rows = min(kMvTile, k - r0);
     bool there = true;                               // the entry is where it goes
     if (t < rows) {
       const int j = __ldg(W.from + (int64_t)b * W.from_stride + r0 + t), r = r0 + t;
@@ -474,7 +504,6 @@ __global__ void __launch_bounds__(kMvThreads, 4) evict_move_kernel(const __grid_
       dst_sh[t] = ok ? (int64_t)pd * A.page + (r - cd * A.page) : -1;
     }
     const bool still = __syncthreads_and(there) != 0;
-    uint32_t *flag = W.flag + (int64_t)b * W.tile_stride;
     if (still) {
       if (A.in_place && t == 0) ptx::st_release_u32(flag + i, 1u);
       __syncthreads();
@@ -495,15 +524,7 @@ __global__ void __launch_bounds__(kMvThreads, 4) evict_move_kernel(const __grid_
       __syncthreads();                               // (all of the tile is read)
       if (t == 0) {
         ptx::st_release_u32(flag + i, 1u);
-        // the entries at places r0 .. r0 + 127 (those below n) have ranks [lo, hi): one tile or two, none behind this one
-        const int32_t *before = W.before + (int64_t)b * W.tile_stride;
-        const int lo = __ldcg(before + i), hi = r0 + kMvTile <= n ? __ldcg(before + i + 1) : k;
-        for (int x = lo / kMvTile; x <= (hi - 1) / kMvTile && lo < hi; x++)
-          if (x != i && !ptx::poll_at_least_u32(flag + x, 1u)) {
-            record_error(A.status, CSA2_ERR_TIMEOUT);
-            break;
-          }
-        __threadfence();
+        wait_read(i, i);
       }
       __syncthreads();
     }
@@ -551,7 +572,7 @@ cudaError_t launch_evict(EvictArgs A, void *ws, cudaStream_t st) {
   // no more CTAs than there can be tiles, and many more than run at a time: SMs differ in speed (8 x 1M entries cut to
   // half: 720 us with four CTAs an SM that take equal shares)
   const int64_t dst_row = A.dst_stride * A.page, most = dst_row < row ? dst_row : row;
-  const int64_t tiles = A.n_seq * ((most + kMvTile - 1) / kMvTile), grid = tiles < 64 * sms ? tiles : 64 * sms;
+  const int64_t tiles = A.n_seq * ((most + kMvTile - 1) / kMvTile + (A.in_place ? 1 : 0)), grid = tiles < 64 * sms ? tiles : 64 * sms;
   return launch_pdl(evict_move_kernel, dim3((unsigned)grid), dim3(kMvThreads), 0, st, 1u, A, W);
 }
 

@@ -9,8 +9,10 @@
   lightning-indexer note: decoder Reindex layers score only a 16,384-position
   pool picked earlier as blocks of 8; perchy.ai/models/deepseek, card "Full.
   Reindex. Reuse.": the pool feeds the top-512 that attention reads.)
-* Paged cache (PagedCache): csa2_page_plan -> csa2_qk_norm_rope, which writes the
-  new latents -> csa2_paged_attn, over every visible entry or a selection.
+* Paged cache (PagedCache): csa2_page_plan_at -> csa2_qk_norm_rope, which writes the
+  new latents -> csa2_paged_attn, over every visible entry or a selection; and what
+  the cache keeps: csa2_verify_drafts and csa2_page_trim for drafted tokens,
+  csa2_attn_weight and csa2_evict for its entries.
 """
 from __future__ import annotations
 
@@ -178,16 +180,27 @@ class PagedCache:
     ring is sure to hold (swa_cap - 127), a sequence whose new tokens would overwrite
     their own windows gets none, which is reported as CSA2_ERR_BOUNDS; finding them takes
     four small launches more.
-    max_tokens is at most 65,535.  Pages are taken and not returned: what ends a
-    sequence, and gives its pages to others, is the caller's."""
+    max_tokens is at most 65,535.  What ends a sequence, and gives its pages to others, is the caller's.
+
+    Drafts: verify says which of a step's tokens the target model's probabilities
+    accept, and accept, in advance's place, makes those part of their sequences and
+    gives the pages of the others back.
+
+    Eviction: a cache of `voters` keeps the attention weight that each entry has got
+    (weight, by slot); weigh, behind advance or accept, adds that of a step of up to `voters`
+    rows, and evict, between steps, cuts sequences down to their heaviest and latest entries
+    and gives pages back.  An entry's place changes then, its position does not: a
+    sequence's next position is seq_len + gone."""
 
     def __init__(self, n_seq: int, n_pages: int, page_size: int, max_len: int, max_tokens: int, swa_cap: int = None,
-                 out_dtype=L.CSA2_OUT_BF16, device="cuda"):
+                 out_dtype=L.CSA2_OUT_BF16, device="cuda", voters: int = 0):
         self.n_seq, self.n_pages, self.page_size, self.max_tokens = n_seq, n_pages, page_size, max_tokens
         swa_cap = SWA - 1 + max_tokens if swa_cap is None else swa_cap
         if not 1 <= max_tokens <= 65535 or swa_cap < 0 or n_seq * swa_cap >= 2**31:
             raise ValueError(f"max_tokens 1 .. 65535 and n_seq x swa_cap below 2^31 expected, not {max_tokens}, {n_seq} x {swa_cap}")
-        self.swa_cap, self.out_dtype = swa_cap, out_dtype
+        if not 0 <= voters <= max_tokens:
+            raise ValueError(f"voters: 0 .. {max_tokens} expected, not {voters}")
+        self.swa_cap, self.out_dtype, self.voters = swa_cap, out_dtype, voters
         i32 = dict(dtype=torch.int32, device=device)
         self.pages = torch.zeros((n_pages, page_size, 288), dtype=torch.uint8, device=device)
         self.swa = torch.zeros((n_seq, swa_cap, 528), dtype=torch.uint8, device=device)
@@ -214,6 +227,20 @@ class PagedCache:
         self.lse = torch.empty((max_tokens, 64), dtype=torch.float32, device=device)
         self.ws = torch.empty(L.csa2_workspace_size(L.CSA2_OP_PAGED_ATTN, max_tokens, 0), dtype=torch.uint8,
                               device=device)
+        # what evictions took from the sequences, and the weights and workspaces that they need
+        self.gone = torch.zeros(n_seq, **i32)
+        self._lens = torch.zeros((3, n_seq), **i32)
+        self._rows_at = torch.arange(max_tokens, **i32)
+        self._limit = (torch.zeros(max_tokens, **i32), torch.zeros(max_tokens, dtype=torch.bool, device=device))
+        self.kept, self.next = torch.zeros(n_seq, **i32), torch.full((n_seq,), -1, **i32)
+        self._open, self._weighable = False, False        # a planned step is not advanced yet; the last one may be weighed
+        self.weight = None
+        u8 = dict(dtype=torch.uint8, device=device)
+        self._ws_verify = torch.empty(max(1, L.csa2_workspace_size(L.CSA2_OP_VERIFY, max_tokens, 0)), **u8)
+        if voters > 0:
+            self.weight = torch.zeros(n_pages * page_size, dtype=torch.float32, device=device)
+            self._ws_weigh = torch.empty(L.csa2_workspace_size(L.CSA2_OP_ATTN_WEIGHT, voters, n_seq, TOPK), **u8)
+            self._ws_evict = torch.empty(L.csa2_workspace_size(L.CSA2_OP_EVICT, n_seq, self.table.shape[1] * page_size), **u8)
         # the fills above ran on the current stream, the steps may run on any
         if self.pages.is_cuda and not torch.cuda.is_current_stream_capturing():
             torch.cuda.current_stream(self.pages.device).synchronize()
@@ -258,18 +285,22 @@ class PagedCache:
         if 0 < self.swa_cap < min(SWA, self.swa_cap) - 1 + rows:
             new_len = self._that_fit(new_len, stream)
         self._use_rows(rows)
-        L.csa2_page_plan(self.seq_len, new_len, self.n_seq, self.page_size, self.n_pages, self.free, self.n_pages,
-                         self.free_head, self.table, self.table.shape[1], self.swa_cap, self.desc, rows, self.first,
-                         self.totals, stream)
+        L.csa2_page_plan_at(self.seq_len, new_len, self.gone, self.n_seq, self.page_size, self.n_pages, self.free,
+                            self.n_pages, self.free_head, self.table, self.table.shape[1], self.swa_cap, self.desc,
+                            rows, self.first, self.totals, stream)
+        self._open, self._weighable = True, False
 
     def _that_fit(self, new_len, stream):
         """new_len, and -1, which the plan reports and gives no tokens, where the ring does not hold the records of the
-        new tokens beside the first one's window, which reaches back to min(window - 1, seq_len) positions before it."""
+        new tokens beside the first one's window, which reaches back to min(window - 1, its position) positions before it."""
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self._that_fit(new_len, None)
         room, over, fit, none, cap = self._fit
-        torch.clamp(self.seq_len, 0, min(SWA, self.swa_cap) - 1, out=room)
+        ahead = self.seq_len
+        if self.weight is not None:
+            ahead = torch.add(ahead, self.gone, out=room)
+        torch.clamp(ahead, 0, min(SWA, self.swa_cap) - 1, out=room)
         torch.sub(cap, room, out=room)
         torch.gt(new_len, room, out=over)
         return torch.where(over, none, new_len, out=fit)
@@ -322,6 +353,107 @@ class PagedCache:
             first.copy_(self._d[5])
         torch.ge(counted, 0, out=added)
         self._state.index_add_(0, place, add)
+        self._open, self._weighable = False, True
+
+    def verify(self, tokens, target, draft=None, u=None, v=None, greedy=False, stream=None):
+        """(kept, next), device int32 [n_seq]: how many of each sequence's planned tokens stay, and the token that follows.
+        tokens (int32 [rows]): a sequence's last sampled token, then its drafts; target ([rows][vocab], fp32, bf16 or fp16): the
+        target model's probabilities of the token after each (logits will do where greedy); draft, of the same type: those that
+        the next row's token was drawn from (None: it was not drawn); u (fp32 [rows]), v (fp32 [n_seq]): random numbers in [0, 1)."""
+        self._here()
+        self._want("tokens", tokens, self.rows, 1, torch.int32)
+        kind = {torch.float32: L.CSA2_PROB_F32, torch.bfloat16: L.CSA2_PROB_BF16, torch.float16: L.CSA2_PROB_F16}.get(target.dtype)
+        if kind is None or target.dim() != 2 or not tokens.is_contiguous():
+            raise ValueError("verify: contiguous int32 tokens and [rows][vocab] fp32, bf16 or fp16 probabilities expected")
+        vocab = target.shape[1]
+        self._want("target", target, self.rows, vocab, target.dtype)
+        if draft is not None:
+            self._want("draft", draft, self.rows, vocab, target.dtype)
+        if greedy and draft is not None:
+            raise ValueError("verify: draft probabilities have no part in greedy decoding")
+        if not greedy:
+            for name, x, n in (("u", u, self.rows), ("v", v, self.n_seq)):
+                if x is None or not x.is_contiguous():
+                    raise ValueError(f"{name}: contiguous fp32 expected")
+                self._want(name, x, n, 1, torch.float32)
+        stride = lambda x: 0 if x is None else x.stride(0) if self.rows > 1 else vocab
+        L.csa2_verify_drafts(L.CSA2_VERIFY_GREEDY if greedy else L.CSA2_VERIFY_SAMPLE, target, stride(target), draft, stride(draft),
+                             kind, vocab, tokens, self.first, self.n_seq, self.rows, u, v, self.kept, self.next, self._ws_verify,
+                             self._ws_verify.numel(), stream)
+        return self.kept, self.next
+
+    def accept(self, kept=None, stream=None):
+        """In advance's place: of the tokens that were written the first kept[b] (device int32 [n_seq]; verify's, by default)
+        become part of sequence b; the pages of the others go back, and weigh passes their queries over."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.accept(kept)
+        self._here()
+        kept = self.kept if kept is None else kept
+        if not kept.is_contiguous():
+            raise ValueError("kept: contiguous int32 expected")
+        self._want("kept", kept, self.n_seq, 1, torch.int32)
+        old, to, stays = self._lens.unbind()
+        old.copy_(self.seq_len)
+        self.advance()
+        torch.clamp(kept, min=0, out=stays)
+        torch.add(old, stays, out=to)
+        torch.minimum(to, self.seq_len, out=to)
+        self._trim(to)
+        # queries of tokens that did not stay see nothing any more
+        limit, gone = self._limit[0][:self.rows], self._limit[1][:self.rows]
+        torch.add(self.first[:self.n_seq], stays, out=stays)
+        torch.index_select(stays, 0, self._count[1], out=limit)        # (the tokens' sequences, as advance left them)
+        torch.ge(self._rows_at[:self.rows], limit, out=gone)
+        self._d[1].masked_fill_(gone, 0)
+
+    def _trim(self, to):
+        """The sequences end at `to` entries: the pages behind go back to the free list."""
+        L.csa2_page_trim(self.seq_len, to, self.n_seq, self.page_size, self.n_pages, self.free, self.n_pages, self.free_head,
+                         self.table, self.table.shape[1])
+        self.seq_len.copy_(to)
+
+    def _keeps_weights(self):
+        self._here()
+        if self.weight is None:
+            raise ValueError("the cache keeps no weights: voters expected")
+        if self._open:
+            raise ValueError("a step is not over: advance or accept first")
+
+    def weigh(self, sel=None, decay=1.0, params=None, stream=None):
+        """weight = decay x weight + what the last step's queries gave (over sel, where they attended to it), of the
+        entries that its sequences see; behind advance or accept, once."""
+        self._keeps_weights()
+        if not self._weighable:
+            raise ValueError("no step since the last eviction")
+        if self.rows > self.voters:
+            raise ValueError(f"a step of up to {self.voters} rows expected, not {self.rows}")
+        if sel is not None:
+            if not sel.is_contiguous():
+                raise ValueError("sel: contiguous int32 expected")
+            self._want("sel", sel, self.rows, sel.shape[1], torch.int32)
+        L.csa2_attn_weight(self.q, self.pages, self.n_pages, self.page_size, self.table, self.table.shape[1], self.first,
+                           self.n_seq, sel, 0 if sel is None else sel.shape[1], self._d[1], self.lse, self.rows, decay,
+                           self.weight, self.weight, params, self._ws_weigh, self._ws_weigh.numel(), stream)
+
+    def evict(self, keep, recent=SWA, stream=None):
+        """Cuts sequence b down to keep[b] (device int32 [n_seq]) entries: its last `recent`, and the heaviest of the others;
+        entries of the last step's descriptors are elsewhere afterwards."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.evict(keep, recent)
+        self._keeps_weights()
+        if not keep.is_contiguous():
+            raise ValueError("keep: contiguous int32 expected")
+        self._want("keep", keep, self.n_seq, 1, torch.int32)
+        left, to, _ = self._lens.unbind()
+        L.csa2_evict(self.pages, self.weight, self.n_pages, self.page_size, self.table, self.table.shape[1], self.seq_len, keep,
+                     self.n_seq, recent, self.pages, self.weight, self.n_pages, self.table, self.table.shape[1], to, None, 0,
+                     self._ws_evict, self._ws_evict.numel())
+        torch.sub(self.seq_len, to, out=left)
+        self.gone.add_(left)
+        self._trim(to)
+        self._weighable = False
 
     def step(self, new_len, q, latent, q_gain=None, latent_gain=None, eps=1e-6, sel=None, params=None, stream=None):
         """plan, write, attend and advance on as many rows as q and latent have."""

@@ -649,7 +649,8 @@ csa2_status csa2_page_plan_at(const int32_t *seq_len, const int32_t *new_len, co
  *                sequence is skipped.  A sequence without queries is left as it is.
  *   sel          NULL, or (device) int32 [n_q][sel_stride], as csa2_paged_attn's: a
  *                query sees the entries sel[q] only; one named twice counts twice.
- *                decay still takes all entries below the largest n_vis.
+ *                decay still takes all entries below the largest n_vis.  (An entry
+ *                without a page is recorded where it is selected.)
  *   n_vis        (device) int32 [n_q]; outside [0, table_stride * page_size]:
  *                recorded, the query adds nothing.
  *   lse          (device) fp32 [n_q][64].
@@ -658,9 +659,10 @@ csa2_status csa2_page_plan_at(const int32_t *seq_len, const int32_t *new_len, co
  *   weight       (device) fp32 [n_pages * page_size].  Slots of other entries are
  *                left as they are.
  *   workspace    (device) >= csa2_workspace_size(CSA2_OP_ATTN_WEIGHT, n_q, n_seq,
- *                sel_stride or 0) bytes, 256-B aligned; no initialisation.
- *   Limits: n_q <= 65535; n_seq <= 16384; n_pages * page_size and table_stride *
- *   page_size below 2^31; n_q * (row / 128 + 1) up to 2^30, row = sel_stride or table_stride * page_size.
+ *                sel_stride or 0) bytes, 256-B aligned; no initialisation.  Calls
+ *                that may run at the same time need one each.
+ *   Limits: n_q <= 65535; n_seq <= 16384; n_pages * page_size below 2^31, table_stride *
+ *   page_size up to 2^31 - 256; n_q * (row / 128 + 1) up to 2^30, row = sel_stride or table_stride * page_size.
  */
 csa2_status csa2_attn_weight(const void *q, const void *pages, int n_pages, int page_size, const int32_t *block_table,
                              int64_t table_stride, const int32_t *first, int n_seq, const int32_t *sel, int sel_stride,
@@ -674,7 +676,7 @@ csa2_status csa2_attn_weight(const void *q, const void *pages, int n_pages, int 
  * and of the others those of largest weight (of equal ones those at the lowest
  * places; -0 equals 0; NaN is lighter than everything).  They keep their order, and
  * their records and weights go to places 0 .. k - 1 of row b of the destination.
- * Records and weights of no other slot are written.
+ * In place, the weights of the places behind become 0.  Nothing else is written.
  *
  *   pages .. table_stride, seq_len   the paged cache; weight (device) fp32
  *                [n_pages * page_size] by slot, 16-B aligned.  An entry on a column
@@ -695,8 +697,9 @@ csa2_status csa2_attn_weight(const void *q, const void *pages, int n_pages, int 
  *   kept entries than the destination or from can: CSA2_ERR_BOUNDS is recorded,
  *   nothing of the sequence moves, and new_len is seq_len in place, else 0.
  *   workspace    (device) >= csa2_workspace_size(CSA2_OP_EVICT, n_seq, table_stride
- *                * page_size, 0) bytes, 256-B aligned; no initialisation.
- *   Limits: n_seq <= 16384; pages and rows of fewer than 2^31 entries.
+ *                * page_size, 0) bytes, 256-B aligned; no initialisation.  Calls
+ *                that may run at the same time need one each.
+ *   Limits: n_seq <= 16384; caches of fewer than 2^31 entries, rows of up to 2^31 - 256.
  */
 csa2_status csa2_evict(const void *pages, const float *weight, int n_pages, int page_size, const int32_t *block_table,
                        int64_t table_stride, const int32_t *seq_len, const int32_t *keep, int n_seq, int recent,
@@ -753,7 +756,8 @@ csa2_status csa2_page_trim(const int32_t *len, const int32_t *new_len, int n_seq
  *   next         (device) int32 [n_seq]; -1 for a sequence without rows, and, recorded,
  *                where target[r] has no entry above zero (GREEDY: nothing but NaN).
  *   workspace    GREEDY: (device) >= csa2_workspace_size(CSA2_OP_VERIFY, n_rows, 0, 0)
- *                bytes, 256-B aligned; no initialisation.  SAMPLE: NULL will do.
+ *                bytes, 256-B aligned; no initialisation.  Calls that may run at the
+ *                same time need one each.  SAMPLE: NULL will do.
  *   Limits: n_seq <= 16384; n_rows <= 65535; vocab <= 2^28.
  */
 csa2_status csa2_verify_drafts(int mode, const void *target, int64_t target_stride, const void *draft,

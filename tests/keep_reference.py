@@ -88,6 +88,10 @@ def evict(pages, weight, page, table, seq_len, keep, recent, dst_pages, dst_weig
             fine &= to >= 0
             if to >= 0 and src[j] >= 0:
                 dst[to], w_out[to] = flat[src[j]], weight[src[j]]
+        if in_place:
+            for j in range(k, n):
+                if src[j] >= 0:
+                    w_out[src[j]] = 0.0
         new_len.append(k)
         source.append(stay)
     return out, w_out, np.array(new_len), source, fine

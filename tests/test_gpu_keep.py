@@ -226,6 +226,32 @@ def test_weights_far_in_a_large_cache(lib, oracle_lib):
     assert np.array_equal(pages[n_pages - 1, :100].cpu().numpy(), rec[stay])
 
 
+def test_weights_far_in_a_long_row(lib, oracle_lib):
+    """A row of nearly 2^31 places, most of them without a page; selected entries at its end, and one behind it."""
+    page = 1 << 20
+    stride = (2**31 - 256) // page
+    n = stride * page
+    table = np.full((1, stride), -1)
+    table[0, -1] = 1
+    pages = torch.zeros((2, page, 288), dtype=torch.uint8, device="cuda")
+    rec = _records(oracle_lib, 300, 5)
+    pages[1, page - 300:] = torch.from_numpy(rec).cuda()
+    w = torch.full((2 * page,), -7.0, device="cuda")
+    q = G.normal_block_bf16(3, G.S_Q, 5, 0, 64, 512).reshape(1, 64, 512)
+    lse = np.full((1, 64), 3.0, np.float32)
+    ws = torch.empty(lib.csa2_workspace_size(lib.CSA2_OP_ATTN_WEIGHT, 1, 1, 5), dtype=torch.uint8, device="cuda")
+    lib.csa2_attn_weight(_bf16(q), pages, 2, page, _i32(table), stride, _i32([0, 1]), 1, _i32([[n - 1, n - 2, n - 300, n, -1]]), 5,
+                         _i32([n]), _f32(lse), 1, 1.0, w, w, None, ws, ws.numel())
+    assert lib.csa2_get_device_status() == BOUNDS
+    k = R.kv_values(rec[[299, 298, 0]])
+    x = 512 ** -0.5 * (k @ R.bf16_values(q)[0].astype(np.float64).T) - 3.0
+    got = w.cpu().numpy()
+    at = page + np.array([page - 1, page - 2, page - 300])
+    # fp32 sums of 512 products of magnitudes that add up to about 15 (2^-14 of them), and the sum with -7
+    assert np.all(np.abs(got[at] + 7.0 - np.exp(x).sum(1)) <= 2.0**-9 * np.exp(x).sum(1) + 2.0**-20)
+    assert np.count_nonzero(got != -7.0) == 3
+
+
 # ------------------------------------------------------------------ eviction
 def _evict(lib, seed, lens, keep, recent, page, in_place, weights="random", want_from=True, spoil=None):
     r = np.random.default_rng(seed)

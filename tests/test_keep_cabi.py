@@ -29,7 +29,7 @@ def _weigh(L, **kw):
     (dict(stride=0), INVALID), (dict(decay=NAN), INVALID), (dict(decay=INF), INVALID), (dict(sel=FAKE, sel_stride=0), INVALID),
     (dict(sel=FAKE, sel_stride=513), INVALID), (dict(n_q=65536), UNSUP), (dict(n_seq=16385), UNSUP),
     (dict(stride=1 << 31), UNSUP), (dict(n_pages=1 << 26), UNSUP), (dict(stride=1 << 26), UNSUP),
-    (dict(n_q=60000, stride=1 << 20), UNSUP), (dict(q=FAKE + 8), INVALID), (dict(pages=FAKE + 16), INVALID),
+    (dict(page=1, stride=2**31 - 255, n_q=1), UNSUP), (dict(page=1, stride=2**31 - 256, n_q=1, q=None), INVALID), (dict(n_q=60000, stride=1 << 20), UNSUP), (dict(q=FAKE + 8), INVALID), (dict(pages=FAKE + 16), INVALID),
     (dict(table=None), INVALID), (dict(first=None), INVALID), (dict(n_vis=None), INVALID), (dict(lse=FAKE + 2), INVALID),
     (dict(prior=FAKE + 1), INVALID), (dict(weight=None), INVALID), (dict(ws=None), WS), (dict(ws=FAKE + 128), WS),
     (dict(ws_bytes=0), WS), (dict(n_q=0, q=None), 0), (dict(n_seq=0, first=None), 0)])
@@ -52,6 +52,7 @@ HERE = dict(dst=FAKE, dst_weight=FAKE, n_dst=100, dst_table=FAKE, dst_stride=8)
     (dict(n_seq=-1), INVALID), (dict(n_pages=0), INVALID), (dict(page=0), INVALID), (dict(stride=0), INVALID),
     (dict(recent=-1), INVALID), (dict(n_dst=0), INVALID), (dict(dst_stride=0), INVALID), (dict(from_=FAKE), INVALID),
     (dict(n_seq=16385), UNSUP), (dict(stride=1 << 26), UNSUP), (dict(dst_stride=1 << 26), UNSUP),
+    (dict(page=1, stride=2**31 - 255), UNSUP), (dict(page=1, dst_stride=2**31 - 255), UNSUP),
     (dict(n_pages=1 << 26), UNSUP), (dict(n_dst=1 << 26), UNSUP), (dict(pages=FAKE + 16), INVALID),
     (dict(dst=FAKE + 16), INVALID), (dict(weight=FAKE + 4), INVALID), (dict(dst_weight=FAKE + 2), INVALID),
     (dict(table=None), INVALID), (dict(dst_table=None), INVALID), (dict(seq_len=None), INVALID), (dict(keep=None), INVALID),
