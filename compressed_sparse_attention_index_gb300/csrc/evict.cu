@@ -29,6 +29,7 @@ constexpr int kEvThreads = 1024, kEvWarps = kEvThreads / 32, kEvBits = 11, kEvBi
 constexpr int kEvMaxCtas = 16;
 constexpr int kEvKeyTiles = 12;                     // tiles of a warp's part whose keys fit shared memory (192 KB)
 constexpr int kMvTile = 128, kMvThreads = 288, kMvUnits = 8;     // a record is 18 units of 16 B
+constexpr int kMvClear = 16;                        // tiles of places that are cleared at a time
 static_assert(kMvThreads / 18 * kMvUnits == kMvTile, "a tile's units");
 
 // ------------------------------------------------------------------ workspace
@@ -439,9 +440,9 @@ __global__ void __launch_bounds__(kMvThreads, 4) evict_move_kernel(const __grid_
     }
     // (every warp finds the sequence for itself)
     int b = -1, i = 0, k = 0, n = 0;
-    // tiles of k kept entries, and of the places behind them
+    // tiles of k kept entries, and kMvClear at a time of the places behind them
     auto moved = [](int k) { return (k + kMvTile - 1) / kMvTile; };
-    auto cleared = [&](int n, int k) { return A.in_place && k < n ? (n - 1) / kMvTile - k / kMvTile + 1 : 0; };
+    auto cleared = [&](int n, int k) { return A.in_place && k < n ? ((n - 1) / kMvTile - k / kMvTile + kMvClear) / kMvClear : 0; };
     while (b0 < A.n_seq) {
       const int4 M = b0 + lane < A.n_seq ? W.meta[b0 + lane] : make_int4(0, 0, 0, 0);
       const int own = moved(M.y) + cleared(M.x, M.y);
@@ -466,12 +467,12 @@ __global__ void __launch_bounds__(kMvThreads, 4) evict_move_kernel(const __grid_
     if (b < 0) return;                               // (no tile is left: the whole CTA)
     const int32_t *table = A.table + (int64_t)b * A.table_stride, *dst_table = A.dst_table + (int64_t)b * A.dst_stride;
     uint32_t *flag = W.flag + (int64_t)b * W.tile_stride;
-    // waits until the entries at the places of tile p are read: those have ranks [lo, hi), of one tile or two, and none of a
-    // tile behind this one
-    auto wait_read = [&](int p, int self) {
+    // waits, the x-th tile for x = t, t + step, .., until the entries at the places of tiles [p0, p1) are read: those have
+    // consecutive ranks, and none is of a tile behind this one (`self`)
+    auto wait_read = [&](int p0, int p1, int self, int from, int step) {
       const int32_t *before = W.before + (int64_t)b * W.tile_stride;
-      const int lo = __ldcg(before + p), hi = __ldcg(before + p + 1);
-      for (int x = lo / kMvTile; lo < hi && x <= (hi - 1) / kMvTile; x++)
+      const int lo = __ldcg(before + p0), hi = __ldcg(before + p1);
+      for (int x = lo / kMvTile + from; lo < hi && x <= (hi - 1) / kMvTile; x += step)
         if (x != self && !ptx::poll_at_least_u32(flag + x, 1u)) {
           record_error(A.status, CSA2_ERR_TIMEOUT);
           break;
@@ -479,12 +480,12 @@ __global__ void __launch_bounds__(kMvThreads, 4) evict_move_kernel(const __grid_
       __threadfence();
     };
     if (i >= moved(k)) {                             // places that nothing is at any more
-      const int p = k / kMvTile + (i - moved(k)), j = p * kMvTile + t;
+      const int p0 = k / kMvTile + (i - moved(k)) * kMvClear, p1 = min(p0 + kMvClear, (n - 1) / kMvTile + 1);
       if (k > 0) {
-        if (t == 0) wait_read(p, -1);
+        wait_read(p0, p1, -1, t, kMvThreads);
         __syncthreads();
       }
-      if (t < kMvTile && j >= k && j < n) {
+      for (int j = max(k, p0 * kMvTile) + t; j < min(n, p1 * kMvTile); j += kMvThreads) {
         const int c = (int)(((uint64_t)(unsigned)j * A.page_mul) >> A.page_shift), id = __ldg(table + c);
         if (id >= 0 && id < A.n_pages) A.dst_weight[(int64_t)id * A.page + (j - c * A.page)] = 0.f;
       }
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(kMvThreads, 4) evict_move_kernel(const __grid_
       __syncthreads();                               // (all of the tile is read)
       if (t == 0) {
         ptx::st_release_u32(flag + i, 1u);
-        wait_read(i, i);
+        wait_read(i, i + 1, i, 0, 1);
       }
       __syncthreads();
     }
