@@ -109,22 +109,22 @@ struct EvictRow {
     return id >= 0 && id < n_pages ? (int64_t)id * page + (j - c * page) : -1;
   }
   __device__ __forceinline__ uint32_t key(float w) const { return w == w ? order_key(w) : 0u; }
-  // keys of four tiles from `tile` on, four entries from j on of each for this lane: those below n (0 elsewhere)
-  __device__ __forceinline__ void keys(int tile, int lane, int n, bool report, uint32_t (&x)[4][4]) const {
+  // keys of two tiles from `tile` on, four entries from j on of each for this lane: those below n (0 elsewhere)
+  __device__ __forceinline__ void keys(int tile, int lane, int n, bool report, uint32_t (&x)[2][4]) const {
     const int j0 = tile * kMvTile + lane * 4;
     bool out = false;
     if ((page & 3) == 0) {                           // (one page holds the lane's four, on a 16-byte boundary)
-      int64_t s[4];
-      float4 w[4];
+      int64_t s[2];
+      float4 w[2];
 #pragma unroll
-      for (int u = 0; u < 4; u++) s[u] = j0 + u * kMvTile < n ? slot(j0 + u * kMvTile, col(j0 + u * kMvTile)) : -1;
+      for (int u = 0; u < 2; u++) s[u] = j0 + u * kMvTile < n ? slot(j0 + u * kMvTile, col(j0 + u * kMvTile)) : -1;
 #pragma unroll
-      for (int u = 0; u < 4; u++) {
+      for (int u = 0; u < 2; u++) {
         out |= s[u] < 0 && j0 + u * kMvTile < n;
         w[u] = s[u] >= 0 ? __ldg(reinterpret_cast<const float4 *>(weight + s[u])) : make_float4(NAN, NAN, NAN, NAN);
       }
 #pragma unroll
-      for (int u = 0; u < 4; u++) {
+      for (int u = 0; u < 2; u++) {
         const int left = n - (j0 + u * kMvTile);
         x[u][0] = left > 0 ? key(w[u].x) : 0u;
         x[u][1] = left > 1 ? key(w[u].y) : 0u;
@@ -133,7 +133,7 @@ struct EvictRow {
       }
     } else {
 #pragma unroll
-      for (int u = 0; u < 4; u++) {
+      for (int u = 0; u < 2; u++) {
         int64_t s[4];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
@@ -186,78 +186,111 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
   R.mul = A.page_mul;
   R.shift = A.page_shift;
   R.status = A.status;
-  // (the first cache_tiles of this warp's part stay in shared memory, a multiple of four, or all of them)
+  // Keys in shared memory: of this warp's first kept_tiles tiles, and behind them two tiles at a time of the others.
   uint32_t *mine = ev_keys + (size_t)warp * cache_tiles * kMvTile + lane * 4;
-  const int kept_tiles = per_warp <= cache_tiles ? per_warp : cache_tiles & ~3;
-  // four tiles' keys
-  auto keys_of = [&](int tile, uint32_t (&x)[4][4]) {
-    if (tile - w0 < kept_tiles) {
-#pragma unroll
-      for (int u = 0; u < 4; u++) {
-        if (tile + u >= w1) break;
-        const uint4 y = *reinterpret_cast<const uint4 *>(mine + (tile - w0 + u) * kMvTile);
-        x[u][0] = y.x;
-        x[u][1] = y.y;
-        x[u][2] = y.z;
-        x[u][3] = y.w;
-      }
-    } else {
-      R.keys(tile, lane, min(n, w1 * kMvTile), true, x);
-    }
-  };
-  // the row's keys, read once where they fit
-  if (kept_tiles > 0)
-    for (int tile = w0; tile < min(w1, w0 + kept_tiles); tile += 4) {
-      uint32_t x[4][4];
-      R.keys(tile, lane, min(n, w1 * kMvTile), true, x);
-#pragma unroll
-      for (int u = 0; u < 4; u++)
-        if (tile + u < w1) *reinterpret_cast<uint4 *>(mine + (tile - w0 + u) * kMvTile) = make_uint4(x[u][0], x[u][1], x[u][2], x[u][3]);
-    }
+  const int kept_tiles = per_warp <= cache_tiles ? per_warp : cache_tiles - 2;
   auto meet = [&]() {                                // all threads of the cluster
     if (ctas > 1) ev_cluster_sync();
     else __syncthreads();
   };
-  uint32_t T = 0u, ties = 0u;                        // stay: keys above T, and the first `ties` of those at T
-  if (kk > 0 && kk < m) {
-    int low = 32;                                    // bits that are not known yet
-    uint32_t known = 0u, need = (uint32_t)kk;
-    // bins 2 t and 2 t + 1 of this CTA's slice of the histogram
-    const int bins = kEvBins / ctas, bin = (int)rank * bins + 2 * t, warps = max(1, bins / 64);
-    while (low > 0) {
-      const int w = min(kEvBits, low);
+  const bool all = kk == m;
+  uint32_t T = kk == 0 ? 0xFFFFFFFFu : 0u, ties = 0u;                  // stay: keys above T, and the first `ties` of those at T
+  uint32_t gt = 0u, eq = 0u;                         // entries that stay for sure, that tie: of the warp's part, then ahead of it
+  int low = 32;                                      // bits of T that are not known yet
+  uint32_t known = 0u, need = (uint32_t)kk;
+  // bins 2 t and 2 t + 1 of this CTA's slice of a histogram
+  const int bins = kEvBins / ctas, bin = (int)rank * bins + 2 * t, warps = max(1, bins / 64);
+  int32_t *from = W.from + (int64_t)b * W.from_stride, *before = W.before + (int64_t)b * W.tile_stride;
+  bool first = true;
+  // 0 .. 2: a histogram of the next bits; 3: counts; 4: the places.  (One loop over the tiles for all of them: in a short row
+  // each instruction runs once, and fetching them is most of the time.)
+#pragma unroll 1
+  for (int phase = kk > 0 && kk < m ? 0 : 3; phase < 5; phase++) {
+    const int w = min(kEvBits, low);
+    const uint32_t mask = (1u << w) - 1u;
+    if (phase < 3) {
       for (int i = t; i < kEvBins; i += kEvThreads) S.hist[i] = 0u;
       __syncthreads();
-      const uint32_t mask = (1u << w) - 1u;
-      for (int tile = w0; tile < w1; tile += 4) {
-        uint32_t x[4][4];
-        keys_of(tile, x);
+    }
+#pragma unroll 1
+    for (int tile0 = w0; tile0 < w1; tile0 += 2) {
+      const bool kept = tile0 - w0 < kept_tiles;
+      uint32_t *at = mine + (kept ? tile0 - w0 : kept_tiles) * kMvTile;
+      if (first || !kept) {
+        uint32_t x[2][4];
+        R.keys(tile0, lane, min(n, w1 * kMvTile), first, x);
 #pragma unroll
-        for (int u = 0; u < 4; u++) {
-          if (tile + u >= w1) break;
-          const int left = m - ((tile + u) * kMvTile + lane * 4);        // the lane's candidates
-          if (low == 32) {
-            uint32_t d[4];
+        for (int u = 0; u < 2; u++)
+          if (tile0 + u < w1) *reinterpret_cast<uint4 *>(at + u * kMvTile) = make_uint4(x[u][0], x[u][1], x[u][2], x[u][3]);
+      }
+#pragma unroll 1
+      for (int tile = tile0; tile < min(tile0 + 2, w1); tile++, at += kMvTile) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(at);          // (the lane's own)
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        const int j = tile * kMvTile + lane * 4, left = m - j;         // the lane's entries, its candidates
+        if (phase == 0) {
+          uint32_t d[4];
 #pragma unroll
-            for (int i = 0; i < 4; i++) d[i] = x[u][i] >> (32 - kEvBits);
-            // (many equal weights: one lane counts for all)
-            const uint32_t one = __shfl_sync(0xFFFFFFFFu, d[0], 0);
-            if (__all_sync(0xFFFFFFFFu, left >= 4 && d[0] == one && d[1] == one && d[2] == one && d[3] == one)) {
-              if (lane == 0) atomicAdd(&S.hist[one], (uint32_t)kMvTile);
-              continue;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-              if (i < left) atomicAdd(&S.hist[d[i]], 1u);
+          for (int i = 0; i < 4; i++) d[i] = x[i] >> (32 - kEvBits);
+          // (many equal weights: one lane counts for all)
+          const uint32_t one = __shfl_sync(0xFFFFFFFFu, d[0], 0);
+          if (__all_sync(0xFFFFFFFFu, left >= 4 && d[0] == one && d[1] == one && d[2] == one && d[3] == one)) {
+            if (lane == 0) atomicAdd(&S.hist[one], (uint32_t)kMvTile);
           } else {
 #pragma unroll
             for (int i = 0; i < 4; i++)
-              if (x[u][i] >> low == known && i < left) atomicAdd(&S.hist[(x[u][i] >> (low - w)) & mask], 1u);
+              if (i < left) atomicAdd(&S.hist[d[i]], 1u);
           }
+          continue;
         }
+        if (phase < 3) {
+#pragma unroll
+          for (int i = 0; i < 4; i++)
+            if (x[i] >> low == known && i < left) atomicAdd(&S.hist[(x[i] >> (low - w)) & mask], 1u);
+          continue;
+        }
+        // bits of the lane's entries that stay for sure, that tie
+        uint32_t g = 0u, e = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          if (i >= left ? j + i < n : all || x[i] > T) g |= 1u << i;
+          if (i < left && !all && x[i] == T) e |= 1u << i;
+        }
+        if (phase == 3) {
+          gt += (uint32_t)__popc(g);
+          eq += (uint32_t)__popc(e);
+          continue;
+        }
+        uint32_t sum = (uint32_t)__popc(g) | (uint32_t)__popc(e) << 16;      // (at most 128 each)
+        const uint32_t own = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t z = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+          if (lane >= o) sum += z;
+        }
+        const uint32_t all_sum = __shfl_sync(0xFFFFFFFFu, sum, 31), r0 = gt + min(eq, ties);
+        uint32_t a = gt + ((sum - own) & 0xFFFFu), c = eq + ((sum - own) >> 16);
+        // (through shared memory: the places of a tile's kept entries are neighbours)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const bool tie = (e >> i) & 1u;
+          if (((g >> i) & 1u) || (tie && c < ties)) S.stage[warp][a + min(c, ties) - r0] = j + i;
+          a += (g >> i) & 1u;
+          c += tie ? 1u : 0u;
+        }
+        __syncwarp();
+        gt += all_sum & 0xFFFFu;
+        eq += all_sum >> 16;
+        const uint32_t count = gt + min(eq, ties) - r0;
+        for (uint32_t i = lane; i < count; i += 32) from[r0 + i] = S.stage[warp][i];
+        if (lane == 0) before[tile] = (int32_t)r0;
+        __syncwarp();
       }
-      meet();
+    }
+    first = false;
+    if (phase < 3) {
       // the digit at which the count from the top passes `need`: each CTA sums a slice of the histograms
+      meet();
       uint32_t h0 = 0u, h1 = 0u, above = 0u;
       if (2 * t < bins) {
         if (ctas == 1) {
@@ -292,7 +325,8 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
         if (t < ctas) ev_put2(S.slice[rank], (uint32_t)t, sum, 0u);
         __syncwarp();
         ev_cluster_sync();
-        above += __reduce_add_sync(0xFFFFFFFFu, lane > (int)rank && lane < ctas ? S.slice[lane & (kEvMaxCtas - 1)][0] : 0u);
+        const uint32_t other = lane > (int)rank && lane < ctas ? S.slice[lane & (kEvMaxCtas - 1)][0] : 0u;
+        above += __reduce_add_sync(0xFFFFFFFFu, other);
       }
       if (2 * t < bins) {
         const uint32_t top1 = above - h0 - h1, top0 = above - h0;        // above bin + 1, above bin
@@ -312,92 +346,32 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
       known = known << w | S.found[0];
       need = S.found[1];
       low -= w;
-    }
-    T = known;
-    ties = need;
-  } else if (kk == 0) {
-    T = 0xFFFFFFFFu;                                 // (none: no key is above, and no tie stays)
-  }
-  const bool all = kk == m;
-  // ---------------------------------------------------- ranks
-  // bits of the lane's entries of a tile that stay for sure, that tie
-  auto stays = [&](int tile, const uint32_t (&x)[4], uint32_t &g, uint32_t &e) {
-    const int j = tile * kMvTile + lane * 4;
-    g = e = 0u;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      if (j + i >= m ? j + i < n : all || x[i] > T) g |= 1u << i;
-      if (j + i < m && !all && x[i] == T) e |= 1u << i;
-    }
-  };
-  uint32_t gt = 0u, eq = 0u;
-  for (int tile = w0; tile < w1; tile += 4) {
-    uint32_t x[4][4];
-    keys_of(tile, x);
-#pragma unroll
-    for (int u = 0; u < 4; u++) {
-      if (tile + u >= w1) break;
-      uint32_t g, e;
-      stays(tile + u, x[u], g, e);
-      gt += (uint32_t)__popc(g);
-      eq += (uint32_t)__popc(e);
-    }
-  }
-  gt = __reduce_add_sync(0xFFFFFFFFu, gt);
-  eq = __reduce_add_sync(0xFFFFFFFFu, eq);
-  if (lane == 0) {
-    S.gt[warp] = gt;
-    S.eq[warp] = eq;
-  }
-  __syncthreads();
-  gt = lane < warp ? S.gt[lane] : 0u;
-  eq = lane < warp ? S.eq[lane] : 0u;
-  if (ctas > 1) {
-    if (warp == 0) {
-      const uint32_t a = __reduce_add_sync(0xFFFFFFFFu, S.gt[lane]), c = __reduce_add_sync(0xFFFFFFFFu, S.eq[lane]);
-      if (lane < ctas) ev_put2(S.count[rank], (uint32_t)lane, a, c);
-      __syncwarp();
-    }
-    ev_cluster_sync();                               // (nothing of another CTA is read or written from here on)
-    gt += lane < (int)rank ? S.count[lane & (kEvMaxCtas - 1)][0] : 0u;
-    eq += lane < (int)rank ? S.count[lane & (kEvMaxCtas - 1)][1] : 0u;
-  }
-  gt = __reduce_add_sync(0xFFFFFFFFu, gt);           // ahead of this warp's part
-  eq = __reduce_add_sync(0xFFFFFFFFu, eq);
-  int32_t *from = W.from + (int64_t)b * W.from_stride, *before = W.before + (int64_t)b * W.tile_stride;
-  for (int tile4 = w0; tile4 < w1; tile4 += 4) {
-    uint32_t y[4][4];
-    keys_of(tile4, y);
-#pragma unroll
-    for (int v = 0; v < 4; v++) {
-      const int tile = tile4 + v;
-      if (tile >= w1) break;
-      uint32_t g, e;
-      stays(tile, y[v], g, e);
-      uint32_t sum = (uint32_t)__popc(g) | (uint32_t)__popc(e) << 16;      // (at most 128 each)
-      const uint32_t own = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t z = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-        if (lane >= o) sum += z;
+      if (low == 0) {
+        T = known;
+        ties = need;
       }
-      const uint32_t all_sum = __shfl_sync(0xFFFFFFFFu, sum, 31), r0 = gt + min(eq, ties);
-      uint32_t a = gt + ((sum - own) & 0xFFFFu), c = eq + ((sum - own) >> 16);
-      // (through shared memory: the places of a tile's kept entries are neighbours)
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const bool tie = (e >> i) & 1u;
-        if (((g >> i) & 1u) || (tie && c < ties)) S.stage[warp][a + min(c, ties) - r0] = tile * kMvTile + lane * 4 + i;
-        a += (g >> i) & 1u;
-        c += tie ? 1u : 0u;
+    } else if (phase == 3) {
+      gt = __reduce_add_sync(0xFFFFFFFFu, gt);
+      eq = __reduce_add_sync(0xFFFFFFFFu, eq);
+      if (lane == 0) {
+        S.gt[warp] = gt;
+        S.eq[warp] = eq;
       }
-      __syncwarp();
-      gt += all_sum & 0xFFFFu;
-      eq += all_sum >> 16;
-      const uint32_t count = gt + min(eq, ties) - r0;
-      for (uint32_t i = lane; i < count; i += 32) from[r0 + i] = S.stage[warp][i];
-      if (lane == 0) before[tile] = (int32_t)r0;
-      __syncwarp();
+      __syncthreads();
+      gt = lane < warp ? S.gt[lane] : 0u;
+      eq = lane < warp ? S.eq[lane] : 0u;
+      if (ctas > 1) {
+        if (warp == 0) {
+          const uint32_t a = __reduce_add_sync(0xFFFFFFFFu, S.gt[lane]), c = __reduce_add_sync(0xFFFFFFFFu, S.eq[lane]);
+          if (lane < ctas) ev_put2(S.count[rank], (uint32_t)lane, a, c);
+          __syncwarp();
+        }
+        ev_cluster_sync();                           // (nothing of another CTA is read or written from here on)
+        gt += lane < (int)rank ? S.count[lane & (kEvMaxCtas - 1)][0] : 0u;
+        eq += lane < (int)rank ? S.count[lane & (kEvMaxCtas - 1)][1] : 0u;
+      }
+      gt = __reduce_add_sync(0xFFFFFFFFu, gt);
+      eq = __reduce_add_sync(0xFFFFFFFFu, eq);
     }
   }
   if (w1 == tiles && w0 < w1 && lane == 0) before[tiles] = k;
