@@ -5,7 +5,7 @@
 // all; they move together, in order, to places 0 .. k - 1.  Two launches:
 //
 // evict_select_kernel: a cluster per sequence finds the smallest weight that stays, as an order key,
-// by histograms of 11, 11 and 10 of its bits, one pass over the keys each (they stay in shared memory, 49,152 of a CTA's
+// by histograms of 11, 11 and 10 of its bits, one pass over the keys each (they stay in shared memory, up to 49,152 of a CTA's
 // part of the row; those behind are read again).  Each warp has a contiguous part of the row, so that
 // one count of every part gives every kept entry its rank, and writes which entry each new place comes from.
 //

@@ -6,7 +6,7 @@
 // Work: the entries that a sequence's queries see form chunks of 128, its queries groups
 // of NQ.  All sequences' (chunk, group) products are dealt to the CTAs (one an SM) in contiguous runs of equal
 // numbers, cut between chunks, so that one CTA has all of an entry's queries and sums them in a fixed order.
-// With several groups a CTA takes 24 chunks at a time (one query a group: 8), group by group: Q stays in shared memory
+// With several groups a CTA takes up to 24 chunks at a time (one query a group: 8), group by group: Q stays in shared memory
 // for them, their records in L2 for the groups, and their sums in shared memory.  A selection is a
 // sequence of its own: its chunks' weights go to scratch, and are added query by query.
 //
@@ -301,7 +301,11 @@ struct WgWalk {
   int g, c;
   int group;                    // groups of the run that have begun, less one
   __device__ __forceinline__ void block() {
-    hi = I.y > 1 ? min(lo + WgSmem<NQ>::kBlock, seq_hi) : seq_hi;
+    hi = seq_hi;
+    if (I.y > 1) {                                   // (what is left in equal parts: a short one fetches Q for a few chunks)
+      const int left = seq_hi - lo, parts = (left + WgSmem<NQ>::kBlock - 1) / WgSmem<NQ>::kBlock;
+      hi = lo + (left + parts - 1) / parts;
+    }
     g = 0;
     c = lo;
     group++;
