@@ -15,7 +15,8 @@
 // sequences: a chain of loads).  A sequence's row is dealt to the warps of a cluster in
 // contiguous segments, whose sums meet in each CTA through distributed shared memory; the CTA that has the
 // segment where the running sum passes looks through it with all its threads (one warp, 32 groups at a
-// time, took 25 us of a 4,096-entry segment).
+// time, took 25 us of a 4,096-entry segment).  256 rows of 131,072 fp32 probabilities: 30 us, 4.5 TB/s; 64 pairs of rows of
+// 100,003 in bf16: 15; one row: 6.5, a chain of seven loads or barriers.  Greedy, 384 rows of 131,072 in bf16: 15, 6.7 TB/s of all rows.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
