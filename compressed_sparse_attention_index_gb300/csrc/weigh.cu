@@ -598,14 +598,14 @@ __device__ __forceinline__ void wg_load(const WeighArgs &A, WgShared &S, const u
         const int j = 2 * hf + i;
         const uint32_t w[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
         const uint32_t two = e4m3x2_to_f16x2((hf == 0 ? sc.x : sc.y) >> (16 * i));
-        const uint32_t s2[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
+        const __half2 sh = *reinterpret_cast<const __half2 *>(&two), s2[2] = {__low2half2(sh), __high2half2(sh)};
 #pragma unroll
         for (int u = 0; u < 4; u++) {
           uint32_t x[4];
           e2m1x8_to_f16(w[u], x);
 #pragma unroll
           for (int q = 0; q < 4; q++) {
-            const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x[q]), *reinterpret_cast<const __half2 *>(&s2[u >> 1]));
+            const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x[q]), s2[u >> 1]);
             o[i][4 * u + q] = *reinterpret_cast<const uint32_t *>(&y);
           }
         }
