@@ -381,10 +381,11 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
 
 // ------------------------------------------------------------------ move
 // Loads that stay where they stand between barriers (what they read is written by other CTAs of the
-// same launch once this one has said that it has read it).
+// same launch once this one has said that it has read it).  Records come by 64 B of L2's lines of 128: neighbours
+// are often not kept (8 x 1M cut to half 560 -> 544 us).
 __device__ __forceinline__ uint4 mv_load16(const uint8_t *p) {
   uint4 v;
-  asm volatile("ld.relaxed.gpu.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.relaxed.gpu.global.L1::no_allocate.L2::64B.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p)
                : "memory");
@@ -408,11 +409,15 @@ __global__ void __launch_bounds__(kMvThreads, 4) evict_move_kernel(const __grid_
   int b0 = 0;                                        // 32 sequences from b0 on have tiles from base on
   int64_t base = 0;
   uint32_t tile = blockIdx.x;
+  if (A.in_place && t == 0) next_sh = atomicAdd(W.ticket, 1u);
   for (;; tile += gridDim.x) {
+    __syncthreads();                                 // (the last tile's slots are read)
     if (A.in_place) {
-      if (t == 0) next_sh = atomicAdd(W.ticket, 1u);
-      __syncthreads();
       tile = next_sh;
+      __syncthreads();
+      // the next ticket is on its way during this tile (33 x 40,001 to 9,999: 105 us with one at a time, 88 so).  A CTA's tickets
+      // ascend and are done in turn, so the least tile that is not done is always one that some CTA is at, and waits for none.
+      if (t == 0) next_sh = atomicAdd(W.ticket, 1u);
     }
     // (every warp finds the sequence for itself)
     int b = -1, i = 0, k = 0, n = 0;
@@ -465,7 +470,6 @@ __global__ void __launch_bounds__(kMvThreads, 4) evict_move_kernel(const __grid_
         const int c = (int)(((uint64_t)(unsigned)j * A.page_mul) >> A.page_shift), id = __ldg(table + c);
         if (id >= 0 && id < A.n_pages) A.dst_weight[(int64_t)id * A.page + (j - c * A.page)] = 0.f;
       }
-      __syncthreads();
       continue;
     }
     const int r0 = i * kMvTile, rows = min(kMvTile, k - r0);
@@ -483,7 +487,6 @@ __global__ void __launch_bounds__(kMvThreads, 4) evict_move_kernel(const __grid_
     const bool still = __syncthreads_and(there) != 0;
     if (still) {
       if (A.in_place && t == 0) ptx::st_release_u32(flag + i, 1u);
-      __syncthreads();
       continue;
     }
     uint4 x[kMvUnits];
@@ -508,10 +511,9 @@ __global__ void __launch_bounds__(kMvThreads, 4) evict_move_kernel(const __grid_
 #pragma unroll
     for (int u = 0; u < kMvUnits; u++) {
       const int r = u * (kMvThreads / 18) + sub;
-      if (r < rows && dst_sh[r] >= 0) __stcs(reinterpret_cast<uint4 *>(A.dst_pages + dst_sh[r] * kKvBytes + unit * 16), x[u]);
+      if (r < rows && dst_sh[r] >= 0) *reinterpret_cast<uint4 *>(A.dst_pages + dst_sh[r] * kKvBytes + unit * 16) = x[u];
     }
     if (t < rows && dst_sh[t] >= 0) A.dst_weight[dst_sh[t]] = w;
-    __syncthreads();                                 // (the slots are read)
   }
 }
 
@@ -546,10 +548,11 @@ cudaError_t launch_evict(EvictArgs A, void *ws, cudaStream_t st) {
   const int cache = (int)(warp_share < kEvKeyTiles ? warp_share : kEvKeyTiles);
   e = launch_pdl(evict_select_kernel, dim3((unsigned)ctas, (unsigned)A.n_seq), dim3(kEvThreads), cache * kTileBytes, st, (unsigned)ctas, A, W, cache);
   if (e != cudaSuccess) return e;
-  // no more CTAs than there can be tiles, and many more than run at a time: SMs differ in speed (8 x 1M entries cut to
-  // half: 720 us with four CTAs an SM that take equal shares)
+  // Into other pages: no more CTAs than there can be tiles, and many more than run at a time, as SMs differ in speed (8 x 1M
+  // entries cut to half: 720 us with four CTAs an SM that take equal shares).  In place: as many as run, which take tickets.
   const int64_t dst_row = A.dst_stride * A.page, most = dst_row < row ? dst_row : row;
-  const int64_t tiles = A.n_seq * ((most + kMvTile - 1) / kMvTile + (A.in_place ? 1 : 0)), grid = tiles < 64 * sms ? tiles : 64 * sms;
+  const int64_t tiles = A.n_seq * ((most + kMvTile - 1) / kMvTile + (A.in_place ? 1 : 0)), waves = A.in_place ? 4 : 64;
+  const int64_t grid = tiles < waves * sms ? tiles : waves * sms;
   return launch_pdl(evict_move_kernel, dim3((unsigned)grid), dim3(kMvThreads), 0, st, 1u, A, W);
 }
 
