@@ -97,7 +97,9 @@ struct __align__(16) EvictShared {
   int32_t stage[kEvWarps][kMvTile];
 };
 
-// Order key of entry j's weight, larger is heavier (NaN: 0, below everything).
+// Order key of entry j's weight, larger is heavier (NaN: 1, below everything).  The last entries, which stay in any case,
+// have the largest key of all and those behind the row 0, so that no pass over the keys asks where an entry stands.
+constexpr uint32_t kEvLeast = 1u;
 struct EvictRow {
   const float *weight;
   const int32_t *table;
@@ -110,9 +112,9 @@ struct EvictRow {
     const int id = __ldg(table + c);
     return id >= 0 && id < n_pages ? (int64_t)id * page + (j - c * page) : -1;
   }
-  __device__ __forceinline__ uint32_t key(float w) const { return w == w ? order_key(w) : 0u; }
-  // keys of two tiles from `tile` on, four entries from j on of each for this lane: those below n (0 elsewhere)
-  __device__ __forceinline__ void keys(int tile, int lane, int n, bool report, uint32_t (&x)[2][4]) const {
+  __device__ __forceinline__ uint32_t key(float w) const { return w == w ? order_key(w) : kEvLeast; }
+  // keys of two tiles from `tile` on, four entries from j on of each for this lane: those below n, of which those from m on stay
+  __device__ __forceinline__ void keys(int tile, int lane, int m, int n, bool report, uint32_t (&x)[2][4]) const {
     const int j0 = tile * kMvTile + lane * 4;
     bool out = false;
     if ((page & 3) == 0) {                           // (one page holds the lane's four, on a 16-byte boundary)
@@ -144,8 +146,20 @@ struct EvictRow {
           out |= s[i] < 0 && j < n;
         }
 #pragma unroll
-        for (int i = 0; i < 4; i++) x[u][i] = s[i] >= 0 ? key(__ldg(weight + s[i])) : 0u;
+        for (int i = 0; i < 4; i++) {
+          const float w = s[i] >= 0 ? __ldg(weight + s[i]) : NAN;
+          x[u][i] = j0 + u * kMvTile + i < n ? key(w) : 0u;
+        }
       }
+    }
+    if ((tile + 2) * kMvTile > m) {
+#pragma unroll
+      for (int u = 0; u < 2; u++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const int j = j0 + u * kMvTile + i;
+          if (j >= m && j < n) x[u][i] = 0xFFFFFFFFu;
+        }
     }
     if (report && out) record_error(status, CSA2_ERR_BOUNDS);
   }
@@ -195,11 +209,11 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
     if (ctas > 1) ev_cluster_sync();
     else __syncthreads();
   };
-  const bool all = kk == m;
-  uint32_t T = kk == 0 ? 0xFFFFFFFFu : 0u, ties = 0u;                  // stay: keys above T, and the first `ties` of those at T
-  uint32_t gt = 0u, eq = 0u;                         // entries that stay for sure, that tie: of the warp's part, then ahead of it
+  // stay: keys above T, and the first `ties` of those at T (all entries: those above 0; no candidate: those of the largest key)
+  uint32_t T = kk == m ? 0u : 0xFFFFFFFEu, ties = 0u;
+  uint32_t gt = 0u, eq = 0u;                         // entries that stay for sure, that tie: of the warp's part; then that stay, that tie ahead
   int low = 32;                                      // bits of T that are not known yet
-  uint32_t known = 0u, need = (uint32_t)kk;
+  uint32_t known = 0u, top = 0u, need = (uint32_t)k;  // T's known bits, at the low end and in their places
   // bins 2 t and 2 t + 1 of this CTA's slice of a histogram
   const int bins = kEvBins / ctas, bin = (int)rank * bins + 2 * t, warps = max(1, bins / 64);
   int32_t *from = W.from + (int64_t)b * W.from_stride, *before = W.before + (int64_t)b * W.tile_stride;
@@ -209,7 +223,6 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
 #pragma unroll 1
   for (int phase = kk > 0 && kk < m ? 0 : 3; phase < 5; phase++) {
     const int w = min(kEvBits, low);
-    const uint32_t mask = (1u << w) - 1u;
     if (phase < 3) {
       for (int i = t; i < kEvBins; i += kEvThreads) S.hist[i] = 0u;
       __syncthreads();
@@ -220,7 +233,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
       uint32_t *at = mine + (kept ? tile0 - w0 : kept_tiles) * kMvTile;
       if (first || !kept) {
         uint32_t x[2][4];
-        R.keys(tile0, lane, min(n, w1 * kMvTile), first, x);
+        R.keys(tile0, lane, m, min(n, w1 * kMvTile), first, x);
 #pragma unroll
         for (int u = 0; u < 2; u++)
           if (tile0 + u < w1) *reinterpret_cast<uint4 *>(at + u * kMvTile) = make_uint4(x[u][0], x[u][1], x[u][2], x[u][3]);
@@ -229,63 +242,62 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
       for (int tile = tile0; tile < min(tile0 + 2, w1); tile++, at += kMvTile) {
         const uint4 v = *reinterpret_cast<const uint4 *>(at);          // (the lane's own)
         const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-        const int j = tile * kMvTile + lane * 4, left = m - j;         // the lane's entries, its candidates
-        if (phase == 0) {
+        if (phase < 3) {
+          // the next w bits of the keys that begin as T does; of others the result is above them
           uint32_t d[4];
 #pragma unroll
-          for (int i = 0; i < 4; i++) d[i] = x[i] >> (32 - kEvBits);
+          for (int i = 0; i < 4; i++) d[i] = (x[i] ^ top) >> (low - w);
           // (many equal weights: one lane counts for all)
           const uint32_t one = __shfl_sync(0xFFFFFFFFu, d[0], 0);
-          if (__all_sync(0xFFFFFFFFu, left >= 4 && d[0] == one && d[1] == one && d[2] == one && d[3] == one)) {
-            if (lane == 0) atomicAdd(&S.hist[one], (uint32_t)kMvTile);
+          if (__all_sync(0xFFFFFFFFu, d[0] == one && d[1] == one && d[2] == one && d[3] == one)) {
+            if (lane == 0 && one >> w == 0u) atomicAdd(&S.hist[one], (uint32_t)kMvTile);
           } else {
 #pragma unroll
             for (int i = 0; i < 4; i++)
-              if (i < left) atomicAdd(&S.hist[d[i]], 1u);
+              if (d[i] >> w == 0u) atomicAdd(&S.hist[d[i]], 1u);
           }
           continue;
         }
-        if (phase < 3) {
-#pragma unroll
-          for (int i = 0; i < 4; i++)
-            if (x[i] >> low == known && i < left) atomicAdd(&S.hist[(x[i] >> (low - w)) & mask], 1u);
-          continue;
-        }
-        // bits of the lane's entries that stay for sure, that tie
-        uint32_t g = 0u, e = 0u;
+        uint32_t g = 0u, e = 0u;                     // bits of the lane's entries that stay for sure, that tie
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-          if (i >= left ? j + i < n : all || x[i] > T) g |= 1u << i;
-          if (i < left && !all && x[i] == T) e |= 1u << i;
+          if (x[i] > T) g |= 1u << i;
+          if (x[i] == T) e |= 1u << i;
         }
         if (phase == 3) {
           gt += (uint32_t)__popc(g);
           eq += (uint32_t)__popc(e);
           continue;
         }
-        uint32_t sum = (uint32_t)__popc(g) | (uint32_t)__popc(e) << 16;      // (at most 128 each)
-        const uint32_t own = sum;
+        auto scan = [&](uint32_t v) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t z = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-          if (lane >= o) sum += z;
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t z = __shfl_up_sync(0xFFFFFFFFu, v, o);
+            if (lane >= o) v += z;
+          }
+          return v;
+        };
+        if (__any_sync(0xFFFFFFFFu, e != 0u) && eq < ties) {           // (eq: the whole warp's)
+          const uint32_t sum = scan((uint32_t)__popc(e));
+          uint32_t c = eq + sum - (uint32_t)__popc(e);
+#pragma unroll
+          for (int i = 0; i < 4; i++)
+            if ((e >> i) & 1u) {
+              if (c < ties) g |= 1u << i;
+              c++;
+            }
+          eq += __shfl_sync(0xFFFFFFFFu, sum, 31);
         }
-        const uint32_t all_sum = __shfl_sync(0xFFFFFFFFu, sum, 31), r0 = gt + min(eq, ties);
-        uint32_t a = gt + ((sum - own) & 0xFFFFu), c = eq + ((sum - own) >> 16);
+        const uint32_t sum = scan((uint32_t)__popc(g)), count = __shfl_sync(0xFFFFFFFFu, sum, 31);
         // (through shared memory: the places of a tile's kept entries are neighbours)
+        int32_t *to = &S.stage[warp][sum - (uint32_t)__popc(g)];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const bool tie = (e >> i) & 1u;
-          if (((g >> i) & 1u) || (tie && c < ties)) S.stage[warp][a + min(c, ties) - r0] = j + i;
-          a += (g >> i) & 1u;
-          c += tie ? 1u : 0u;
-        }
+        for (int i = 0; i < 4; i++)
+          if ((g >> i) & 1u) *to++ = tile * kMvTile + lane * 4 + i;
         __syncwarp();
-        gt += all_sum & 0xFFFFu;
-        eq += all_sum >> 16;
-        const uint32_t count = gt + min(eq, ties) - r0;
-        for (uint32_t i = lane; i < count; i += 32) from[r0 + i] = S.stage[warp][i];
-        if (lane == 0) before[tile] = (int32_t)r0;
+        for (uint32_t i = lane; i < count; i += 32) from[gt + i] = S.stage[warp][i];
+        if (lane == 0) before[tile] = (int32_t)gt;
+        gt += count;
         __syncwarp();
       }
     }
@@ -348,6 +360,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
       known = known << w | S.found[0];
       need = S.found[1];
       low -= w;
+      top = known << low;
       if (low == 0) {
         T = known;
         ties = need;
@@ -374,6 +387,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
       }
       gt = __reduce_add_sync(0xFFFFFFFFu, gt);
       eq = __reduce_add_sync(0xFFFFFFFFu, eq);
+      gt += min(eq, ties);                           // the rank of the warp's first
     }
   }
   if (w1 == tiles && w0 < w1 && lane == 0) before[tiles] = k;
