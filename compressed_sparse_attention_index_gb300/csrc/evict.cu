@@ -16,10 +16,12 @@
 // entries belong to.  A tile that is waited for has been handed out, and reads without waiting for any.
 // The places behind the kept entries are tiles too, behind a sequence's others: their weights are cleared in the same way.
 //
-// What bounds it: 288 B read and written for each entry that stays (HBM; records are 5 or 6 granules of 64 B, 1.21 times their
-// bytes), and for the selection the instructions of its five passes.  8 x 1,048,576 entries cut to half: 607 us, 135 of them the
-// selection (in place 660); 33 x 40,001 to 9,999: 58; 1 x 4,096: 16, a chain of latencies and cold code.
+// What bounds it: 288 B read and written for each entry that stays (HBM; a record is in 5 granules of 64 B, so 1.1 times its
+// bytes are read), and for the selection the instructions of its five passes.  8 x 1,048,576 entries cut to half: 490 us, 100 of
+// them the selection (in place 600); 33 x 40,001 to 9,999: 57; 1 x 4,096: 15, a chain of latencies and cold code.
 #include <limits.h>
+
+#include <algorithm>
 
 #include "common.cuh"
 #include "launch.cuh"
@@ -215,7 +217,8 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
   int low = 32;                                      // bits of T that are not known yet
   uint32_t known = 0u, top = 0u, need = (uint32_t)k;  // T's known bits, at the low end and in their places
   // bins 2 t and 2 t + 1 of this CTA's slice of a histogram
-  const int bins = kEvBins / ctas, bin = (int)rank * bins + 2 * t, warps = max(1, bins / 64);
+  const int pairs = (kEvBins / 2 + ctas - 1) / ctas, bin = 2 * ((int)rank * pairs + t), warps = (pairs + 31) / 32;
+  const bool has_bins = t < pairs && bin < kEvBins;
   int32_t *from = W.from + (int64_t)b * W.from_stride, *before = W.before + (int64_t)b * W.tile_stride;
   bool first = true;
   // 0 .. 2: a histogram of the next bits; 3: counts; 4: the places.  (One loop over the tiles for all of them: in a short row
@@ -306,7 +309,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
       // the digit at which the count from the top passes `need`: each CTA sums a slice of the histograms
       meet();
       uint32_t h0 = 0u, h1 = 0u, above = 0u;
-      if (2 * t < bins) {
+      if (has_bins) {
         if (ctas == 1) {
           h0 = S.hist[bin];
           h1 = S.hist[bin + 1];
@@ -342,7 +345,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
         const uint32_t other = lane > (int)rank && lane < ctas ? S.slice[lane & (kEvMaxCtas - 1)][0] : 0u;
         above += __reduce_add_sync(0xFFFFFFFFu, other);
       }
-      if (2 * t < bins) {
+      if (has_bins) {
         const uint32_t top1 = above - h0 - h1, top0 = above - h0;        // above bin + 1, above bin
         const bool hit1 = top1 < need && need <= top1 + h1, hit0 = top0 < need && need <= above;
         if (hit0 || hit1) {                          // (one thread of the cluster)
@@ -542,10 +545,29 @@ static void evict_magic(unsigned n, uint64_t &mul, int &shift) {
 cudaError_t launch_evict(EvictArgs A, void *ws, cudaStream_t st) {
   const int dev = current_device();
   constexpr size_t kTileBytes = (size_t)kEvWarps * kMvTile * 4;
-  static std::atomic<int> attr_done[kMaxDevices];
+  static std::atomic<int> attr_done[kMaxDevices], fit[kMaxDevices][kEvMaxCtas + 1];     // clusters that run at a time (0: unknown)
   cudaError_t e = once_per_device(attr_done, dev, [&] {
-    const cudaError_t f = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kEvKeyTiles * kTileBytes));
-    return f != cudaSuccess ? f : cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaError_t f = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kEvKeyTiles * kTileBytes));
+    if (f == cudaSuccess) f = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    // The move's loads in flight stand in L1 (147 KB an SM), which the selection's CTAs leave small: 8 % of it for shared memory
+    // hold four CTAs' 3 KB (8 x 1M cut to half, the move: 388 us, 445 as the selection leaves it, 505 with all for shared memory)
+    if (f == cudaSuccess) f = cudaFuncSetAttribute(evict_move_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 8);
+    for (int c = 1; f == cudaSuccess && dev >= 0 && dev < kMaxDevices && c <= kEvMaxCtas; c++) {
+      cudaLaunchAttribute a;
+      a.id = cudaLaunchAttributeClusterDimension;
+      a.val.clusterDim.x = (unsigned)c;
+      a.val.clusterDim.y = a.val.clusterDim.z = 1;
+      cudaLaunchConfig_t config = {};
+      config.gridDim = dim3((unsigned)c, 64);
+      config.blockDim = dim3(kEvThreads);
+      config.dynamicSmemBytes = kEvKeyTiles * kTileBytes;
+      config.attrs = &a;
+      config.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, evict_select_kernel, &config) == cudaSuccess) fit[dev][c].store(n, std::memory_order_relaxed);
+      else cudaGetLastError();
+    }
+    return f;
   });
   if (e != cudaSuccess) return e;
   const int64_t sms = device_sm_count(dev), row = A.table_stride * A.page;
@@ -555,9 +577,20 @@ cudaError_t launch_evict(EvictArgs A, void *ws, cudaStream_t st) {
     W.from = A.from;
     W.from_stride = A.from_stride;
   }
-  // CTAs of a row: one for each 8,192 entries, up to 16, while the sequences leave SMs for more
+  // CTAs of a row: up to one for each 8,192 entries, as many as give the least time when a CTA takes that of 6,500 entries beside
+  // its own and only so many clusters run at a time (an SM holds one CTA and a cluster has to fit one of the chip's groups of SMs:
+  // of 16 CTAs seven fit, of 12 eight; 8 x 1M entries: 139 us of selection with 16, 100 with 12)
   int ctas = 1;
-  while (ctas < kEvMaxCtas && (int64_t)ctas * 8192 < row && (int64_t)A.n_seq * ctas * 2 <= sms) ctas *= 2;
+  int64_t least = LLONG_MAX;
+  for (int c = 1; c <= kEvMaxCtas && (c == 1 || (int64_t)(c - 1) * 8192 < row); c++) {
+    const int fits = dev >= 0 && dev < kMaxDevices ? fit[dev][c].load(std::memory_order_relaxed) : 0;
+    const int64_t at_once = fits > 0 ? fits : std::max<int64_t>(1, sms / c);
+    const int64_t cost = (A.n_seq + at_once - 1) / at_once * (6500 + row / c);
+    if (cost < least) {
+      least = cost;
+      ctas = c;
+    }
+  }
   const int64_t share = ((row + kMvTile - 1) / kMvTile + ctas - 1) / ctas, warp_share = (share + kEvWarps - 1) / kEvWarps;
   const int cache = (int)(warp_share < kEvKeyTiles ? warp_share : kEvKeyTiles);
   e = launch_pdl(evict_select_kernel, dim3((unsigned)ctas, (unsigned)A.n_seq), dim3(kEvThreads), cache * kTileBytes, st, (unsigned)ctas, A, W, cache);

@@ -319,6 +319,17 @@ def test_evict_long_rows(lib, in_place):
     _evict(lib, 4, [1_000_003], [500_000], 4096, 100, in_place)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("n_seq,n,recent", [(1, 20_000, 0), (14, 30_000, 5), (9, 45_000, 0), (3, 110_003, 700), (8, 70_001, 0), (20, 24_000, 24_000)])
+def test_evict_clusters_of_any_size(lib, n_seq, n, recent, in_place):
+    """Rows that 3, 4, 6, 9 or more CTAs share: histograms that do not divide evenly among them."""
+    r = np.random.default_rng(n)
+    lens = [n] + r.integers(0, n + 1, n_seq - 1).tolist()
+    keep = r.integers(1, n, n_seq).tolist()
+    for weights in ("random", "odd"):
+        _evict(lib, n_seq, lens, keep, recent, 32, in_place, weights, want_from=weights == "odd")
+
+
 def test_evict_out_of_range(lib):
     def lengths(lens, keep, table, dst_table):
         lens[0], keep[1], lens[2] = -1, -5, table.shape[1] * 16 + 1
