@@ -180,7 +180,8 @@ class PagedCache:
     ring is sure to hold (swa_cap - 127), a sequence whose new tokens would overwrite
     their own windows gets none, which is reported as CSA2_ERR_BOUNDS; finding them takes
     four small launches more.
-    max_tokens is at most 65,535.  What ends a sequence, and gives its pages to others, is the caller's.
+    max_tokens is at most 65,535.  What ends a sequence, and gives its pages to others (with their weights at 0), is the
+    caller's.
 
     Drafts: verify says which of a step's tokens the target model's probabilities
     accept, and accept, in advance's place, makes those part of their sequences and

@@ -1,5 +1,9 @@
 """A run of the operators that decide what a paged cache keeps, together, through PagedCache: steps of drafts that are
 verified and accepted in part, weighed, and now and then cut down, against a model of the cache in plain Python."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -228,3 +232,42 @@ def test_on_another_stream(oracle_lib):
     _weigh(lib, c, stream=s, out=out)
     s.synchronize()
     assert torch.equal(out, want)
+
+
+_FIRST_CALLS = """
+import torch
+import compressed_sparse_attention_index_gb300 as lib
+n, page = 70_000, 16
+cols = n // page + 1
+i32 = dict(dtype=torch.int32, device="cuda")
+pages = torch.randint(0, 256, (cols, page, 288), dtype=torch.uint8, device="cuda")
+weight = torch.rand(cols * page, device="cuda")
+was, old = pages.view(-1, 288).clone(), weight.clone()
+table, lens, keep = torch.arange(cols, **i32), torch.tensor([n], **i32), torch.tensor([n // 2], **i32)
+p, u, v = torch.softmax(torch.randn(2, 5000, device="cuda"), 1), torch.tensor([0.5, 0.5], device="cuda"), torch.tensor([0.25], device="cuda")
+tokens, first, kept, after = torch.tensor([1, 2], **i32), torch.tensor([0, 2], **i32), torch.zeros(1, **i32), torch.zeros(1, **i32)
+from_ = torch.full((1, n), -1, **i32)
+ws = torch.empty(lib.csa2_workspace_size(lib.CSA2_OP_EVICT, 1, cols * page), dtype=torch.uint8, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    lib.csa2_evict(pages, weight, cols, page, table, cols, lens, keep, 1, 10, pages, weight, cols, table, cols, lens, from_, n, ws, ws.numel())
+    lib.csa2_verify_drafts(lib.CSA2_VERIFY_SAMPLE, p, 5000, None, 0, lib.CSA2_PROB_F32, 5000, tokens, first, 1, 2, u, v, kept, after)
+assert lens.item() == n
+g.replay()
+torch.cuda.synchronize()
+assert lib.csa2_get_device_status() == 0 and lens.item() == n // 2
+j = from_[0, :n // 2].long()
+assert torch.equal(pages.view(-1, 288)[:n // 2], was[j]) and torch.equal(weight[:n // 2], old[j])
+heaviest = torch.topk(old[:n - 10], n // 2 - 10).values
+assert torch.equal(torch.sort(old[j[:-10]], descending=True).values, heaviest) and torch.equal(j[-10:], torch.arange(n - 10, n, device="cuda"))
+assert kept.item() == (2 if 0.5 < p[0, 2].item() else 1) and after.item() >= 0
+print("first calls captured")
+"""
+
+
+def test_first_calls_of_a_process_captured():
+    """What is set up once a device is set up in a capture too."""
+    r = subprocess.run([sys.executable, "-c", _FIRST_CALLS], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "first calls captured" in r.stdout, r.stdout + r.stderr
