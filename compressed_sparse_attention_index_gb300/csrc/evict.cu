@@ -6,7 +6,7 @@
 //
 // evict_select_kernel: a cluster per sequence finds the smallest weight that stays, as an order key,
 // by histograms of 11, 11 and 10 of its bits, one pass over the keys each (they stay in shared memory, up to 49,152 of a CTA's
-// part of the row; those behind are read again).  Each warp has a contiguous part of the row, so that
+// part of the row; those behind in the workspace, 8 x 1M 490 -> 475 us against reading the weights again).  Each warp has a contiguous part of the row, so that
 // one count of every part gives every kept entry its rank, and writes which entry each new place comes from.
 //
 // evict_move_kernel: tiles of kMvTile new places, read whole and then written.  In place, a tile's
@@ -17,8 +17,8 @@
 // The places behind the kept entries are tiles too, behind a sequence's others: their weights are cleared in the same way.
 //
 // What bounds it: 288 B read and written for each entry that stays (HBM; a record is in 5 granules of 64 B, so 1.1 times its
-// bytes are read), and for the selection the instructions of its five passes.  8 x 1,048,576 entries cut to half: 490 us, 100 of
-// them the selection (in place 600); 33 x 40,001 to 9,999: 57; 1 x 4,096: 15, a chain of latencies and cold code.
+// bytes are read), and for the selection the instructions of its five passes.  8 x 1,048,576 entries cut to half: 475 us, 80 of
+// them the selection (in place 585); 33 x 40,001 to 9,999: 57; 1 x 4,096: 15, a chain of latencies and cold code.
 #include <limits.h>
 
 #include <algorithm>
@@ -32,6 +32,7 @@ namespace csa2 {
 constexpr int kEvThreads = 1024, kEvWarps = kEvThreads / 32, kEvBits = 11, kEvBins = 1 << kEvBits;
 constexpr int kEvMaxCtas = 16;
 constexpr int kEvKeyTiles = 12;                     // tiles of a warp's part whose keys fit shared memory (192 KB)
+constexpr int kEvRowKeys = kEvKeyTiles * kEvWarps * 128;             // entries of a row that one CTA holds
 constexpr int kMvTile = 128, kMvThreads = 288, kMvUnits = 8;     // a record is 18 units of 16 B
 constexpr int kMvClear = 16;                        // tiles of places that are cleared at a time
 static_assert(kMvThreads / 18 * kMvUnits == kMvTile, "a tile's units");
@@ -46,11 +47,13 @@ struct EvictWs {
   int32_t *before;            // kept entries ahead of every kMvTile-th place
   uint32_t *flag;             // of each tile: read
   int64_t tile_stride;
+  uint32_t *keys;             // of entries that shared memory does not hold, by place (rows that may have some)
 };
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 size_t evict_workspace_bytes(int n_seq, int64_t row) {
   const size_t tiles = (size_t)(row / kMvTile + 2);
-  return 256 + up256((size_t)n_seq * sizeof(int4)) + up256((size_t)n_seq * (size_t)row * 4) + 2 * up256((size_t)n_seq * tiles * 4);
+  const size_t keys = row > kEvRowKeys ? (size_t)n_seq * tiles * kMvTile * 4 : 0;
+  return 256 + up256((size_t)n_seq * sizeof(int4)) + up256((size_t)n_seq * (size_t)row * 4) + 2 * up256((size_t)n_seq * tiles * 4) + keys;
 }
 static EvictWs evict_ws(void *ws, int n_seq, int64_t row) {
   char *p = static_cast<char *>(ws);
@@ -66,6 +69,8 @@ static EvictWs evict_ws(void *ws, int n_seq, int64_t row) {
   W.before = reinterpret_cast<int32_t *>(p);
   p += up256((size_t)n_seq * (size_t)W.tile_stride * 4);
   W.flag = reinterpret_cast<uint32_t *>(p);
+  p += up256((size_t)n_seq * (size_t)W.tile_stride * 4);
+  W.keys = row > kEvRowKeys ? reinterpret_cast<uint32_t *>(p) : nullptr;
   return W;
 }
 
@@ -116,7 +121,7 @@ struct EvictRow {
   }
   __device__ __forceinline__ uint32_t key(float w) const { return w == w ? order_key(w) : kEvLeast; }
   // keys of two tiles from `tile` on, four entries from j on of each for this lane: those below n, of which those from m on stay
-  __device__ __forceinline__ void keys(int tile, int lane, int m, int n, bool report, uint32_t (&x)[2][4]) const {
+  __device__ __forceinline__ void keys(int tile, int lane, int m, int n, uint32_t (&x)[2][4]) const {
     const int j0 = tile * kMvTile + lane * 4;
     bool out = false;
     if ((page & 3) == 0) {                           // (one page holds the lane's four, on a 16-byte boundary)
@@ -163,7 +168,7 @@ struct EvictRow {
           if (j >= m && j < n) x[u][i] = 0xFFFFFFFFu;
         }
     }
-    if (report && out) record_error(status, CSA2_ERR_BOUNDS);
+    if (out) record_error(status, CSA2_ERR_BOUNDS);
   }
 };
 
@@ -206,6 +211,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
   R.status = A.status;
   // Keys in shared memory: of this warp's first kept_tiles tiles, and behind them two tiles at a time of the others.
   uint32_t *mine = ev_keys + (size_t)warp * cache_tiles * kMvTile + lane * 4;
+  uint4 *far_keys = reinterpret_cast<uint4 *>(W.keys + (int64_t)b * W.tile_stride * kMvTile) + lane;
   const int kept_tiles = per_warp <= cache_tiles ? per_warp : cache_tiles - 2;
   auto meet = [&]() {                                // all threads of the cluster
     if (ctas > 1) ev_cluster_sync();
@@ -234,12 +240,24 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
     for (int tile0 = w0; tile0 < w1; tile0 += 2) {
       const bool kept = tile0 - w0 < kept_tiles;
       uint32_t *at = mine + (kept ? tile0 - w0 : kept_tiles) * kMvTile;
-      if (first || !kept) {
+      uint4 *far = far_keys + (int64_t)tile0 * (kMvTile / 4);
+      if (first) {
         uint32_t x[2][4];
-        R.keys(tile0, lane, m, min(n, w1 * kMvTile), first, x);
+        R.keys(tile0, lane, m, min(n, w1 * kMvTile), x);
 #pragma unroll
         for (int u = 0; u < 2; u++)
-          if (tile0 + u < w1) *reinterpret_cast<uint4 *>(at + u * kMvTile) = make_uint4(x[u][0], x[u][1], x[u][2], x[u][3]);
+          if (tile0 + u < w1) {
+            const uint4 y = make_uint4(x[u][0], x[u][1], x[u][2], x[u][3]);
+            *reinterpret_cast<uint4 *>(at + u * kMvTile) = y;
+            if (!kept) __stcg(far + u * (kMvTile / 4), y);
+          }
+      } else if (!kept) {                            // (what this lane has written)
+        uint4 y[2];
+#pragma unroll
+        for (int u = 0; u < 2; u++) y[u] = tile0 + u < w1 ? __ldcg(far + u * (kMvTile / 4)) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int u = 0; u < 2; u++)
+          if (tile0 + u < w1) *reinterpret_cast<uint4 *>(at + u * kMvTile) = y[u];
       }
 #pragma unroll 1
       for (int tile = tile0; tile < min(tile0 + 2, w1); tile++, at += kMvTile) {
