@@ -6,8 +6,9 @@
 //
 // evict_select_kernel: a cluster per sequence finds the smallest weight that stays, as an order key,
 // by histograms of 11, 11 and 10 of its bits, one pass over the keys each (they stay in shared memory, up to 49,152 of a CTA's
-// part of the row; those behind in the workspace, 8 x 1M 490 -> 475 us against reading the weights again).  Each warp has a contiguous part of the row, so that
-// one count of every part gives every kept entry its rank, and writes which entry each new place comes from.
+// part of the row; those behind in the workspace, 8 x 1M 490 -> 475 us against reading the weights again).  Each warp has a
+// contiguous part of the row, so that one count of every part gives every kept entry its rank, and writes which entry each
+// new place comes from.
 //
 // evict_move_kernel: tiles of kMvTile new places, read whole and then written.  In place, a tile's
 // places may hold entries that are still to be moved, but only those of its own and of earlier tiles
@@ -17,8 +18,8 @@
 // The places behind the kept entries are tiles too, behind a sequence's others: their weights are cleared in the same way.
 //
 // What bounds it: 288 B read and written for each entry that stays (HBM; a record is in 5 granules of 64 B, so 1.1 times its
-// bytes are read), and for the selection the instructions of its five passes.  8 x 1,048,576 entries cut to half: 475 us, 80 of
-// them the selection (in place 585); 33 x 40,001 to 9,999: 57; 1 x 4,096: 15, a chain of latencies and cold code.
+// bytes are read), and for the selection the instructions of its five passes.  8 x 1,048,576 entries cut to half: 471 us, 80 of
+// them the selection (in place 580); 33 x 40,001 to 9,999: 56; 1 x 4,096: 15, a chain of latencies and cold code.
 #include <limits.h>
 
 #include <algorithm>
@@ -30,7 +31,7 @@
 namespace csa2 {
 
 constexpr int kEvThreads = 1024, kEvWarps = kEvThreads / 32, kEvBits = 11, kEvBins = 1 << kEvBits;
-constexpr int kEvMaxCtas = 16;
+constexpr int kEvMaxCtas = 16, kEvWhole = 4;
 constexpr int kEvKeyTiles = 12;                     // tiles of a warp's part whose keys fit shared memory (192 KB)
 constexpr int kEvRowKeys = kEvKeyTiles * kEvWarps * 128;             // entries of a row that one CTA holds
 constexpr int kMvTile = 128, kMvThreads = 288, kMvUnits = 8;     // a record is 18 units of 16 B
@@ -98,7 +99,7 @@ __device__ __forceinline__ void ev_put2(const uint32_t *p, uint32_t rank, uint32
 }
 
 struct __align__(16) EvictShared {
-  uint32_t hist[kEvBins];
+  uint32_t hist[2][kEvBins];                         // of the phases by turns
   uint32_t slice[kEvMaxCtas][2], found[2], count[kEvMaxCtas][2];       // by CTA of the cluster
   uint32_t above[kEvWarps], gt[kEvWarps], eq[kEvWarps];
   int32_t stage[kEvWarps][kMvTile];
@@ -223,7 +224,11 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
   int low = 32;                                      // bits of T that are not known yet
   uint32_t known = 0u, top = 0u, need = (uint32_t)k;  // T's known bits, at the low end and in their places
   // bins 2 t and 2 t + 1 of this CTA's slice of a histogram
-  const int pairs = (kEvBins / 2 + ctas - 1) / ctas, bin = 2 * ((int)rank * pairs + t), warps = (pairs + 31) / 32;
+  // (of a few CTAs each sums all of the histograms: no exchange of its sums, one barrier of the cluster instead of three; 33 rows of
+  // four CTAs each 52 -> 51 us, but eight rows of twelve 471 -> 476)
+  const bool whole = ctas <= kEvWhole;
+  const int pairs = whole ? kEvBins / 2 : (kEvBins / 2 + ctas - 1) / ctas;
+  const int bin = 2 * ((whole ? 0 : (int)rank * pairs) + t), warps = (pairs + 31) / 32;
   const bool has_bins = t < pairs && bin < kEvBins;
   int32_t *from = W.from + (int64_t)b * W.from_stride, *before = W.before + (int64_t)b * W.tile_stride;
   bool first = true;
@@ -232,8 +237,9 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
 #pragma unroll 1
   for (int phase = kk > 0 && kk < m ? 0 : 3; phase < 5; phase++) {
     const int w = min(kEvBits, low);
+    uint32_t *hist = S.hist[phase & 1];
     if (phase < 3) {
-      for (int i = t; i < kEvBins; i += kEvThreads) S.hist[i] = 0u;
+      for (int i = t; i < kEvBins; i += kEvThreads) hist[i] = 0u;
       __syncthreads();
     }
 #pragma unroll 1
@@ -271,11 +277,11 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
           // (many equal weights: one lane counts for all)
           const uint32_t one = __shfl_sync(0xFFFFFFFFu, d[0], 0);
           if (__all_sync(0xFFFFFFFFu, d[0] == one && d[1] == one && d[2] == one && d[3] == one)) {
-            if (lane == 0 && one >> w == 0u) atomicAdd(&S.hist[one], (uint32_t)kMvTile);
+            if (lane == 0 && one >> w == 0u) atomicAdd(&hist[one], (uint32_t)kMvTile);
           } else {
 #pragma unroll
             for (int i = 0; i < 4; i++)
-              if (d[i] >> w == 0u) atomicAdd(&S.hist[d[i]], 1u);
+              if (d[i] >> w == 0u) atomicAdd(&hist[d[i]], 1u);
           }
           continue;
         }
@@ -329,14 +335,14 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
       uint32_t h0 = 0u, h1 = 0u, above = 0u;
       if (has_bins) {
         if (ctas == 1) {
-          h0 = S.hist[bin];
-          h1 = S.hist[bin + 1];
+          h0 = hist[bin];
+          h1 = hist[bin + 1];
         } else {
 #pragma unroll 1
           for (int c = 0; c < ctas; c += 8) {        // (eight loads in flight)
             uint2 y[8];
 #pragma unroll
-            for (int i = 0; i < 8; i++) y[i] = c + i < ctas ? ev_get2(&S.hist[bin], (uint32_t)(c + i)) : make_uint2(0u, 0u);
+            for (int i = 0; i < 8; i++) y[i] = c + i < ctas ? ev_get2(&hist[bin], (uint32_t)(c + i)) : make_uint2(0u, 0u);
 #pragma unroll
             for (int i = 0; i < 8; i++) {
               h0 += y[i].x;
@@ -355,7 +361,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
       __syncthreads();
       const uint32_t part = lane < warps ? S.above[lane] : 0u;
       above += __reduce_add_sync(0xFFFFFFFFu, lane > warp ? part : 0u);
-      if (ctas > 1) {
+      if (!whole) {
         const uint32_t sum = __reduce_add_sync(0xFFFFFFFFu, part);
         if (t < ctas) ev_put2(S.slice[rank], (uint32_t)t, sum, 0u);
         __syncwarp();
@@ -366,9 +372,9 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
       if (has_bins) {
         const uint32_t top1 = above - h0 - h1, top0 = above - h0;        // above bin + 1, above bin
         const bool hit1 = top1 < need && need <= top1 + h1, hit0 = top0 < need && need <= above;
-        if (hit0 || hit1) {                          // (one thread of the cluster)
+        if (hit0 || hit1) {                          // (one thread of the cluster, or of each CTA)
           const uint32_t digit = (uint32_t)bin + (hit1 ? 1u : 0u), rest = need - (hit1 ? top1 : top0);
-          if (ctas == 1) {
+          if (whole) {
             S.found[0] = digit;
             S.found[1] = rest;
           } else {
@@ -377,7 +383,8 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
         }
       }
       __syncwarp();
-      meet();
+      if (whole) __syncthreads();
+      else ev_cluster_sync();
       known = known << w | S.found[0];
       need = S.found[1];
       low -= w;
