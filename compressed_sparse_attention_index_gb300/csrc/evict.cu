@@ -19,7 +19,7 @@
 //
 // What bounds it: 288 B read and written for each entry that stays (HBM; a record is in 5 granules of 64 B, so 1.1 times its
 // bytes are read), and for the selection the instructions of its five passes.  8 x 1,048,576 entries cut to half: 471 us, 80 of
-// them the selection (in place 580); 33 x 40,001 to 9,999: 56; 1 x 4,096: 15, a chain of latencies and cold code.
+// them the selection (in place 530); 33 x 40,001 to 9,999: 56; 1 x 4,096: 15, a chain of latencies and cold code.
 #include <limits.h>
 
 #include <algorithm>
@@ -490,22 +490,20 @@ __global__ void __launch_bounds__(kMvThreads, 4) evict_move_kernel(const __grid_
     if (b < 0) return;                               // (no tile is left: the whole CTA)
     const int32_t *table = A.table + (int64_t)b * A.table_stride, *dst_table = A.dst_table + (int64_t)b * A.dst_stride;
     uint32_t *flag = W.flag + (int64_t)b * W.tile_stride;
-    // waits, the x-th tile for x = t, t + step, .., until the entries at the places of tiles [p0, p1) are read: those have
-    // consecutive ranks, and none is of a tile behind this one (`self`)
-    auto wait_read = [&](int p0, int p1, int self, int from, int step) {
-      const int32_t *before = W.before + (int64_t)b * W.tile_stride;
-      const int lo = __ldcg(before + p0), hi = __ldcg(before + p1);
+    const int32_t *before = W.before + (int64_t)b * W.tile_stride;
+    // waits, the x-th tile for x = t, t + step, .., until the entries at the places of ranks [lo, hi) are read, and none is of
+    // a tile behind this one (`self`)
+    auto wait_read = [&](int lo, int hi, int self, int from, int step) {
       for (int x = lo / kMvTile + from; lo < hi && x <= (hi - 1) / kMvTile; x += step)
         if (x != self && !ptx::poll_at_least_u32(flag + x, 1u)) {
           record_error(A.status, CSA2_ERR_TIMEOUT);
           break;
         }
-      __threadfence();
     };
     if (i >= moved(k)) {                             // places that nothing is at any more
       const int p0 = k / kMvTile + (i - moved(k)) * kMvClear, p1 = min(p0 + kMvClear, (n - 1) / kMvTile + 1);
       if (k > 0) {
-        wait_read(p0, p1, -1, t, kMvThreads);
+        wait_read(__ldcg(before + p0), __ldcg(before + p1), -1, t, kMvThreads);
         __syncthreads();
       }
       for (int j = max(k, p0 * kMvTile) + t; j < min(n, p1 * kMvTile); j += kMvThreads) {
@@ -531,6 +529,8 @@ __global__ void __launch_bounds__(kMvThreads, 4) evict_move_kernel(const __grid_
       if (A.in_place && t == 0) ptx::st_release_u32(flag + i, 1u);
       continue;
     }
+    // kept entries ahead of this tile's places and of the next one's: they are read by the tiles that hold those ranks
+    const int lo = A.in_place && t < 2 ? __ldcg(before + i) : 0, hi = A.in_place && t < 2 ? __ldcg(before + i + 1) : 0;
     uint4 x[kMvUnits];
     float w = 0.f;
     const int unit = t % 18, sub = t / 18;
@@ -542,12 +542,15 @@ __global__ void __launch_bounds__(kMvThreads, 4) evict_move_kernel(const __grid_
     }
     if (t < rows && src_sh[t] >= 0) w = mv_load4(A.weight + src_sh[t]);
     if (A.in_place) {
-      __threadfence();
-      __syncthreads();                               // (all of the tile is read)
-      if (t == 0) {
-        ptx::st_release_u32(flag + i, 1u);
-        wait_read(i, i + 1, i, 0, 1);
-      }
+      // All of the tile is read once every thread has used what it loaded.  The barriers and one thread's release and acquire
+      // order these reads ahead of the other CTAs' stores; a fence of every thread would wait for its stores of the tile before
+      // as well (8 x 1M: 549 us, 530 so).
+      uint32_t used = __float_as_uint(w);
+#pragma unroll
+      for (int u = 0; u < kMvUnits; u++) used |= x[u].x | x[u].w;
+      __syncthreads_or((int)used);
+      if (t == 0) ptx::st_release_u32(flag + i, 1u);
+      if (t < 2) wait_read(lo, hi, i, t, 2);
       __syncthreads();
     }
 #pragma unroll
