@@ -183,15 +183,13 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
   const int64_t row = A.table_stride * A.page, dst_row = A.dst_stride * A.page;
   int n = __ldg(A.seq_len + b), k = __ldg(A.keep + b);
   const bool bad = n < 0 || k < 0 || n > row || min(n, k) > dst_row || (A.from != nullptr && min(n, k) > A.from_stride);
-  if (bad) {
-    if (t == 0 && rank == 0) record_error(A.status, CSA2_ERR_BOUNDS);
-    if (!A.in_place) n = 0;
-    k = 0;
-  }
+  // (a sequence that is out of range keeps its length and moves nothing: from here on it has no entries)
+  const int stays = !bad ? min(n, k) : A.in_place ? n : 0;
+  if (bad) n = k = 0;
   k = min(n, k);
   if (t == 0 && rank == 0) {
-    // (a sequence that is out of range keeps its length and moves nothing)
-    W.meta[b] = make_int4(bad ? 0 : n, k, bad ? n : k, 0);
+    if (bad) record_error(A.status, CSA2_ERR_BOUNDS);
+    W.meta[b] = make_int4(n, k, stays, 0);
     if (b == 0) *W.ticket = 0u;
   }
   const int last = min(A.recent, k), m = n - last, kk = k - last;        // candidates, those of them that stay
@@ -201,7 +199,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
   const int per_warp = (t1 - t0 + kEvWarps - 1) / kEvWarps;
   const int w0 = min(t0 + warp * per_warp, t1), w1 = min(w0 + per_warp, t1);
   for (int i = t0 + t; i < t1; i += kEvThreads) W.flag[(int64_t)b * W.tile_stride + i] = 0u;
-  if (bad || k == 0) return;                         // (the whole cluster)
+  if (k == 0) return;                                // (the whole cluster)
   EvictRow R;
   R.weight = A.weight;
   R.table = A.table + (int64_t)b * A.table_stride;

@@ -1,0 +1,57 @@
+"""GPU tests of the operators that decide what a paged cache keeps at the calls that their contracts allow and ordinary
+steps do not make: lengths far out of range, ranges that cross, runs long enough for every buffer to be used again."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from tests import keep_reference as K  # noqa: E402
+from tests.test_gpu_keep import BOUNDS, _i32, _tables  # noqa: E402
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import compressed_sparse_attention_index_gb300 as c
+    return c
+
+
+# ------------------------------------------------------------------ eviction
+def _evict_told(lib, r, lens, told, keep, recent, page, in_place):
+    """An eviction of sequences that have `lens` entries and are said to have `told`: (what the kernels leave, what they
+    should, the bytes behind the workspace's declared size)."""
+    n_seq, cols = len(lens), max(-(-n // page) for n in lens) + 1
+    n_pages = sum(-(-n // page) for n in lens) + 2
+    table, _ = _tables(r, lens, page, cols, n_pages)
+    kept = [max(0, min(a, k)) for a, k in zip(lens, keep)]
+    dst_cols, n_dst = max(1, max(-(-k // page) for k in kept)), sum(-(-k // page) for k in kept) + 2
+    dst_table, _ = _tables(r, kept, page, dst_cols, n_dst)
+    pages = r.integers(0, 256, (n_pages, page, 288), dtype=np.uint8)
+    w = np.exp(2 * r.normal(size=n_pages * page)).astype(np.float32)
+    P, W, T, L = torch.from_numpy(pages.copy()).cuda(), torch.from_numpy(w.copy()).cuda(), _i32(table), _i32(told)
+    dP, dW, dT = torch.zeros((n_dst, page, 288), dtype=torch.uint8, device="cuda"), torch.zeros(n_dst * page, device="cuda"), _i32(dst_table)
+    size = lib.csa2_workspace_size(lib.CSA2_OP_EVICT, n_seq, cols * page)
+    ws = torch.full((size + (80 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    if in_place:
+        lib.csa2_evict(P, W, n_pages, page, T, cols, L, _i32(keep), n_seq, recent, P, W, n_pages, T, cols, L, None, 0, ws, size)
+    else:
+        lib.csa2_evict(P, W, n_pages, page, T, cols, L, _i32(keep), n_seq, recent, dP, dW, n_dst, dT, dst_cols, L, None, 0, ws, size)
+    status = lib.csa2_get_device_status()
+    want = K.evict(pages, w, page, table, told, keep, recent, np.zeros_like(dP.cpu().numpy()), np.zeros(n_dst * page, np.float32),
+                   table if in_place else dst_table, None, in_place)
+    assert np.array_equal(L.cpu().numpy(), want[2])
+    assert np.array_equal((P if in_place else dP).cpu().numpy(), want[0])
+    assert np.array_equal((W if in_place else dW).cpu().numpy(), want[1].astype(np.float32))
+    assert status == (0 if want[4] else BOUNDS)
+    assert bool((ws[size:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("told", [{0: 90_000}, {4: 30_000}, {0: 2**31 - 1}, {4: 2**31 - 1}, {2: -1000}, {0: -(2**31)},
+                                  {0: -5000, 1: 2**31 - 1, 3: -129}])
+def test_evict_lengths_far_out_of_range(lib, in_place, told):
+    """A sequence of an impossible length is left as it is, the others move, and nothing behind the workspace is written
+    (its tiles were taken from the length that it was told)."""
+    lens = [400, 700, 130, 1000, 260]
+    _evict_told(lib, np.random.default_rng(len(told) + in_place), lens, [told.get(b, n) for b, n in enumerate(lens)],
+                [150, 300, 70, 999, 5], 10, 16, in_place)
