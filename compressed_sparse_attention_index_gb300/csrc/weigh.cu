@@ -457,7 +457,7 @@ __device__ __forceinline__ void wg_fetch_rows(const WeighArgs &A, const WgWs &W,
         const int i = C.c * kWgChunk + 32 * g + lane;
         j[g] = i < A.sel_stride && seq >= 0 ? __ldg(A.sel + (int64_t)C.b * A.sel_stride + i) : -1;
         if (j[g] >= vis) {
-          out |= vis >= 0;                           // (a query that is out of range itself is recorded already)
+          out |= vis > 0;                            // (one that sees nothing has no selection; one out of range is recorded already)
           j[g] = -1;
         }
       }

@@ -650,7 +650,8 @@ csa2_status csa2_page_plan_at(const int32_t *seq_len, const int32_t *new_len, co
  *   sel          NULL, or (device) int32 [n_q][sel_stride], as csa2_paged_attn's: a
  *                query sees the entries sel[q] only; one named twice counts twice.
  *                decay still takes all entries below the largest n_vis.  (An entry
- *                without a page is recorded where it is selected.)
+ *                without a page is recorded where it is selected.)  Of a query
+ *                with an n_vis of 0 it is not read.
  *   n_vis        (device) int32 [n_q]; outside [0, table_stride * page_size]:
  *                recorded, the query adds nothing.
  *   lse          (device) fp32 [n_q][64].

@@ -55,3 +55,43 @@ def test_evict_lengths_far_out_of_range(lib, in_place, told):
     lens = [400, 700, 130, 1000, 260]
     _evict_told(lib, np.random.default_rng(len(told) + in_place), lens, [told.get(b, n) for b, n in enumerate(lens)],
                 [150, 300, 70, 999, 5], 10, 16, in_place)
+
+
+# ------------------------------------------------------------------ attention weights
+def test_weigh_selections_of_refused_drafts():
+    """plan, write, attend(sel), accept, weigh(sel), as a step is documented: refused drafts and rows without a token, whose
+    selections still name entries, vote for nothing and are no error."""
+    import compressed_sparse_attention_index_gb300 as lib
+    from compressed_sparse_attention_index_gb300.decode import PagedCache
+    g = torch.Generator().manual_seed(4)
+    rows = lambda n: (torch.randn((n, 64, 512), generator=g).bfloat16().cuda(), torch.randn((n, 512), generator=g).bfloat16().cuda())
+    c = PagedCache(3, 90, 16, 400, 160, voters=20)
+    c.step(_i32([90, 1, 69]), *rows(160))
+    new, kept, k = [5, 4, 6], [2, 0, 6], 33
+    for step in range(2):
+        lens = c.seq_len.tolist()
+        n = sum(new) + 3
+        c.plan(_i32(new), rows=n)
+        q, latent = rows(n)
+        c.write(q, latent)
+        sel = np.full((n, k), -1)
+        at = 0
+        for b in range(3):
+            for t in range(new[b]):
+                js = np.sort(np.random.default_rng(at + 50 * step).permutation(lens[b] + t + 1)[:k])
+                sel[at, :len(js)] = js
+                at += 1
+        sel[at:] = np.arange(k)
+        c.attend(_i32(sel))
+        c.accept(_i32(kept))
+        assert lib.csa2_get_device_status() == 0
+        before = c.weight.cpu().numpy()
+        c.weigh(_i32(sel), decay=0.5)
+        status = lib.csa2_get_device_status()
+        first, n_vis = np.concatenate([[0], np.cumsum(new)]), np.zeros(n, np.int64)
+        for b in range(3):
+            n_vis[first[b]:first[b] + kept[b]] = lens[b] + 1 + np.arange(kept[b])
+        want, room, fine = K.attn_weight(c.q[:n].double().cpu().numpy(), c.pages.cpu().numpy(), 16, c.table.cpu().numpy(), first,
+                                         np.where(n_vis[:, None] > 0, sel, -1), n_vis, c.lse[:n].cpu().numpy(), 0.5, before, before)
+        assert fine and np.all(np.abs(c.weight.cpu().numpy() - want) <= room)
+        assert status == 0
