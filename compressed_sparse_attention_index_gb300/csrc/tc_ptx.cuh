@@ -118,6 +118,13 @@ __device__ __forceinline__ bool poll_nonzero_u64(const uint64_t *p, uint64_t &v,
   return true;
 }
 
+// ------------------------------------------------------------------ clusters
+// Another CTA's shared memory may be touched only once that CTA has begun.  cluster_begin() says that this one has, and
+// cluster_begun() returns when all of the cluster have: in this order, by every thread, before the first such access unless a
+// whole cluster barrier comes ahead of it.
+__device__ __forceinline__ void cluster_begin() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_begun() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // ------------------------------------------------------------------ copies
 __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int32_t x, int32_t y, uint64_t *bar) {
   asm volatile(

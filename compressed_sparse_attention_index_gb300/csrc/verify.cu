@@ -307,6 +307,7 @@ __global__ void __launch_bounds__(kVfThreads, kVfCtas) verify_sample_kernel(cons
     }
     return;
   }
+  if (parts > 1) ptx::cluster_begin();
   const T *target = static_cast<const T *>(A.target), *draft = static_cast<const T *>(A.draft);
   // the first refused draft, a lane to a draft
   const int drafts = c1 - c0 - 1;
@@ -357,6 +358,7 @@ __global__ void __launch_bounds__(kVfThreads, kVfCtas) verify_sample_kernel(cons
 #pragma unroll 1
   for (int pass = 0; pass < 2; pass++) {
     Pair32 s = warp_scan(W.sum(g0, g1, lane), lane).from(31);
+    if (parts > 1 && pass == 0) ptx::cluster_begun();          // (the others' sums may be written)
     if (lane < parts) put_pair(&sums[pass][seg], (uint32_t)lane, s);
     __syncwarp();
     cluster_sync();

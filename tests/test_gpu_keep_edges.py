@@ -95,3 +95,56 @@ def test_weigh_selections_of_refused_drafts():
                                          np.where(n_vis[:, None] > 0, sel, -1), n_vis, c.lse[:n].cpu().numpy(), 0.5, before, before)
         assert fine and np.all(np.abs(c.weight.cpu().numpy() - want) <= room)
         assert status == 0
+
+
+# ------------------------------------------------------------------ clusters
+def test_clusters_beside_other_work(lib):
+    """Rows that clusters share, verified and evicted while another stream's kernels hold SMs, so that the CTAs of a cluster
+    do not find the chip empty: what they give alone."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    n_seq, vocab, n, page = 24, 131_072, 60_000, 16
+    i32 = dict(dtype=torch.int32, device="cuda")
+    rows = 3 * n_seq
+    target = torch.softmax(2.5 * torch.randn((rows, vocab), generator=g, device="cuda"), 1)
+    draft = torch.softmax(torch.log(target) + 0.5 * torch.randn((rows, vocab), generator=g, device="cuda"), 1)
+    tokens = torch.randint(0, vocab, (rows,), generator=g, **i32)
+    u, v = torch.rand(rows, generator=g, device="cuda") * 0.3, torch.rand(n_seq, generator=g, device="cuda")
+    first = torch.arange(n_seq + 1, **i32) * 3
+    cols = n // page
+    table = torch.randperm(n_seq * cols, generator=g, device="cuda").to(torch.int32).view(n_seq, cols)
+    pages = torch.randint(0, 256, (n_seq * cols, page, 288), generator=g, dtype=torch.uint8, device="cuda")
+    weight = torch.rand(n_seq * n, generator=g, device="cuda")
+    lens = torch.full((n_seq,), n, **i32)
+    # all stay; the latest alone; some of both
+    keeps = [(lens, 100), (lens // 2, n), (lens // 2, 500)]
+    ws = torch.empty(lib.csa2_workspace_size(lib.CSA2_OP_EVICT, n_seq, n), dtype=torch.uint8, device="cuda")
+
+    def call(stream):
+        out = []
+        for d in (draft, None):
+            kept, nxt = torch.full((n_seq,), -5, **i32), torch.full((n_seq,), -5, **i32)
+            lib.csa2_verify_drafts(lib.CSA2_VERIFY_SAMPLE, target, vocab, d, vocab if d is not None else 0, lib.CSA2_PROB_F32, vocab, tokens, first,
+                                   n_seq, rows, u, v, kept, nxt, None, 0, stream)
+            out += [kept, nxt]
+        for keep, recent in keeps:
+            dst, w, new = torch.zeros_like(pages), torch.zeros_like(weight), torch.zeros(n_seq, **i32)
+            source = torch.full((n_seq, n), -1, **i32)
+            lib.csa2_evict(pages, weight, len(pages), page, table, cols, lens, keep, n_seq, recent, dst, w, len(pages), table.flip(0).contiguous(), cols,
+                           new, source, n, ws, ws.numel(), stream)
+            out += [source, w, new]
+        return out
+    want = call(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    assert all((want[4 + 3 * i][:, :k] >= 0).all() for i, k in ((0, n), (1, n // 2), (2, n // 2)))
+    assert torch.equal(want[4], torch.arange(n, **i32).expand(n_seq, n)) and torch.equal(want[7][:, :n // 2], torch.arange(n - n // 2, n, **i32).expand(n_seq, -1))
+    side, a = torch.cuda.Stream(), torch.randn((4096, 4096), device="cuda")
+    for _ in range(4):
+        with torch.cuda.stream(side):
+            b = a
+            for _ in range(20):
+                b = torch.sin(b @ a)
+        got = call(torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+    assert lib.csa2_get_device_status() == 0
