@@ -208,6 +208,9 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
   R.mul = A.page_mul;
   R.shift = A.page_shift;
   R.status = A.status;
+  // (without a histogram the counts are the first that one CTA writes into another: all have to have begun by then)
+  const bool counts_first = ctas > 1 && !(kk > 0 && kk < m);
+  if (counts_first) ptx::cluster_begin();
   // Keys in shared memory: of this warp's first kept_tiles tiles, and behind them two tiles at a time of the others.
   uint32_t *mine = ev_keys + (size_t)warp * cache_tiles * kMvTile + lane * 4;
   uint4 *far_keys = reinterpret_cast<uint4 *>(W.keys + (int64_t)b * W.tile_stride * kMvTile) + lane;
@@ -399,6 +402,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
         S.eq[warp] = eq;
       }
       __syncthreads();
+      if (counts_first) ptx::cluster_begun();
       gt = lane < warp ? S.gt[lane] : 0u;
       eq = lane < warp ? S.eq[lane] : 0u;
       if (ctas > 1) {
