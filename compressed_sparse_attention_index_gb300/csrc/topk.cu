@@ -1071,6 +1071,7 @@ __global__ void __launch_bounds__(kCollectThreads) topk_collect_kernel(TopkSrc S
   __shared__ uint64_t kth_sh;                                // (CTA 0) the smallest selected key
   griddep_wait();
   griddep_launch();
+  ptx::cluster_begin();
   const int q = blockIdx.y, P = gridDim.x, part = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool plain = GROUPS || (S.pool == nullptr && S.block == 1);
@@ -1376,6 +1377,7 @@ __global__ void __launch_bounds__(kCollectThreads) topk_collect_kernel(TopkSrc S
   // another CTA's shared memory, so the others may leave
   const int slot_cap = kCandCap / P;
   __syncthreads();                                     // the sorted lc is written
+  ptx::cluster_begun();                                // CTA 0 may be written to
   if (W.hand.flag != nullptr) {
     // hand this CTA's candidates to the attention grid (already running): in
     // index order or not at all; they are counted in after the cluster
