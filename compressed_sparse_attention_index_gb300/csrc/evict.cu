@@ -494,19 +494,20 @@ __global__ void __launch_bounds__(kMvThreads, 4) evict_move_kernel(const __grid_
     uint32_t *flag = W.flag + (int64_t)b * W.tile_stride;
     const int32_t *before = W.before + (int64_t)b * W.tile_stride;
     // waits, the x-th tile for x = t, t + step, .., until the entries at the places of ranks [lo, hi) are read, and none is of
-    // a tile behind this one (`self`)
+    // a tile behind this one (`self`); false: a wait ran out
     auto wait_read = [&](int lo, int hi, int self, int from, int step) {
       for (int x = lo / kMvTile + from; lo < hi && x <= (hi - 1) / kMvTile; x += step)
         if (x != self && !ptx::poll_at_least_u32(flag + x, 1u)) {
           record_error(A.status, CSA2_ERR_TIMEOUT);
-          break;
+          return false;
         }
+      return true;
     };
     if (i >= moved(k)) {                             // places that nothing is at any more
       const int p0 = k / kMvTile + (i - moved(k)) * kMvClear, p1 = min(p0 + kMvClear, (n - 1) / kMvTile + 1);
       if (k > 0) {
-        wait_read(__ldcg(before + p0), __ldcg(before + p1), -1, t, kMvThreads);
-        __syncthreads();
+        const bool read = wait_read(__ldcg(before + p0), __ldcg(before + p1), -1, t, kMvThreads);
+        if (!__syncthreads_and(read)) return;        // (as below)
       }
       for (int j = max(k, p0 * kMvTile) + t; j < min(n, p1 * kMvTile); j += kMvThreads) {
         const int c = (int)(((uint64_t)(unsigned)j * A.page_mul) >> A.page_shift), id = __ldg(table + c);
@@ -552,8 +553,10 @@ __global__ void __launch_bounds__(kMvThreads, 4) evict_move_kernel(const __grid_
       for (int u = 0; u < kMvUnits; u++) used |= x[u].x | x[u].w;
       __syncthreads_or((int)used);
       if (t == 0) ptx::st_release_u32(flag + i, 1u);
-      if (t < 2) wait_read(lo, hi, i, t, 2);
-      __syncthreads();
+      // Nothing is written where something may not have been read.  The CTA ends, and the waits for its next tile run out too, so
+      // that all end in bounded time.
+      const bool read = t >= 2 || wait_read(lo, hi, i, t, 2);
+      if (!__syncthreads_and(read)) return;
     }
 #pragma unroll
     for (int u = 0; u < kMvUnits; u++) {

@@ -697,6 +697,9 @@ csa2_status csa2_attn_weight(const void *q, const void *pages, int n_pages, int 
  *   A negative length or keep, a length that the block table cannot hold, or more
  *   kept entries than the destination or from can: CSA2_ERR_BOUNDS is recorded,
  *   nothing of the sequence moves, and new_len is seq_len in place, else 0.
+ *   In place the kernel's blocks wait for one another's reads.  A wait that runs
+ *   out (2 s) is recorded as CSA2_ERR_TIMEOUT: places that had not been written by
+ *   then keep what they held, and the sequences are not whole any more.
  *   workspace    (device) >= csa2_workspace_size(CSA2_OP_EVICT, n_seq, table_stride
  *                * page_size, 0) bytes, 256-B aligned; no initialisation.  Calls
  *                that may run at the same time need one each.
