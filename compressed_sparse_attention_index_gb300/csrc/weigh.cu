@@ -233,6 +233,8 @@ __global__ void __launch_bounds__(kPrepThreads) weigh_prep_kernel(const __grid_c
   const bool sel = A.sel != nullptr;
   const int items = sel ? A.n_q : A.n_seq;
   __shared__ int wt[kPrepThreads / 32], base_sh;
+  // (ranges that cross may have more products than 31 bits hold: sums stay at INT_MAX then)
+  auto sum = [](int a, int b) { return (int)min((unsigned)a + (unsigned)b, (unsigned)INT_MAX); };
   if (t == 0) base_sh = 0;
   for (int i0 = 0; i0 < items; i0 += kPrepThreads) {
     const int i = i0 + t;
@@ -278,21 +280,26 @@ __global__ void __launch_bounds__(kPrepThreads) weigh_prep_kernel(const __grid_c
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-      if (lane >= o) inc += y;
+      if (lane >= o) inc = sum(inc, y);
     }
     if (lane == 31) wt[warp] = inc;
     __syncthreads();
-    int ahead = base_sh + inc - own;
-    for (int w = 0; w < warp; w++) ahead += wt[w];
+    int ahead = sum(base_sh, inc - own);
+    for (int w = 0; w < warp; w++) ahead = sum(ahead, wt[w]);
     if (i < items) {
       W.item[i] = make_int4(most, groups, c0, cnt);
       W.off[i] = ahead;
     }
     __syncthreads();
-    if (t == kPrepThreads - 1) base_sh = ahead + own;
+    if (t == kPrepThreads - 1) base_sh = sum(ahead, own);
     __syncthreads();
   }
-  if (t == 0) W.off[items] = base_sh;
+  // more products than ranges that do not cross can have: none (nothing else of the items is read then)
+  if (t == 0) {
+    const bool fits = base_sh < INT_MAX;
+    if (!fits) record_error(A.status, CSA2_ERR_BOUNDS);
+    W.off[items] = fits ? base_sh : 0;
+  }
 }
 
 // ------------------------------------------------------------------ a CTA's run

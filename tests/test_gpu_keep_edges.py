@@ -148,3 +148,17 @@ def test_clusters_beside_other_work(lib):
         for x, y in zip(got, want):
             assert torch.equal(x, y)
     assert lib.csa2_get_device_status() == 0
+
+
+def test_weigh_ranges_that_cross(lib):
+    """Ranges of queries that descend and cross: whose work passes 32 bits, nothing is weighed and the error recorded."""
+    page, stride, n_q, n_seq = 1 << 20, 2000, 60, 12             # 30 groups of two over 16 M chunks, from six of the ranges
+    pages, w = torch.zeros((1, page, 288), dtype=torch.uint8, device="cuda"), torch.full((page,), -7.0, device="cuda")
+    table = torch.zeros((n_seq, stride), dtype=torch.int32, device="cuda")
+    q, lse = torch.ones((n_q, 64, 512), dtype=torch.bfloat16, device="cuda"), torch.zeros((n_q, 64), device="cuda")
+    n_vis = torch.full((n_q,), page * stride, dtype=torch.int32, device="cuda")
+    ws = torch.empty(lib.csa2_workspace_size(lib.CSA2_OP_ATTN_WEIGHT, n_q, n_seq, 0), dtype=torch.uint8, device="cuda")
+    first = [0, n_q] * (n_seq // 2) + [n_q]
+    lib.csa2_attn_weight(q, pages, 1, page, table, stride, _i32(first), n_seq, None, 0, n_vis, lse, n_q, 1.0, None, w, None, ws, ws.numel())
+    assert lib.csa2_get_device_status() == BOUNDS
+    assert bool((w == -7.0).all())
