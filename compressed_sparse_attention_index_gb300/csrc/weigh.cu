@@ -184,15 +184,22 @@ __global__ void __launch_bounds__(kPrepThreads) weigh_prep_kernel(const __grid_c
   }
   if (blockIdx.x > 0) {
     const int q = ((int)blockIdx.x - 1) / kPrepCtas, part = ((int)blockIdx.x - 1) % kPrepCtas;
-    if (A.sel != nullptr && part == 0 && t == 0) {
-      int lo = 0, hi = A.n_seq;                      // the last sequence with first <= q
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(A.first + mid) <= q) lo = mid;
+    if (A.sel != nullptr && part == 0 && warp == 0) {
+      int seq = 0, hi = A.n_seq;                     // the last sequence with first <= q
+      while (hi - seq > 1) {
+        const int mid = (seq + hi) >> 1;
+        if (__ldg(A.first + mid) <= q) seq = mid;
         else hi = mid;
       }
       int c0, c1;
-      W.q_seq[q] = weigh_queries(A, lo, c0, c1) && q >= c0 && q < c1 ? lo : -1;
+      if (!(weigh_queries(A, seq, c0, c1) && q >= c0 && q < c1)) {
+        // a query of no sequence, or ranges that do not ascend: the first one that has it
+        seq = INT_MAX;
+        for (int b = lane; b < A.n_seq && seq == INT_MAX; b += 32)
+          if (weigh_queries(A, b, c0, c1) && q >= c0 && q < c1) seq = b;
+        seq = __reduce_min_sync(0xFFFFFFFFu, seq);
+      }
+      if (lane == 0) W.q_seq[q] = seq < INT_MAX ? seq : -1;
     }
     // a head a warp, 16 dims a lane
     {
@@ -909,9 +916,9 @@ __global__ void __launch_bounds__(kWgThreads, 1) weigh_kernel(const __grid_const
 // Adds the selections' weights, a CTA per sequence, query by query: entries that several queries
 // selected get their parts in the queries' order, so the sums are the same on every call.  (Within
 // a query an entry named twice gets the same part twice: their order does not matter.)
-// Slots and parts of kAddAhead queries are read at a time.
+// Slots and parts of kAddAhead queries are read at a time.  (Ranges that cross: a query's part is that of one of its sequences.)
 constexpr int kAddAhead = 8;
-__global__ void __launch_bounds__(kTopK) weigh_add_kernel(const __grid_constant__ WeighArgs A, const float *part) {
+__global__ void __launch_bounds__(kTopK) weigh_add_kernel(const __grid_constant__ WeighArgs A, const float *part, const int32_t *q_seq) {
   const int t = threadIdx.x, b = blockIdx.x;
   griddep_wait();
   griddep_launch();
@@ -925,7 +932,7 @@ __global__ void __launch_bounds__(kTopK) weigh_add_kernel(const __grid_constant_
     for (int i = 0; i < kAddAhead; i++) j[i] = q0 + i < c1 && t < A.sel_stride ? __ldg(A.sel + (int64_t)(q0 + i) * A.sel_stride + t) : -1;
 #pragma unroll
     for (int i = 0; i < kAddAhead; i++) {
-      const bool in = j[i] >= 0 && j[i] < weigh_vis(A, q0 + i);
+      const bool in = j[i] >= 0 && j[i] < weigh_vis(A, q0 + i) && __ldg(q_seq + q0 + i) == b;
       s[i] = in ? weigh_slot(A, b, j[i]) : -1;
       w[i] = in ? __ldg(part + (int64_t)(q0 + i) * A.sel_stride + t) : 0.f;
     }
@@ -973,7 +980,7 @@ cudaError_t launch_weigh(WeighArgs A, void *ws, cudaStream_t st) {
   const int decay_parts = A.prior == A.weight && A.decay == 1.f ? 0 : (int)(tiles < 512 ? tiles : 512);
   const cudaError_t e = launch_products<1, true>(A, W, decay_parts, dev, st);
   if (e != cudaSuccess) return e;
-  return launch_pdl(weigh_add_kernel, dim3((unsigned)A.n_seq), dim3(kTopK), 0, st, 1u, A, (const float *)W.part);
+  return launch_pdl(weigh_add_kernel, dim3((unsigned)A.n_seq), dim3(kTopK), 0, st, 1u, A, (const float *)W.part, (const int32_t *)W.q_seq);
 }
 
 }  // namespace csa2

@@ -647,7 +647,8 @@ csa2_status csa2_page_plan_at(const int32_t *seq_len, const int32_t *new_len, co
  *   first        (device) int32 [n_seq + 1]: sequence b's queries are first[b] ..
  *                first[b + 1] - 1 (csa2_page_plan's); out of range of n_q: recorded, the
  *                sequence is skipped (and all, where ranges cross so often that their work
- *                passes 32 bits).  A sequence without queries is left as it is.
+ *                passes 32 bits; with sel a query that several ranges have counts for
+ *                one of them).  A sequence without queries is left as it is.
  *   sel          NULL, or (device) int32 [n_q][sel_stride], as csa2_paged_attn's: a
  *                query sees the entries sel[q] only; one named twice counts twice.
  *                decay still takes all entries below the largest n_vis.  (An entry

@@ -162,3 +162,37 @@ def test_weigh_ranges_that_cross(lib):
     lib.csa2_attn_weight(q, pages, 1, page, table, stride, _i32(first), n_seq, None, 0, n_vis, lse, n_q, 1.0, None, w, None, ws, ws.numel())
     assert lib.csa2_get_device_status() == BOUNDS
     assert bool((w == -7.0).all())
+
+
+@pytest.mark.parametrize("first", [[0, 2, 100, 4, 6], [0, 2, -7, 4, 6], [0, 2, 1, 6, 6], [6, 0, 2, 2, 5]])
+def test_weigh_selections_beside_a_range_that_is_out(lib, oracle_lib, first):
+    """A range that is out of range takes its own sequence out, and no other, also where it stands in the way of a search."""
+    from tests import paged_reference as R
+    from tests.test_gpu_keep import _weigh, _weigh_case
+    c = _weigh_case(oracle_lib, 21, [300, 200, 150, 400], 16, [2, 1, 1, 2], 40)
+    c["first"] = np.array(first)
+    c["n_vis"][:] = 140
+    r = np.random.default_rng(1)
+    c["sel"] = np.stack([np.sort(r.permutation(140)[:40]) for _ in range(6)])
+    args = [R.bf16_values(c["q"]).astype(np.float64), c["pages"], 16, c["table"]]
+    tail = [c["lse"], c["decay"], c["prior"], np.full(len(c["pages"]) * 16, -7.0)]
+    # a query that two ranges have is one of theirs: here the one that a search of the starts comes upon, else the first
+    valid = [b for b in range(4) if 0 <= first[b] <= first[b + 1] <= 6]
+    owner = [[b for b in valid if first[b] <= i < first[b + 1]] for i in range(6)]
+    got = _weigh(lib, c)
+    status = lib.csa2_get_device_status()
+    got = got.cpu().numpy()
+    fits = []
+    for pick in (0, -1):
+        sel = []
+        for b in range(4):                                    # one sequence at a time, the others' queries without a selection
+            mine = np.array([bool(o) and o[pick] == b for o in owner])
+            sel.append(np.where(mine[:, None], c["sel"], -1))
+        want, room = tail[3].copy(), np.zeros(len(got))
+        for b in valid:
+            f = np.array([first[b], first[b + 1]])
+            x, e, _ = K.attn_weight(*args[:3], args[3][b:b + 1], f, sel[b], c["n_vis"], *tail)
+            touched = (x != -7.0) | (e > 0)
+            want[touched], room[touched] = x[touched], e[touched]
+        fits.append(bool(np.all(np.abs(got - want) <= room)))
+    assert any(fits) and status == BOUNDS
