@@ -163,8 +163,8 @@ class PagedCache:
     costs that of a few rows, whatever max_tokens is.  Everything stays on the
     device and on one stream (the current one, or `stream`, a torch.cuda.Stream),
     so a step can be captured into a CUDA graph and replayed: new_len and the
-    inputs are read where they lie.  (write, attend and advance go with the last plan that
-    the host made: a graph that plans should hold the whole step.)  A new cache is whole when its constructor returns
+    inputs are read where they lie.  (write, attend, advance and weigh go with the last plan that
+    the host made: a graph that plans should hold the whole step; weigh and evict may be behind it.)  A new cache is whole when its constructor returns
     (it waits for its fills); from then on the order of calls on different streams is the
     caller's, and so is the cache's life until work on other streams than the
     constructor's is over.
@@ -234,7 +234,9 @@ class PagedCache:
         self._rows_at = torch.arange(max_tokens, **i32)
         self._limit = (torch.zeros(max_tokens, **i32), torch.zeros(max_tokens, dtype=torch.bool, device=device))
         self.kept, self.next = torch.zeros(n_seq, **i32), torch.full((n_seq,), -1, **i32)
-        self._open, self._weighable = False, False        # a planned step is not advanced yet; the last one may be weighed
+        # A planned step is not advanced yet; the last one may be weighed.  What graphs hold the host sees once, however often
+        # it is replayed: the last step is in one; what followed it is in one.
+        self._open, self._weighable, self._step_in_graph, self._spent_in_graph = False, False, False, False
         self.weight = None
         u8 = dict(dtype=torch.uint8, device=device)
         self._ws_verify = torch.empty(max(1, L.csa2_workspace_size(L.CSA2_OP_VERIFY, max_tokens, 0)), **u8)
@@ -260,6 +262,9 @@ class PagedCache:
                                      (self.out[:rows], self.lse[:rows]))
         self.rows = rows
         self.desc, self._d, self._count, self._rows = v
+
+    def _capturing(self):
+        return self.pages.is_cuda and torch.cuda.is_current_stream_capturing()
 
     def _here(self):
         """The kernels run on the current device, and read the cache there."""
@@ -289,7 +294,7 @@ class PagedCache:
         L.csa2_page_plan_at(self.seq_len, new_len, self.gone, self.n_seq, self.page_size, self.n_pages, self.free,
                             self.n_pages, self.free_head, self.table, self.table.shape[1], self.swa_cap, self.desc,
                             rows, self.first, self.totals, stream)
-        self._open, self._weighable = True, False
+        self._open, self._weighable, self._step_in_graph = True, False, False
 
     def _that_fit(self, new_len, stream):
         """new_len, and -1, which the plan reports and gives no tokens, where the ring does not hold the records of the
@@ -354,7 +359,7 @@ class PagedCache:
             first.copy_(self._d[5])
         torch.ge(counted, 0, out=added)
         self._state.index_add_(0, place, add)
-        self._open, self._weighable = False, True
+        self._open, self._weighable, self._step_in_graph = False, True, self._capturing()
 
     def verify(self, tokens, target, draft=None, u=None, v=None, greedy=False, stream=None):
         """(kept, next), device int32 [n_seq]: how many of each sequence's planned tokens stay, and the token that follows.
@@ -421,12 +426,22 @@ class PagedCache:
         if self._open:
             raise ValueError("a step is not over: advance or accept first")
 
+    def _no_step_since(self):
+        """The last step is weighed, or its entries have moved (of a step in a graph: until that is replayed)."""
+        self._weighable, self._spent_in_graph = False, self._capturing()
+        if self._spent_in_graph:
+            self._step_in_graph = False
+
     def weigh(self, sel=None, decay=1.0, params=None, stream=None):
         """weight = decay x weight + what the last step's queries gave (over sel, where they attended to it), of the
-        entries that its sequences see; behind advance or accept, once."""
+        entries that its sequences see; behind advance or accept, once (which of a graph's replays it is behind, the cache
+        does not know)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.weigh(sel, decay, params)
         self._keeps_weights()
-        if not self._weighable:
-            raise ValueError("no step since the last eviction")
+        if not self._weighable and not self._step_in_graph and (self._spent_in_graph or not self._capturing()):
+            raise ValueError("no step since the last weigh or eviction")
         if self.rows > self.voters:
             raise ValueError(f"a step of up to {self.voters} rows expected, not {self.rows}")
         if sel is not None:
@@ -435,7 +450,8 @@ class PagedCache:
             self._want("sel", sel, self.rows, sel.shape[1], torch.int32)
         L.csa2_attn_weight(self.q, self.pages, self.n_pages, self.page_size, self.table, self.table.shape[1], self.first,
                            self.n_seq, sel, 0 if sel is None else sel.shape[1], self._d[1], self.lse, self.rows, decay,
-                           self.weight, self.weight, params, self._ws_weigh, self._ws_weigh.numel(), stream)
+                           self.weight, self.weight, params, self._ws_weigh, self._ws_weigh.numel())
+        self._no_step_since()
 
     def evict(self, keep, recent=SWA, stream=None):
         """Cuts sequence b down to keep[b] (device int32 [n_seq]) entries: its last `recent`, and the heaviest of the others;
@@ -454,7 +470,7 @@ class PagedCache:
         torch.sub(self.seq_len, to, out=left)
         self.gone.add_(left)
         self._trim(to)
-        self._weighable = False
+        self._no_step_since()
 
     def step(self, new_len, q, latent, q_gain=None, latent_gain=None, eps=1e-6, sel=None, params=None, stream=None):
         """plan, write, attend and advance on as many rows as q and latent have."""

@@ -196,3 +196,42 @@ def test_weigh_selections_beside_a_range_that_is_out(lib, oracle_lib, first):
             want[touched], room[touched] = x[touched], e[touched]
         fits.append(bool(np.all(np.abs(got - want) <= room)))
     assert any(fits) and status == BOUNDS
+
+
+def test_weigh_and_evict_behind_a_replayed_step():
+    """A graph that holds a step up to accept; weigh and evict behind each replay, on the host's stream: the eager state."""
+    import compressed_sparse_attention_index_gb300 as lib
+    from compressed_sparse_attention_index_gb300.decode import PagedCache
+    from tests.test_gpu_keep_run import _state, _step_inputs
+    new, keep = _i32([4, 3]), _i32([60, 1000])
+    eager, graph = (PagedCache(2, 60, 16, 400, 100, voters=8) for _ in range(2))
+    x = _step_inputs(3, 7)
+
+    def step(c):
+        c.plan(new, rows=7)
+        c.write(x["q"], x["latent"])
+        c.attend()
+        c.verify(x["tokens"], x["target"], x["draft"], x["u"], x["v"])
+        c.accept()
+    for c in (eager, graph):
+        c.step(_i32([60, 37]), *(_step_inputs(1, 97)[k] for k in ("q", "latent")))
+        step(c)
+        c.weigh(decay=0.5)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(graph)
+    for seed in range(4, 8):
+        for k, v in _step_inputs(seed, 7).items():
+            x[k].copy_(v)
+        step(eager)
+        g.replay()
+        for c in (eager, graph):
+            c.weigh(decay=0.5, stream=torch.cuda.current_stream())
+            if seed % 2 == 0:
+                c.evict(keep, 20)
+        a, b = _state(eager), _state(graph)
+        for k in a:
+            assert torch.equal(a[k].view(torch.uint8), b[k].view(torch.uint8)), (seed, k)
+    with pytest.raises(ValueError):
+        eager.weigh()
+    assert eager.gone[0] > 0 and lib.csa2_get_device_status() == 0
