@@ -453,20 +453,26 @@ class PagedCache:
                            self.weight, self.weight, params, self._ws_weigh, self._ws_weigh.numel())
         self._no_step_since()
 
-    def evict(self, keep, recent=SWA, stream=None):
+    def evict(self, keep, recent=SWA, stream=None, source=None):
         """Cuts sequence b down to keep[b] (device int32 [n_seq]) entries: its last `recent`, and the heaviest of the others;
-        entries of the last step's descriptors are elsewhere afterwards."""
+        entries of the last step's descriptors are elsewhere afterwards.  source (device int32 [n_seq][m]) gets the places that
+        the entries which stay come from, in order, for what else is kept by place (an indexer's keys); a sequence that keeps
+        more than m is reported and stays as it is."""
         if stream is not None:
             with torch.cuda.stream(stream):
-                return self.evict(keep, recent)
+                return self.evict(keep, recent, source=source)
         self._keeps_weights()
         if not keep.is_contiguous():
             raise ValueError("keep: contiguous int32 expected")
         self._want("keep", keep, self.n_seq, 1, torch.int32)
+        if source is not None:
+            if source.dim() != 2 or not source.is_contiguous():
+                raise ValueError("source: contiguous int32 [n_seq][m] expected")
+            self._want("source", source, self.n_seq, source.shape[1], torch.int32)
         left, to, _ = self._lens.unbind()
         L.csa2_evict(self.pages, self.weight, self.n_pages, self.page_size, self.table, self.table.shape[1], self.seq_len, keep,
-                     self.n_seq, recent, self.pages, self.weight, self.n_pages, self.table, self.table.shape[1], to, None, 0,
-                     self._ws_evict, self._ws_evict.numel())
+                     self.n_seq, recent, self.pages, self.weight, self.n_pages, self.table, self.table.shape[1], to, source,
+                     0 if source is None else source.shape[1], self._ws_evict, self._ws_evict.numel())
         torch.sub(self.seq_len, to, out=left)
         self.gone.add_(left)
         self._trim(to)

@@ -235,3 +235,28 @@ def test_weigh_and_evict_behind_a_replayed_step():
     with pytest.raises(ValueError):
         eager.weigh()
     assert eager.gone[0] > 0 and lib.csa2_get_device_status() == 0
+
+
+def test_evict_of_a_cache_says_which_entries_stayed():
+    """What a caller keeps by place moves along by `source`; a sequence that it cannot hold stays."""
+    import compressed_sparse_attention_index_gb300 as lib
+    from compressed_sparse_attention_index_gb300.decode import PagedCache
+    g = torch.Generator().manual_seed(7)
+    c = PagedCache(3, 60, 16, 300, 240, voters=240)
+    c.step(_i32([150, 20, 70]), torch.randn((240, 64, 512), generator=g).bfloat16().cuda(), torch.randn((240, 512), generator=g).bfloat16().cuda())
+    c.weigh()
+    slot = lambda b, j: c.table[b].long()[j // 16] * 16 + j % 16
+    was = [c.pages.view(-1, 288)[slot(b, torch.arange(n, device="cuda"))] for b, n in enumerate((150, 20, 70))]
+    w = [c.weight[slot(b, torch.arange(n, device="cuda"))] for b, n in enumerate((150, 20, 70))]
+    source = torch.full((3, 61), -9, dtype=torch.int32, device="cuda")
+    c.evict(_i32([60, 30, 5]), 10, source=source)
+    assert c.seq_len.tolist() == [60, 20, 5] and c.gone.tolist() == [90, 0, 65]
+    for b, n in enumerate((60, 20, 5)):
+        j = source[b, :n].long()
+        assert torch.equal(c.pages.view(-1, 288)[slot(b, torch.arange(n, device="cuda"))], was[b][j]) and bool((j[1:] > j[:-1]).all())
+        assert torch.equal(c.weight[slot(b, torch.arange(n, device="cuda"))], w[b][j]) and bool((source[b, n:] == -9).all())
+    assert lib.csa2_get_device_status() == 0
+    few = torch.full((3, 10), -9, dtype=torch.int32, device="cuda")
+    c.evict(_i32([40, 9, 5]), 10, source=few)
+    assert c.seq_len.tolist() == [60, 9, 5] and lib.csa2_get_device_status() == BOUNDS
+    assert bool((few[0] == -9).all()) and few[2, :5].tolist() == [0, 1, 2, 3, 4]

@@ -62,3 +62,14 @@ def test_steps_of_a_graph(cache, monkeypatch):
     cache.weigh()
     with pytest.raises(ValueError):
         cache.weigh()
+
+
+def test_source_refusals(cache):
+    cache.plan(torch.zeros(2, **I32), rows=3)
+    cache.advance()
+    keep = torch.full((2,), 9, **I32)
+    for bad in (torch.zeros(2, **I32), torch.zeros((3, 9), **I32), torch.zeros((2, 9)), torch.zeros((9, 2), **I32).t(), torch.zeros((2, 18), **I32)[:, ::2]):
+        with pytest.raises(ValueError, match="source"):
+            cache.evict(keep, source=bad)
+    cache.evict(keep, source=torch.zeros((2, 9), **I32))
+    assert cache.done.count("csa2_evict") == 1
