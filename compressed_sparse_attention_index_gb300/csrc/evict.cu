@@ -14,12 +14,13 @@
 // places may hold entries that are still to be moved, but only those of its own and of earlier tiles
 // (an entry never moves behind its place, so ranks are not above places): tiles are handed out in order, each
 // raises a flag when it has read, and before it writes waits for the at most two tiles that its places'
-// entries belong to.  A tile that is waited for has been handed out, and reads without waiting for any.
+// entries belong to.  A tile that is waited for has been handed out, and reads without waiting for any.  One whose wait runs out
+// writes nothing.
 // The places behind the kept entries are tiles too, behind a sequence's others: their weights are cleared in the same way.
 //
 // What bounds it: 288 B read and written for each entry that stays (HBM; a record is in 5 granules of 64 B, so 1.1 times its
-// bytes are read), and for the selection the instructions of its five passes.  8 x 1,048,576 entries cut to half: 471 us, 80 of
-// them the selection (in place 530); 33 x 40,001 to 9,999: 56; 1 x 4,096: 15, a chain of latencies and cold code.
+// bytes are read), and for the selection the instructions of its five passes.  8 x 1,048,576 entries cut to half: 464 us, 80 of
+// them the selection (in place 520); 33 x 40,001 to 9,999: 49 (60); 1 x 4,096: 12 (13), a chain of latencies and cold code.
 #include <limits.h>
 
 #include <algorithm>

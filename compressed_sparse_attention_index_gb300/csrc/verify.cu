@@ -9,14 +9,16 @@
 // A token is a whole number, so which side of a border a sum falls on has to be that of the exact
 // one: u q is a product of two fp32 in fp64 (exact), and p - q and the running sums are pairs of fp32
 // (an fp32 sum of 131,072 probabilities picks another token in a call of a few hundred; fp64 has a
-// sixtieth of fp32's rate here, and a few sums of it in every warp took half of the kernel's time).
+// sixtieth of fp32's rate here, and a few sums of it in every warp took half of the kernel's time).  Pairs are good
+// to 2^-46 of the total in rows of up to 2^20, and to 2^-42 in the longest, where the lower halves add up many roundings.
 //
 // What bounds it: one row of p, and of q where a draft was refused, for each sequence (HBM; a few
 // sequences: a chain of loads).  A sequence's row is dealt to the warps of a cluster in
 // contiguous segments, whose sums meet in each CTA through distributed shared memory; the CTA that has the
 // segment where the running sum passes looks through it with all its threads (one warp, 32 groups at a
-// time, took 25 us of a 4,096-entry segment).  256 rows of 131,072 fp32 probabilities: 30 us, 4.5 TB/s; 64 pairs of rows of
-// 100,003 in bf16: 15; one row: 6.5, a chain of seven loads or barriers.  Greedy, 384 rows of 131,072 in bf16: 15, 6.7 TB/s of all rows.
+// time, took 25 us of a 4,096-entry segment).  With rows that are not in L2 yet: 256 of 131,072 fp32 probabilities 34 us, 4.0 TB/s; 64 pairs of
+// 100,003 in bf16 15; one row 6.7, a chain of seven loads or barriers.  Greedy, 384 rows of 131,072 in bf16: 20, 5.0 TB/s of all rows, in two
+// launches, the first of 768 CTAs (five or six an SM).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

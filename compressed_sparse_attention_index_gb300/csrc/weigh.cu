@@ -23,9 +23,9 @@
 // two threads issue the MMAs; eight sum S.
 //
 // What bounds it.  One query a sequence: a chunk's records take 1,600 cycles of HBM and its MMAs 1,060; it takes 2,200, as the 6,000 instructions
-// of its roles (2,600 of them conversions) leave little room for their latencies: 8 x 1,048,576 entries 452 us, 5.5 TB/s.  Two
-// queries: the MMAs' 2,050 cycles a chunk; 8 x 262,144 entries x 16 queries 1,304 us, 1.69 PFLOP/s; 32 x 65,536 x 5: 470 us (its fifth
-// query costs nearly as much as two).  One short row is a chain of latencies: 1 x 4,096 entries 9.7 us, the preparation's 4 among them.
+// of its roles (2,600 of them conversions) leave little room for their latencies: 8 x 1,048,576 entries 452 us, 5.5 TB/s, in short runs, and 488 in long ones, where the power
+// limit lowers the clock.  Two queries: the MMAs' 2,050 cycles a chunk; 8 x 262,144 entries x 16 queries 1,304 us, 1.69 PFLOP/s; 32 x 65,536 x 5: 470 us
+// (505; its fifth query costs nearly as much as two).  One short row is a chain of latencies: 1 x 4,096 entries 9 us, the preparation's 4 among them.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <limits.h>
@@ -973,7 +973,9 @@ cudaError_t launch_weigh(WeighArgs A, void *ws, cudaStream_t st) {
   weigh_magic((unsigned)A.page, A.page_mul, A.page_shift);
   WgWs W;
   wg_layout(&W, ws, A.n_q, A.n_seq, A.sel_stride);
-  if (A.sel == nullptr)                              // two queries at a time where a sequence can have two
+  // Two queries at a time where there are more queries than sequences, so that some sequence has two for sure (how many each has
+  // is on the device).  Else one at a time: right for any, slower where few sequences have all of the queries.
+  if (A.sel == nullptr)
     return A.n_q > A.n_seq ? launch_products<2, false>(A, W, 0, dev, st) : launch_products<1, false>(A, W, 0, dev, st);
   // a CTA for each 1,024 places of a row, up to 512
   const int64_t tiles = (A.table_stride * A.page + 4 * kPrepThreads - 1) / (4 * kPrepThreads);

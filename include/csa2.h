@@ -741,7 +741,7 @@ csa2_status csa2_page_trim(const int32_t *len, const int32_t *new_len, int n_seq
  *     target: the lowest index whose running sum is above v[b] times the total (where
  *     rounding leaves none, the last index of any weight).  If nothing is above zero
  *     there, next is drawn from target[r].  Decided as by exact arithmetic (sums to
- *     about 2^-46 of the total).
+ *     about 2^-46 of the total for a vocab of up to 2^20, 2^-42 for 2^28).
  *   draft NULL: the drafts were not drawn (a lookup): draft[r] is 1 at x, 0 elsewhere.
  *   CSA2_VERIFY_GREEDY: x stays while it is the index of row r's largest entry (the
  *     lowest of equal ones; -0 equals 0; NaN is none), which is next otherwise;
@@ -754,8 +754,8 @@ csa2_status csa2_page_trim(const int32_t *len, const int32_t *new_len, int n_seq
  *   tokens       (device) int32 [n_rows].  A draft outside [0, vocab) is refused and
  *                recorded as CSA2_ERR_BOUNDS.
  *   first        (device) int32 [n_seq + 1], as csa2_page_plan's; out of range of
- *                n_rows: recorded, the sequence gets 0 and -1.  Rows from
- *                first[n_seq] on are not read.
+ *                n_rows (GREEDY: or of first[n_seq]): recorded, the sequence gets 0 and
+ *                -1.  Rows from first[n_seq] on belong to no sequence.
  *   u, v         (device) fp32 [n_rows], [n_seq]: random numbers in [0, 1).
  *   kept         (device) int32 [n_seq]: the step's tokens that stay, the accepted
  *                drafts and the one before them; 0 for a sequence without rows.
